@@ -107,6 +107,8 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_CUDA: return "CUDA runtime or launch error";
     case FA_ERR_DEVICE_TIMEOUT: return "device pipeline wait exceeded its time limit";
     case FA_ERR_CU_SEQLENS: return "cu_seqlens malformed or a sequence longer than N";
+    case FA_ERR_PAGE: return "a page outside the pool, or pages whose copies clash";
+    case FA_ERR_POSITION: return "a position outside the table of angles";
   }
   return "unknown status";
 }
@@ -512,6 +514,246 @@ fa_status fa_fwd_fp8(const void* fp8_buf, size_t fp8_bytes, void* o, float* lse,
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
   return fa::launch_fwd_fp8(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+// Checks of the sizes, weights and angles of the norm and rotation calls, and
+// their places in p (everything but q, k, v and the outputs).
+static fa_status norm_rope_args(fa::NormRopeParams* p, const float* q_weight, const float* k_weight,
+                                float eps, const float* cos, const float* sin, long long T, int Hq,
+                                int Hkv, int d, int rot_dim, int max_pos, int interleaved) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv == 0 || d <= 0 || rot_dim < 0 || rot_dim > d || max_pos < 0)
+    return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hkv > 65535 || T >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  // a warp takes at least 4 rows of a token; 1-D grids must fit 2^31 - 1
+  if (T * ((Hq + 2ll * Hkv + 3) / 4) >= (1ll << 33)) return FA_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return FA_ERR_UNSUPPORTED;
+  if (!q_weight != !k_weight) return FA_ERR_NULL;
+  if (rot_dim && (!cos || !sin)) return FA_ERR_NULL;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return FA_ERR_ALIGN;
+  if (rot_dim && (!aligned16(cos) || !aligned16(sin))) return FA_ERR_ALIGN;
+  p->q_weight = q_weight;
+  p->k_weight = k_weight;
+  p->eps = eps;
+  p->cos = cos;
+  p->sin = sin;
+  p->T = T;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->d = d;
+  p->rot = rot_dim;
+  p->max_pos = max_pos;
+  p->interleaved = interleaved;
+  return FA_OK;
+}
+
+// One [T, H, d] tensor given by its token stride: FA_OK if H heads fit the
+// stride and the rows are 16-byte aligned (a tensor without elements passes).
+static fa_status check_rows(const void* x, long long stride, long long T, int H, int d, int esize) {
+  if (H == 0 || T == 0) return FA_OK;
+  if (!x) return FA_ERR_NULL;
+  if (T > 1 && stride < (long long)H * d) return FA_ERR_SHAPE;
+  if (!aligned16(x) || (stride * esize) % 16 != 0) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+// Sizes of a cache in pages, and their places in p.
+static fa_status page_args(fa::NormRopeParams* p, int B, int N, int page_size, int num_pages, int max_pages) {
+  if (B < 0 || N < 0 || num_pages < 0 || max_pages < 0 || page_size <= 0) return FA_ERR_SHAPE;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  // slots and positions are 32-bit in the kernels
+  if ((long long)num_pages * page_size >= (1ll << 31) || (long long)max_pages * page_size >= (1ll << 30))
+    return FA_ERR_UNSUPPORTED;
+  p->B = B;
+  p->N = N;
+  p->page_size = page_size;
+  p->page_shift = 0;
+  while ((1 << p->page_shift) < page_size) ++p->page_shift;
+  p->num_pages = num_pages;
+  p->max_pages = max_pages;
+  return FA_OK;
+}
+
+fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                          long long q_stride, long long k_stride, const float* q_weight,
+                          const float* k_weight, float eps, const float* cos, const float* sin,
+                          const int32_t* positions, long long T, int Hq, int Hkv, int d,
+                          int rot_dim, int max_pos, int interleaved, fa_dtype dtype, void* stream) {
+  fa::NormRopeParams p = {};
+  fa_status st = norm_rope_args(&p, q_weight, k_weight, eps, cos, sin, T, Hq, Hkv, d, rot_dim, max_pos, interleaved);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_UNSUPPORTED;
+  if (!q_weight && rot_dim == 0) return FA_ERR_UNSUPPORTED;
+  const int esize = dtype == FA_FP32 ? 4 : 2;
+  if ((st = check_rows(q, q_stride, T, Hq, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(k, k_stride, T, Hkv, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(q_out, (long long)Hq * d, T, Hq, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(k_out, (long long)Hkv * d, T, Hkv, d, esize)) != FA_OK) return st;
+  if (rot_dim && !positions) return FA_ERR_NULL;
+  if (T == 0) return FA_OK;
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.positions = positions;
+  p.f32 = dtype == FA_FP32;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return fa::launch_norm_rope(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
+  return d > 0 ? round256((size_t)fa::kNormRopeBwdBlocks * 2 * d * sizeof(float)) : 0;
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
+                              const void* dk_out, long long q_stride, long long k_stride,
+                              const float* q_weight, const float* k_weight, float eps,
+                              const float* cos, const float* sin, const int32_t* positions,
+                              void* dq, void* dk, long long dq_stride, long long dk_stride,
+                              float* dq_weight, float* dk_weight, long long T, int Hq, int Hkv,
+                              int d, int rot_dim, int max_pos, int interleaved, fa_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  fa::NormRopeParams p = {};
+  fa_status st = norm_rope_args(&p, q_weight, k_weight, eps, cos, sin, T, Hq, Hkv, d, rot_dim, max_pos, interleaved);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_UNSUPPORTED;
+  if (!q_weight && rot_dim == 0) return FA_ERR_UNSUPPORTED;
+  const int esize = dtype == FA_FP32 ? 4 : 2;
+  if ((st = check_rows(q, q_stride, T, Hq, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(k, k_stride, T, Hkv, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(dq_out, (long long)Hq * d, T, Hq, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(dk_out, (long long)Hkv * d, T, Hkv, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(dq, dq_stride, T, Hq, d, esize)) != FA_OK) return st;
+  if ((st = check_rows(dk, dk_stride, T, Hkv, d, esize)) != FA_OK) return st;
+  if (rot_dim && !positions) return FA_ERR_NULL;
+  if (q_weight) {
+    if (!dq_weight || !dk_weight) return FA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u) return FA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d)) return FA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
+  }
+  if (T == 0) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (q_weight && (cudaMemsetAsync(dq_weight, 0, d * sizeof(float), s) != cudaSuccess ||
+                     cudaMemsetAsync(dk_weight, 0, d * sizeof(float), s) != cudaSuccess))
+      return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  p.q = q;
+  p.k = k;
+  p.dq_out = dq_out;
+  p.dk_out = dk_out;
+  p.dq = dq;
+  p.dk = dk;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.dq_stride = dq_stride;
+  p.dk_stride = dk_stride;
+  p.dq_weight = dq_weight;
+  p.dk_weight = dk_weight;
+  p.dw_part = static_cast<float*>(workspace);
+  p.positions = positions;
+  p.f32 = dtype == FA_FP32;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return fa::launch_norm_rope_bwd(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+// fa_cache_append (no q, no norm, no rotation) and fa_qk_norm_rope_append.
+static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k, const void* v,
+                             void* q_out, void* k_pages, void* v_pages, long long q_stride,
+                             long long k_stride, long long v_stride, const int32_t* block_table,
+                             const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B, int N,
+                             long long total_tokens, int page_size, int num_pages, int max_pages,
+                             void* stream) {
+  if (p.Hkv == 0) return FA_ERR_SHAPE;
+  fa_status st = page_args(&p, B, N, page_size, num_pages, max_pages);
+  if (st != FA_OK) return st;
+  const long long dense = (long long)B * N;
+  if (!cu_seqlens && total_tokens != 0 && total_tokens != dense) return FA_ERR_SHAPE;
+  if (!cu_seqlens && dense >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  p.T = cu_seqlens ? total_tokens : dense;
+  if (p.T * ((p.Hq + 2ll * p.Hkv + 3) / 4) >= (1ll << 33)) return FA_ERR_UNSUPPORTED;
+  if ((st = check_rows(q, q_stride, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
+  if ((st = check_rows(q_out, (long long)p.Hq * p.d, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
+  if ((st = check_rows(k, k_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
+  if ((st = check_rows(v, v_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
+  if (!k_pages || !v_pages || !block_table || !cache_seqlens) return FA_ERR_NULL;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if (p.T == 0 || B == 0 || N == 0) return FA_OK;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_out = k_pages;
+  p.v_out = v_pages;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.block_table = block_table;
+  p.cache_seqlens = cache_seqlens;
+  p.cu_seqlens = cu_seqlens;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return fa::launch_norm_rope_pages(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                          long long k_stride, long long v_stride, const int32_t* block_table,
+                          const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B, int Hkv,
+                          int N, int d, long long total_tokens, int page_size, int num_pages,
+                          int max_pages, void* stream) {
+  fa::NormRopeParams p = {};
+  const fa_status st = norm_rope_args(&p, nullptr, nullptr, 0.f, nullptr, nullptr, total_tokens, 0, Hkv, d, 0, 0, 0);
+  if (st != FA_OK) return st;
+  return append_impl(p, nullptr, k, v, nullptr, k_pages, v_pages, 0, k_stride, v_stride, block_table,
+                     cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
+}
+
+fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                                 void* k_pages, void* v_pages, long long q_stride,
+                                 long long k_stride, long long v_stride, const float* q_weight,
+                                 const float* k_weight, float eps, const float* cos,
+                                 const float* sin, const int32_t* block_table,
+                                 const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B,
+                                 int Hq, int Hkv, int N, int d, long long total_tokens,
+                                 int rot_dim, int max_pos, int interleaved, int page_size,
+                                 int num_pages, int max_pages, void* stream) {
+  fa::NormRopeParams p = {};
+  const fa_status st = norm_rope_args(&p, q_weight, k_weight, eps, cos, sin, total_tokens, Hq, Hkv, d, rot_dim, max_pos, interleaved);
+  if (st != FA_OK) return st;
+  if (Hq == 0) return FA_ERR_SHAPE;
+  if (!q_weight && rot_dim == 0) return FA_ERR_UNSUPPORTED;
+  return append_impl(p, q, k, v, q_out, k_pages, v_pages, q_stride, k_stride, v_stride, block_table,
+                     cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
+}
+
+fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
+                        int n, int num_pages, int page_size, int Hkv, int d, void* stream) {
+  if (n < 0 || Hkv <= 0 || d <= 0) return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  fa::NormRopeParams sizes = {};
+  const fa_status st = page_args(&sizes, 0, 0, page_size, num_pages, 0);
+  if (st != FA_OK) return st;
+  if (n == 0) return FA_OK;
+  if (!k_pages || !v_pages || !src || !dst) return FA_ERR_NULL;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  fa::CachePagesCopy p = {};
+  p.k = k_pages;
+  p.v = v_pages;
+  p.src = src;
+  p.dst = dst;
+  p.n = n;
+  p.num_pages = num_pages;
+  p.page_bytes = (long long)page_size * Hkv * d * 2;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return fa::launch_copy_pages(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {

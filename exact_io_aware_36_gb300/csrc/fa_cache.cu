@@ -1,0 +1,73 @@
+// fa_cache.cu -- copies of whole pages of a key / value cache.
+//
+// Pair i copies page src[i] to page dst[i], in the key pool and in the value
+// pool.  A page is page_size * Hkv * d bf16 elements in one run, so a copy is
+// bound by HBM: every byte read once and written once.  One block moves up to
+// kChunk bytes of one page of one pool, all its loads in flight before its
+// first store.
+//
+// The pairs run in no order, so a page written by one pair must not be read
+// or written by another.  Each block looks for such pairs itself, while its
+// loads are in flight: it compares its pair with all n (8 n bytes out of L1
+// and L2, against the chunk's 2 * kChunk).  A pair in such a conflict copies
+// nothing and is recorded, and so is one with a page outside the pool.
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 8;                              // 16-byte pieces per thread
+constexpr int kChunk = kThreads * kPer * 16;         // bytes per block
+
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CachePagesCopy p) {
+  const unsigned per_pair = 2 * p.chunks;            // key and value chunks of one pair
+  const int i = (int)(blockIdx.x / per_pair);
+  const unsigned c = blockIdx.x % per_pair;
+  char* pool = static_cast<char*>(c < p.chunks ? p.k : p.v);
+  const long long off = (long long)(c % p.chunks) * kChunk;
+  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
+  if (s < 0 || s >= p.num_pages || d < 0 || d >= p.num_pages) {
+    if (threadIdx.x == 0) record_status(p.status, FA_ERR_PAGE);
+    return;
+  }
+  if (s == d) return;
+  const uint4* from = reinterpret_cast<const uint4*>(pool + (long long)s * p.page_bytes + off);
+  uint4* to = reinterpret_cast<uint4*>(pool + (long long)d * p.page_bytes + off);
+  const int n16 = (int)(min((long long)kChunk, p.page_bytes - off) / 16);
+  uint4 x[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int at = u * kThreads + threadIdx.x;
+    if (at < n16) x[u] = __ldcs(from + at);
+  }
+  bool clash = false;
+  for (int j = threadIdx.x; j < p.n; j += kThreads) {
+    const int sj = __ldg(p.src + j), dj = __ldg(p.dst + j);
+    if (j != i && sj != dj) clash |= dj == d || sj == d || dj == s;
+  }
+  if (__syncthreads_or(clash)) {
+    if (threadIdx.x == 0) record_status(p.status, FA_ERR_PAGE);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int at = u * kThreads + threadIdx.x;
+    if (at < n16) __stcs(to + at, x[u]);
+  }
+}
+
+}  // namespace
+
+int launch_copy_pages(CachePagesCopy p, void* stream) {
+  p.chunks = (unsigned)((p.page_bytes + kChunk - 1) / kChunk);
+  const long long grid = (long long)p.n * 2 * p.chunks;
+  if (grid >= (1ll << 31)) return (int)cudaErrorInvalidConfiguration;
+  copy_pages_kernel<<<(unsigned)grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace fa

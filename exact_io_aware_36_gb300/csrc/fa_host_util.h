@@ -49,4 +49,23 @@ int sm_count(int* nsm);
 void host_cache_stats(unsigned long long* encoded, unsigned long long* reused,
                       unsigned long long* attr_set);
 
+// Launches a kernel that begins while the one before it on the stream still
+// runs: its blocks take their places as that kernel's finish and wait in
+// grid_dependency_wait for its memory, which hides the launch.  Returns 0 or
+// a cudaError_t value.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace fa

@@ -119,6 +119,55 @@ inline int decode_chunk(int B, int Hkv, int S_max) {
   return c;
 }
 
+// Norm and rotation of q and k rows (fa_norm_rope.cu), their gradient, and
+// the form that writes k and v into cache pages.
+struct NormRopeParams {
+  const void* q;               // [T, Hq, d], token stride q_stride (elements)
+  const void* k;               // [T, Hkv, d], token stride k_stride
+  const void* v;               // pages: [T, Hkv, d], token stride v_stride
+  void* q_out;                 // [T, Hq, d]
+  void* k_out;                 // [T, Hkv, d], or the key pages
+  void* v_out;                 // the value pages
+  const void* dq_out;          // gradients of q_out, k_out
+  const void* dk_out;
+  void* dq;                    // gradients of q, k (token strides dq_stride, dk_stride)
+  void* dk;
+  long long q_stride, k_stride, v_stride, dq_stride, dk_stride;
+  const float* q_weight;       // [d]; both nullptr: no norm
+  const float* k_weight;
+  float* dq_weight;
+  float* dk_weight;
+  float* dw_part;              // workspace: [blocks][2][d]
+  const float* cos;            // [max_pos, rot / 2]
+  const float* sin;
+  const int32_t* positions;    // [T] (not with pages)
+  unsigned int* status;
+  long long T;
+  float eps;
+  int Hq, Hkv, d, rot, max_pos, interleaved, f32;
+  int units_per_token;
+  // pages
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* cache_seqlens;  // [B], the new tokens included
+  const int32_t* cu_seqlens;   // [B + 1] or nullptr (every sequence brings N tokens)
+  int B, N, page_size, page_shift, num_pages, max_pages;
+};
+
+// Blocks of the gradient kernel: four per SM of GB300 (152).
+constexpr int kNormRopeBwdBlocks = 4 * 152;
+
+// Page copies (fa_cache.cu).
+struct CachePagesCopy {
+  void* k;
+  void* v;
+  const int32_t* src;          // [n]
+  const int32_t* dst;          // [n]
+  unsigned int* status;
+  long long page_bytes;
+  int n, num_pages;
+  unsigned chunks;
+};
+
 // The host-side argument checks of fa_bwd (everything but the workspace), in
 // fa_bwd's order.  On FA_OK, *T is the total token count, or 0 when the call
 // has nothing to compute.
@@ -139,6 +188,10 @@ int launch_bwd_dq_bf16(const AttnParams& p, void* stream);            // determi
 int launch_decode_bf16(const DecodeParams& p, void* stream);          // split + combine
 int launch_fp8_quantize(const QuantParams& p, void* stream);
 int launch_fwd_fp8(const AttnParams& p, void* stream);
+int launch_norm_rope(const NormRopeParams& p, void* stream);
+int launch_norm_rope_pages(const NormRopeParams& p, void* stream);    // into cache pages
+int launch_norm_rope_bwd(const NormRopeParams& p, void* stream);      // rows, then the weights' sums
+int launch_copy_pages(CachePagesCopy p, void* stream);
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__

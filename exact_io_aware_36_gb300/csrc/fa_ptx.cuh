@@ -190,6 +190,19 @@ __device__ __forceinline__ bool wait_warp_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// --------------------------------------------------- launches that overlap
+
+// Lets the next kernel of the stream, launched by launch_dependent, take its
+// place; its memory reads still wait for this whole grid.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Waits until the kernel before this one has ended and its writes can be seen.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------- named barriers
 
 // Barrier `id` over the first `nthreads` threads (a multiple of 32) that

@@ -23,11 +23,14 @@ FA_BF16, FA_FP32 = 0, 1
 STATUS = {
     0: "FA_OK", 1: "FA_ERR_NULL", 2: "FA_ERR_SHAPE", 3: "FA_ERR_UNSUPPORTED", 4: "FA_ERR_ALIGN",
     5: "FA_ERR_WORKSPACE", 6: "FA_ERR_CUDA", 7: "FA_ERR_DEVICE_TIMEOUT", 8: "FA_ERR_CU_SEQLENS",
+    9: "FA_ERR_PAGE", 10: "FA_ERR_POSITION",
 }
 EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_stage", "fa_bwd_workspace_size", "fa_check_device_error",
            "fa_status_string", "fa_version", "fa_bwd_static_scratch", "fa_selftest_wait_timeout",
            "fa_decode", "fa_decode_workspace_size", "fa_fp8_layout_get", "fa_fp8_quantize",
-           "fa_fwd_fp8", "fa_host_cache_stats", "fa_bwd_workspace_size_gqa", "fa_bwd_dkdv_split")
+           "fa_fwd_fp8", "fa_host_cache_stats", "fa_bwd_workspace_size_gqa", "fa_bwd_dkdv_split",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
+           "fa_qk_norm_rope_append", "fa_cache_append", "fa_cache_copy")
 FA_BWD_PREPROCESS, FA_BWD_DKDV, FA_BWD_DQ_CONVERT = 0, 1, 2
 
 
@@ -85,6 +88,20 @@ def load(path: Optional[str] = None):
     lib.fa_fp8_quantize.restype = i
     lib.fa_fwd_fp8.argtypes = [vp, sz, vp, vp, i, i, i, i, i, f, i, i, vp, ll, vp, i, vp]
     lib.fa_fwd_fp8.restype = i
+    lib.fa_qk_norm_rope.argtypes = [vp, vp, vp, vp, ll, ll, vp, vp, f, vp, vp, vp, ll, i, i, i, i, i, i, i, vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, ll, ll, vp, vp, f, vp, vp, vp, vp, vp, ll, ll, vp, vp,
+                                        ll, i, i, i, i, i, i, i, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_cache_append.argtypes = [vp, vp, vp, vp, ll, ll, vp, vp, vp, i, i, i, i, ll, i, i, i, vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_qk_norm_rope_append.argtypes = [vp, vp, vp, vp, vp, vp, ll, ll, ll, vp, vp, f, vp, vp, vp, vp, vp,
+                                           i, i, i, i, i, ll, i, i, i, i, i, i, vp]
+    lib.fa_qk_norm_rope_append.restype = i
+    lib.fa_cache_copy.argtypes = [vp, vp, vp, vp, i, i, i, i, i, vp]
+    lib.fa_cache_copy.restype = i
     lib.fa_check_device_error.argtypes = [vp]
     lib.fa_check_device_error.restype = i
     lib.fa_status_string.argtypes = [i]
@@ -167,6 +184,50 @@ def fa_fwd_fp8(fp8_buf, fp8_bytes, o, lse, B, Hq, Hkv, N, d, scale, causal, wind
                total_tokens, alibi_slopes, o_dtype, stream) -> int:
     return load().fa_fwd_fp8(fp8_buf, fp8_bytes, o, lse, B, Hq, Hkv, N, d, scale, int(causal),
                              int(window), cu_seqlens, total_tokens, alibi_slopes, o_dtype, stream)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, q_stride, k_stride, q_weight, k_weight, eps, cos, sin,
+                    positions, T, Hq, Hkv, d, rot_dim, max_pos, interleaved, dtype, stream) -> int:
+    return load().fa_qk_norm_rope(q, k, q_out, k_out, q_stride, k_stride, q_weight, k_weight, eps,
+                                  cos, sin, positions, T, Hq, Hkv, d, rot_dim, max_pos,
+                                  int(interleaved), dtype, stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
+    return load().fa_qk_norm_rope_bwd_workspace_size(d)
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_stride, k_stride, q_weight, k_weight, eps, cos,
+                        sin, positions, dq, dk, dq_stride, dk_stride, dq_weight, dk_weight, T, Hq,
+                        Hkv, d, rot_dim, max_pos, interleaved, dtype, workspace, workspace_bytes,
+                        stream) -> int:
+    return load().fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_stride, k_stride, q_weight, k_weight,
+                                      eps, cos, sin, positions, dq, dk, dq_stride, dk_stride,
+                                      dq_weight, dk_weight, T, Hq, Hkv, d, rot_dim, max_pos,
+                                      int(interleaved), dtype, workspace, workspace_bytes, stream)
+
+
+def fa_cache_append(k, v, k_pages, v_pages, k_stride, v_stride, block_table, cache_seqlens,
+                    cu_seqlens, B, Hkv, N, d, total_tokens, page_size, num_pages, max_pages,
+                    stream) -> int:
+    return load().fa_cache_append(k, v, k_pages, v_pages, k_stride, v_stride, block_table,
+                                  cache_seqlens, cu_seqlens, B, Hkv, N, d, total_tokens, page_size,
+                                  num_pages, max_pages, stream)
+
+
+def fa_qk_norm_rope_append(q, k, v, q_out, k_pages, v_pages, q_stride, k_stride, v_stride,
+                           q_weight, k_weight, eps, cos, sin, block_table, cache_seqlens,
+                           cu_seqlens, B, Hq, Hkv, N, d, total_tokens, rot_dim, max_pos,
+                           interleaved, page_size, num_pages, max_pages, stream) -> int:
+    return load().fa_qk_norm_rope_append(q, k, v, q_out, k_pages, v_pages, q_stride, k_stride,
+                                         v_stride, q_weight, k_weight, eps, cos, sin, block_table,
+                                         cache_seqlens, cu_seqlens, B, Hq, Hkv, N, d, total_tokens,
+                                         rot_dim, max_pos, int(interleaved), page_size, num_pages,
+                                         max_pages, stream)
+
+
+def fa_cache_copy(k_pages, v_pages, src, dst, n, num_pages, page_size, Hkv, d, stream) -> int:
+    return load().fa_cache_copy(k_pages, v_pages, src, dst, n, num_pages, page_size, Hkv, d, stream)
 
 
 def fa_bwd_workspace_size(B, Hq, N, d, total_tokens) -> int:
@@ -381,3 +442,260 @@ def attention_forward_fp8(q, k, v, signs, *, causal: bool, scale: Optional[float
     if check:
         _check(fa_check_device_error(sp), "fa_fwd_fp8 (device)")
     return out, lse, fp8_buf, lay
+
+
+# ------------------------------------------- norm, rotation and a cache in pages
+
+def _checked(name, t, dtype, device, shape=None):
+    """`t` as a contiguous tensor of `dtype` on `device` (and of `shape`), else TypeError / ValueError."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, device, shape=None):
+    """(pointer, token stride) of a [T, H, d] tensor whose tokens may lie apart."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: shape {shape or '[T, H, d]'} expected, got {tuple(t.shape)}")
+    T, H, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H * d)
+
+
+def _cuda_device(t, stream):
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return t.device
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor that belongs to `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _run(what, fn, device, stream, check, *args):
+    """fn(*args, stream) with `device` current; raises on a status that is not FA_OK."""
+    import torch
+    sp = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, sp)
+        dev = fa_check_device_error(sp) if check and st == 0 else 0
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, sp)
+            dev = fa_check_device_error(sp) if check and st == 0 else 0
+    _check(st, what)
+    _check(dev, what + " (device)")
+
+
+def _angles(q_weight, k_weight, cos, sin, d, device):
+    """Pointers of the weights and of the angles, rot_dim and max_pos."""
+    import torch
+    f32 = torch.float32
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    w = (None, None) if q_weight is None else (_checked("q_weight", q_weight, f32, device, (d,)),
+                                               _checked("k_weight", k_weight, f32, device, (d,)))
+    if cos is None:
+        return (*w, None, None, 0, 0)
+    if cos.dim() != 2:
+        raise ValueError("cos: [max_pos, rot_dim / 2] expected")
+    return (*w, _checked("cos", cos, f32, device), _checked("sin", sin, f32, device, tuple(cos.shape)),
+            2 * cos.shape[1], cos.shape[0])
+
+
+def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos=None, sin=None,
+                 positions=None, interleaved: bool = False, q_out=None, k_out=None, stream=None,
+                 check: bool = False):
+    """RMS norm of every head of q and k and rotation by position through ``fa_qk_norm_rope``.
+
+    q: [T, Hq, d], k: [T, Hkv, d] (bf16 or fp32; both may be parts of one
+    projection's output: only the heads of a token have to be contiguous).
+    q_weight, k_weight: float32 [d] (None: no norm); cos, sin: float32
+    [max_pos, rot_dim / 2] with positions int32 [T] (None: no rotation).
+    Pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) with ``interleaved``.
+    Returns (q_out, k_out), contiguous, of q's type.  For training the result
+    goes to ``attention_forward`` and ``attention_backward``'s dq, dk to
+    ``qk_norm_rope_backward``.
+    """
+    import torch
+    device = _cuda_device(q, stream)
+    qp, qs = _rows("q", q, q.dtype, device)
+    kp, ks = _rows("k", k, q.dtype, device)
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and head dimension")
+    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    pos = None
+    if cos is not None:
+        if positions is None:
+            raise ValueError("positions are required with cos and sin")
+        pos = _checked("positions", positions, torch.int32, device, (T,))
+    if q_out is None:
+        q_out = _empty((T, Hq, d), q.dtype, device, stream)
+    if k_out is None:
+        k_out = _empty((T, Hkv, d), q.dtype, device, stream)
+    _run("fa_qk_norm_rope", fa_qk_norm_rope, device, stream, check, qp, kp,
+         _checked("q_out", q_out, q.dtype, device, (T, Hq, d)),
+         _checked("k_out", k_out, q.dtype, device, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
+         ang[2], ang[3], pos, T, Hq, Hkv, d, ang[4], ang[5], interleaved, _dtype_code(q.dtype))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
+                          eps: float = 1e-6, cos=None, sin=None, positions=None,
+                          interleaved: bool = False, dq=None, dk=None, workspace=None,
+                          stream=None, check: bool = False):
+    """Gradient of ``qk_norm_rope`` through ``fa_qk_norm_rope_bwd``.
+
+    q, k and the other arguments as given to ``qk_norm_rope``; dq_out, dk_out:
+    gradients of its results (contiguous).  dq, dk may be parts of one buffer, as
+    q and k.  Returns (dq, dk, dq_weight, dk_weight); the weights' gradients are
+    float32 [d], or None without norm.  Results do not vary from run to run.
+    """
+    import torch
+    device = _cuda_device(q, stream)
+    qp, qs = _rows("q", q, q.dtype, device)
+    kp, ks = _rows("k", k, q.dtype, device)
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and head dimension")
+    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    pos = None
+    if cos is not None:
+        if positions is None:
+            raise ValueError("positions are required with cos and sin")
+        pos = _checked("positions", positions, torch.int32, device, (T,))
+    if dq is None:
+        dq = _empty((T, Hq, d), q.dtype, device, stream)
+    if dk is None:
+        dk = _empty((T, Hkv, d), q.dtype, device, stream)
+    dqp, dqs = _rows("dq", dq, q.dtype, device, (T, Hq, d))
+    dkp, dks = _rows("dk", dk, q.dtype, device, (T, Hkv, d))
+    dw = (None, None)
+    if q_weight is not None:
+        both = _empty((2, d), torch.float32, device, stream)
+        dw = (both[0], both[1])
+        if workspace is None:
+            workspace = _empty((fa_qk_norm_rope_bwd_workspace_size(d),), torch.uint8, device, stream)
+        _checked("workspace", workspace, torch.uint8, device)
+    _run("fa_qk_norm_rope_bwd", fa_qk_norm_rope_bwd, device, stream, check, qp, kp,
+         _checked("dq_out", dq_out, q.dtype, device, (T, Hq, d)),
+         _checked("dk_out", dk_out, q.dtype, device, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
+         ang[2], ang[3], pos, dqp, dkp, dqs, dks, _ptr(dw[0]), _ptr(dw[1]), T, Hq, Hkv, d, ang[4],
+         ang[5], interleaved, _dtype_code(q.dtype), _ptr(workspace),
+         workspace.numel() if workspace is not None else 0)
+    return dq, dk, dw[0], dw[1]
+
+
+def _pages(k_pages, v_pages, device):
+    """(k pointer, v pointer, num_pages, page_size, Hkv, d) of the two pools."""
+    import torch
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages: [num_pages, page_size, Hkv, d] expected")
+    kp = _checked("k_pages", k_pages, torch.bfloat16, device)
+    vp = _checked("v_pages", v_pages, torch.bfloat16, device, tuple(k_pages.shape))
+    return (kp, vp, *k_pages.shape)
+
+
+def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device):
+    """(table, cache_seqlens, cu_seqlens pointers, B, N, max_pages)."""
+    import torch
+    if block_table.dim() != 2:
+        raise ValueError("block_table: [B, max_pages] expected")
+    B, max_pages = block_table.shape
+    tp = _checked("block_table", block_table, torch.int32, device)
+    cp = _checked("cache_seqlens", cache_seqlens, torch.int32, device, (B,))
+    if cu_seqlens is not None:
+        if max_seqlen is None:
+            raise ValueError("max_seqlen is required with cu_seqlens")
+        return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, device, (B + 1,)), B, int(max_seqlen), max_pages
+    if B == 0 or T % B:
+        raise ValueError("without cu_seqlens every sequence brings the same number of tokens")
+    return tp, cp, None, B, T // B, max_pages
+
+
+def cache_append(k, v, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqlens=None,
+                 max_seqlen: Optional[int] = None, stream=None, check: bool = False):
+    """Write the new tokens' k and v into the pages of a cache through ``fa_cache_append``.
+
+    k, v: bf16 [T, Hkv, d] (the heads of a token contiguous); k_pages, v_pages:
+    bf16 [num_pages, page_size, Hkv, d]; block_table: int32 [B, max_pages];
+    cache_seqlens: int32 [B], the new tokens included.  Sequence b's new tokens
+    are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1], with
+    ``max_seqlen`` their largest number), or T / B each without it.
+    """
+    import torch
+    device = _cuda_device(k, stream)
+    kp, ks = _rows("k", k, torch.bfloat16, device)
+    vp, vs = _rows("v", v, torch.bfloat16, device, tuple(k.shape))
+    T, Hkv, d = k.shape
+    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, device)
+    if (Hp, dp) != (Hkv, d):
+        raise ValueError("the pages have other heads than k")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
+    _run("fa_cache_append", fa_cache_append, device, stream, check, kp, vp, kpool, vpool, ks, vs, tp,
+         cp, cup, B, Hkv, N, d, T, page_size, num_pages, max_pages)
+
+
+def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqlens=None,
+                        max_seqlen: Optional[int] = None, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, cos=None, sin=None, interleaved: bool = False,
+                        q_out=None, stream=None, check: bool = False):
+    """``qk_norm_rope`` of new tokens and ``cache_append`` of their k and v in
+    one launch (``fa_qk_norm_rope_append``).  A token's position is its place
+    in its sequence's cache.  Returns q_out [T, Hq, d], ready for
+    ``attention_forward_paged`` over the same pages."""
+    import torch
+    device = _cuda_device(q, stream)
+    qp, qs = _rows("q", q, torch.bfloat16, device)
+    kp, ks = _rows("k", k, torch.bfloat16, device)
+    vp, vs = _rows("v", v, torch.bfloat16, device, tuple(k.shape))
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, device)
+    if k.shape[0] != T or k.shape[2] != d or (Hp, dp) != (Hkv, d):
+        raise ValueError("q, k and the pages must have the same tokens, key heads and head dimension")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
+    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    if q_out is None:
+        q_out = _empty((T, Hq, d), q.dtype, device, stream)
+    _run("fa_qk_norm_rope_append", fa_qk_norm_rope_append, device, stream, check, qp, kp, vp,
+         _checked("q_out", q_out, q.dtype, device, (T, Hq, d)), kpool, vpool, qs, ks, vs, ang[0],
+         ang[1], float(eps), ang[2], ang[3], tp, cp, cup, B, Hq, Hkv, N, d, T, ang[4], ang[5],
+         interleaved, page_size, num_pages, max_pages)
+    return q_out
+
+
+def cache_copy(k_pages, v_pages, src, dst, *, stream=None, check: bool = False):
+    """Copy pages src[i] to dst[i] (int32 [n], on the GPU) of both pools through
+    ``fa_cache_copy``: the fork of a sequence's last page, a compaction's moves.
+    The copies run in no order; see include/fa.h on pairs that clash."""
+    import torch
+    device = _cuda_device(k_pages, stream)
+    kpool, vpool, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages, device)
+    n = src.numel()
+    _run("fa_cache_copy", fa_cache_copy, device, stream, check, kpool, vpool,
+         _checked("src", src, torch.int32, device, (n,)), _checked("dst", dst, torch.int32, device, (n,)),
+         n, num_pages, page_size, Hkv, d)

@@ -46,7 +46,8 @@
  * Errors.  Argument checks run on the host before any launch; a failing
  * check returns its status and launches nothing.  Launch failures return
  * FA_ERR_CUDA.  Faults found on the device (malformed cu_seqlens, a sequence
- * longer than N, a pipeline wait that ran out of its time limit) set a
+ * longer than N, a pipeline wait that ran out of its time limit, a page or a
+ * position out of range) set a
  * per-device status word and make the affected blocks return early;
  * fa_check_device_error() reads and clears it.  No C++ exception crosses
  * this interface.
@@ -70,7 +71,9 @@ typedef enum {
   FA_ERR_WORKSPACE = 5,       /* workspace NULL or smaller than required */
   FA_ERR_CUDA = 6,            /* a CUDA runtime / launch error */
   FA_ERR_DEVICE_TIMEOUT = 7,  /* device: a pipeline wait exceeded its limit */
-  FA_ERR_CU_SEQLENS = 8       /* device: cu_seqlens malformed or length > N */
+  FA_ERR_CU_SEQLENS = 8,      /* device: cu_seqlens malformed or length > N */
+  FA_ERR_PAGE = 9,            /* device: a page outside the pool, or pages whose copies clash */
+  FA_ERR_POSITION = 10        /* device: a position outside the table of angles */
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_FP32 = 1 } fa_dtype;
@@ -340,11 +343,125 @@ fa_status fa_fwd_fp8(const void* fp8_buf, size_t fp8_bytes, void* o, float* lse,
                      const float* alibi_slopes, fa_dtype o_dtype, void* stream);
 
 /*
+ * What is done to Q and K on their way to attention: an RMS norm of every
+ * head and the rotation by position ("RoPE"), in one pass over both.  For
+ * each row x (d elements of one head of one token) with the weight w of its
+ * tensor:
+ *     r = (mean(x^2) + eps)^-1/2,   y = x r w,   z = R y
+ * where R turns rot_dim / 2 pairs of elements by the token's angles:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * pair i being elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * `interleaved`; elements from rot_dim on are not turned.  Computed in
+ * float32, rounded once.
+ *   q, k          [T, Hq, d] and [T, Hkv, d] of `dtype` (bf16 or fp32); token t
+ *                 starts q_stride (k_stride) elements after token t - 1, so
+ *                 both may be parts of one projection's output
+ *   q_out, k_out  [T, Hq, d] and [T, Hkv, d], contiguous; q_out == q (k_out ==
+ *                 k) is allowed where the stride is Hq * d (Hkv * d)
+ *   q_weight,
+ *   k_weight      device float32 [d], or both NULL: no norm (y = x)
+ *   eps           >= 0, finite
+ *   cos, sin      device float32 [max_pos, rot_dim / 2]
+ *   positions     device int32 [T], each in [0, max_pos); a token with another
+ *                 value is not written and sets FA_ERR_POSITION
+ *   d             64 or 128
+ *   rot_dim       a multiple of 16, 0 <= rot_dim <= d; 0: no rotation (z = y;
+ *                 cos, sin and positions are not used)
+ * A call with neither norm nor rotation is FA_ERR_UNSUPPORTED.  All tensors
+ * start on a 16-byte boundary and strides are multiples of 16 bytes (the
+ * weights, cos and sin too).  Hq or Hkv may be 0 (not both): q (or k) alone.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                          long long q_stride, long long k_stride, const float* q_weight,
+                          const float* k_weight, float eps, const float* cos, const float* sin,
+                          const int32_t* positions, long long T, int Hq, int Hkv, int d,
+                          int rot_dim, int max_pos, int interleaved, fa_dtype dtype, void* stream);
+
+/*
+ * Gradient of fa_qk_norm_rope: from its inputs and the gradients dq_out,
+ * dk_out of its outputs (contiguous, of `dtype`), writes dq and dk (token
+ * strides dq_stride, dk_stride) and, with norm, dq_weight and dk_weight
+ * (float32 [d], summed over all tokens and heads):
+ *     dy = R^T dz,   dw = sum dy x r,   dx = r (dy w - xh mean(dy w xh)),  xh = x r.
+ * Results do not vary from run to run.  dq, dk may not overlap an input.  A
+ * token whose position is out of range gets no dq, dk and adds nothing to the
+ * weights' gradients.  With T = 0 the weights' gradients are set to zero.
+ *   workspace  device, >= fa_qk_norm_rope_bwd_workspace_size bytes, 256-byte
+ *              aligned, contents irrelevant on entry (not used without norm)
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+fa_status fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
+                              const void* dk_out, long long q_stride, long long k_stride,
+                              const float* q_weight, const float* k_weight, float eps,
+                              const float* cos, const float* sin, const int32_t* positions,
+                              void* dq, void* dk, long long dq_stride, long long dk_stride,
+                              float* dq_weight, float* dk_weight, long long T, int Hq, int Hkv,
+                              int d, int rot_dim, int max_pos, int interleaved, fa_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A cache in pages.  Keys and values live in two pools, bf16
+ * [num_pages, page_size, Hkv, d] (page_size 16, 32, 64, 128 or 256; d 64 or
+ * 128).  Sequence b holds L_b = cache_seqlens[b] tokens; its token j is slot
+ * j % page_size of page block_table[b * max_pages + j / page_size]
+ * (block_table: device int32 [B, max_pages]).  Entries of the table behind a
+ * sequence's last page are not read.  Several sequences may share pages.
+ *
+ * fa_cache_append writes the new tokens' keys and values: sequence b brings n_b
+ * tokens, the last n_b of its L_b (cache_seqlens counts them already).
+ *   k, v          bf16 [T, Hkv, d], token strides k_stride and v_stride
+ *                 (elements)
+ *   cu_seqlens    device int32 [B + 1]: b's new tokens are rows
+ *                 cu_seqlens[b] .. cu_seqlens[b + 1] - 1; rows from
+ *                 cu_seqlens[B] on (a padded batch) are left alone.  n_b may
+ *                 be 0.  NULL: every sequence brings N tokens (T = B * N).
+ *   N             the largest n_b
+ *   total_tokens  T; without cu_seqlens 0 or B * N
+ * A sequence with L_b < n_b or L_b > max_pages * page_size, or n_b > N, sets
+ * FA_ERR_CU_SEQLENS, and a table entry outside the pool FA_ERR_PAGE; the
+ * tokens concerned are not written.
+ *
+ * fa_qk_norm_rope_append is fa_qk_norm_rope for such tokens, in one launch:
+ * token i of b's n_b has position L_b - n_b + i, q goes to q_out
+ * ([T, Hq, d], contiguous), k to the key pages and v, unchanged, to the value
+ * pages.  bf16.  A position outside [0, max_pos) sets FA_ERR_POSITION and the
+ * token is not written.
+ */
+fa_status fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                          long long k_stride, long long v_stride, const int32_t* block_table,
+                          const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B, int Hkv,
+                          int N, int d, long long total_tokens, int page_size, int num_pages,
+                          int max_pages, void* stream);
+
+fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                                 void* k_pages, void* v_pages, long long q_stride,
+                                 long long k_stride, long long v_stride, const float* q_weight,
+                                 const float* k_weight, float eps, const float* cos,
+                                 const float* sin, const int32_t* block_table,
+                                 const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B,
+                                 int Hq, int Hkv, int N, int d, long long total_tokens,
+                                 int rot_dim, int max_pos, int interleaved, int page_size,
+                                 int num_pages, int max_pages, void* stream);
+
+/*
+ * Copies whole pages of both pools: page src[i] to page dst[i], i < n (device
+ * int32 arrays): the partly filled last page of a sequence that is forked, or
+ * the moves of a compaction.  The copies run in no order: a pair whose dst is
+ * another pair's src or dst, or whose src is another pair's dst (pairs with
+ * src == dst, which do nothing, aside), is not copied and sets FA_ERR_PAGE, and so
+ * is a pair with a page outside the pool; the other pairs are copied.
+ */
+fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
+                        int n, int num_pages, int page_size, int Hkv, int d, void* stream);
+
+/*
  * Error reporting of this library (the pages have no counterpart; their
  * usage contract only names the inputs a call takes).
  * Synchronises `stream`, then reads and clears the current device's status
- * word.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_CU_SEQLENS, or
- * FA_ERR_CUDA if the synchronisation itself failed.
+ * word.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_CU_SEQLENS,
+ * FA_ERR_PAGE, FA_ERR_POSITION, or FA_ERR_CUDA if the synchronisation itself
+ * failed.
  */
 fa_status fa_check_device_error(void* stream);
 
