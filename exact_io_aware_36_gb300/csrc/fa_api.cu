@@ -732,6 +732,89 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
                      cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
 }
 
+// Rows of the largest item of the paged forward: two tiles of 128 / group
+// tokens, times the group's heads.
+static long long paged_part_rows(int group, int N) { return (long long)std::min(2 * (128 / group), N) * group; }
+
+size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || N < 0 || d <= 0) return 0;
+  const size_t rows = 2 * (size_t)fa::kPagedCtas * paged_part_rows(Hq / Hkv, N);
+  return round256(rows * d * sizeof(float)) + round256(rows * 4 * sizeof(float)) +
+         round256(2 * fa::kPagedCtas * sizeof(int4));
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                       const int32_t* block_table, const int32_t* cache_seqlens,
+                       const int32_t* cu_seqlens, void* o, float* lse, int B, int Hq, int Hkv,
+                       int N, int d, long long total_tokens, int page_size, int num_pages,
+                       int max_pages, float scale, int causal, int window,
+                       const float* alibi_slopes, fa_dtype o_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (Hq <= 0 || Hkv <= 0 || d <= 0 || total_tokens < 0) return FA_ERR_SHAPE;
+  if (Hq % Hkv != 0) return FA_ERR_SHAPE;
+  fa::NormRopeParams sizes = {};
+  fa_status st = page_args(&sizes, B, N, page_size, num_pages, max_pages);
+  if (st != FA_OK) return st;
+  const long long dense = (long long)B * N;
+  if (!cu_seqlens && total_tokens != 0 && total_tokens != dense) return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 128 || Hq > 65535 || B > fa::kPagedMaxBatch) return FA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_UNSUPPORTED;
+  if (causal != 0 && causal != 1) return FA_ERR_UNSUPPORTED;
+  if (!causal && (window >= 0 || alibi_slopes)) return FA_ERR_UNSUPPORTED;
+  if (o_dtype != FA_FP32 && o_dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+  const long long T = cu_seqlens ? total_tokens : dense;
+  if (T >= (1ll << 31) || N >= (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0 || N == 0) return FA_OK;
+  if (num_pages == 0) return FA_ERR_SHAPE;
+  if (!q || !k_pages || !v_pages || !block_table || !cache_seqlens || !o || !lse) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < fa_fwd_paged_workspace_size(Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
+  fa::PagedParams p = {};
+  p.q = q;
+  p.k = k_pages;
+  p.v = v_pages;
+  p.o = o;
+  p.lse = lse;
+  p.block_table = block_table;
+  p.cache_seqlens = cache_seqlens;
+  p.cu_seqlens = cu_seqlens;
+  p.alibi = alibi_slopes;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.N = N;
+  p.d = d;
+  p.group = Hq / Hkv;
+  p.tpt = 128 / p.group;
+  p.part_rows = (int)paged_part_rows(p.group, N);
+  const size_t rows = 2 * (size_t)fa::kPagedCtas * p.part_rows;
+  char* ws = static_cast<char*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + round256(rows * d * sizeof(float)));
+  p.part_meta = reinterpret_cast<int4*>(ws + round256(rows * d * sizeof(float)) + round256(rows * 4 * sizeof(float)));
+  // lanes that add up a sequence's q blocks: enough for the longest chunk
+  const int blocks = (N + 2 * p.tpt - 1) / (2 * p.tpt);
+  p.plan_lanes = 1;
+  while (p.plan_lanes < 32 && p.plan_lanes < blocks) p.plan_lanes *= 2;
+  p.page_size = page_size;
+  p.page_shift = sizes.page_shift;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.causal = causal;
+  const long long reach = (long long)max_pages * page_size;
+  p.window = window < 0 || window >= reach - 1 ? fa::kNoWindow : window;
+  p.o_f32 = o_dtype == FA_FP32;
+  p.scale = scale;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.status = status_ptr();
+  if (!p.status) return FA_ERR_CUDA;
+  return fa::launch_fwd_paged(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
                         int n, int num_pages, int page_size, int Hkv, int d, void* stream) {
   if (n < 0 || Hkv <= 0 || d <= 0) return FA_ERR_SHAPE;

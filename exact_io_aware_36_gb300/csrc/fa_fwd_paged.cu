@@ -1,0 +1,1034 @@
+// fa_fwd_paged.cu -- tensor-core attention of each sequence's newest tokens
+// over a cache in pages, for sm_103a.
+//
+// Method ("FlashAttention: Faster Attention Without Dropping a Single
+// Interaction"): S = scale Q K^T (+ ALiBi), O = softmax(S) V by tiles of 128
+// keys with a running reference max m and sum l; parts of a row's keys are
+// merged with the pages' (m, l, O) rule (Key design 2):
+//     m = max_s m_s,  l = sum_s 2^(m_s - m) l_s,  O = sum_s 2^(m_s - m) O_s / l.
+//
+// Rows.  The query heads of one kv head share its keys, so they share tiles:
+// row r of a 128-row tile is token r / group, head r % group (a TMA box of
+// group heads x 128 / group tokens).  An item is (sequence, kv head, block of
+// two such tiles): up to 256 rows against the keys any of them sees.
+//   two tiles   both run over the same K/V tiles, each with its own S, P, O in
+//               TMEM: one tile's softmax overlaps the other's products.
+//               Bound by the tensor cores and the softmax.
+//   one tile    (a token or a few per sequence) the same two streams share the
+//               rows and take the key tiles in turn; their O and (m, l) are
+//               merged at the end.  64 KB of K/V per 128 keys come from HBM
+//               (1.4 us of one SM's share at d = 128) against 0.8 us of
+//               products, so HBM bounds it, and the tensor cores have time to
+//               take P as two bf16 parts (high and low, 16 bits of P instead
+//               of 8): O then carries its own rounding only.
+//
+// Work.  Lengths are known on the device alone (so a captured call can be
+// replayed with others).  Every CTA, one per SM, adds up the key tiles of all
+// items (two-tile items' tiles weigh 3, others 2: their measured times) and
+// takes an equal run of this one line of tiles.  A run begins and ends inside
+// items; such parts go to the workspace, two at most per CTA, and
+// paged_merge_kernel joins an item's parts in a fixed order.  No SM waits for
+// a long sequence and nothing depends on timing: the result is the same from
+// run to run.
+//
+// Roles (320 threads):
+//   warp 9     TMA producer: Q of an item, then per step one slot with K of
+//              this step's tile and V of the step before.  A tile is 128 /
+//              page_size boxes, one lane each, at the pages the table names;
+//              pages with no visible key are not read.  Page numbers of the
+//              next step are loaded before the wait for its slot.
+//   warp 8     MMA issuer (one lane).  Where a V tile reaches past the visible
+//              keys, the warp first zeroes those rows: a slot no token filled
+//              may hold NaN, and 0 x NaN would reach O.
+//   warps 0-3  softmax of stream 0 (one TMEM lane = one row), warps 4-7 of
+//              stream 1, then the item's epilogue.
+// Steps, rings and TMEM buffers run on across items: an item's first loads
+// and products overlap the previous item's last ones.  Key tiles are visited
+// from the newest backwards (ALiBi's largest scores come first).
+// Registers: three warps share a quarter of the SM, so a thread has 168, too
+// few for a row's 128 scores and what is done with them.  The softmax takes a
+// row's scores from TMEM 16 columns at a time, the next 16 in flight, and
+// holds P (64 registers), not S.
+// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D);
+// P overwrites S: 64 columns, or all 128 (each 16 keys' high part, then low).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fa_host_util.h"
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;
+constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
+constexpr float kSpecSum = 256.0f;     // 2^kTau
+constexpr int kWeightTwo = 3, kWeightOne = 2;   // of one key tile of an item
+constexpr int kMinTiles = 2;                    // tiles a CTA takes at least: both streams busy
+
+template <int D>
+struct Cfg {
+  static constexpr int NB = D / 64;                 // 64-column boxes per row
+  static constexpr int BOX_BYTES = 128 * 64 * 2;
+  static constexpr int TILE_BYTES = NB * BOX_BYTES;
+  static constexpr int NS = D == 128 ? 2 : 5;       // slots (K of a step, V of the one before)
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
+  static constexpr int V_OFF = K_OFF + NS * TILE_BYTES;
+  static constexpr int ML_OFF = V_OFF + NS * TILE_BYTES;   // (m, l, l~) of both streams' rows
+  static constexpr int WALK_OFF = ML_OFF + 2 * 128 * 3 * 4;
+  static constexpr int BAR_OFF = WALK_OFF + (kThreads / 32) * 64;
+  static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  // the work plan's prefix sums borrow the K/V slots before the first load
+  static_assert(kPagedMaxBatch * 8 <= 2 * NS * TILE_BYTES, "plan");
+  static constexpr uint32_t S_COL0 = 0, S_COL1 = 128;
+  static constexpr uint32_t O_COL0 = 256, O_COL1 = 256 + D;
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_done, o_free, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  // the plan: where this CTA's run begins
+  unsigned long long warp_sum[kThreads / 32];
+  long long w0, w1, base;
+  int b, g, qb;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// New tokens [c0, c0 + n) of sequence b and its cached length L; n = 0 where
+// there is nothing to do.  False: malformed (n is 0 then).
+__device__ __forceinline__ bool load_seq(const PagedParams& p, int b, int* c0, int* n, int* L) {
+  int c1;
+  if (p.cu_seqlens) {
+    *c0 = __ldg(p.cu_seqlens + b);
+    c1 = __ldg(p.cu_seqlens + b + 1);
+  } else {
+    *c0 = b * p.N;
+    c1 = *c0 + p.N;
+  }
+  *L = __ldg(p.cache_seqlens + b);
+  *n = 0;
+  if (*c0 < 0 || (b == 0 && *c0 != 0) || c1 < *c0 || (long long)c1 > p.T || c1 - *c0 > p.N) return false;
+  if (c1 == *c0) return true;
+  if (*L < (p.causal ? c1 - *c0 : 0) || (long long)*L > (long long)p.max_pages * p.page_size) return false;
+  *n = c1 - *c0;
+  return true;
+}
+
+// The block of query tokens from tok0 on of a sequence (n new tokens, L
+// cached): tile t holds nt[t] tokens at positions f[t] .. and needs key tiles
+// lo[t] .. hi[t]; the item's steps visit key tiles hi_all, hi_all - 1, ...
+// (kt of them).  Keys outside [vlo, vhi) are seen by no row.
+struct Block {
+  int nt[2], f[2], lo[2], hi[2];
+  int hi_all, kt, vlo, vhi;
+  bool two;
+};
+
+__device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int L, int tok0, Block& k) {
+  const int left = n - tok0;
+  k.two = left > p.tpt;
+  k.nt[0] = min(left, p.tpt);
+  k.nt[1] = min(max(left - p.tpt, 0), p.tpt);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    k.f[t] = L - n + tok0 + t * p.tpt;
+    const int last = p.causal ? k.f[t] + k.nt[t] - 1 : L - 1;
+    k.hi[t] = max(last, 0) >> 7;
+    k.lo[t] = max(k.f[t] - p.window, 0) >> 7;      // window: kNoWindow without a band
+    if (!p.causal) k.lo[t] = 0;
+  }
+  if (!k.two) {
+    k.hi[1] = k.hi[0];
+    k.lo[1] = k.lo[0];
+  }
+  k.hi_all = k.hi[1];
+  k.kt = k.hi_all - k.lo[0] + 1;
+  k.vlo = p.causal ? max(k.f[0] - p.window, 0) : 0;
+  k.vhi = p.causal ? k.f[0] + k.nt[0] + k.nt[1] : L;
+}
+
+__device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
+
+// A CTA's walk over its run [w0, w1) of the line of tiles.  Every role walks
+// the same items by itself; each warp keeps its state in shared memory, as it
+// is needed at the items' ends only.
+struct Walk {
+  long long w0, w1, base;      // base: place of item (b, g, qb) on the line
+  int b, g, qb, c0, n, L;
+};
+
+static_assert(sizeof(Walk) <= 64, "walk");
+
+struct Seg {
+  Block k;
+  int g, tok, ntok;            // kv head; first token (row of q) and tokens of the item
+  int b, L, ib, ie;            // sequence, its length; steps [ib, ie) of the item's kt
+};
+
+// Warp-collective, as is walk_next.
+__device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bars, Walk* state) {
+  if ((threadIdx.x & 31) == 0) {
+    Walk w;
+    w.w0 = bars->w0;
+    w.w1 = bars->w1;
+    w.base = bars->base;
+    w.b = bars->b;
+    w.g = bars->g;
+    w.qb = bars->qb;
+    w.c0 = w.n = w.L = 0;
+    if (w.w0 < w.w1) load_seq(p, w.b, &w.c0, &w.n, &w.L);
+    *state = w;
+  }
+  __syncwarp();
+}
+
+// The next part of an item in the run; false at its end.
+__device__ __forceinline__ bool walk_next(const PagedParams& p, Walk* state, Seg& s) {
+  Walk w = *state;
+  __syncwarp();
+  bool found = false;
+  while (!found && w.base < w.w1) {
+    if (w.qb * 2 * p.tpt >= w.n) {
+      w.qb = 0;
+      if (++w.g >= p.Hkv) {
+        w.g = 0;
+        do {
+          if (++w.b >= p.B) return false;              // not reached: the run ends with an item
+          load_seq(p, w.b, &w.c0, &w.n, &w.L);
+        } while (w.n == 0);
+      }
+    }
+    const int tok0 = w.qb * 2 * p.tpt;
+    block_geometry(p, w.n, w.L, tok0, s.k);
+    const int wt = tile_weight(s.k);
+    const long long len = (long long)s.k.kt * wt;
+    s.ib = w.base >= w.w0 ? 0 : ((int)(w.w0 - w.base) + wt - 1) / wt;
+    s.ie = w.w1 - w.base >= len ? s.k.kt : ((int)(w.w1 - w.base) + wt - 1) / wt;
+    s.b = w.b;
+    s.L = w.L;
+    s.g = w.g;
+    s.tok = w.c0 + tok0;
+    s.ntok = s.k.nt[0] + s.k.nt[1];
+    w.base += len;
+    ++w.qb;
+    found = s.ib < s.ie;
+  }
+  if ((threadIdx.x & 31) == 0) *state = w;
+  __syncwarp();
+  return found;
+}
+
+// Weight of all q blocks of one kv head of sequence (n, L), lane of nl lanes
+// taking every nl-th block.
+__device__ __forceinline__ long long seq_weight(const PagedParams& p, int n, int L, int lane, int nl) {
+  long long sum = 0;
+  for (int tok0 = lane * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) {
+    Block k;
+    block_geometry(p, n, L, tok0, k);
+    sum += (long long)k.kt * tile_weight(k);
+  }
+  return sum;
+}
+
+// Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
+// threads; `pre` holds B 64-bit words of shared memory.
+__device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // 1. every sequence's weight, nl lanes per sequence
+  const int nl = p.plan_lanes;
+  const int sub = lane & (nl - 1);
+  for (int b0 = 0; b0 < p.B; b0 += kThreads / nl) {
+    const int b = b0 + tid / nl;
+    long long wsum = 0;
+    if (b < p.B) {
+      int c0, n, L;
+      if (!load_seq(p, b, &c0, &n, &L) && blockIdx.x == 0 && sub == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
+      wsum = seq_weight(p, n, L, sub, nl);
+    }
+    for (int o = nl / 2; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+    if (b < p.B && sub == 0) pre[b] = (unsigned long long)wsum * p.Hkv;
+  }
+  __syncthreads();
+  // 2. exclusive prefix sums: each thread a run of sequences
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int f = min(tid * per, p.B), e = min(f + per, p.B);
+  unsigned long long own = 0;
+  for (int b = f; b < e; ++b) own += pre[b];
+  unsigned long long inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) bars->warp_sum[warp] = inc;
+  __syncthreads();
+  unsigned long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += bars->warp_sum[w];
+    total += bars->warp_sum[w];
+  }
+  before += inc - own;
+  // 3. this CTA's run, and the sequence it begins in
+  const long long G = gridDim.x;
+  const long long active = min(G, max(1ll, (long long)total / (kMinTiles * kWeightOne)));
+  const long long c = blockIdx.x;
+  const long long w0 = c < active ? (long long)total * c / active : (long long)total;
+  const long long w1 = c < active ? (long long)total * (c + 1) / active : (long long)total;
+  if (tid == 0) {
+    bars->w0 = w0;
+    bars->w1 = w1;
+    bars->base = w1;             // an empty run
+    bars->b = bars->g = bars->qb = 0;
+  }
+  __syncthreads();
+  if (w0 < w1) {
+    unsigned long long at = before;
+    for (int b = f; b < e; ++b) {
+      const unsigned long long x = pre[b];
+      if (at <= (unsigned long long)w0 && (unsigned long long)w0 < at + x) {
+        bars->b = b;
+        bars->base = (long long)at;
+      }
+      at += x;
+    }
+  }
+  __syncthreads();
+  // 4. the kv head and the q block
+  if (warp == 0 && w0 < w1) {
+    const int b = bars->b;
+    const long long sw = (long long)(pre[b] / (unsigned)p.Hkv);
+    int c0, n, L;
+    load_seq(p, b, &c0, &n, &L);
+    const int g = (int)((w0 - bars->base) / sw);
+    long long base = bars->base + g * sw;
+    int qb = 0;
+    for (int q0 = 0;; q0 += 32) {
+      const int tok0 = (q0 + lane) * 2 * p.tpt;
+      long long x = 0;
+      if (tok0 < n) {
+        Block k;
+        block_geometry(p, n, L, tok0, k);
+        x = (long long)k.kt * tile_weight(k);
+      }
+      long long run = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, x > 0 && base + run > w0);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        qb = q0 + src;
+        base += __shfl_sync(0xffffffffu, run - x, src);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, run, 31);
+      if ((q0 + 32) * 2 * p.tpt >= n) break;      // not reached: w0 lies in this head's blocks
+    }
+    __syncwarp();
+    if (lane == 0) {
+      bars->g = g;
+      bars->qb = qb;
+      bars->base = base;
+    }
+  }
+  __syncthreads();
+}
+
+// O row (D columns at tO) *= alpha, in TMEM.  Warp-collective.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 16) {
+    uint32_t o[16];
+    tmem_ld16(tO + c0, o);
+    tmem_wait_ld();
+    reg_fence16(o);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+    tmem_st16(tO + c0, o);
+  }
+}
+
+// 16 columns of a finished row, or of a part (float32, not divided).
+__device__ __forceinline__ void store_row16(const float* v, bool f32, void* base, long long at) {
+  if (f32) {
+    float4* O = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) O[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint4* O = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      O[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+template <int D, bool ALIBI>
+__global__ void __launch_bounds__(kThreads, 1)
+fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::BAR_OFF);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 4);
+    }
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->o_free, 8);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  // Q rows past the box (128 % group of them) are zero for good.
+  const int rows_box = p.tpt * p.group;
+  for (int i = threadIdx.x; i < 2 * C::NB * (128 - rows_box) * 8; i += kThreads) {
+    const int box = i / ((128 - rows_box) * 8), j = i % ((128 - rows_box) * 8);
+    reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
+  }
+  make_plan(p, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF));
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const WaitCtx wc{&bars->abort_flag, p.status};
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp(bar, parity, wc); };
+  Walk* walk = reinterpret_cast<Walk*>(smem + C::WALK_OFF + warp * 64);
+  walk_begin(p, bars, walk);
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int box_rows = min(p.page_size, 128);
+    const int nbox = 128 / box_rows;
+    const uint32_t box_bytes = box_rows * 128;
+    Seg s;
+    bool ok = true;
+    unsigned q_any = 0, q_par = 0;   // bit x: Q buffer x was loaded; its last load's parity
+    int qsel = 0;              // buffer of the next one-tile item
+    int gs = 0;                // steps over all items
+    // what the parts of this CTA are, for the merge: kind of the part that goes
+    // on from the CTA before (2: the item's last), and the item begun here
+    int cont = 0;
+    int4 begun = make_int4(0, 0, 0, 0);
+    int vrow = -1, vg = 0;     // the step before: this lane's page row (-1: no box), kv head
+    while (ok && walk_next(p, walk, s)) {
+      if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
+      else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
+      for (int t = 0; t < (s.k.two ? 2 : 1); ++t) {
+        const int x = s.k.two ? t : qsel;
+        if ((q_any >> x & 1) && !(ok = wait(&bars->q_empty[x], q_par >> x & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[x], C::NB * rows_box * 128);
+#pragma unroll
+          for (int bx = 0; bx < C::NB; ++bx)
+            tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bx * 64, s.g * p.group,
+                        s.tok + t * p.tpt, &bars->q_full[x]);
+        }
+        __syncwarp();
+        if (q_any >> x & 1) q_par ^= 1u << x;
+        q_any |= 1u << x;
+      }
+      if (!ok) break;
+      if (!s.k.two) qsel ^= 1;
+      const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
+      for (int i = s.ib; i < s.ie; ++i, ++gs) {
+        const int key0 = (s.k.hi_all - i) * 128 + lane * box_rows;
+        int krow = -1;
+        if (lane < nbox && key0 < s.k.vhi && key0 + box_rows > s.k.vlo) {
+          int page = __ldg(table + (key0 >> p.page_shift));
+          if (page < 0 || page >= p.num_pages) {
+            record_status(p.status, FA_ERR_PAGE);
+            page = 0;
+          }
+          krow = page * p.page_size + (key0 & (p.page_size - 1));
+        }
+        const int sl = gs % C::NS;
+        if (gs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) break;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, krow >= 0)) + __popc(__ballot_sync(0xffffffffu, vrow >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[sl], boxes * C::NB * box_bytes);
+        __syncwarp();
+#pragma unroll
+        for (int bx = 0; bx < C::NB; ++bx) {
+          const int off = sl * C::TILE_BYTES + bx * C::BOX_BYTES + lane * box_bytes;
+          if (krow >= 0) tma_load_3d(smem + C::K_OFF + off, &tmK, bx * 64, s.g, krow, &bars->kv_full[sl]);
+          if (vrow >= 0) tma_load_3d(smem + C::V_OFF + off, &tmV, bx * 64, vg, vrow, &bars->kv_full[sl]);
+        }
+        __syncwarp();
+        vrow = krow;
+        vg = s.g;
+      }
+    }
+    if (ok && gs > 0) {                           // the last step's V
+      const int sl = gs % C::NS;
+      if (gs < C::NS || (ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) {
+        const int boxes = __popc(__ballot_sync(0xffffffffu, vrow >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(&bars->kv_full[sl], boxes * C::NB * box_bytes);
+        __syncwarp();
+#pragma unroll
+        for (int bx = 0; bx < C::NB; ++bx)
+          if (vrow >= 0)
+            tma_load_3d(smem + C::V_OFF + sl * C::TILE_BYTES + bx * C::BOX_BYTES + lane * box_bytes, &tmV, bx * 64, vg,
+                        vrow, &bars->kv_full[sl]);
+        __syncwarp();
+        ++gs;
+      }
+    }
+    if (lane == 0) {
+      p.part_meta[2 * blockIdx.x] = make_int4(ok ? cont : 0, 0, 0, 0);
+      p.part_meta[2 * blockIdx.x + 1] = ok ? begun : make_int4(0, 0, 0, 0);
+    }
+    // Loads in flight must land before this CTA's shared memory goes away.
+    for (int x = 0; x < 2; ++x)
+      if (q_any >> x & 1) wait_warp_drain(&bars->q_full[x], q_par >> x & 1);
+    for (int i = max(0, gs - C::NS); i < gs; ++i) wait_warp_drain(&bars->kv_full[i % C::NS], (i / C::NS) & 1);
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, 0, 1);
+    const uint64_t qdesc0 = smem_desc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024);
+    const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::K_OFF), 16, 1024);
+    const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::V_OFF), C::BOX_BYTES, 1024);
+    Seg s;
+    bool ok = true;
+    int gs = 0, nseg = 0;
+    unsigned q_par = 0;          // bit x: parity of Q buffer x's next load
+    int qsel = 0, flip = 0;
+    unsigned p_par = 0;          // bit t: parity of stream t's next p_full
+    // The step before, whose PV products are due: streams (bit t), those
+    // that begin an item there (bit t), whether its item is a one-tile one,
+    // whether it ends its item, and the V rows [vlo, vhi) that are visible.
+    int pv = 0, pv_first = 0, v_lo = 0, v_hi = 128;
+    bool pv_dual = false, pv_last = false;
+    auto issue_s = [&](int t, int x, int sl) {
+      if (lane == 0) {
+        const uint64_t qd = desc_add(qdesc0, x * C::TILE_BYTES), kd = desc_add(kdesc0, sl * C::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
+          mma_ss(tmem + (t ? C::S_COL1 : C::S_COL0), desc_add(qd, off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars->s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, int sl) -> bool {
+      if (!wait(&bars->p_full[t], p_par >> t & 1)) return false;
+      p_par ^= 1u << t;
+      // the first PV_t of an item overwrites O_t, which the item before
+      // must have read
+      const bool first = (pv_first >> t) & 1;
+      if (first && nseg > 0 && !wait(&bars->o_free, (nseg - 1) & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+        const uint32_t pcols = pv_dual ? 16 : 8;          // 16 keys of P: one part, or two
+        const uint32_t colP = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(colO, colP + kk * pcols, desc_add(vd, kk * 2048), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+        if (pv_dual) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colP + 8 + kk * 16, desc_add(vd, kk * 2048), IDESC_O, 1u);
+        }
+      }
+      __syncwarp();
+      return true;
+    };
+    // V rows that no row sees are zeroed before the tile's products.
+    auto clean_v = [&](int sl) {
+      if (v_lo <= 0 && v_hi >= 128) return;
+      for (int i = lane; i < 128 * 8; i += 32) {
+        const int r = i >> 3;
+        if (r >= v_lo && r < v_hi) continue;
+#pragma unroll
+        for (int bx = 0; bx < C::NB; ++bx)
+          reinterpret_cast<uint4*>(smem + C::V_OFF + sl * C::TILE_BYTES + bx * C::BOX_BYTES)[i] = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    while (ok && walk_next(p, walk, s)) {
+      int started = 0;                                  // streams that have begun this item
+      for (int i = s.ib; i < s.ie; ++i, ++gs) {
+        const int sl = gs % C::NS;
+        const int kt = s.k.hi_all - i;
+        const int cur = s.k.two ? ((kt >= s.k.lo[0] && kt <= s.k.hi[0]) | ((kt >= s.k.lo[1] && kt <= s.k.hi[1]) << 1))
+                                : 1 << ((flip + i - s.ib) & 1);
+        if (!(ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) break;
+        if (i == s.ib) {
+          for (int t = 0; ok && t < (s.k.two ? 2 : 1); ++t) {
+            const int x = s.k.two ? t : qsel;
+            ok = wait(&bars->q_full[x], q_par >> x & 1);
+          }
+          if (!ok) break;
+        }
+        // S of a stream whose P is not waited for comes first
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if ((cur & ~pv) >> t & 1) issue_s(t, s.k.two ? t : qsel, sl);
+        clean_v(sl);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (pv >> t & 1)
+            if (!(ok = issue_pv(t, sl))) break;
+          if ((cur & pv) >> t & 1) issue_s(t, s.k.two ? t : qsel, sl);
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (pv_last) mma_commit(&bars->o_done);
+          mma_commit(&bars->kv_empty[sl]);
+          if (i == s.ie - 1) {
+            if (s.k.two) {
+              mma_commit(&bars->q_empty[0]);
+              mma_commit(&bars->q_empty[1]);
+            } else {
+              mma_commit(&bars->q_empty[qsel]);
+            }
+          }
+        }
+        __syncwarp();
+        nseg += pv_last;
+        pv = cur;
+        pv_first = cur & ~started;
+        started |= cur;
+        pv_dual = !s.k.two;
+        pv_last = i == s.ie - 1;
+        v_lo = s.k.vlo - kt * 128;
+        v_hi = s.k.vhi - kt * 128;
+      }
+      if (!ok) break;
+      if (s.k.two) {
+        q_par ^= 3u;
+      } else {
+        q_par ^= 1u << qsel;
+        qsel ^= 1;
+        flip = (flip + s.ie - s.ib) & 1;
+      }
+    }
+    if (ok && gs > 0) {                                 // the last step's PV
+      const int sl = gs % C::NS;
+      if ((ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) {
+        clean_v(sl);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && (pv >> t & 1)) ok = issue_pv(t, sl);
+        if (ok && lane == 0) mma_commit(&bars->o_done);
+        __syncwarp();
+      }
+    }
+    // Tensor-core work must be finished before the TMEM is released.
+    if (lane == 0) mma_commit(&bars->drain);
+    __syncwarp();
+    wait_warp_drain(&bars->drain, 0);
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const int q4 = warp & 3;
+    const int r = 32 * q4 + lane;                       // row of the tile
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t tS = lane_base + (t ? C::S_COL1 : C::S_COL0);
+    const uint32_t tO = lane_base + (t ? C::O_COL1 : C::O_COL0);
+    const float c2 = p.scale_log2;
+    float* mls = reinterpret_cast<float*>(smem + C::ML_OFF);
+    const int rq = r / p.group, rh = r % p.group;       // token and head of this row
+    bool ok = true;
+    int cs = 0;                  // S products consumed (s_full phases)
+    int nseg = 0, flip = 0;
+    // A warp that gives up (a wait ran out) still walks the items: it meets
+    // the others at the barrier of every one-tile item, and they give up too.
+    while (true) {
+      int n0, steps, diag, low, kend, tl, part, head, tok;
+      bool valid, dual, both;
+      {
+        Seg s;
+        if (!walk_next(p, walk, s)) break;
+        dual = !s.k.two;
+        const bool second = !dual && t;                 // holds the second tile's rows
+        const int f = second ? s.k.f[1] : s.k.f[0], nt = second ? s.k.nt[1] : s.k.nt[0];
+        int kt0;
+        if (dual) {
+          const int first = (t - flip) & 1;             // this stream's first step
+          kt0 = s.k.hi_all - s.ib - first;
+          steps = (s.ie - s.ib - first + 1) >> 1;
+          both = s.ie - s.ib > 1;
+          flip = (flip + s.ie - s.ib) & 1;
+        } else {
+          kt0 = min(s.k.hi_all - s.ib, second ? s.k.hi[1] : s.k.hi[0]);
+          steps = max(0, kt0 - max(s.k.hi_all - s.ie + 1, second ? s.k.lo[1] : s.k.lo[0]) + 1);
+          both = false;
+        }
+        n0 = 128 * kt0;                                 // first key of the tile
+        valid = rq < nt;
+        tl = (dual ? 0 : t * p.tpt) + rq;               // token within the item
+        kend = p.causal ? f + rq : s.L - 1;      // last key this row sees
+        // tiles that reach past `diag` or begin before `low` hold keys that
+        // some row does not see
+        diag = p.causal ? f : s.L - 1;
+        low = f + nt - 1 - p.window;
+        head = s.g * p.group + rh;
+        tok = s.tok + tl;
+        // 0: the whole item; else the slot of the part: 1 its continuation
+        // from the CTA before, 2 its beginning
+        part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
+      }
+      const bool warp_rows = __any_sync(0xffffffffu, valid);
+      float slope2 = 0.f;
+      if (ALIBI) slope2 = valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
+      float m_ref = -INFINITY;
+      float l = 0.f;     // sum of p in fp32: gives the LSE
+      float lr = 0.f;    // sum of the p that the PV products see: normalises O
+      // The steps of this stream; one copy of the loop for each kind of item.
+      auto run_steps = [&](auto kind) {
+        constexpr bool DUAL = decltype(kind)::value;
+        for (int j = 0; j < steps; ++j, ++cs, n0 -= DUAL ? 256 : 128) {
+          if (!(ok = wait(&bars->s_full[t], cs & 1))) break;
+          if (!warp_rows) {                             // no row of this warp holds a token
+            if (lane == 0) mbar_arrive(&bars->p_full[t]);
+            continue;
+          }
+          tc_fence_after();
+          // Tiles on the diagonal, at the end or at the band's lower edge:
+          // scores of keys that the row does not see become -inf, whatever
+          // the slots hold.
+          const bool need_mask = n0 + 127 > diag || n0 < low;
+          const int ub = kend - n0, lb = p.causal ? ub - p.window : 0;
+          // ALiBi bias of column c in log2 units: slope2 * (n0 + c -
+          // position); causal, so the row's position is its last key.
+          const float base = ALIBI ? slope2 * (float)(n0 - kend) : 0.f;
+          const uint64_t c2p = f2(c2, c2);
+          // use(c, scores 16 c .. 16 c + 15) for c = 0 .. 7, the next 16 in
+          // flight meanwhile
+          auto each16 = [&](auto use) {
+            uint32_t s[2][16];
+            tmem_ld16(tS, s[0]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              tmem_wait_ld();
+              reg_fence16(s[c & 1]);
+              if (c < 7) tmem_ld16(tS + 16 * (c + 1), s[(c + 1) & 1]);
+              if (need_mask) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (16 * c + i > ub || 16 * c + i < lb) s[c & 1][i] = __float_as_uint(-INFINITY);
+              }
+              use(c, s[c & 1]);
+            }
+          };
+          // p = 2^(x - mb) of 16 scores: 8 packed pairs (and, DUAL, what the
+          // rounding left of them); sums of p and of the rounded p
+          uint64_t acc[2], accr[2];
+          auto exp16 = [&](int c, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
+            uint64_t bm = ALIBI ? f2(fmaf(slope2, (float)(16 * c), base - mb), fmaf(slope2, (float)(16 * c + 1), base - mb))
+                                : f2(-mb, -mb);
+            const uint64_t step = f2(2.f * slope2, 2.f * slope2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t ex = ffma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2p, bm);
+              if (ALIBI) bm = fadd2(bm, step);
+              float e0, e1;
+              f2split(ex, e0, e1);
+              const float p0 = ex2_approx(e0);
+              const float p1 = ex2_approx(e1);
+              const uint64_t pp = f2(p0, p1);
+              acc[i & 1] = fadd2(acc[i & 1], pp);
+              hi[i] = pack_bf16x2(p0, p1);
+              const uint64_t ph = f2(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xFFFF0000u));
+              if (DUAL) {
+                float r0, r1;
+                f2split(fsub2(pp, ph), r0, r1);
+                lo[i] = pack_bf16x2(r0, r1);
+              } else {
+                accr[i & 1] = fadd2(accr[i & 1], ph);
+              }
+            }
+          };
+          auto pair_sum = [](const uint64_t* a) {
+            float x, y;
+            f2split(fadd2(a[0], a[1]), x, y);
+            return x + y;
+          };
+          // The tile's max, and with it the reference.  Any reference gives
+          // the same result: it is raised where the max grew past tau, and
+          // where this row's own sum overflowed (`over`).
+          auto raise_ref = [&](bool over) {
+            float mx[2] = {-INFINITY, -INFINITY};
+            each16([&](int c, const uint32_t* x) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                if (ALIBI) {
+#pragma unroll
+                  for (int u = 0; u < 2; ++u)
+                    mx[u] = fmax3(mx[u], fmaf(__uint_as_float(x[i + 2 * u]), c2, fmaf(slope2, (float)(16 * c + i + 2 * u), base)),
+                                  fmaf(__uint_as_float(x[i + 2 * u + 1]), c2, fmaf(slope2, (float)(16 * c + i + 2 * u + 1), base)));
+                } else {
+#pragma unroll
+                  for (int u = 0; u < 2; ++u)
+                    mx[u] = fmax3(mx[u], __uint_as_float(x[i + 2 * u]), __uint_as_float(x[i + 2 * u + 1]));
+                }
+              }
+            });
+            float xmax = fmaxf(mx[0], mx[1]);
+            if (!ALIBI) xmax *= c2;
+            const bool raise = xmax > m_ref + kTau || over;
+            const float m_new = raise ? xmax : m_ref;
+            const float alpha = raise ? ex2_approx(m_ref - m_new) : 1.f;
+            l *= alpha;
+            lr *= alpha;
+            // The commit that published S_t also covers this stream's last PV.
+            if (j > 0 && __any_sync(0xffffffffu, raise)) rescale_row<D>(tO, alpha);
+            m_ref = m_new;
+          };
+          if constexpr (DUAL) {
+            // HBM sets the pace here: always the max first, then P, whose two
+            // parts take the 16 columns of their scores.
+            raise_ref(false);
+            const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+            acc[0] = acc[1] = 0;
+            each16([&](int c, const uint32_t* x) {
+              uint32_t pl[16];
+              exp16(c, x, mb, pl, pl + 8);
+              tmem_st16(tS + 16 * c, pl);
+            });
+            const float ts = pair_sum(acc);
+            l += ts;
+            lr += ts;
+          } else {
+            // Once a row has a reference, P is computed with it at once.  A
+            // sum of at most 2^tau shows that no score passed the reference
+            // by more than tau, so no raise is due.
+            uint32_t pk[64];
+            auto exp_pass = [&](float mb) {
+              acc[0] = acc[1] = accr[0] = accr[1] = 0;
+              each16([&](int c, const uint32_t* x) { exp16(c, x, mb, pk + 8 * c, nullptr); });
+            };
+            bool full = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
+            bool over = false;
+            if (!full) {
+              exp_pass(m_ref);
+              over = valid && !(pair_sum(acc) <= kSpecSum);   // also catches inf / nan
+              full = __any_sync(0xffffffffu, over);
+            }
+            if (full) {
+              raise_ref(over);
+              exp_pass(m_ref == -INFINITY ? 0.f : m_ref);
+            }
+            tmem_st32(tS, pk);
+            tmem_st32(tS + 32, pk + 32);
+            l += pair_sum(acc);
+            lr += pair_sum(accr);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[t]);
+        }
+      };
+      if (ok) {
+        if (dual) run_steps(std::true_type{});
+        else run_steps(std::false_type{});
+      }
+      // ---------------------------------------------------------- epilogue
+      if (ok) ok = wait(&bars->o_done, nseg & 1);
+      tc_fence_after();
+      // A stream without a step in this part has no O: weight 0 and its
+      // columns are not used.
+      float w0 = steps > 0 ? 1.f : 0.f, w1 = 0.f;       // of the own columns, of the other stream's
+      int c_from = 0, c_to = D;
+      bool use0 = steps > 0, use1 = false;
+      if (dual) {
+        // join the two streams: each warp takes half of the columns
+        float* own = mls + (t * 128 + r) * 3;
+        const float* oth = mls + ((t ^ 1) * 128 + r) * 3;
+        own[0] = m_ref;
+        own[1] = l;
+        own[2] = lr;
+        if (named_bar_any(1, 256, !ok)) ok = false;
+        const float mo = oth[0];
+        const float M = fmaxf(m_ref, mo);
+        w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
+        w1 = mo == -INFINITY ? 0.f : ex2_approx(mo - M);
+        l = fmaf(w0, l, w1 * oth[1]);
+        lr = fmaf(w0, lr, w1 * oth[2]);
+        m_ref = M;
+        use0 = steps > 0;
+        use1 = both || steps == 0;
+        c_from = t * (D / 2);
+        c_to = c_from + D / 2;
+      }
+      if (!ok) continue;
+      const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
+      const int row = tl * p.group + rh;                 // row of the item
+      const long long orow = (long long)tok * p.Hq + head;
+      const int slot = 2 * (int)blockIdx.x + part - 1;
+      const long long prow = (long long)slot * p.part_rows + row;
+      float sc = 1.f;
+      if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
+      if (warp_rows) {
+#pragma unroll 1
+        for (int c = c_from; c < c_to; c += 16) {
+          uint32_t a[16], b[16];
+          if (use0) tmem_ld16(tO + c, a);
+          if (use1) tmem_ld16(tX + c, b);
+          tmem_wait_ld();
+          reg_fence16(a);
+          reg_fence16(b);
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = use0 ? __uint_as_float(a[i]) * w0 : 0.f;
+            if (use1) v[i] = fmaf(__uint_as_float(b[i]), w1, v[i]);
+            v[i] *= sc;
+          }
+          if (valid) {
+            if (part) store_row16(v, true, p.part_o, prow * D + c);
+            else store_row16(v, p.o_f32, p.o, orow * D + c);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_free);
+      if (valid && !(dual && t)) {                      // a one-tile item's rows: stream 0 reports
+        if (part) {
+          float* ml = p.part_ml + prow * 4;
+          *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, 0.f);
+        } else {
+          p.lse[(long long)head * p.T + tok] = l > 0.f ? (m_ref + lg2_approx(l)) * kLn2 : -INFINITY;
+        }
+      }
+      ++nseg;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  grid_launch_dependents();
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
+// following ones, in their order.  One warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
+  grid_dependency_wait();
+  const int c = blockIdx.x;
+  const int4 it = p.part_meta[2 * c + 1];
+  if (it.x == 0) return;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= it.z * p.group) return;
+  // parts: slot 2 c + 1, then slot 2 c' of c' = c + 1 .. until an end
+  int nparts = 1;
+  for (int c0 = c + 1; c0 < nctas; c0 += 32) {
+    const int kind = c0 + lane < nctas ? p.part_meta[2 * (c0 + lane)].x : 2;
+    const unsigned stop = __ballot_sync(0xffffffffu, kind != 1);
+    if (stop) {
+      const int at = __ffs(stop) - 1;
+      nparts += at + (c0 + at < nctas && __shfl_sync(0xffffffffu, kind, at) == 2 ? 1 : 0);
+      break;
+    }
+    nparts += 32;
+  }
+  auto prow = [&](int s) { return (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row; };
+  float M = -INFINITY;
+  for (int s = lane; s < nparts; s += 32) M = fmaxf(M, p.part_ml[prow(s) * 4]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int PER = D / 32;
+  float o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  float l = 0.f, lr = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < nparts; ++s) {
+    const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + prow(s) * 4);
+    const float wgt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+    l = fmaf(wgt, ml.y, l);
+    lr = fmaf(wgt, ml.z, lr);
+    const float* src = p.part_o + prow(s) * D;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = fmaf(wgt, src[lane + 32 * i], o[i]);
+  }
+  const float inv = lr > 0.f ? 1.f / lr : 0.f;
+  const long long tok = it.y + row / p.group;
+  const int h = it.w * p.group + row % p.group;
+  const long long at = (tok * p.Hq + h) * D;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (p.o_f32) static_cast<float*>(p.o)[at + lane + 32 * i] = o[i] * inv;
+    else static_cast<__nv_bfloat16*>(p.o)[at + lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
+  }
+  if (lane == 0) p.lse[(long long)h * p.T + tok] = l > 0.f ? (M + lg2_approx(l)) * kLn2 : -INFINITY;
+}
+
+template <int D, bool ALIBI>
+int launch_impl(const PagedParams& p, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kern = fwd_paged_kernel<D, ALIBI>;
+  if (const int ea = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ea;
+  CUtensorMap tq, tk, tv;
+  const long long slots = (long long)p.num_pages * p.page_size;
+  const int box = std::min(p.page_size, 128);
+  int r = make_tmap_bf16_3d_box(&tq, p.q, D, p.Hq, p.T, p.group, p.tpt);
+  if (!r) r = make_tmap_bf16_3d(&tk, p.k, D, p.Hkv, slots, box);
+  if (!r) r = make_tmap_bf16_3d(&tv, p.v, D, p.Hkv, slots, box);
+  if (r) return r;
+  int nsm = 0;
+  if (const int es = sm_count(&nsm)) return es;
+  const int grid = std::min(nsm, kPagedCtas);
+  kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+  if (const cudaError_t e = cudaGetLastError()) return (int)e;
+  return launch_dependent(paged_merge_kernel<D>, dim3(grid, (p.part_rows + 7) / 8), dim3(256), 0, stream, p, grid);
+}
+
+}  // namespace
+
+int launch_fwd_paged(const PagedParams& p, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (p.alibi) return p.d == 128 ? launch_impl<128, true>(p, stream) : launch_impl<64, true>(p, stream);
+  return p.d == 128 ? launch_impl<128, false>(p, stream) : launch_impl<64, false>(p, stream);
+}
+
+}  // namespace fa

@@ -1,6 +1,7 @@
 // fa_internal.h -- parameters shared by the host library and its kernels.
 #pragma once
 #include <stdint.h>
+#include <vector_types.h>
 
 #include "../../include/fa.h"
 
@@ -168,6 +169,36 @@ struct CachePagesCopy {
   unsigned chunks;
 };
 
+// Attention of new tokens over a cache in pages (fa_fwd_paged.cu).
+struct PagedParams {
+  const void* q;               // bf16 [T, Hq, d]
+  const void* k;               // bf16 [num_pages, page_size, Hkv, d]
+  const void* v;
+  void* o;                     // [T, Hq, d], fp32 or bf16
+  float* lse;                  // [Hq, T]
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* cache_seqlens;  // [B], the new tokens included
+  const int32_t* cu_seqlens;   // [B + 1] or nullptr (every sequence brings N tokens)
+  const float* alibi;          // [Hq] or nullptr
+  float* part_o;               // workspace: [2 * CTAs][part_rows][d], a part's O, not divided
+  float* part_ml;              // workspace: [2 * CTAs][part_rows][4]: m (log2 units), l, the
+                               // sum of P as the PV products saw it
+  int4* part_meta;             // workspace: [2 * CTAs]
+  unsigned int* status;
+  long long T;
+  int B, Hq, Hkv, N, d, group;
+  int tpt;                     // tokens per tile of 128 rows: 128 / group
+  int part_rows;               // rows of the largest item
+  int plan_lanes;              // lanes that add up one sequence's work
+  int page_size, page_shift, num_pages, max_pages;
+  int causal, window, o_f32;   // window: kNoWindow when unbanded
+  float scale, scale_log2;
+};
+
+// CTAs of the paged forward: GB300's SMs; each leaves at most two parts.
+constexpr int kPagedCtas = 152;
+constexpr int kPagedMaxBatch = 8192;
+
 // The host-side argument checks of fa_bwd (everything but the workspace), in
 // fa_bwd's order.  On FA_OK, *T is the total token count, or 0 when the call
 // has nothing to compute.
@@ -192,6 +223,7 @@ int launch_norm_rope(const NormRopeParams& p, void* stream);
 int launch_norm_rope_pages(const NormRopeParams& p, void* stream);    // into cache pages
 int launch_norm_rope_bwd(const NormRopeParams& p, void* stream);      // rows, then the weights' sums
 int launch_copy_pages(CachePagesCopy p, void* stream);
+int launch_fwd_paged(const PagedParams& p, void* stream);             // runs + merge of parts
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__

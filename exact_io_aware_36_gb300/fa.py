@@ -30,7 +30,8 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_stage", "fa_bwd_workspace_size", "fa_chec
            "fa_decode", "fa_decode_workspace_size", "fa_fp8_layout_get", "fa_fp8_quantize",
            "fa_fwd_fp8", "fa_host_cache_stats", "fa_bwd_workspace_size_gqa", "fa_bwd_dkdv_split",
            "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
-           "fa_qk_norm_rope_append", "fa_cache_append", "fa_cache_copy")
+           "fa_qk_norm_rope_append", "fa_cache_append", "fa_cache_copy", "fa_fwd_paged",
+           "fa_fwd_paged_workspace_size")
 FA_BWD_PREPROCESS, FA_BWD_DKDV, FA_BWD_DQ_CONVERT = 0, 1, 2
 
 
@@ -100,6 +101,11 @@ def load(path: Optional[str] = None):
     lib.fa_qk_norm_rope_append.argtypes = [vp, vp, vp, vp, vp, vp, ll, ll, ll, vp, vp, f, vp, vp, vp, vp, vp,
                                            i, i, i, i, i, ll, i, i, i, i, i, i, vp]
     lib.fa_qk_norm_rope_append.restype = i
+    lib.fa_fwd_paged_workspace_size.argtypes = [i, i, i, i]
+    lib.fa_fwd_paged_workspace_size.restype = sz
+    lib.fa_fwd_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, ll, i, i, i, f, i, i, vp, i,
+                                 vp, sz, vp]
+    lib.fa_fwd_paged.restype = i
     lib.fa_cache_copy.argtypes = [vp, vp, vp, vp, i, i, i, i, i, vp]
     lib.fa_cache_copy.restype = i
     lib.fa_check_device_error.argtypes = [vp]
@@ -228,6 +234,19 @@ def fa_qk_norm_rope_append(q, k, v, q_out, k_pages, v_pages, q_stride, k_stride,
 
 def fa_cache_copy(k_pages, v_pages, src, dst, n, num_pages, page_size, Hkv, d, stream) -> int:
     return load().fa_cache_copy(k_pages, v_pages, src, dst, n, num_pages, page_size, Hkv, d, stream)
+
+
+def fa_fwd_paged_workspace_size(Hq, Hkv, N, d) -> int:
+    return load().fa_fwd_paged_workspace_size(Hq, Hkv, N, d)
+
+
+def fa_fwd_paged(q, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens, o, lse, B, Hq, Hkv,
+                 N, d, total_tokens, page_size, num_pages, max_pages, scale, causal, window,
+                 alibi_slopes, o_dtype, workspace, workspace_bytes, stream) -> int:
+    return load().fa_fwd_paged(q, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens, o, lse,
+                               B, Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages,
+                               scale, int(causal), int(window), alibi_slopes, o_dtype, workspace,
+                               workspace_bytes, stream)
 
 
 def fa_bwd_workspace_size(B, Hq, N, d, total_tokens) -> int:
@@ -699,3 +718,43 @@ def cache_copy(k_pages, v_pages, src, dst, *, stream=None, check: bool = False):
     _run("fa_cache_copy", fa_cache_copy, device, stream, check, kpool, vpool,
          _checked("src", src, torch.int32, device, (n,)), _checked("dst", dst, torch.int32, device, (n,)),
          n, num_pages, page_size, Hkv, d)
+
+
+def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqlens=None,
+                            max_seqlen: Optional[int] = None, causal: bool = True,
+                            scale: Optional[float] = None, alibi_slopes=None,
+                            window: Optional[int] = None, out=None, lse=None, out_dtype=None,
+                            workspace=None, stream=None, check: bool = False):
+    """O, LSE of each sequence's newest tokens over its pages through ``fa_fwd_paged``.
+
+    q: bf16 [T, Hq, d]; pools, table, lengths and ``cu_seqlens`` / ``max_seqlen``
+    as ``cache_append`` (which has put the new tokens' k and v there).  Causal:
+    the last new token sees the whole sequence, the one before all but one
+    key; otherwise every row sees all of its sequence's keys.  Returns
+    (o [T, Hq, d] of ``out_dtype`` (default: ``out``'s dtype, else q's), lse
+    float32 [Hq, T]).
+    """
+    import torch
+    device = _cuda_device(q, stream)
+    if q.dim() != 3:
+        raise ValueError("q: [T, Hq, d] expected")
+    T, Hq, d = q.shape
+    qp = _checked("q", q, torch.bfloat16, device)
+    kpool, vpool, num_pages, page_size, Hkv, dp = _pages(k_pages, v_pages, device)
+    if dp != d:
+        raise ValueError("q and the pages must have the same head dimension")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
+    slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, device, (Hq,))
+    if out is None:
+        out = _empty((T, Hq, d), out_dtype or q.dtype, device, stream)
+    if lse is None:
+        lse = _empty((Hq, T), torch.float32, device, stream)
+    need = fa_fwd_paged_workspace_size(Hq, Hkv, N, d)
+    if workspace is None:
+        workspace = _empty((max(need, 1),), torch.uint8, device, stream)
+    _run("fa_fwd_paged", fa_fwd_paged, device, stream, check, qp, kpool, vpool, tp, cp, cup,
+         _checked("out", out, out.dtype, device, (T, Hq, d)), _checked("lse", lse, torch.float32, device, (Hq, T)),
+         B, Hq, Hkv, N, d, T, page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale),
+         causal, -1 if window is None else window, slopes, _dtype_code(out.dtype),
+         _checked("workspace", workspace, torch.uint8, device), workspace.numel())
+    return out, lse

@@ -445,6 +445,43 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
                                  int num_pages, int max_pages, void* stream);
 
 /*
+ * Attention of each sequence's newest tokens over its cache in pages (the new
+ * tokens' keys and values are in the pages already: fa_cache_append).  Row i
+ * of sequence b's n_b new tokens is the token at position L_b - n_b + i.
+ *   causal 1: it sees keys j <= L_b - n_b + i, with the sliding window and
+ *             the ALiBi bias of fa_fwd; the result equals the last n_b rows of
+ *             fa_fwd over the whole sequence.  Needs L_b >= n_b.
+ *   causal 0: it sees all L_b keys, whatever n_b (an encoder's states, kept
+ *             in pages).  A window or ALiBi is FA_ERR_UNSUPPORTED.
+ * A row that sees no key (L_b = 0) has o = 0 and lse = -inf.  One token per
+ * sequence, long chunks and any mixture of both go in one call; with lengths
+ * on the device alone, a captured call can be replayed with others.  Results
+ * do not vary from run to run.
+ *   q             bf16 [T, Hq, d], contiguous; rows of b as in fa_cache_append
+ *                 (cu_seqlens, N = the largest n_b, total_tokens)
+ *   o, lse        [T, Hq, d] of o_dtype (FA_FP32 or FA_BF16), float32 [Hq, T]
+ *                 (natural log); rows behind the last sequence are left alone
+ *   Hq / Hkv      <= 128;  B <= 8192
+ *   workspace     device, >= fa_fwd_paged_workspace_size bytes, 256-byte
+ *                 aligned, contents irrelevant on entry; calls that may overlap
+ *                 need one each
+ * Pages without a key that some row sees (below the window) are not read, nor
+ * their table entries; slots behind a sequence's last token may hold anything.
+ * Device errors as fa_cache_append; a sequence with a wrong length is skipped.
+ * Scores and sums are float32; P is rounded to bf16 for the P V product, and
+ * where an item has at most 128 rows (n_b * Hq / Hkv), to two bf16 parts.
+ */
+size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d);
+
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                       const int32_t* block_table, const int32_t* cache_seqlens,
+                       const int32_t* cu_seqlens, void* o, float* lse, int B, int Hq, int Hkv,
+                       int N, int d, long long total_tokens, int page_size, int num_pages,
+                       int max_pages, float scale, int causal, int window,
+                       const float* alibi_slopes, fa_dtype o_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
  * Copies whole pages of both pools: page src[i] to page dst[i], i < n (device
  * int32 arrays): the partly filled last page of a sequence that is forked, or
  * the moves of a compaction.  The copies run in no order: a pair whose dst is
