@@ -526,8 +526,6 @@ static fa_status norm_rope_args(fa::NormRopeParams* p, const float* q_weight, co
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_UNSUPPORTED;
   if (Hq > 65535 || Hkv > 65535 || T >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  // a warp takes at least 4 rows of a token; 1-D grids must fit 2^31 - 1
-  if (T * ((Hq + 2ll * Hkv + 3) / 4) >= (1ll << 33)) return FA_ERR_UNSUPPORTED;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return FA_ERR_UNSUPPORTED;
   if (!q_weight != !k_weight) return FA_ERR_NULL;
   if (rot_dim && (!cos || !sin)) return FA_ERR_NULL;
@@ -677,7 +675,6 @@ static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k
   if (!cu_seqlens && total_tokens != 0 && total_tokens != dense) return FA_ERR_SHAPE;
   if (!cu_seqlens && dense >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   p.T = cu_seqlens ? total_tokens : dense;
-  if (p.T * ((p.Hq + 2ll * p.Hkv + 3) / 4) >= (1ll << 33)) return FA_ERR_UNSUPPORTED;
   if ((st = check_rows(q, q_stride, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(q_out, (long long)p.Hq * p.d, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(k, k_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;

@@ -146,7 +146,8 @@ struct NormRopeParams {
   long long T;
   float eps;
   int Hq, Hkv, d, rot, max_pos, interleaved, f32;
-  int units_per_token;
+  int sets_q, sets_k, sets_v;  // row sets of a token's query, key and value heads
+  int sets_per_unit, units_per_token;
   // pages
   const int32_t* block_table;  // [B, max_pages]
   const int32_t* cache_seqlens;  // [B], the new tokens included
@@ -156,6 +157,8 @@ struct NormRopeParams {
 
 // Blocks of the gradient kernel: four per SM of GB300 (152).
 constexpr int kNormRopeBwdBlocks = 4 * 152;
+// Warps that a large batch is cut into: two rounds of what 152 SMs hold.
+constexpr int kNormRopeWarps = 2 * 152 * 48;
 
 // Page copies (fa_cache.cu).
 struct CachePagesCopy {

@@ -12,12 +12,16 @@
 // All arithmetic is float32; each output is rounded once.  r is recomputed in
 // the backward: x has to be read anyway, so saving r would only add bytes.
 //
-// Bound by HBM: a row is read and written once (twice read in the backward)
-// against about 10 operations per element.  A lane holds 8 consecutive
-// elements (16 bytes of bf16), so d / 8 lanes share a row and a warp holds
-// 32 * 8 / d rows at a time, two such sets per unit of work: the loads of both
-// are in flight before the first is used.  A unit's rows belong to one token,
-// so its angles are loaded once for all of them.
+// Bound by HBM: a row is read and written once (two are read in the backward).
+// A lane holds 8 consecutive elements (16 bytes of bf16), so d / 8 lanes share
+// a row and a warp holds a set of 32 * 8 / d rows of one kind (query, key or
+// value heads) of one token.  A warp takes several sets of its token, two at
+// a time and the next two in flight, so that a token's angles, multiplied by
+// the weights, are made once:
+//     z = r (x (w c) + x' (w' s)),   x', w': the pair's other member.
+// With these packed in float32 pairs a set of bf16 rows costs some 70
+// instructions (105 in the backward), which leaves the issue slots half idle
+// at HBM's rate; the first form, at about 400 a set of two, was bound by them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,51 +37,66 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSets = 2;                      // row sets of one unit of work
-
-// 8 consecutive elements of a row, as stored and as float32.
+// 8 consecutive elements of a row as stored; as 4 float32 pairs; swapped within
+// their pairs; and another lane's.
 template <typename T>
 struct Vec8;
 
 template <>
 struct Vec8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  __device__ __forceinline__ void get(float* f) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   }
-  __device__ __forceinline__ void set(const float* f) {
-    a = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    return f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ uint64_t swapped(int i) const {
+    return f2(__uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(w[i] << 16));
+  }
+  __device__ __forceinline__ Vec8 from_lane(int src) const {
+    Vec8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], src);
+    return r;
+  }
+  __device__ __forceinline__ void set(int i, uint64_t v) {
+    float a, b;
+    f2split(v, a, b);
+    w[i] = pack_bf16x2(a, b);
   }
 };
 
 template <>
 struct Vec8<float> {
-  float4 a, b;
+  float w[8];
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.f;
+  }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+    reinterpret_cast<float4*>(p)[0] = make_float4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(w[4], w[5], w[6], w[7]);
   }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ uint64_t pair(int i) const { return f2(w[2 * i], w[2 * i + 1]); }
+  __device__ __forceinline__ uint64_t swapped(int i) const { return f2(w[2 * i + 1], w[2 * i]); }
+  __device__ __forceinline__ Vec8 from_lane(int src) const {
+    Vec8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], src);
+    return r;
   }
-  __device__ __forceinline__ void set(const float* f) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
+  __device__ __forceinline__ void set(int i, uint64_t v) { f2split(v, w[2 * i], w[2 * i + 1]); }
 };
 
 // Sum over the LPR lanes that share a row; every one of them gets it.
@@ -88,28 +107,36 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The angles of a lane's 8 elements at one position.  Not interleaved: the
-// lane's elements 8 l .. 8 l + 7 are all first or all second members of their
-// pairs (rot is a multiple of 16), the other members sit 8 elements per lane
-// at lane `mate`, and c / s hold 8 angles (s negated for first members, so
-// z = y c + y' s for both).  Interleaved: 4 pairs within the lane.
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float a, b;
+  f2split(v, a, b);
+  return a + b;
+}
+
+// The angles of a lane's 8 elements at one position, as 4 pairs of (c, c) and
+// (s, s), s signed so that z = y c + y' s.  Not interleaved: the lane's elements
+// are all first or all second members of their pairs (rot is a multiple of
+// 16), and the other members are those of lane `mate` of the row.  Lanes
+// without rotation have c = 1, s = 0 and must not use y'.
 struct Angles {
-  float c[8], s[8];
-  int mate;
-  bool on;                                    // the lane's elements are rotated
+  uint64_t c[4], s[4];
 };
 
-// INV: the transposed rotation.
-template <int LPR>
+// The lane whose elements are this lane's partners (itself without rotation or
+// interleaved).
+__device__ __forceinline__ int mate_lane(const NormRopeParams& p, int l) {
+  if (8 * l >= p.rot || p.interleaved) return l;
+  return 16 * l < p.rot ? l + p.rot / 16 : l - p.rot / 16;
+}
+
+// `inv`: the transposed rotation.
 __device__ __forceinline__ void load_angles(const NormRopeParams& p, int pos, int l, bool inv, Angles& g) {
-  g.on = 8 * l < p.rot;
-  g.mate = l;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    g.c[i] = 1.f;
-    g.s[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    g.c[i] = f2(1.f, 1.f);
+    g.s[i] = f2(0.f, 0.f);
   }
-  if (!g.on) return;
+  if (8 * l >= p.rot) return;
   const int half = p.rot / 2;
   const float* cs = p.cos + (long long)pos * half;
   const float* sn = p.sin + (long long)pos * half;
@@ -119,51 +146,48 @@ __device__ __forceinline__ void load_angles(const NormRopeParams& p, int pos, in
     const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      g.c[2 * i] = g.c[2 * i + 1] = c[i];
-      g.s[2 * i] = inv ? s[i] : -s[i];
-      g.s[2 * i + 1] = inv ? -s[i] : s[i];
+      g.c[i] = f2(c[i], c[i]);
+      g.s[i] = inv ? f2(s[i], -s[i]) : f2(-s[i], s[i]);
     }
   } else {
     const bool first = 8 * l < half;
     const int i0 = first ? 8 * l : 8 * l - half;
-    g.mate = first ? l + half / 8 : l - half / 8;
     const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + i0));
     const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + i0) + 1);
     const float4 s0 = __ldg(reinterpret_cast<const float4*>(sn + i0));
     const float4 s1 = __ldg(reinterpret_cast<const float4*>(sn + i0) + 1);
     const float sg = first != inv ? -1.f : 1.f;
-    g.c[0] = c0.x; g.c[1] = c0.y; g.c[2] = c0.z; g.c[3] = c0.w;
-    g.c[4] = c1.x; g.c[5] = c1.y; g.c[6] = c1.z; g.c[7] = c1.w;
-    g.s[0] = sg * s0.x; g.s[1] = sg * s0.y; g.s[2] = sg * s0.z; g.s[3] = sg * s0.w;
-    g.s[4] = sg * s1.x; g.s[5] = sg * s1.y; g.s[6] = sg * s1.z; g.s[7] = sg * s1.w;
+    g.c[0] = f2(c0.x, c0.y); g.c[1] = f2(c0.z, c0.w); g.c[2] = f2(c1.x, c1.y); g.c[3] = f2(c1.z, c1.w);
+    g.s[0] = f2(sg * s0.x, sg * s0.y); g.s[1] = f2(sg * s0.z, sg * s0.w);
+    g.s[2] = f2(sg * s1.x, sg * s1.y); g.s[3] = f2(sg * s1.z, sg * s1.w);
   }
 }
 
-// f <- rotated f.  Warp-collective (the pair's other member may sit in another
-// lane of the row); lanes without rotation keep f.
-template <int LPR>
-__device__ __forceinline__ void rotate(const NormRopeParams& p, const Angles& g, int lane, float* f) {
-  if (p.rot == 0) return;
-  float o[8];
-  if (p.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
-  } else {
-    const int src = (lane & ~(LPR - 1)) + g.mate;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, f[i], src);
+// The partners of a lane's elements.  Warp-collective; zero where there is no
+// rotation, so that an infinity there meets no 0.
+template <typename T>
+struct Partners {
+  Vec8<T> v;
+  bool swap;
+  __device__ __forceinline__ Partners(const NormRopeParams& p, const Vec8<T>& x, int src, bool on) {
+    swap = p.interleaved;
+    v = x;
+    if (!swap && p.rot) v = x.from_lane(src);
+    if (!on) v.zero();
   }
-  if (g.on) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], g.c[i], o[i] * g.s[i]);
-  }
-}
+  __device__ __forceinline__ uint64_t pair(int i) const { return swap ? v.swapped(i) : v.pair(i); }
+};
 
-__device__ __forceinline__ void load_weights(const float* w, int l, float* f) {
+__device__ __forceinline__ void load_weights(const float* w, int l, uint64_t* f) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(w + 8 * l));
   const float4 b = __ldg(reinterpret_cast<const float4*>(w + 8 * l) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  f[0] = f2(a.x, a.y); f[1] = f2(a.z, a.w); f[2] = f2(b.x, b.y); f[3] = f2(b.z, b.w);
+}
+
+__device__ __forceinline__ uint64_t swap_pair(uint64_t v) {
+  float a, b;
+  f2split(v, a, b);
+  return f2(b, a);
 }
 
 // The sequence that token t belongs to, its position there and its row in the
@@ -217,33 +241,51 @@ __device__ __forceinline__ bool locate(const NormRopeParams& p, long long t, int
   return true;
 }
 
-// Rows of a token, in this order: Hq query heads, Hkv key heads and, with
-// PAGES, Hkv value heads (copied).  One warp per unit: kSets sets of
-// 32 / LPR rows of one token.
+// What one warp does: sets [sa, sb) of token t.  A token's sets are those of its
+// query heads, of its key heads and, with pages, of its value heads.
+struct Unit {
+  long long t;
+  int sa, sb;
+};
+
+__device__ __forceinline__ bool unit_at(const NormRopeParams& p, unsigned unit, Unit& u) {
+  const unsigned t = unit / (unsigned)p.units_per_token;
+  if (t >= (unsigned long long)p.T) return false;
+  u.t = t;
+  u.sa = (int)(unit - t * p.units_per_token) * p.sets_per_unit;
+  u.sb = min(u.sa + p.sets_per_unit, p.sets_q + p.sets_k + p.sets_v);
+  return true;
+}
+
+// Kind (0 query, 1 key, 2 value) of set s and this lane's head in it; true if
+// the head exists.
+template <int RPS>
+__device__ __forceinline__ bool set_head(const NormRopeParams& p, int s, int sub, int* kind, int* h) {
+  *kind = s < p.sets_q ? 0 : s < p.sets_q + p.sets_k ? 1 : 2;
+  *h = (s - (*kind == 0 ? 0 : *kind == 1 ? p.sets_q : p.sets_q + p.sets_k)) * RPS + sub;
+  return *h < (*kind == 0 ? p.Hq : p.Hkv);
+}
+
 template <int D, typename T, bool PAGES>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;                // rows per set
   const int lane = threadIdx.x & 31;
-  const int l = lane & (LPR - 1);
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int per_token = p.units_per_token;
-  const long long t = unit / per_token;
-  if (t >= p.T) return;
-  const int h0 = (int)(unit - t * per_token) * (kSets * RPS);
-  const int nrow = p.Hq + (PAGES ? 2 : 1) * p.Hkv;
-
-  Vec8<T> x[kSets];
-#pragma unroll
-  for (int s = 0; s < kSets; ++s) {
-    const int h = h0 + s * RPS + lane / LPR;
-    const T* src = h < p.Hq ? static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * D
-                 : h < p.Hq + p.Hkv
-                     ? static_cast<const T*>(p.k) + t * p.k_stride + (long long)(h - p.Hq) * D
-                     : static_cast<const T*>(p.v) + t * p.v_stride + (long long)(h - p.Hq - p.Hkv) * D;
-    if (h < nrow) x[s].load(src + 8 * l);
-    else x[s].zero();
-  }
+  const int l = lane & (LPR - 1), sub = lane / LPR;
+  Unit u;
+  if (!unit_at(p, blockIdx.x * kWarps + (threadIdx.x >> 5), u)) return;
+  const long long t = u.t;
+  auto load = [&](int s, Vec8<T>& x) {
+    int kind, h;
+    x.zero();
+    if (s < u.sb && set_head<RPS>(p, s, sub, &kind, &h))
+      x.load((kind == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
+              : kind == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
+                          : static_cast<const T*>(p.v) + t * p.v_stride) + (long long)h * D + 8 * l);
+  };
+  Vec8<T> x[2];
+  load(u.sa, x[0]);
+  load(u.sa + 1, x[1]);
   int pos = 0;
   long long page_row = 0;
   if constexpr (PAGES) {
@@ -256,34 +298,64 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
     return;
   }
   Angles ang;
-  load_angles<LPR>(p, pos, l, false, ang);
+  load_angles(p, pos, l, false, ang);
+  const bool on = 8 * l < p.rot;
+  const int ml = mate_lane(p, l), src = sub * LPR + ml;
+  uint64_t wc[4], ws[4];                       // angles times weights, of kind `have`
+  int have = -1;
+  for (int s = u.sa; s < u.sb; s += 2) {
+    Vec8<T> next[2];
+    load(s + 2, next[0]);
+    load(s + 3, next[1]);
 #pragma unroll
-  for (int s = 0; s < kSets; ++s) {
-    const int h = h0 + s * RPS + lane / LPR;
-    const bool is_q = h < p.Hq, is_v = PAGES && h >= p.Hq + p.Hkv;
-    float f[8];
-    x[s].get(f);
-    if (p.q_weight) {
-      float ss = 0.f;
+    for (int k = 0; k < 2; ++k) {
+      if (s + k >= u.sb) break;                // warp-uniform, as is a set's kind
+      int kind, h;
+      const bool live = set_head<RPS>(p, s + k, sub, &kind, &h);
+      if (kind < 2) {
+        if (kind != have) {
+          have = kind;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-      float w[8];
-      load_weights(is_q ? p.q_weight : p.k_weight, l, w);
+          for (int i = 0; i < 4; ++i) {
+            wc[i] = ang.c[i];
+            ws[i] = ang.s[i];
+          }
+          if (p.q_weight) {
+            const float* w = kind == 0 ? p.q_weight : p.k_weight;
+            uint64_t a[4], b[4];
+            load_weights(w, l, a);
+            load_weights(w, ml, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+            for (int i = 0; i < 4; ++i) {
+              wc[i] = fmul2(wc[i], a[i]);
+              ws[i] = fmul2(ws[i], p.interleaved ? swap_pair(b[i]) : b[i]);
+            }
+          }
+        }
+        float r = 1.f;
+        if (p.q_weight) {
+          uint64_t ss = f2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = ffma2(x[k].pair(i), x[k].pair(i), ss);
+          r = rsqrtf(row_sum<LPR>(pair_sum(ss)) * (1.f / D) + p.eps);
+        }
+        const uint64_t r2 = f2(r, r);
+        const Partners<T> y(p, x[k], src, on);
+        Vec8<T> z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z.set(i, fmul2(ffma2(x[k].pair(i), wc[i], fmul2(y.pair(i), ws[i])), r2));
+        if (live) {
+          T* dst = kind == 0 ? static_cast<T*>(p.q_out) + t * p.Hq * D
+                             : static_cast<T*>(p.k_out) + (PAGES ? page_row : t) * p.Hkv * D;
+          z.store(dst + (long long)h * D + 8 * l);
+        }
+      } else if (live) {                       // value rows pass as they are
+        x[k].store(static_cast<T*>(p.v_out) + (page_row * p.Hkv + h) * D + 8 * l);
+      }
     }
-    rotate<LPR>(p, ang, lane, f);
-    if (!is_v) x[s].set(f);                    // value rows pass as they are
-    if (h < nrow) {
-      T* dst;
-      if (is_q) dst = static_cast<T*>(p.q_out) + (t * p.Hq + h) * D;
-      else if constexpr (PAGES)
-        dst = is_v ? static_cast<T*>(p.v_out) + (page_row * p.Hkv + (h - p.Hq - p.Hkv)) * D
-                   : static_cast<T*>(p.k_out) + (page_row * p.Hkv + (h - p.Hq)) * D;
-      else dst = static_cast<T*>(p.k_out) + (t * p.Hkv + (h - p.Hq)) * D;
-      x[s].store(dst + 8 * l);
-    }
+    x[0] = next[0];
+    x[1] = next[1];
   }
 }
 
@@ -298,91 +370,104 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
   __shared__ float red[kWarps][2][D];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const int l = lane & (LPR - 1);
-  const int per_token = p.units_per_token;
-  const long long units = p.T * per_token;
-  const int nrow = p.Hq + p.Hkv;
-  float dwq[8], dwk[8];
+  const int l = lane & (LPR - 1), sub = lane / LPR;
+  const bool on = 8 * l < p.rot;
+  const int src = sub * LPR + mate_lane(p, l);
+  uint64_t dw[2][4];                           // of the query and the key weight
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2(0.f, 0.f);
 
-  for (long long unit = (long long)blockIdx.x * kWarps + warp; unit < units; unit += (long long)gridDim.x * kWarps) {
-    const long long t = unit / per_token;
-    const int h0 = (int)(unit - t * per_token) * (kSets * RPS);
-    Vec8<T> x[kSets], z[kSets];
-#pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-      const int h = h0 + s * RPS + lane / LPR;
-      const bool is_q = h < p.Hq;
-      const int hk = h - p.Hq;
-      if (h < nrow) {
-        x[s].load((is_q ? static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * D
-                        : static_cast<const T*>(p.k) + t * p.k_stride + (long long)hk * D) + 8 * l);
-        z[s].load((is_q ? static_cast<const T*>(p.dq_out) + (t * p.Hq + h) * D
-                        : static_cast<const T*>(p.dk_out) + (t * p.Hkv + hk) * D) + 8 * l);
-      } else {
-        x[s].zero();
-        z[s].zero();
+  Unit u;
+  for (unsigned unit = blockIdx.x * kWarps + warp; unit_at(p, unit, u); unit += gridDim.x * kWarps) {
+    const long long t = u.t;
+    auto load = [&](int s, Vec8<T>& x, Vec8<T>& z) {
+      int kind, h;
+      x.zero();
+      z.zero();
+      if (s < u.sb && set_head<RPS>(p, s, sub, &kind, &h)) {
+        const long long at = (long long)h * D + 8 * l;
+        x.load((kind == 0 ? static_cast<const T*>(p.q) + t * p.q_stride : static_cast<const T*>(p.k) + t * p.k_stride) + at);
+        z.load((kind == 0 ? static_cast<const T*>(p.dq_out) + t * p.Hq * D : static_cast<const T*>(p.dk_out) + t * p.Hkv * D) + at);
       }
-    }
+    };
+    Vec8<T> x, z;
+    load(u.sa, x, z);
     const int pos = p.rot ? __ldg(p.positions + t) : 0;
     if (p.rot && (pos < 0 || pos >= p.max_pos)) {
       if (lane == 0) record_status(p.status, FA_ERR_POSITION);
       continue;
     }
     Angles ang;
-    load_angles<LPR>(p, pos, l, true, ang);
+    load_angles(p, pos, l, true, ang);
+    uint64_t w[4];
+    int have = -1;
+    for (int s = u.sa; s < u.sb; ++s) {
+      Vec8<T> xn, zn;
+      load(s + 1, xn, zn);
+      int kind, h;
+      const bool live = set_head<RPS>(p, s, sub, &kind, &h);
+      uint64_t dy[4];
+      {
+        const Partners<T> y(p, z, src, on);
 #pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-      const int h = h0 + s * RPS + lane / LPR;
-      const bool is_q = h < p.Hq;
-      float f[8], dy[8];
-      x[s].get(f);
-      z[s].get(dy);
-      rotate<LPR>(p, ang, lane, dy);
+        for (int i = 0; i < 4; ++i) dy[i] = ffma2(z.pair(i), ang.c[i], fmul2(y.pair(i), ang.s[i]));
+      }
       if (p.q_weight) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        float w[8];
-        load_weights(is_q ? p.q_weight : p.k_weight, l, w);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] *= r;                           // xh
-          const float dw = h < nrow ? dy[i] * f[i] : 0.f;
-          dwq[i] += is_q ? dw : 0.f;
-          dwk[i] += is_q ? 0.f : dw;
-          dy[i] *= w[i];
-          dot = fmaf(dy[i], f[i], dot);
+        if (kind != have) {
+          have = kind;
+          load_weights(kind == 0 ? p.q_weight : p.k_weight, l, w);
         }
-        const float m = row_sum<LPR>(dot) * (1.f / D);
+        uint64_t ss = f2(0.f, 0.f), dot = f2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dy[i] = r * fmaf(-f[i], m, dy[i]);
+        for (int i = 0; i < 4; ++i) {
+          ss = ffma2(x.pair(i), x.pair(i), ss);
+          dot = ffma2(fmul2(dy[i], w[i]), x.pair(i), dot);
+        }
+        float a = pair_sum(ss), b = pair_sum(dot);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        const float r = rsqrtf(a * (1.f / D) + p.eps);
+        // xh = x r, dw += dy xh, dx = r (dy w - xh mean(dy w xh)); a row that
+        // is not there has xh = 0, whatever its r
+        const float rl = live ? r : 0.f, m = -(b * r * (1.f / D)) * r;
+        const uint64_t r2 = f2(r, r), m2 = f2(m, m), rl2 = f2(rl, rl);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t xh = fmul2(x.pair(i), rl2);
+          if (kind == 0) dw[0][i] = ffma2(dy[i], xh, dw[0][i]);
+          else dw[1][i] = ffma2(dy[i], xh, dw[1][i]);
+          dy[i] = ffma2(xh, m2, fmul2(fmul2(dy[i], w[i]), r2));
+        }
       }
-      if (h < nrow) {
-        x[s].set(dy);
-        T* dst = is_q ? static_cast<T*>(p.dq) + t * p.dq_stride + (long long)h * D
-                      : static_cast<T*>(p.dk) + t * p.dk_stride + (long long)(h - p.Hq) * D;
-        x[s].store(dst + 8 * l);
+      if (live) {
+        Vec8<T> d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d.set(i, dy[i]);
+        d.store((kind == 0 ? static_cast<T*>(p.dq) + t * p.dq_stride : static_cast<T*>(p.dk) + t * p.dk_stride) +
+                (long long)h * D + 8 * l);
       }
+      x = xn;
+      z = zn;
     }
   }
   if (p.q_weight) {
     // the warp's row groups, then the block's warps, in a fixed order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) {
-        dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-        dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2split(dw[k][i], a, b);
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if (lane < LPR) *reinterpret_cast<float2*>(&red[warp][k][8 * l + 2 * i]) = make_float2(a, b);
       }
-      if (lane < LPR) {
-        red[warp][0][8 * l + i] = dwq[i];
-        red[warp][1][8 * l + i] = dwk[i];
-      }
-    }
     __syncthreads();
     if (threadIdx.x < 2 * D) {
       float s = 0.f;
@@ -416,20 +501,31 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* part, in
   }
 }
 
+// Cuts a token's sets into units: as many sets per warp as still leave a GPU
+// of GB300's size `want` warps, at least two (the loads of both overlap).
+template <int D>
+long long cut_units(NormRopeParams& p, bool values, int want) {
+  constexpr int RPS = 32 / (D / 8);
+  p.sets_q = (p.Hq + RPS - 1) / RPS;
+  p.sets_k = (p.Hkv + RPS - 1) / RPS;
+  p.sets_v = values ? p.sets_k : 0;
+  const long long sets = p.sets_q + p.sets_k + p.sets_v;
+  p.sets_per_unit = (int)std::min(sets, std::max(2ll, p.T * sets / want));
+  p.units_per_token = (int)((sets + p.sets_per_unit - 1) / p.sets_per_unit);
+  return p.T * p.units_per_token;
+}
+
 template <int D, typename T, bool PAGES>
 int launch_fwd(NormRopeParams p, cudaStream_t stream) {
-  constexpr int rows = kSets * (32 / (D / 8));
-  p.units_per_token = (p.Hq + (PAGES ? 2 : 1) * p.Hkv + rows - 1) / rows;
-  const long long grid = (p.T * p.units_per_token + kWarps - 1) / kWarps;
-  norm_rope_kernel<D, T, PAGES><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+  const long long units = cut_units<D>(p, PAGES, kNormRopeWarps);
+  norm_rope_kernel<D, T, PAGES><<<(unsigned)((units + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
   return (int)cudaGetLastError();
 }
 
 template <int D, typename T>
 int launch_bwd(NormRopeParams p, cudaStream_t stream) {
-  constexpr int rows = kSets * (32 / (D / 8));
-  p.units_per_token = (p.Hq + p.Hkv + rows - 1) / rows;
-  const int grid = (int)std::min<long long>((p.T * p.units_per_token + kWarps - 1) / kWarps, kNormRopeBwdBlocks);
+  const long long units = cut_units<D>(p, false, kNormRopeWarps);
+  const int grid = (int)std::min<long long>((units + kWarps - 1) / kWarps, kNormRopeBwdBlocks);
   norm_rope_bwd_kernel<D, T><<<grid, kThreads, 0, stream>>>(p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
   if (!p.q_weight) return 0;

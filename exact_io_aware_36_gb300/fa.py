@@ -465,66 +465,73 @@ def attention_forward_fp8(q, k, v, signs, *, causal: bool, scale: Optional[float
 
 # ------------------------------------------- norm, rotation and a cache in pages
 
-def _checked(name, t, dtype, device, shape=None):
-    """`t` as a contiguous tensor of `dtype` on `device` (and of `shape`), else TypeError / ValueError."""
-    if t.dtype != dtype:
+# Single-token calls are as short as a few microseconds on the GPU, so what runs
+# before them here is kept lean: devices are compared by index, shapes as
+# tuples, and a message is made only for a call that is refused.
+
+def _refuse(name, t, dtype, index, shape, contiguous=True):
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
+    if contiguous:
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name}: [T, H, d] with the heads of a token contiguous expected")
+
+
+def _checked(name, t, dtype, index, shape=None):
+    """The pointer of a contiguous tensor of `dtype` on GPU `index` (and of `shape`), else TypeError / ValueError."""
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        _refuse(name, t, dtype, index, shape)
     return t.data_ptr()
 
 
-def _rows(name, t, dtype, device, shape=None):
+def _rows(name, t, dtype, index, shape=None):
     """(pointer, token stride) of a [T, H, d] tensor whose tokens may lie apart."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: shape {shape or '[T, H, d]'} expected, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 3 or (shape is not None and t.shape != shape):
+        _refuse(name, t, dtype, index, shape, False)
     T, H, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * d)
+    st, sh, sd = t.stride()
+    if (sd != 1 or (H > 1 and sh != d)) and t.numel():
+        _refuse(name, t, dtype, index, shape, False)
+    return t.data_ptr(), (st if T > 1 else H * d)
 
 
-def _cuda_device(t, stream):
-    if t.device.type != "cuda":
+def _gpu(t, stream):
+    """Index of the GPU that `t` is on; `stream` (if any) must be there too."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    return t.device
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    return index
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor that belongs to `stream` (None: the current one)."""
-    import torch
+def _empty(like, shape, stream, dtype=None):
+    """An uninitialised tensor on `like`'s GPU that belongs to `stream` (None: the current one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _run(what, fn, device, stream, check, *args):
-    """fn(*args, stream) with `device` current; raises on a status that is not FA_OK."""
+        return like.new_empty(shape, dtype=dtype or like.dtype)
     import torch
-    sp = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, sp)
-        dev = fa_check_device_error(sp) if check and st == 0 else 0
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, sp)
-            dev = fa_check_device_error(sp) if check and st == 0 else 0
-    _check(st, what)
-    _check(dev, what + " (device)")
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
-def _angles(q_weight, k_weight, cos, sin, d, device):
+def _run(what, index, stream, check, *args):
+    """The library's `what`(*args, stream) with GPU `index` current; raises on a status that is not FA_OK."""
+    import torch
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _run(what, index, stream, check, *args)
+    sp = torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
+    _check(getattr(load(), what)(*args, sp), what)
+    if check:
+        _check(fa_check_device_error(sp), what + " (device)")
+
+
+def _angles(q_weight, k_weight, cos, sin, d, index):
     """Pointers of the weights and of the angles, rot_dim and max_pos."""
     import torch
     f32 = torch.float32
@@ -532,13 +539,13 @@ def _angles(q_weight, k_weight, cos, sin, d, device):
         raise ValueError("q_weight and k_weight go together")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    w = (None, None) if q_weight is None else (_checked("q_weight", q_weight, f32, device, (d,)),
-                                               _checked("k_weight", k_weight, f32, device, (d,)))
+    w = (None, None) if q_weight is None else (_checked("q_weight", q_weight, f32, index, (d,)),
+                                               _checked("k_weight", k_weight, f32, index, (d,)))
     if cos is None:
         return (*w, None, None, 0, 0)
     if cos.dim() != 2:
         raise ValueError("cos: [max_pos, rot_dim / 2] expected")
-    return (*w, _checked("cos", cos, f32, device), _checked("sin", sin, f32, device, tuple(cos.shape)),
+    return (*w, _checked("cos", cos, f32, index), _checked("sin", sin, f32, index, cos.shape),
             2 * cos.shape[1], cos.shape[0])
 
 
@@ -557,26 +564,26 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos=N
     ``qk_norm_rope_backward``.
     """
     import torch
-    device = _cuda_device(q, stream)
-    qp, qs = _rows("q", q, q.dtype, device)
-    kp, ks = _rows("k", k, q.dtype, device)
+    index = _gpu(q, stream)
+    qp, qs = _rows("q", q, q.dtype, index)
+    kp, ks = _rows("k", k, q.dtype, index)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     if k.shape[0] != T or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dimension")
-    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    ang = _angles(q_weight, k_weight, cos, sin, d, index)
     pos = None
     if cos is not None:
         if positions is None:
             raise ValueError("positions are required with cos and sin")
-        pos = _checked("positions", positions, torch.int32, device, (T,))
+        pos = _checked("positions", positions, torch.int32, index, (T,))
     if q_out is None:
-        q_out = _empty((T, Hq, d), q.dtype, device, stream)
+        q_out = _empty(q, (T, Hq, d), stream)
     if k_out is None:
-        k_out = _empty((T, Hkv, d), q.dtype, device, stream)
-    _run("fa_qk_norm_rope", fa_qk_norm_rope, device, stream, check, qp, kp,
-         _checked("q_out", q_out, q.dtype, device, (T, Hq, d)),
-         _checked("k_out", k_out, q.dtype, device, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
+        k_out = _empty(q, (T, Hkv, d), stream)
+    _run("fa_qk_norm_rope", index, stream, check, qp, kp,
+         _checked("q_out", q_out, q.dtype, index, (T, Hq, d)),
+         _checked("k_out", k_out, q.dtype, index, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
          ang[2], ang[3], pos, T, Hq, Hkv, d, ang[4], ang[5], interleaved, _dtype_code(q.dtype))
     return q_out, k_out
 
@@ -593,63 +600,63 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     float32 [d], or None without norm.  Results do not vary from run to run.
     """
     import torch
-    device = _cuda_device(q, stream)
-    qp, qs = _rows("q", q, q.dtype, device)
-    kp, ks = _rows("k", k, q.dtype, device)
+    index = _gpu(q, stream)
+    qp, qs = _rows("q", q, q.dtype, index)
+    kp, ks = _rows("k", k, q.dtype, index)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     if k.shape[0] != T or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dimension")
-    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    ang = _angles(q_weight, k_weight, cos, sin, d, index)
     pos = None
     if cos is not None:
         if positions is None:
             raise ValueError("positions are required with cos and sin")
-        pos = _checked("positions", positions, torch.int32, device, (T,))
+        pos = _checked("positions", positions, torch.int32, index, (T,))
     if dq is None:
-        dq = _empty((T, Hq, d), q.dtype, device, stream)
+        dq = _empty(q, (T, Hq, d), stream)
     if dk is None:
-        dk = _empty((T, Hkv, d), q.dtype, device, stream)
-    dqp, dqs = _rows("dq", dq, q.dtype, device, (T, Hq, d))
-    dkp, dks = _rows("dk", dk, q.dtype, device, (T, Hkv, d))
+        dk = _empty(q, (T, Hkv, d), stream)
+    dqp, dqs = _rows("dq", dq, q.dtype, index, (T, Hq, d))
+    dkp, dks = _rows("dk", dk, q.dtype, index, (T, Hkv, d))
     dw = (None, None)
     if q_weight is not None:
-        both = _empty((2, d), torch.float32, device, stream)
+        both = _empty(q, (2, d), stream, torch.float32)
         dw = (both[0], both[1])
         if workspace is None:
-            workspace = _empty((fa_qk_norm_rope_bwd_workspace_size(d),), torch.uint8, device, stream)
-        _checked("workspace", workspace, torch.uint8, device)
-    _run("fa_qk_norm_rope_bwd", fa_qk_norm_rope_bwd, device, stream, check, qp, kp,
-         _checked("dq_out", dq_out, q.dtype, device, (T, Hq, d)),
-         _checked("dk_out", dk_out, q.dtype, device, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
+            workspace = _empty(q, (fa_qk_norm_rope_bwd_workspace_size(d),), stream, torch.uint8)
+        _checked("workspace", workspace, torch.uint8, index)
+    _run("fa_qk_norm_rope_bwd", index, stream, check, qp, kp,
+         _checked("dq_out", dq_out, q.dtype, index, (T, Hq, d)),
+         _checked("dk_out", dk_out, q.dtype, index, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
          ang[2], ang[3], pos, dqp, dkp, dqs, dks, _ptr(dw[0]), _ptr(dw[1]), T, Hq, Hkv, d, ang[4],
          ang[5], interleaved, _dtype_code(q.dtype), _ptr(workspace),
          workspace.numel() if workspace is not None else 0)
     return dq, dk, dw[0], dw[1]
 
 
-def _pages(k_pages, v_pages, device):
+def _pages(k_pages, v_pages, index):
     """(k pointer, v pointer, num_pages, page_size, Hkv, d) of the two pools."""
     import torch
     if k_pages.dim() != 4:
         raise ValueError("k_pages: [num_pages, page_size, Hkv, d] expected")
-    kp = _checked("k_pages", k_pages, torch.bfloat16, device)
-    vp = _checked("v_pages", v_pages, torch.bfloat16, device, tuple(k_pages.shape))
+    kp = _checked("k_pages", k_pages, torch.bfloat16, index)
+    vp = _checked("v_pages", v_pages, torch.bfloat16, index, k_pages.shape)
     return (kp, vp, *k_pages.shape)
 
 
-def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device):
+def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index):
     """(table, cache_seqlens, cu_seqlens pointers, B, N, max_pages)."""
     import torch
     if block_table.dim() != 2:
         raise ValueError("block_table: [B, max_pages] expected")
     B, max_pages = block_table.shape
-    tp = _checked("block_table", block_table, torch.int32, device)
-    cp = _checked("cache_seqlens", cache_seqlens, torch.int32, device, (B,))
+    tp = _checked("block_table", block_table, torch.int32, index)
+    cp = _checked("cache_seqlens", cache_seqlens, torch.int32, index, (B,))
     if cu_seqlens is not None:
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
-        return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, device, (B + 1,)), B, int(max_seqlen), max_pages
+        return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, index, (B + 1,)), B, int(max_seqlen), max_pages
     if B == 0 or T % B:
         raise ValueError("without cu_seqlens every sequence brings the same number of tokens")
     return tp, cp, None, B, T // B, max_pages
@@ -666,15 +673,15 @@ def cache_append(k, v, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqle
     ``max_seqlen`` their largest number), or T / B each without it.
     """
     import torch
-    device = _cuda_device(k, stream)
-    kp, ks = _rows("k", k, torch.bfloat16, device)
-    vp, vs = _rows("v", v, torch.bfloat16, device, tuple(k.shape))
+    index = _gpu(k, stream)
+    kp, ks = _rows("k", k, torch.bfloat16, index)
+    vp, vs = _rows("v", v, torch.bfloat16, index, k.shape)
     T, Hkv, d = k.shape
-    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, device)
+    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, index)
     if (Hp, dp) != (Hkv, d):
         raise ValueError("the pages have other heads than k")
-    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
-    _run("fa_cache_append", fa_cache_append, device, stream, check, kp, vp, kpool, vpool, ks, vs, tp,
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    _run("fa_cache_append", index, stream, check, kp, vp, kpool, vpool, ks, vs, tp,
          cp, cup, B, Hkv, N, d, T, page_size, num_pages, max_pages)
 
 
@@ -687,21 +694,21 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, cache_seqlens, *
     in its sequence's cache.  Returns q_out [T, Hq, d], ready for
     ``attention_forward_paged`` over the same pages."""
     import torch
-    device = _cuda_device(q, stream)
-    qp, qs = _rows("q", q, torch.bfloat16, device)
-    kp, ks = _rows("k", k, torch.bfloat16, device)
-    vp, vs = _rows("v", v, torch.bfloat16, device, tuple(k.shape))
+    index = _gpu(q, stream)
+    qp, qs = _rows("q", q, torch.bfloat16, index)
+    kp, ks = _rows("k", k, torch.bfloat16, index)
+    vp, vs = _rows("v", v, torch.bfloat16, index, k.shape)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, device)
+    kpool, vpool, num_pages, page_size, Hp, dp = _pages(k_pages, v_pages, index)
     if k.shape[0] != T or k.shape[2] != d or (Hp, dp) != (Hkv, d):
         raise ValueError("q, k and the pages must have the same tokens, key heads and head dimension")
-    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
-    ang = _angles(q_weight, k_weight, cos, sin, d, device)
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    ang = _angles(q_weight, k_weight, cos, sin, d, index)
     if q_out is None:
-        q_out = _empty((T, Hq, d), q.dtype, device, stream)
-    _run("fa_qk_norm_rope_append", fa_qk_norm_rope_append, device, stream, check, qp, kp, vp,
-         _checked("q_out", q_out, q.dtype, device, (T, Hq, d)), kpool, vpool, qs, ks, vs, ang[0],
+        q_out = _empty(q, (T, Hq, d), stream)
+    _run("fa_qk_norm_rope_append", index, stream, check, qp, kp, vp,
+         _checked("q_out", q_out, q.dtype, index, (T, Hq, d)), kpool, vpool, qs, ks, vs, ang[0],
          ang[1], float(eps), ang[2], ang[3], tp, cp, cup, B, Hq, Hkv, N, d, T, ang[4], ang[5],
          interleaved, page_size, num_pages, max_pages)
     return q_out
@@ -712,11 +719,11 @@ def cache_copy(k_pages, v_pages, src, dst, *, stream=None, check: bool = False):
     ``fa_cache_copy``: the fork of a sequence's last page, a compaction's moves.
     The copies run in no order; see include/fa.h on pairs that clash."""
     import torch
-    device = _cuda_device(k_pages, stream)
-    kpool, vpool, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages, device)
+    index = _gpu(k_pages, stream)
+    kpool, vpool, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages, index)
     n = src.numel()
-    _run("fa_cache_copy", fa_cache_copy, device, stream, check, kpool, vpool,
-         _checked("src", src, torch.int32, device, (n,)), _checked("dst", dst, torch.int32, device, (n,)),
+    _run("fa_cache_copy", index, stream, check, kpool, vpool,
+         _checked("src", src, torch.int32, index, (n,)), _checked("dst", dst, torch.int32, index, (n,)),
          n, num_pages, page_size, Hkv, d)
 
 
@@ -735,26 +742,26 @@ def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, 
     float32 [Hq, T]).
     """
     import torch
-    device = _cuda_device(q, stream)
+    index = _gpu(q, stream)
     if q.dim() != 3:
         raise ValueError("q: [T, Hq, d] expected")
     T, Hq, d = q.shape
-    qp = _checked("q", q, torch.bfloat16, device)
-    kpool, vpool, num_pages, page_size, Hkv, dp = _pages(k_pages, v_pages, device)
+    qp = _checked("q", q, torch.bfloat16, index)
+    kpool, vpool, num_pages, page_size, Hkv, dp = _pages(k_pages, v_pages, index)
     if dp != d:
         raise ValueError("q and the pages must have the same head dimension")
-    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, device)
-    slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, device, (Hq,))
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, index, (Hq,))
     if out is None:
-        out = _empty((T, Hq, d), out_dtype or q.dtype, device, stream)
+        out = _empty(q, (T, Hq, d), stream, out_dtype)
     if lse is None:
-        lse = _empty((Hq, T), torch.float32, device, stream)
+        lse = _empty(q, (Hq, T), stream, torch.float32)
     need = fa_fwd_paged_workspace_size(Hq, Hkv, N, d)
     if workspace is None:
-        workspace = _empty((max(need, 1),), torch.uint8, device, stream)
-    _run("fa_fwd_paged", fa_fwd_paged, device, stream, check, qp, kpool, vpool, tp, cp, cup,
-         _checked("out", out, out.dtype, device, (T, Hq, d)), _checked("lse", lse, torch.float32, device, (Hq, T)),
+        workspace = _empty(q, (max(need, 1),), stream, torch.uint8)
+    _run("fa_fwd_paged", index, stream, check, qp, kpool, vpool, tp, cp, cup,
+         _checked("out", out, out.dtype, index, (T, Hq, d)), _checked("lse", lse, torch.float32, index, (Hq, T)),
          B, Hq, Hkv, N, d, T, page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale),
          causal, -1 if window is None else window, slopes, _dtype_code(out.dtype),
-         _checked("workspace", workspace, torch.uint8, device), workspace.numel())
+         _checked("workspace", workspace, torch.uint8, index), workspace.numel())
     return out, lse
