@@ -68,7 +68,8 @@ constexpr int kThreads = 320;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
-constexpr float kSpecSum = 256.0f;     // 2^kTau
+constexpr float kRaiseSum = 256.0f;    // 2^kTau
+constexpr float kMaxSum = 1.0995116e12f;   // 2^40
 constexpr int kWeightTwo = 3, kWeightOne = 2;   // of one key tile of an item
 constexpr int kMinTiles = 2;                    // tiles a CTA takes at least: both streams busy
 
@@ -171,6 +172,8 @@ __device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWei
 struct Walk {
   long long w0, w1, base;      // base: place of item (b, g, qb) on the line
   int b, g, qb, c0, n, L;
+  // softmax warps: what the epilogue of the current item needs
+  int item_g, item_tok, item_part, item_streams;
 };
 
 static_assert(sizeof(Walk) <= 64, "walk");
@@ -199,7 +202,8 @@ __device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bar
 }
 
 // The next part of an item in the run; false at its end.
-__device__ __forceinline__ bool walk_next(const PagedParams& p, Walk* state, Seg& s) {
+// One copy of this code serves all roles (see the note on code size).
+static __device__ __noinline__ bool walk_next(const PagedParams& p, Walk* state, Seg& s) {
   Walk w = *state;
   __syncwarp();
   bool found = false;
@@ -382,10 +386,11 @@ __device__ __forceinline__ void store_row16(const float* v, bool f32, void* base
   }
 }
 
-template <int D, bool ALIBI>
+// ONE: no item has two tiles (the host knows from N).
+template <int D, bool ALIBI, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
 fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -425,6 +430,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
   const WaitCtx wc{&bars->abort_flag, p.status};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp(bar, parity, wc); };
@@ -561,14 +567,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       tc_fence_after();
       if (lane == 0) {
         const uint64_t vd = desc_add(vdesc0, sl * C::TILE_BYTES);
-        const uint32_t pcols = pv_dual ? 16 : 8;          // 16 keys of P: one part, or two
         const uint32_t colP = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
+        if (ONE || pv_dual) {                             // 16 keys of P: high part, low part
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(colO, colP + kk * pcols, desc_add(vd, kk * 2048), IDESC_O, (!first || kk > 0) ? 1u : 0u);
-        if (pv_dual) {
+          for (int kk = 0; kk < 8; ++kk) {
+            mma_ts(colO, colP + kk * 16, desc_add(vd, kk * 2048), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+            mma_ts(colO, colP + kk * 16 + 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
+          }
+        } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colP + 8 + kk * 16, desc_add(vd, kk * 2048), IDESC_O, 1u);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(colO, colP + kk * 8, desc_add(vd, kk * 2048), IDESC_O, (!first || kk > 0) ? 1u : 0u);
         }
       }
       __syncwarp();
@@ -603,11 +612,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (!ok) break;
         }
         // S of a stream whose P is not waited for comes first
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t)
           if ((cur & ~pv) >> t & 1) issue_s(t, s.k.two ? t : qsel, sl);
         clean_v(sl);
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (pv >> t & 1)
             if (!(ok = issue_pv(t, sl))) break;
@@ -649,7 +658,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int sl = gs % C::NS;
       if ((ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) {
         clean_v(sl);
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t)
           if (ok && (pv >> t & 1)) ok = issue_pv(t, sl);
         if (ok && lane == 0) mma_commit(&bars->o_done);
@@ -664,25 +673,25 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
     const int q4 = warp & 3;
-    const int r = 32 * q4 + lane;                       // row of the tile
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t tS = lane_base + (t ? C::S_COL1 : C::S_COL0);
     const uint32_t tO = lane_base + (t ? C::O_COL1 : C::O_COL0);
     const float c2 = p.scale_log2;
     float* mls = reinterpret_cast<float*>(smem + C::ML_OFF);
-    const int rq = r / p.group, rh = r % p.group;       // token and head of this row
     bool ok = true;
     int cs = 0;                  // S products consumed (s_full phases)
     int nseg = 0, flip = 0;
     // A warp that gives up (a wait ran out) still walks the items: it meets
     // the others at the barrier of every one-tile item, and they give up too.
     while (true) {
-      int n0, steps, diag, low, kend, tl, part, head, tok;
-      bool valid, dual, both;
+      int n0, steps, diag, low, kend;
+      bool valid, dual;
+      float slope2 = 0.f;
       {
         Seg s;
         if (!walk_next(p, walk, s)) break;
-        dual = !s.k.two;
+        const int r = 32 * q4 + lane, rq = r / p.group;  // row of the tile, its token
+        dual = ONE || !s.k.two;
         const bool second = !dual && t;                 // holds the second tile's rows
         const int f = second ? s.k.f[1] : s.k.f[0], nt = second ? s.k.nt[1] : s.k.nt[0];
         int kt0;
@@ -690,191 +699,208 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const int first = (t - flip) & 1;             // this stream's first step
           kt0 = s.k.hi_all - s.ib - first;
           steps = (s.ie - s.ib - first + 1) >> 1;
-          both = s.ie - s.ib > 1;
           flip = (flip + s.ie - s.ib) & 1;
         } else {
           kt0 = min(s.k.hi_all - s.ib, second ? s.k.hi[1] : s.k.hi[0]);
           steps = max(0, kt0 - max(s.k.hi_all - s.ie + 1, second ? s.k.lo[1] : s.k.lo[0]) + 1);
-          both = false;
         }
         n0 = 128 * kt0;                                 // first key of the tile
         valid = rq < nt;
-        tl = (dual ? 0 : t * p.tpt) + rq;               // token within the item
-        kend = p.causal ? f + rq : s.L - 1;      // last key this row sees
+        kend = p.causal ? f + rq : s.L - 1;             // last key this row sees
         // tiles that reach past `diag` or begin before `low` hold keys that
         // some row does not see
         diag = p.causal ? f : s.L - 1;
         low = f + nt - 1 - p.window;
-        head = s.g * p.group + rh;
-        tok = s.tok + tl;
-        // 0: the whole item; else the slot of the part: 1 its continuation
-        // from the CTA before, 2 its beginning
-        part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
+        if (ALIBI) slope2 = valid ? __ldg(p.alibi + s.g * p.group + r % p.group) * kLog2e : 0.f;
+        if (lane == 0) {
+          walk->item_g = s.g;
+          walk->item_tok = s.tok;
+          // 0: the whole item; else the slot of the part: 1 its continuation
+          // from the CTA before, 2 its beginning
+          walk->item_part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
+          // streams with a step (one-tile items: of both)
+          walk->item_streams = dual ? (s.ie - s.ib > 1 ? 3 : steps > 0 ? 1 << t : 2 >> t) : steps > 0 ? 1 << t : 0;
+        }
+        __syncwarp();
       }
       const bool warp_rows = __any_sync(0xffffffffu, valid);
-      float slope2 = 0.f;
-      if (ALIBI) slope2 = valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
       float m_ref = -INFINITY;
       float l = 0.f;     // sum of p in fp32: gives the LSE
       float lr = 0.f;    // sum of the p that the PV products see: normalises O
-      // The steps of this stream; one copy of the loop for each kind of item.
-      auto run_steps = [&](auto kind) {
-        constexpr bool DUAL = decltype(kind)::value;
-        for (int j = 0; j < steps; ++j, ++cs, n0 -= DUAL ? 256 : 128) {
-          if (!(ok = wait(&bars->s_full[t], cs & 1))) break;
-          if (!warp_rows) {                             // no row of this warp holds a token
-            if (lane == 0) mbar_arrive(&bars->p_full[t]);
-            continue;
-          }
-          tc_fence_after();
-          // Tiles on the diagonal, at the end or at the band's lower edge:
-          // scores of keys that the row does not see become -inf, whatever
-          // the slots hold.
-          const bool need_mask = n0 + 127 > diag || n0 < low;
+      float grow = 0.f;  // log2 by which the reference is to rise before the next tile
+      for (int j = 0; ok && j < steps; ++j, ++cs, n0 -= dual ? 256 : 128) {
+        if (!(ok = wait(&bars->s_full[t], cs & 1))) break;
+        if (!warp_rows) {                               // no row of this warp holds a token
+          if (lane == 0) mbar_arrive(&bars->p_full[t]);
+          continue;
+        }
+        tc_fence_after();
+        // Tiles on the diagonal, at the end or at the band's lower edge: in
+        // TMEM, scores of keys that the row does not see become -inf,
+        // whatever the slots hold.
+        if (n0 + 127 > diag || n0 < low) {
           const int ub = kend - n0, lb = p.causal ? ub - p.window : 0;
-          // ALiBi bias of column c in log2 units: slope2 * (n0 + c -
-          // position); causal, so the row's position is its last key.
-          const float base = ALIBI ? slope2 * (float)(n0 - kend) : 0.f;
-          const uint64_t c2p = f2(c2, c2);
-          // use(c, scores 16 c .. 16 c + 15) for c = 0 .. 7, the next 16 in
-          // flight meanwhile
-          auto each16 = [&](auto use) {
-            uint32_t s[2][16];
-            tmem_ld16(tS, s[0]);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(tS + c, x);
+            tmem_wait_ld();
+            reg_fence16(x);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              tmem_wait_ld();
-              reg_fence16(s[c & 1]);
-              if (c < 7) tmem_ld16(tS + 16 * (c + 1), s[(c + 1) & 1]);
-              if (need_mask) {
+            for (int i = 0; i < 16; ++i)
+              if (c + i > ub || c + i < lb) x[i] = __float_as_uint(-INFINITY);
+            tmem_st16(tS + c, x);
+          }
+          tmem_wait_st();
+        }
+        // The commit that published S_t also covers this stream's last PV, so
+        // O may be rescaled now.
+        if (!ONE && __any_sync(0xffffffffu, grow > 0.f)) {
+          const float alpha = ex2_approx(-grow);
+          l *= alpha;
+          lr *= alpha;
+          m_ref += grow;
+          grow = 0.f;
+          rescale_row<D>(tO, alpha);
+        }
+        // ALiBi bias of column c in log2 units: slope2 * (n0 + c - position);
+        // causal, so the row's position is its last key.
+        const float base = ALIBI ? slope2 * (float)(n0 - kend) : 0.f;
+        // p = 2^(x - mb) of 16 scores from column c on: 8 packed pairs, and
+        // with LOW what the rounding left of them; sums of p, of the rounded p
+        uint64_t acc[2], accr[2];
+        auto exp16 = [&](auto low_part, int c, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
+          constexpr bool LOW = decltype(low_part)::value;
+          uint64_t bm = f2(-mb, -mb);
+          if (ALIBI) {
+            const float b0 = fmaf(slope2, (float)c, base - mb);
+            bm = f2(b0, b0 + slope2);
+          }
+          const uint64_t step = f2(2.f * slope2, 2.f * slope2), c2p = f2(c2, c2);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (16 * c + i > ub || 16 * c + i < lb) s[c & 1][i] = __float_as_uint(-INFINITY);
-              }
-              use(c, s[c & 1]);
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t ex = ffma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2p, bm);
+            if (ALIBI) bm = fadd2(bm, step);
+            float e0, e1;
+            f2split(ex, e0, e1);
+            const float p0 = ex2_approx(e0);
+            const float p1 = ex2_approx(e1);
+            const uint64_t pp = f2(p0, p1);
+            acc[i & 1] = fadd2(acc[i & 1], pp);
+            hi[i] = pack_bf16x2(p0, p1);
+            const uint64_t ph = f2(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xFFFF0000u));
+            if (LOW) {
+              float r0, r1;
+              f2split(fsub2(pp, ph), r0, r1);
+              lo[i] = pack_bf16x2(r0, r1);
+            } else {
+              accr[i & 1] = fadd2(accr[i & 1], ph);
             }
-          };
-          // p = 2^(x - mb) of 16 scores: 8 packed pairs (and, DUAL, what the
-          // rounding left of them); sums of p and of the rounded p
-          uint64_t acc[2], accr[2];
-          auto exp16 = [&](int c, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
-            uint64_t bm = ALIBI ? f2(fmaf(slope2, (float)(16 * c), base - mb), fmaf(slope2, (float)(16 * c + 1), base - mb))
-                                : f2(-mb, -mb);
-            const uint64_t step = f2(2.f * slope2, 2.f * slope2);
+          }
+        };
+        auto pair_sum = [](const uint64_t* a) {
+          float x, y;
+          f2split(fadd2(a[0], a[1]), x, y);
+          return x + y;
+        };
+        bool settled = false;
+        if (!ONE && !dual && !__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
+          // P with the reference as it is; kept in registers until its sum
+          // shows that it may stand.  P and O are floats, so a reference that
+          // is too low costs no precision: a sum up to 2^40 stands, and one
+          // above 2^8 raises the reference for the next tile.
+          uint32_t pk[64], x[2][16];
+          acc[0] = acc[1] = accr[0] = accr[1] = 0;
+          tmem_ld16(tS, x[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t ex = ffma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2p, bm);
-              if (ALIBI) bm = fadd2(bm, step);
-              float e0, e1;
-              f2split(ex, e0, e1);
-              const float p0 = ex2_approx(e0);
-              const float p1 = ex2_approx(e1);
-              const uint64_t pp = f2(p0, p1);
-              acc[i & 1] = fadd2(acc[i & 1], pp);
-              hi[i] = pack_bf16x2(p0, p1);
-              const uint64_t ph = f2(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xFFFF0000u));
-              if (DUAL) {
-                float r0, r1;
-                f2split(fsub2(pp, ph), r0, r1);
-                lo[i] = pack_bf16x2(r0, r1);
-              } else {
-                accr[i & 1] = fadd2(accr[i & 1], ph);
+          for (int c = 0; c < 8; ++c) {
+            tmem_wait_ld();
+            reg_fence16(x[c & 1]);
+            if (c < 7) tmem_ld16(tS + 16 * (c + 1), x[(c + 1) & 1]);
+            exp16(std::false_type{}, 16 * c, x[c & 1], m_ref, pk + 8 * c, nullptr);
+          }
+          const float ts = pair_sum(acc);
+          settled = !__any_sync(0xffffffffu, valid && !(ts <= kMaxSum));   // also inf / nan
+          if (settled) {
+            tmem_st32(tS, pk);
+            tmem_st32(tS + 32, pk + 32);
+            l += ts;
+            lr += pair_sum(accr);
+            if (valid && ts > kRaiseSum) grow = ceilf(lg2_approx(ts));
+          }
+        }
+        if (!settled) {
+          // The tile's max first: a row's first tile, a sum past 2^40, and
+          // every tile of a one-tile item (HBM sets its pace).
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(tS + c, x);
+            tmem_wait_ld();
+            reg_fence32(x);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+              if (ALIBI) {
+                x0 = fmaf(x0, c2, fmaf(slope2, (float)(c + i), base));
+                x1 = fmaf(x1, c2, fmaf(slope2, (float)(c + i + 1), base));
               }
+              mx = fmax3(mx, x0, x1);
             }
-          };
-          auto pair_sum = [](const uint64_t* a) {
-            float x, y;
-            f2split(fadd2(a[0], a[1]), x, y);
-            return x + y;
-          };
-          // The tile's max, and with it the reference.  Any reference gives
-          // the same result: it is raised where the max grew past tau, and
-          // where this row's own sum overflowed (`over`).
-          auto raise_ref = [&](bool over) {
-            float mx[2] = {-INFINITY, -INFINITY};
-            each16([&](int c, const uint32_t* x) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                if (ALIBI) {
-#pragma unroll
-                  for (int u = 0; u < 2; ++u)
-                    mx[u] = fmax3(mx[u], fmaf(__uint_as_float(x[i + 2 * u]), c2, fmaf(slope2, (float)(16 * c + i + 2 * u), base)),
-                                  fmaf(__uint_as_float(x[i + 2 * u + 1]), c2, fmaf(slope2, (float)(16 * c + i + 2 * u + 1), base)));
-                } else {
-#pragma unroll
-                  for (int u = 0; u < 2; ++u)
-                    mx[u] = fmax3(mx[u], __uint_as_float(x[i + 2 * u]), __uint_as_float(x[i + 2 * u + 1]));
-                }
-              }
-            });
-            float xmax = fmaxf(mx[0], mx[1]);
-            if (!ALIBI) xmax *= c2;
-            const bool raise = xmax > m_ref + kTau || over;
-            const float m_new = raise ? xmax : m_ref;
+          }
+          if (!ALIBI) mx *= c2;
+          // Any reference gives the same result: it stays until the max has
+          // grown by more than tau.
+          const bool raise = mx > m_ref + kTau;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float m_new = raise ? mx : m_ref;
             const float alpha = raise ? ex2_approx(m_ref - m_new) : 1.f;
             l *= alpha;
             lr *= alpha;
-            // The commit that published S_t also covers this stream's last PV.
-            if (j > 0 && __any_sync(0xffffffffu, raise)) rescale_row<D>(tO, alpha);
             m_ref = m_new;
-          };
-          if constexpr (DUAL) {
-            // HBM sets the pace here: always the max first, then P, whose two
-            // parts take the 16 columns of their scores.
-            raise_ref(false);
-            const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-            acc[0] = acc[1] = 0;
-            each16([&](int c, const uint32_t* x) {
-              uint32_t pl[16];
-              exp16(c, x, mb, pl, pl + 8);
-              tmem_st16(tS + 16 * c, pl);
-            });
-            const float ts = pair_sum(acc);
-            l += ts;
-            lr += ts;
-          } else {
-            // Once a row has a reference, P is computed with it at once.  A
-            // sum of at most 2^tau shows that no score passed the reference
-            // by more than tau, so no raise is due.
-            uint32_t pk[64];
-            auto exp_pass = [&](float mb) {
-              acc[0] = acc[1] = accr[0] = accr[1] = 0;
-              each16([&](int c, const uint32_t* x) { exp16(c, x, mb, pk + 8 * c, nullptr); });
-            };
-            bool full = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
-            bool over = false;
-            if (!full) {
-              exp_pass(m_ref);
-              over = valid && !(pair_sum(acc) <= kSpecSum);   // also catches inf / nan
-              full = __any_sync(0xffffffffu, over);
-            }
-            if (full) {
-              raise_ref(over);
-              exp_pass(m_ref == -INFINITY ? 0.f : m_ref);
-            }
-            tmem_st32(tS, pk);
-            tmem_st32(tS + 32, pk + 32);
-            l += pair_sum(acc);
-            lr += pair_sum(accr);
+            if (j > 0) rescale_row<D>(tO, alpha);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p_full[t]);
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          acc[0] = acc[1] = accr[0] = accr[1] = 0;
+          // P over the scores just read: with two parts each 16 keys' high and
+          // low part take the 16 columns of their scores, else 16 keys take 8
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(tS + c, x);
+            tmem_wait_ld();
+            reg_fence32(x);
+            uint32_t y[32];
+            if (ONE || dual) {
+              exp16(std::true_type{}, c, x, mb, y, y + 8);
+              exp16(std::true_type{}, c + 16, x + 16, mb, y + 16, y + 24);
+              tmem_st32(tS + c, y);
+            } else {
+              exp16(std::false_type{}, c, x, mb, y, nullptr);
+              exp16(std::false_type{}, c + 16, x + 16, mb, y + 8, nullptr);
+              tmem_st16(tS + c / 2, y);
+            }
+          }
+          const float ts = pair_sum(acc);
+          l += ts;
+          lr += ONE || dual ? ts : pair_sum(accr);
         }
-      };
-      if (ok) {
-        if (dual) run_steps(std::true_type{});
-        else run_steps(std::false_type{});
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       // ---------------------------------------------------------- epilogue
       if (ok) ok = wait(&bars->o_done, nseg & 1);
       tc_fence_after();
-      // A stream without a step in this part has no O: weight 0 and its
-      // columns are not used.
-      float w0 = steps > 0 ? 1.f : 0.f, w1 = 0.f;       // of the own columns, of the other stream's
+      // A stream without a step in this part has no O: its columns are not
+      // used.
+      const int r = 32 * q4 + lane;
+      const int streams = walk->item_streams, part = walk->item_part;
+      const bool use0 = streams >> t & 1, use1 = dual && (streams >> (t ^ 1) & 1);
+      float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
-      bool use0 = steps > 0, use1 = false;
       if (dual) {
         // join the two streams: each warp takes half of the columns
         float* own = mls + (t * 128 + r) * 3;
@@ -890,17 +916,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         l = fmaf(w0, l, w1 * oth[1]);
         lr = fmaf(w0, lr, w1 * oth[2]);
         m_ref = M;
-        use0 = steps > 0;
-        use1 = both || steps == 0;
         c_from = t * (D / 2);
         c_to = c_from + D / 2;
       }
       if (!ok) continue;
       const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
-      const int row = tl * p.group + rh;                 // row of the item
-      const long long orow = (long long)tok * p.Hq + head;
+      const int tl = (dual ? 0 : t * p.tpt) + r / p.group;            // token of the item
+      const int rh = r % p.group, head = walk->item_g * p.group + rh;
+      const long long tok = walk->item_tok + tl;
+      const long long orow = tok * p.Hq + head;
       const int slot = 2 * (int)blockIdx.x + part - 1;
-      const long long prow = (long long)slot * p.part_rows + row;
+      const long long prow = (long long)slot * p.part_rows + tl * p.group + rh;
       float sc = 1.f;
       if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
       if (warp_rows) {
@@ -945,7 +971,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  grid_launch_dependents();
+
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
@@ -1003,10 +1029,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
   if (lane == 0) p.lse[(long long)h * p.T + tok] = l > 0.f ? (M + lg2_approx(l)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool ALIBI>
+template <int D, bool ALIBI, bool ONE>
 int launch_impl(const PagedParams& p, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = fwd_paged_kernel<D, ALIBI>;
+  auto kern = fwd_paged_kernel<D, ALIBI, ONE>;
   if (const int ea = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ea;
   CUtensorMap tq, tk, tv;
   const long long slots = (long long)p.num_pages * p.page_size;
@@ -1023,12 +1049,19 @@ int launch_impl(const PagedParams& p, cudaStream_t stream) {
   return launch_dependent(paged_merge_kernel<D>, dim3(grid, (p.part_rows + 7) / 8), dim3(256), 0, stream, p, grid);
 }
 
+template <int D>
+int launch_d(const PagedParams& p, cudaStream_t stream) {
+  // no sequence brings more tokens than one tile holds
+  const bool one = p.N <= p.tpt;
+  if (p.alibi) return one ? launch_impl<D, true, true>(p, stream) : launch_impl<D, true, false>(p, stream);
+  return one ? launch_impl<D, false, true>(p, stream) : launch_impl<D, false, false>(p, stream);
+}
+
 }  // namespace
 
 int launch_fwd_paged(const PagedParams& p, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (p.alibi) return p.d == 128 ? launch_impl<128, true>(p, stream) : launch_impl<64, true>(p, stream);
-  return p.d == 128 ? launch_impl<128, false>(p, stream) : launch_impl<64, false>(p, stream);
+  return p.d == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
 }
 
 }  // namespace fa
