@@ -84,7 +84,8 @@ struct Cfg {
   static constexpr int V_OFF = K_OFF + NS * TILE_BYTES;
   static constexpr int ML_OFF = V_OFF + NS * TILE_BYTES;   // (m, l, l~) of both streams' rows
   static constexpr int WALK_OFF = ML_OFF + 2 * 128 * 3 * 4;
-  static constexpr int BAR_OFF = WALK_OFF + (kThreads / 32) * 64;
+  static constexpr int PAR_OFF = WALK_OFF + (kThreads / 32) * 64;   // a copy of the parameters
+  static constexpr int BAR_OFF = PAR_OFF + 256;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   // the work plan's prefix sums borrow the K/V slots before the first load
@@ -166,6 +167,16 @@ __device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int 
 
 __device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
 
+// Weight of the block of query tokens from tok0 on (0 behind the last).  Not
+// inlined: a short call runs through code that no SM has cached yet, so each
+// copy of this would cost more than the calls.
+static __device__ __noinline__ int block_weight(const PagedParams& p, int n, int L, int tok0) {
+  if (tok0 >= n) return 0;
+  Block k;
+  block_geometry(p, n, L, tok0, k);
+  return k.kt * tile_weight(k);
+}
+
 // A CTA's walk over its run [w0, w1) of the line of tiles.  Every role walks
 // the same items by itself; each warp keeps its state in shared memory, as it
 // is needed at the items' ends only.
@@ -238,18 +249,6 @@ static __device__ __noinline__ bool walk_next(const PagedParams& p, Walk* state,
   return found;
 }
 
-// Weight of all q blocks of one kv head of sequence (n, L), lane of nl lanes
-// taking every nl-th block.
-__device__ __forceinline__ long long seq_weight(const PagedParams& p, int n, int L, int lane, int nl) {
-  long long sum = 0;
-  for (int tok0 = lane * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) {
-    Block k;
-    block_geometry(p, n, L, tok0, k);
-    sum += (long long)k.kt * tile_weight(k);
-  }
-  return sum;
-}
-
 // Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
 // threads; `pre` holds B 64-bit words of shared memory.
 __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre) {
@@ -263,17 +262,17 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     if (b < p.B) {
       int c0, n, L;
       if (!load_seq(p, b, &c0, &n, &L) && blockIdx.x == 0 && sub == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
-      wsum = seq_weight(p, n, L, sub, nl);
+      for (int tok0 = sub * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) wsum += block_weight(p, n, L, tok0);
     }
     for (int o = nl / 2; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-    if (b < p.B && sub == 0) pre[b] = (unsigned long long)wsum * p.Hkv;
+    if (b < p.B && sub == 0) pre[b] = (unsigned long long)wsum;      // of one kv head
   }
   __syncthreads();
   // 2. exclusive prefix sums: each thread a run of sequences
   const int per = (p.B + kThreads - 1) / kThreads;
   const int f = min(tid * per, p.B), e = min(f + per, p.B);
   unsigned long long own = 0;
-  for (int b = f; b < e; ++b) own += pre[b];
+  for (int b = f; b < e; ++b) own += pre[b] * p.Hkv;
   unsigned long long inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -288,12 +287,16 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     total += bars->warp_sum[w];
   }
   before += inc - own;
-  // 3. this CTA's run, and the sequence it begins in
-  const long long G = gridDim.x;
-  const long long active = min(G, max(1ll, (long long)total / (kMinTiles * kWeightOne)));
-  const long long c = blockIdx.x;
-  const long long w0 = c < active ? (long long)total * c / active : (long long)total;
-  const long long w1 = c < active ? (long long)total * (c + 1) / active : (long long)total;
+  // 3. this CTA's run, and the sequence it begins in.  Cut in float: the
+  // same for a CTA's end and its neighbour's beginning, and never falling,
+  // which is all that is needed.
+  const int active = (int)min((unsigned long long)gridDim.x, max(1ull, total / (kMinTiles * kWeightOne)));
+  const int c = min((int)blockIdx.x, active);
+  auto cut = [&](int i) {
+    if (i >= active) return (long long)total;
+    return min((long long)(__ull2float_rz(total) * ((float)i / (float)active)), (long long)total);
+  };
+  const long long w0 = cut(c), w1 = cut(c + 1);
   if (tid == 0) {
     bars->w0 = w0;
     bars->w1 = w1;
@@ -304,7 +307,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
   if (w0 < w1) {
     unsigned long long at = before;
     for (int b = f; b < e; ++b) {
-      const unsigned long long x = pre[b];
+      const unsigned long long x = pre[b] * p.Hkv;
       if (at <= (unsigned long long)w0 && (unsigned long long)w0 < at + x) {
         bars->b = b;
         bars->base = (long long)at;
@@ -316,20 +319,17 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
   // 4. the kv head and the q block
   if (warp == 0 && w0 < w1) {
     const int b = bars->b;
-    const long long sw = (long long)(pre[b] / (unsigned)p.Hkv);
+    const long long sw = (long long)pre[b];
     int c0, n, L;
     load_seq(p, b, &c0, &n, &L);
-    const int g = (int)((w0 - bars->base) / sw);
+    // the head: a float quotient, put right by at most a step
+    int g = min((int)((float)(w0 - bars->base) / (float)sw), p.Hkv - 1);
+    while (g > 0 && bars->base + g * sw > w0) --g;
+    while (bars->base + (g + 1) * sw <= w0) ++g;
     long long base = bars->base + g * sw;
     int qb = 0;
     for (int q0 = 0;; q0 += 32) {
-      const int tok0 = (q0 + lane) * 2 * p.tpt;
-      long long x = 0;
-      if (tok0 < n) {
-        Block k;
-        block_geometry(p, n, L, tok0, k);
-        x = (long long)k.kt * tile_weight(k);
-      }
+      const int x = block_weight(p, n, L, (q0 + lane) * 2 * p.tpt);
       long long run = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -397,6 +397,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   Bars* bars = reinterpret_cast<Bars*>(smem + C::BAR_OFF);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // The functions that are not inlined read the parameters here: through a
+  // pointer to the kernel's own they would come from memory.
+  static_assert(sizeof(PagedParams) <= 256 && sizeof(PagedParams) % 4 == 0, "parameters");
+  const PagedParams& ps = *reinterpret_cast<const PagedParams*>(smem + C::PAR_OFF);
+  if (threadIdx.x < sizeof(PagedParams) / 4)
+    reinterpret_cast<uint32_t*>(smem + C::PAR_OFF)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&p)[threadIdx.x];
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -425,7 +431,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int box = i / ((128 - rows_box) * 8), j = i % ((128 - rows_box) * 8);
     reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
   }
-  make_plan(p, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF));
+  __syncthreads();
+  make_plan(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF));
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -435,7 +442,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const WaitCtx wc{&bars->abort_flag, p.status};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp(bar, parity, wc); };
   Walk* walk = reinterpret_cast<Walk*>(smem + C::WALK_OFF + warp * 64);
-  walk_begin(p, bars, walk);
+  walk_begin(ps, bars, walk);
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ producer
@@ -457,17 +464,19 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int cont = 0;
     int4 begun = make_int4(0, 0, 0, 0);
     int vrow = -1, vg = 0;     // the step before: this lane's page row (-1: no box), kv head
-    while (ok && walk_next(p, walk, s)) {
-      if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
-      else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
-      for (int t = 0; t < (s.k.two ? 2 : 1); ++t) {
-        const int x = s.k.two ? t : qsel;
+    while (ok && walk_next(ps, walk, s)) {
+      const bool two = !ONE && s.k.two;
+      const int g = s.g, ib = s.ib, ie = s.ie, vlo = s.k.vlo, vhi = s.k.vhi, hi_all = s.k.hi_all;
+      if (ib > 0) cont = ie == s.k.kt ? 2 : 1;
+      else if (ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, g);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        const int x = two ? t : qsel;
         if ((q_any >> x & 1) && !(ok = wait(&bars->q_empty[x], q_par >> x & 1))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->q_full[x], C::NB * rows_box * 128);
 #pragma unroll
           for (int bx = 0; bx < C::NB; ++bx)
-            tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bx * 64, s.g * p.group,
+            tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bx * 64, g * p.group,
                         s.tok + t * p.tpt, &bars->q_full[x]);
         }
         __syncwarp();
@@ -475,12 +484,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         q_any |= 1u << x;
       }
       if (!ok) break;
-      if (!s.k.two) qsel ^= 1;
+      if (!two) qsel ^= 1;
       const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
-      for (int i = s.ib; i < s.ie; ++i, ++gs) {
-        const int key0 = (s.k.hi_all - i) * 128 + lane * box_rows;
+      for (int i = ib; i < ie; ++i, ++gs) {
+        const int key0 = (hi_all - i) * 128 + lane * box_rows;
         int krow = -1;
-        if (lane < nbox && key0 < s.k.vhi && key0 + box_rows > s.k.vlo) {
+        if (lane < nbox && key0 < vhi && key0 + box_rows > vlo) {
           int page = __ldg(table + (key0 >> p.page_shift));
           if (page < 0 || page >= p.num_pages) {
             record_status(p.status, FA_ERR_PAGE);
@@ -496,12 +505,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
         for (int bx = 0; bx < C::NB; ++bx) {
           const int off = sl * C::TILE_BYTES + bx * C::BOX_BYTES + lane * box_bytes;
-          if (krow >= 0) tma_load_3d(smem + C::K_OFF + off, &tmK, bx * 64, s.g, krow, &bars->kv_full[sl]);
+          if (krow >= 0) tma_load_3d(smem + C::K_OFF + off, &tmK, bx * 64, g, krow, &bars->kv_full[sl]);
           if (vrow >= 0) tma_load_3d(smem + C::V_OFF + off, &tmV, bx * 64, vg, vrow, &bars->kv_full[sl]);
         }
         __syncwarp();
         vrow = krow;
-        vg = s.g;
+        vg = g;
       }
     }
     if (ok && gs > 0) {                           // the last step's V
@@ -596,43 +605,73 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       fence_proxy_async_smem();
       __syncwarp();
     };
-    while (ok && walk_next(p, walk, s)) {
+    while (ok && walk_next(ps, walk, s)) {
+      const bool two = !ONE && s.k.two;
+      const int ib = s.ib, ie = s.ie, hi_all = s.k.hi_all, vlo = s.k.vlo, vhi = s.k.vhi;
+      const int lo0 = s.k.lo[0], hi0 = s.k.hi[0], lo1 = s.k.lo[1], hi1 = s.k.hi[1];
       int started = 0;                                  // streams that have begun this item
-      for (int i = s.ib; i < s.ie; ++i, ++gs) {
+      for (int i = ib; ok && i < ie; ++i, ++gs) {
         const int sl = gs % C::NS;
-        const int kt = s.k.hi_all - i;
-        const int cur = s.k.two ? ((kt >= s.k.lo[0] && kt <= s.k.hi[0]) | ((kt >= s.k.lo[1] && kt <= s.k.hi[1]) << 1))
-                                : 1 << ((flip + i - s.ib) & 1);
+        const int kt = hi_all - i;
+        const int cur = two ? ((kt >= lo0 && kt <= hi0) | ((kt >= lo1 && kt <= hi1) << 1)) : 1 << ((flip + i - ib) & 1);
         if (!(ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) break;
-        if (i == s.ib) {
-          for (int t = 0; ok && t < (s.k.two ? 2 : 1); ++t) {
-            const int x = s.k.two ? t : qsel;
-            ok = wait(&bars->q_full[x], q_par >> x & 1);
+        if (!ONE && cur == 3 && pv == 3 && !pv_dual && !pv_first && !pv_last && i < ie - 1 && v_lo <= 0 && v_hi >= 128) {
+          // Inside an item of two tiles: PV0, S0, PV1, S1 and nothing else.
+          // The tensor pipe takes only a couple of products ahead, so what
+          // this warp does between two batches is time the pipe idles.
+          const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!(ok = wait(&bars->p_full[t], p_par >> t & 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colS + kk * 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
+                mma_ss(colS, desc_add(qdesc0, t * C::TILE_BYTES + off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars->s_full[t]);
+              if (t) mma_commit(&bars->kv_empty[sl]);
+            }
+            __syncwarp();
           }
           if (!ok) break;
+          p_par ^= 3u;
+          v_lo = vlo - kt * 128;
+          v_hi = vhi - kt * 128;
+          continue;
         }
-        // S of a stream whose P is not waited for comes first
+        // S of a stream whose P is not waited for comes first; but at an
+        // item's head, whose Q may be on its way, PV of the item before.
+        const int s_first = i == ib && two ? 0 : cur & ~pv, s_last = i == ib && two ? cur : 0;
+        if (i == ib && !two && !(ok = wait(&bars->q_full[qsel], q_par >> qsel & 1))) break;
 #pragma unroll 1
         for (int t = 0; t < 2; ++t)
-          if ((cur & ~pv) >> t & 1) issue_s(t, s.k.two ? t : qsel, sl);
+          if (s_first >> t & 1) issue_s(t, two ? t : qsel, sl);
         clean_v(sl);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (pv >> t & 1)
             if (!(ok = issue_pv(t, sl))) break;
-          if ((cur & pv) >> t & 1) issue_s(t, s.k.two ? t : qsel, sl);
+          if ((cur & ~s_first & ~s_last) >> t & 1) issue_s(t, two ? t : qsel, sl);
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int t = 0; s_last && t < 2; ++t) {
+          const int x = two ? t : qsel;
+          if ((two || t == 0) && !(ok = wait(&bars->q_full[x], q_par >> x & 1))) break;
+          if (s_last >> t & 1) issue_s(t, x, sl);
         }
         if (!ok) break;
         if (lane == 0) {
           if (pv_last) mma_commit(&bars->o_done);
           mma_commit(&bars->kv_empty[sl]);
-          if (i == s.ie - 1) {
-            if (s.k.two) {
-              mma_commit(&bars->q_empty[0]);
-              mma_commit(&bars->q_empty[1]);
-            } else {
-              mma_commit(&bars->q_empty[qsel]);
-            }
+          if (i == ie - 1) {
+            mma_commit(&bars->q_empty[two ? 0 : qsel]);
+            if (two) mma_commit(&bars->q_empty[1]);
           }
         }
         __syncwarp();
@@ -640,18 +679,18 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         pv = cur;
         pv_first = cur & ~started;
         started |= cur;
-        pv_dual = !s.k.two;
-        pv_last = i == s.ie - 1;
-        v_lo = s.k.vlo - kt * 128;
-        v_hi = s.k.vhi - kt * 128;
+        pv_dual = !two;
+        pv_last = i == ie - 1;
+        v_lo = vlo - kt * 128;
+        v_hi = vhi - kt * 128;
       }
       if (!ok) break;
-      if (s.k.two) {
+      if (two) {
         q_par ^= 3u;
       } else {
         q_par ^= 1u << qsel;
         qsel ^= 1;
-        flip = (flip + s.ie - s.ib) & 1;
+        flip = (flip + ie - ib) & 1;
       }
     }
     if (ok && gs > 0) {                                 // the last step's PV
@@ -689,7 +728,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float slope2 = 0.f;
       {
         Seg s;
-        if (!walk_next(p, walk, s)) break;
+        if (!walk_next(ps, walk, s)) break;
         const int r = 32 * q4 + lane, rq = r / p.group;  // row of the tile, its token
         dual = ONE || !s.k.two;
         const bool second = !dual && t;                 // holds the second tile's rows
@@ -735,24 +774,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           continue;
         }
         tc_fence_after();
-        // Tiles on the diagonal, at the end or at the band's lower edge: in
-        // TMEM, scores of keys that the row does not see become -inf,
-        // whatever the slots hold.
-        if (n0 + 127 > diag || n0 < low) {
-          const int ub = kend - n0, lb = p.causal ? ub - p.window : 0;
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t x[16];
-            tmem_ld16(tS + c, x);
-            tmem_wait_ld();
-            reg_fence16(x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i > ub || c + i < lb) x[i] = __float_as_uint(-INFINITY);
-            tmem_st16(tS + c, x);
-          }
-          tmem_wait_st();
-        }
         // The commit that published S_t also covers this stream's last PV, so
         // O may be rescaled now.
         if (!ONE && __any_sync(0xffffffffu, grow > 0.f)) {
@@ -804,7 +825,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           return x + y;
         };
         bool settled = false;
-        if (!ONE && !dual && !__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
+        // Tiles on the diagonal, at the end or at the band's lower edge hold
+        // scores of keys that a row does not see.
+        const bool masked = n0 + 127 > diag || n0 < low;
+        if (!ONE && !dual && !masked && !__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
           // P with the reference as it is; kept in registers until its sum
           // shows that it may stand.  P and O are floats, so a reference that
           // is too low costs no precision: a sum up to 2^40 stands, and one
@@ -830,8 +854,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
         }
         if (!settled) {
-          // The tile's max first: a row's first tile, a sum past 2^40, and
-          // every tile of a one-tile item (HBM sets its pace).
+          // The tile's max first: a masked tile, a row's first, a sum past
+          // 2^40, and every tile of a one-tile item (HBM sets its pace).
+          // Masked scores become -inf, in TMEM too, whatever the slots hold.
+          const int ub = kend - n0, lb = p.causal ? ub - p.window : 0;
           float mx = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -839,6 +865,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_ld32(tS + c, x);
             tmem_wait_ld();
             reg_fence32(x);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c + i > ub || c + i < lb) x[i] = __float_as_uint(-INFINITY);
+              tmem_st32(tS + c, x);
+            }
+            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
@@ -846,9 +879,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 x0 = fmaf(x0, c2, fmaf(slope2, (float)(c + i), base));
                 x1 = fmaf(x1, c2, fmaf(slope2, (float)(c + i + 1), base));
               }
-              mx = fmax3(mx, x0, x1);
+              m4[i / 2 & 3] = fmax3(m4[i / 2 & 3], x0, x1);
             }
+            mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
           }
+          if (masked) tmem_wait_st();
           if (!ALIBI) mx *= c2;
           // Any reference gives the same result: it stays until the max has
           // grown by more than tau.
@@ -867,11 +902,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // low part take the 16 columns of their scores, else 16 keys take 8
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
-            uint32_t x[32];
+            uint32_t x[32], y[32];
             tmem_ld32(tS + c, x);
             tmem_wait_ld();
             reg_fence32(x);
-            uint32_t y[32];
             if (ONE || dual) {
               exp16(std::true_type{}, c, x, mb, y, y + 8);
               exp16(std::true_type{}, c + 16, x + 16, mb, y + 16, y + 24);

@@ -525,8 +525,11 @@ def _run(what, index, stream, check, *args):
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _run(what, index, stream, check, *args)
-    sp = torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
-    _check(getattr(load(), what)(*args, sp), what)
+    # the raw handle of the current stream, without a Stream object around it
+    sp = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    st = getattr(_lib or load(), what)(*args, sp)
+    if st:
+        raise FAError(st, what)
     if check:
         _check(fa_check_device_error(sp), what + " (device)")
 
@@ -539,14 +542,15 @@ def _angles(q_weight, k_weight, cos, sin, d, index):
         raise ValueError("q_weight and k_weight go together")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    w = (None, None) if q_weight is None else (_checked("q_weight", q_weight, f32, index, (d,)),
-                                               _checked("k_weight", k_weight, f32, index, (d,)))
+    qw = kw = None
+    if q_weight is not None:
+        qw, kw = _checked("q_weight", q_weight, f32, index, (d,)), _checked("k_weight", k_weight, f32, index, (d,))
     if cos is None:
-        return (*w, None, None, 0, 0)
+        return qw, kw, None, None, 0, 0
     if cos.dim() != 2:
         raise ValueError("cos: [max_pos, rot_dim / 2] expected")
-    return (*w, _checked("cos", cos, f32, index), _checked("sin", sin, f32, index, cos.shape),
-            2 * cos.shape[1], cos.shape[0])
+    shape = cos.shape
+    return qw, kw, _checked("cos", cos, f32, index), _checked("sin", sin, f32, index, shape), 2 * shape[1], shape[0]
 
 
 def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos=None, sin=None,
@@ -621,8 +625,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     dkp, dks = _rows("dk", dk, q.dtype, index, (T, Hkv, d))
     dw = (None, None)
     if q_weight is not None:
-        both = _empty(q, (2, d), stream, torch.float32)
-        dw = (both[0], both[1])
+        dw = _empty(q, (2, d), stream, torch.float32).unbind()
         if workspace is None:
             workspace = _empty(q, (fa_qk_norm_rope_bwd_workspace_size(d),), stream, torch.uint8)
         _checked("workspace", workspace, torch.uint8, index)
