@@ -65,12 +65,12 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 9;
+constexpr int kMmaWarp = 9;
+constexpr int kLoadWarp = 8;
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
-constexpr int kWeightTwo = 3, kWeightOne = 2;   // of one key tile of an item
+constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kMinTiles = 2;                    // tiles a CTA takes at least: both streams busy
 
 template <int D>
