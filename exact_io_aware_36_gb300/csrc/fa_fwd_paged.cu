@@ -31,13 +31,16 @@
 // a long sequence and nothing depends on timing: the result is the same from
 // run to run.
 //
-// Roles (320 threads):
-//   warp 9     TMA producer: Q of an item, then per step one slot with K of
+// Roles:
+//   warp 10    walker: finds the CTA's items one after the other and passes
+//              them on through a ring of four, so that no other role waits
+//              for the lengths and the divisions this takes.
+//   warp 8     TMA producer: Q of an item, then per step one slot with K of
 //              this step's tile and V of the step before.  A tile is 128 /
 //              page_size boxes, one lane each, at the pages the table names;
 //              pages with no visible key are not read.  Page numbers of the
 //              next step are loaded before the wait for its slot.
-//   warp 8     MMA issuer (one lane).  Where a V tile reaches past the visible
+//   warp 9     MMA issuer (one lane).  Where a V tile reaches past the visible
 //              keys, the warp first zeroes those rows: a slot no token filled
 //              may hold NaN, and 0 x NaN would reach O.
 //   warps 0-3  softmax of stream 0 (one TMEM lane = one row), warps 4-7 of
@@ -64,9 +67,11 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;         // warp 11 has no role
 constexpr int kMmaWarp = 9;
 constexpr int kLoadWarp = 8;
+constexpr int kWalkWarp = 10;
+constexpr int kSegs = 4;               // items that the walker may be ahead
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
@@ -83,8 +88,8 @@ struct Cfg {
   static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
   static constexpr int V_OFF = K_OFF + NS * TILE_BYTES;
   static constexpr int ML_OFF = V_OFF + NS * TILE_BYTES;   // (m, l, l~) of both streams' rows
-  static constexpr int WALK_OFF = ML_OFF + 2 * 128 * 3 * 4;
-  static constexpr int PAR_OFF = WALK_OFF + (kThreads / 32) * 64;   // a copy of the parameters
+  static constexpr int SEG_OFF = ML_OFF + 2 * 128 * 3 * 4;          // ring of items
+  static constexpr int PAR_OFF = SEG_OFF + kSegs * 80;              // a copy of the parameters
   static constexpr int BAR_OFF = PAR_OFF + 256;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -99,6 +104,7 @@ struct Bars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_full[2];
   uint64_t o_done, o_free, drain;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem_base;
   int abort_flag;
   // the plan: where this CTA's run begins
@@ -177,48 +183,35 @@ static __device__ __noinline__ int block_weight(const PagedParams& p, int n, int
   return k.kt * tile_weight(k);
 }
 
-// A CTA's walk over its run [w0, w1) of the line of tiles.  Every role walks
-// the same items by itself; each warp keeps its state in shared memory, as it
-// is needed at the items' ends only.
-struct Walk {
-  long long w0, w1, base;      // base: place of item (b, g, qb) on the line
-  int b, g, qb, c0, n, L;
-  // softmax warps: what the epilogue of the current item needs
-  int item_g, item_tok, item_part, item_streams;
-};
-
-static_assert(sizeof(Walk) <= 64, "walk");
-
+// A part of an item, as the walker passes it on: steps [ib, ie) of the item's
+// kt; end of the run: ie < 0.
 struct Seg {
   Block k;
   int g, tok, ntok;            // kv head; first token (row of q) and tokens of the item
-  int b, L, ib, ie;            // sequence, its length; steps [ib, ie) of the item's kt
+  int b, L, ib, ie;            // sequence, its length
+};
+static_assert(sizeof(Seg) <= 80, "segment ring");
+
+// A CTA's walk over its run [w0, w1) of the line of tiles.
+struct Walk {
+  long long w0, w1, base;      // base: place of item (b, g, qb) on the line
+  int b, g, qb, c0, n, L;
 };
 
-// Warp-collective, as is walk_next.
-__device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bars, Walk* state) {
-  if ((threadIdx.x & 31) == 0) {
-    Walk w;
-    w.w0 = bars->w0;
-    w.w1 = bars->w1;
-    w.base = bars->base;
-    w.b = bars->b;
-    w.g = bars->g;
-    w.qb = bars->qb;
-    w.c0 = w.n = w.L = 0;
-    if (w.w0 < w.w1) load_seq(p, w.b, &w.c0, &w.n, &w.L);
-    *state = w;
-  }
-  __syncwarp();
+__device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bars, Walk& w) {
+  w.w0 = bars->w0;
+  w.w1 = bars->w1;
+  w.base = bars->base;
+  w.b = bars->b;
+  w.g = bars->g;
+  w.qb = bars->qb;
+  w.c0 = w.n = w.L = 0;
+  if (w.w0 < w.w1) load_seq(p, w.b, &w.c0, &w.n, &w.L);
 }
 
 // The next part of an item in the run; false at its end.
-// One copy of this code serves all roles (see the note on code size).
-static __device__ __noinline__ bool walk_next(const PagedParams& p, Walk* state, Seg& s) {
-  Walk w = *state;
-  __syncwarp();
-  bool found = false;
-  while (!found && w.base < w.w1) {
+__device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s) {
+  while (w.base < w.w1) {
     if (w.qb * 2 * p.tpt >= w.n) {
       w.qb = 0;
       if (++w.g >= p.Hkv) {
@@ -242,11 +235,9 @@ static __device__ __noinline__ bool walk_next(const PagedParams& p, Walk* state,
     s.ntok = s.k.nt[0] + s.k.nt[1];
     w.base += len;
     ++w.qb;
-    found = s.ib < s.ie;
+    if (s.ib < s.ie) return true;
   }
-  if ((threadIdx.x & 31) == 0) *state = w;
-  __syncwarp();
-  return found;
+  return false;
 }
 
 // Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
@@ -371,18 +362,29 @@ __device__ __forceinline__ void rescale_row(uint32_t tO, float alpha) {
   }
 }
 
-// 16 columns of a finished row, or of a part (float32, not divided).
-__device__ __forceinline__ void store_row16(const float* v, bool f32, void* base, long long at) {
-  if (f32) {
-    float4* O = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) O[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+// 16 columns of a finished row, or of a part (float32, not divided).  A warp's
+// rows lie apart, so each store of it touches 32 lines whatever its width:
+// `wide` (32-byte aligned rows) halves the stores.
+__device__ __forceinline__ void store32(void* at, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(at), FA_W8(v, 0) : "memory");
   } else {
-    uint4* O = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at);
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__device__ __forceinline__ void store_row16(const float* v, bool f32, bool wide, void* base, long long at) {
+  uint32_t w[16];
+  if (f32) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      O[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
+    store32(static_cast<float*>(base) + at, w, wide);
+    store32(static_cast<float*>(base) + at + 8, w + 8, wide);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    store32(static_cast<__nv_bfloat16*>(base) + at, w, wide);
   }
 }
 
@@ -415,6 +417,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], 10);     // producer, MMA issuer, 8 softmax warps
+    }
     mbar_init(&bars->o_done, 1);
     mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drain, 1);
@@ -441,8 +447,19 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t tmem = bars->tmem_base;
   const WaitCtx wc{&bars->abort_flag, p.status};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp(bar, parity, wc); };
-  Walk* walk = reinterpret_cast<Walk*>(smem + C::WALK_OFF + warp * 64);
-  walk_begin(ps, bars, walk);
+  // The ring of items: item n is ring[n % kSegs]; false at the run's end (or if
+  // the wait ran out).  A reader gives the place back with seg_done.
+  const Seg* ring = reinterpret_cast<const Seg*>(smem + C::SEG_OFF);
+  int nitem = 0;
+  auto next_seg = [&](bool& ok) -> bool {
+    if (!wait(&bars->seg_full[nitem % kSegs], (nitem / kSegs) & 1)) return ok = false;
+    return ring[nitem % kSegs].ie >= 0;
+  };
+  auto seg_done = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->seg_empty[nitem % kSegs]);
+    ++nitem;
+  };
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ producer
@@ -454,21 +471,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int box_rows = min(p.page_size, 128);
     const int nbox = 128 / box_rows;
     const uint32_t box_bytes = box_rows * 128;
-    Seg s;
     bool ok = true;
     unsigned q_any = 0, q_par = 0;   // bit x: Q buffer x was loaded; its last load's parity
     int qsel = 0;              // buffer of the next one-tile item
     int gs = 0;                // steps over all items
-    // what the parts of this CTA are, for the merge: kind of the part that goes
-    // on from the CTA before (2: the item's last), and the item begun here
-    int cont = 0;
-    int4 begun = make_int4(0, 0, 0, 0);
     int vrow = -1, vg = 0;     // the step before: this lane's page row (-1: no box), kv head
-    while (ok && walk_next(ps, walk, s)) {
+    while (ok && next_seg(ok)) {
+      const Seg& s = ring[nitem % kSegs];
       const bool two = !ONE && s.k.two;
       const int g = s.g, ib = s.ib, ie = s.ie, vlo = s.k.vlo, vhi = s.k.vhi, hi_all = s.k.hi_all;
-      if (ib > 0) cont = ie == s.k.kt ? 2 : 1;
-      else if (ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, g);
+      const int tok = s.tok, b = s.b;
+      seg_done();
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         const int x = two ? t : qsel;
         if ((q_any >> x & 1) && !(ok = wait(&bars->q_empty[x], q_par >> x & 1))) break;
@@ -477,7 +490,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
           for (int bx = 0; bx < C::NB; ++bx)
             tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bx * 64, g * p.group,
-                        s.tok + t * p.tpt, &bars->q_full[x]);
+                        tok + t * p.tpt, &bars->q_full[x]);
         }
         __syncwarp();
         if (q_any >> x & 1) q_par ^= 1u << x;
@@ -485,7 +498,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       if (!ok) break;
       if (!two) qsel ^= 1;
-      const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
+      const int32_t* table = p.block_table + (long long)b * p.max_pages;
       for (int i = ib; i < ie; ++i, ++gs) {
         const int key0 = (hi_all - i) * 128 + lane * box_rows;
         int krow = -1;
@@ -528,10 +541,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ++gs;
       }
     }
-    if (lane == 0) {
-      p.part_meta[2 * blockIdx.x] = make_int4(ok ? cont : 0, 0, 0, 0);
-      p.part_meta[2 * blockIdx.x + 1] = ok ? begun : make_int4(0, 0, 0, 0);
-    }
     // Loads in flight must land before this CTA's shared memory goes away.
     for (int x = 0; x < 2; ++x)
       if (q_any >> x & 1) wait_warp_drain(&bars->q_full[x], q_par >> x & 1);
@@ -543,7 +552,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint64_t qdesc0 = smem_desc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024);
     const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::K_OFF), 16, 1024);
     const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::V_OFF), C::BOX_BYTES, 1024);
-    Seg s;
     bool ok = true;
     int gs = 0, nseg = 0;
     unsigned q_par = 0;          // bit x: parity of Q buffer x's next load
@@ -605,20 +613,22 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       fence_proxy_async_smem();
       __syncwarp();
     };
-    while (ok && walk_next(ps, walk, s)) {
+    while (ok && next_seg(ok)) {
+      const Seg& s = ring[nitem % kSegs];
       const bool two = !ONE && s.k.two;
       const int ib = s.ib, ie = s.ie, hi_all = s.k.hi_all, vlo = s.k.vlo, vhi = s.k.vhi;
       const int lo0 = s.k.lo[0], hi0 = s.k.hi[0], lo1 = s.k.lo[1], hi1 = s.k.hi[1];
+      seg_done();
       int started = 0;                                  // streams that have begun this item
       for (int i = ib; ok && i < ie; ++i, ++gs) {
         const int sl = gs % C::NS;
         const int kt = hi_all - i;
         const int cur = two ? ((kt >= lo0 && kt <= hi0) | ((kt >= lo1 && kt <= hi1) << 1)) : 1 << ((flip + i - ib) & 1);
-        if (!(ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) break;
         if (!ONE && cur == 3 && pv == 3 && !pv_dual && !pv_first && !pv_last && i < ie - 1 && v_lo <= 0 && v_hi >= 128) {
           // Inside an item of two tiles: PV0, S0, PV1, S1 and nothing else.
           // The tensor pipe takes only a couple of products ahead, so what
-          // this warp does between two batches is time the pipe idles.
+          // this warp does between two batches is time the pipe idles: the
+          // slot's loads were waited for by softmax warp 0 (before p_full[0]).
           const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -644,6 +654,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           v_hi = vhi - kt * 128;
           continue;
         }
+        if (!(ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) break;
         // S of a stream whose P is not waited for comes first; but at an
         // item's head, whose Q may be on its way, PV of the item before.
         const int s_first = i == ib && two ? 0 : cur & ~pv, s_last = i == ib && two ? cur : 0;
@@ -708,7 +719,35 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (lane == 0) mma_commit(&bars->drain);
     __syncwarp();
     wait_warp_drain(&bars->drain, 0);
-  } else {
+  } else if (warp == kWalkWarp) {
+    // -------------------------------------------------------------- walker
+    Walk w;
+    Seg s;
+    walk_begin(p, bars, w);
+    // what the parts of this CTA are, for the merge: kind of the part that
+    // goes on from the CTA before (2: the item's last), and the item begun here
+    int cont = 0;
+    int4 begun = make_int4(0, 0, 0, 0);
+    for (bool more = true; more; ++nitem) {
+      more = walk_next(p, w, s);
+      if (more) {
+        if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
+        else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
+      } else {
+        s.ie = -1;
+        if (lane == 0) {
+          p.part_meta[2 * blockIdx.x] = make_int4(cont, 0, 0, 0);
+          p.part_meta[2 * blockIdx.x + 1] = begun;
+        }
+      }
+      if (nitem >= kSegs && !wait(&bars->seg_empty[nitem % kSegs], (nitem / kSegs - 1) & 1)) break;
+      if (lane == 0) {
+        const_cast<Seg*>(ring)[nitem % kSegs] = s;
+        mbar_arrive(&bars->seg_full[nitem % kSegs]);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
     const int q4 = warp & 3;
@@ -720,15 +759,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool ok = true;
     int cs = 0;                  // S products consumed (s_full phases)
     int nseg = 0, flip = 0;
+    int gs = 0;                  // steps before this item
     // A warp that gives up (a wait ran out) still walks the items: it meets
     // the others at the barrier of every one-tile item, and they give up too.
     while (true) {
       int n0, steps, diag, low, kend;
       bool valid, dual;
       float slope2 = 0.f;
+      int vslot = 0;             // step of this stream's next tile
       {
-        Seg s;
-        if (!walk_next(ps, walk, s)) break;
+        bool got = true;
+        if (!next_seg(got)) {
+          if (!got) ok = false;
+          break;
+        }
+        const Seg& s = ring[nitem % kSegs];
         const int r = 32 * q4 + lane, rq = r / p.group;  // row of the tile, its token
         dual = ONE || !s.k.two;
         const bool second = !dual && t;                 // holds the second tile's rows
@@ -751,16 +796,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         diag = p.causal ? f : s.L - 1;
         low = f + nt - 1 - p.window;
         if (ALIBI) slope2 = valid ? __ldg(p.alibi + s.g * p.group + r % p.group) * kLog2e : 0.f;
-        if (lane == 0) {
-          walk->item_g = s.g;
-          walk->item_tok = s.tok;
-          // 0: the whole item; else the slot of the part: 1 its continuation
-          // from the CTA before, 2 its beginning
-          walk->item_part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
-          // streams with a step (one-tile items: of both)
-          walk->item_streams = dual ? (s.ie - s.ib > 1 ? 3 : steps > 0 ? 1 << t : 2 >> t) : steps > 0 ? 1 << t : 0;
-        }
-        __syncwarp();
+        vslot = gs + s.k.hi_all - s.ib - kt0;
+        gs += s.ie - s.ib;
       }
       const bool warp_rows = __any_sync(0xffffffffu, valid);
       float m_ref = -INFINITY;
@@ -922,6 +959,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         tmem_wait_st();
         tc_fence_before();
+        // On behalf of the MMA issuer: the next step's slot has been loaded.
+        if (!ONE && warp == 0 && !dual) {
+          ++vslot;
+          if (!(ok = wait(&bars->kv_full[vslot % C::NS], (vslot / C::NS) & 1))) break;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
@@ -931,8 +973,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // A stream without a step in this part has no O: its columns are not
       // used.
       const int r = 32 * q4 + lane;
-      const int streams = walk->item_streams, part = walk->item_part;
-      const bool use0 = streams >> t & 1, use1 = dual && (streams >> (t ^ 1) & 1);
+      const Seg& s = ring[nitem % kSegs];
+      // 0: the whole item; else the slot of the part: 1 its continuation from
+      // the CTA before, 2 its beginning
+      const int part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
+      const bool use0 = steps > 0, use1 = dual && (steps == 0 || s.ie - s.ib > 1);
       float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
       if (dual) {
@@ -953,14 +998,18 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         c_from = t * (D / 2);
         c_to = c_from + D / 2;
       }
-      if (!ok) continue;
+      if (!ok) {
+        seg_done();
+        continue;
+      }
       const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
       const int tl = (dual ? 0 : t * p.tpt) + r / p.group;            // token of the item
-      const int rh = r % p.group, head = walk->item_g * p.group + rh;
-      const long long tok = walk->item_tok + tl;
+      const int rh = r % p.group, head = s.g * p.group + rh;
+      const long long tok = s.tok + tl;
       const long long orow = tok * p.Hq + head;
       const int slot = 2 * (int)blockIdx.x + part - 1;
       const long long prow = (long long)slot * p.part_rows + tl * p.group + rh;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
       float sc = 1.f;
       if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
       if (warp_rows) {
@@ -980,8 +1029,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             v[i] *= sc;
           }
           if (valid) {
-            if (part) store_row16(v, true, p.part_o, prow * D + c);
-            else store_row16(v, p.o_f32, p.o, orow * D + c);
+            if (part) store_row16(v, true, true, p.part_o, prow * D + c);
+            else store_row16(v, p.o_f32, wide, p.o, orow * D + c);
           }
         }
       }
@@ -997,6 +1046,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       ++nseg;
+      seg_done();
     }
   }
   tc_fence_before();
