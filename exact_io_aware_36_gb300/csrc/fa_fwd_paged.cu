@@ -624,37 +624,88 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int sl = gs % C::NS;
         const int kt = hi_all - i;
         const int cur = two ? ((kt >= lo0 && kt <= hi0) | ((kt >= lo1 && kt <= hi1) << 1)) : 1 << ((flip + i - ib) & 1);
-        if (!ONE && cur == 3 && pv == 3 && !pv_dual && !pv_first && !pv_last && i < ie - 1 && v_lo <= 0 && v_hi >= 128) {
-          // Inside an item of two tiles: PV0, S0, PV1, S1 and nothing else.
-          // The tensor pipe takes only a couple of products ahead, so what
-          // this warp does between two batches is time the pipe idles: the
-          // slot's loads were waited for by softmax warp 0 (before p_full[0]).
+        // Inside an item, with nothing but products to issue.  The tensor pipe
+        // takes only a couple of products ahead, so what this warp does
+        // between two batches is time the pipe idles.
+        const bool inside = !pv_first && !pv_last && i > ib && i < ie - 1 && v_lo <= 0 && v_hi >= 128;
+        if (!ONE && two && inside && cur == 3 && pv == 3) {
+          // Two tiles: PV0, S0, PV1, S1.  The slot's loads were waited for by
+          // softmax warp 0 (before p_full[0]); P1 is asked for while the
+          // last products of the first batch run.
           const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+          auto batch = [&](int t, bool ask) -> bool {
+            const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
+            bool there = false;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!(ok = wait(&bars->p_full[t], p_par >> t & 1))) break;
+            for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colS + kk * 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
+              if (ask && kk == D / 16 - 2) there = mbar_try_wait(&bars->p_full[1], p_par >> 1 & 1);
+              mma_ss(colS, desc_add(qdesc0, t * C::TILE_BYTES + off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars->s_full[t]);
+            if (t) mma_commit(&bars->kv_empty[sl]);
+            return there;
+          };
+          if (!(ok = wait(&bars->p_full[0], p_par & 1))) break;
+          bool there = false;
+          if (lane == 0) {
             tc_fence_after();
+            there = batch(0, true);
+            if (there) {
+              tc_fence_after();
+              batch(1, false);
+            }
+          }
+          if (!__shfl_sync(0xffffffffu, (int)there, 0)) {
+            if (!(ok = wait(&bars->p_full[1], p_par >> 1 & 1))) break;
             if (lane == 0) {
-              const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colS + kk * 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
-                mma_ss(colS, desc_add(qdesc0, t * C::TILE_BYTES + off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
-              }
-              mma_commit(&bars->s_full[t]);
-              if (t) mma_commit(&bars->kv_empty[sl]);
+              tc_fence_after();
+              batch(1, false);
             }
             __syncwarp();
           }
-          if (!ok) break;
           p_par ^= 3u;
           v_lo = vlo - kt * 128;
           v_hi = vhi - kt * 128;
           continue;
         }
         if (!(ok = wait(&bars->kv_full[sl], (gs / C::NS) & 1))) break;
+        if ((ONE || !two) && inside) {
+          // One tile: S of this step's stream, PV of the other's.
+          const int t = cur >> 1, u = t ^ 1;
+          if (lane == 0) {
+            const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), qd = desc_add(qdesc0, qsel * C::TILE_BYTES);
+            const uint32_t colS = tmem + C::S_COL0 + t * (C::S_COL1 - C::S_COL0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
+              mma_ss(colS, desc_add(qd, off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&bars->s_full[t]);
+          }
+          __syncwarp();
+          if (!(ok = wait(&bars->p_full[u], p_par >> u & 1))) break;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+            const uint32_t colP = tmem + C::S_COL0 + u * (C::S_COL1 - C::S_COL0);
+            const uint32_t colO = tmem + C::O_COL0 + u * (C::O_COL1 - C::O_COL0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              mma_ts(colO, colP + kk * 16, desc_add(vd, kk * 2048), IDESC_O, 1u);
+              mma_ts(colO, colP + kk * 16 + 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
+            }
+            mma_commit(&bars->kv_empty[sl]);
+          }
+          __syncwarp();
+          p_par ^= 1u << u;
+          pv = cur;
+          v_lo = vlo - kt * 128;
+          v_hi = vhi - kt * 128;
+          continue;
+        }
         // S of a stream whose P is not waited for comes first; but at an
         // item's head, whose Q may be on its way, PV of the item before.
         const int s_first = i == ib && two ? 0 : cur & ~pv, s_last = i == ib && two ? cur : 0;
