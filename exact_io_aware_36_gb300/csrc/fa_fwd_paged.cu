@@ -24,8 +24,9 @@
 //
 // Work.  Lengths are known on the device alone (so a captured call can be
 // replayed with others).  Every CTA, one per SM, adds up the key tiles of all
-// items (two-tile items' tiles weigh 3, others 2: their measured times) and
-// takes an equal run of this one line of tiles.  A run begins and ends inside
+// items, weighed by their measured times (a tile of a two-tile item 9, of
+// another 8; what an item costs beside its tiles 36 and 16), and takes an equal
+// run of this one line.  A run begins and ends inside
 // items; such parts go to the workspace, two at most per CTA, and
 // paged_merge_kernel joins an item's parts in a fixed order.  No SM waits for
 // a long sequence and nothing depends on timing: the result is the same from
@@ -76,7 +77,10 @@ constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
-constexpr int kMinTiles = 2;                    // tiles a CTA takes at least: both streams busy
+constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
+// A CTA's run is at least this long, so that none lies between the beginnings
+// of an item's first two tiles: an item's parts are in CTAs next to each other.
+constexpr int kMinRunTwo = kHeadTwo + kWeightTwo + 2, kMinRunOne = kHeadOne + kWeightOne + 2;
 
 template <int D>
 struct Cfg {
@@ -172,6 +176,7 @@ __device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int 
 }
 
 __device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
+__device__ __forceinline__ int head_weight(const Block& k) { return k.two ? kHeadTwo : kHeadOne; }
 
 // Weight of the block of query tokens from tok0 on (0 behind the last).  Not
 // inlined: a short call runs through code that no SM has cached yet, so each
@@ -180,7 +185,7 @@ static __device__ __noinline__ int block_weight(const PagedParams& p, int n, int
   if (tok0 >= n) return 0;
   Block k;
   block_geometry(p, n, L, tok0, k);
-  return k.kt * tile_weight(k);
+  return head_weight(k) + k.kt * tile_weight(k);
 }
 
 // A part of an item, as the walker passes it on: steps [ib, ie) of the item's
@@ -224,10 +229,12 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
     }
     const int tok0 = w.qb * 2 * p.tpt;
     block_geometry(p, w.n, w.L, tok0, s.k);
-    const int wt = tile_weight(s.k);
-    const long long len = (long long)s.k.kt * wt;
-    s.ib = w.base >= w.w0 ? 0 : ((int)(w.w0 - w.base) + wt - 1) / wt;
-    s.ie = w.w1 - w.base >= len ? s.k.kt : ((int)(w.w1 - w.base) + wt - 1) / wt;
+    // On the line an item is its head and then its tiles; the first tile
+    // begins with the head.  A CTA has the tiles that begin in its run.
+    const int wt = tile_weight(s.k), head = head_weight(s.k);
+    const long long len = head + (long long)s.k.kt * wt;
+    s.ib = w.base >= w.w0 ? 0 : max(1, ((int)(w.w0 - w.base) - head + wt - 1) / wt);
+    s.ie = w.w1 - w.base >= len ? s.k.kt : min(s.k.kt, max(1, ((int)(w.w1 - w.base) - head + wt - 1) / wt));
     s.b = w.b;
     s.L = w.L;
     s.g = w.g;
@@ -242,7 +249,7 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
 
 // Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
 // threads; `pre` holds B 64-bit words of shared memory.
-__device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre) {
+__device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre, unsigned min_run) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // 1. every sequence's weight, nl lanes per sequence
   const int nl = p.plan_lanes;
@@ -281,7 +288,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
   // 3. this CTA's run, and the sequence it begins in.  Cut in float: the
   // same for a CTA's end and its neighbour's beginning, and never falling,
   // which is all that is needed.
-  const int active = (int)min((unsigned long long)gridDim.x, max(1ull, total / (kMinTiles * kWeightOne)));
+  const int active = (int)min((unsigned long long)gridDim.x, max(1ull, total / min_run));
   const int c = min((int)blockIdx.x, active);
   auto cut = [&](int i) {
     if (i >= active) return (long long)total;
@@ -438,7 +445,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-  make_plan(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF));
+  make_plan(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF),
+            ONE ? kMinRunOne : kMinRunTwo);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
