@@ -964,7 +964,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (masked) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (c + i > ub || c + i < lb) x[i] = __float_as_uint(-INFINITY);
+                if (c + i > ub) x[i] = __float_as_uint(-INFINITY);
+              if (n0 < low)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (c + i < lb) x[i] = __float_as_uint(-INFINITY);
               tmem_st32(tS + c, x);
             }
             float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
