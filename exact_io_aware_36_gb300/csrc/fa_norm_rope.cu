@@ -257,13 +257,16 @@ __device__ __forceinline__ bool unit_at(const NormRopeParams& p, unsigned unit, 
   return true;
 }
 
-// Kind (0 query, 1 key, 2 value) of set s and this lane's head in it; true if
-// the head exists.
+// This warp's sets [s0, s1) of the kind whose sets are [from, from + n), as
+// heads: the lane's first, and behind the last set.
+struct Heads {
+  int h, sets;
+};
+
 template <int RPS>
-__device__ __forceinline__ bool set_head(const NormRopeParams& p, int s, int sub, int* kind, int* h) {
-  *kind = s < p.sets_q ? 0 : s < p.sets_q + p.sets_k ? 1 : 2;
-  *h = (s - (*kind == 0 ? 0 : *kind == 1 ? p.sets_q : p.sets_q + p.sets_k)) * RPS + sub;
-  return *h < (*kind == 0 ? p.Hq : p.Hkv);
+__device__ __forceinline__ Heads heads_of(const Unit& u, int from, int n, int sub) {
+  const int s0 = max(u.sa, from), s1 = min(u.sb, from + n);
+  return Heads{(s0 - from) * RPS + sub, max(s1 - s0, 0)};
 }
 
 template <int D, typename T, bool PAGES>
@@ -275,17 +278,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
   Unit u;
   if (!unit_at(p, blockIdx.x * kWarps + (threadIdx.x >> 5), u)) return;
   const long long t = u.t;
-  auto load = [&](int s, Vec8<T>& x) {
-    int kind, h;
-    x.zero();
-    if (s < u.sb && set_head<RPS>(p, s, sub, &kind, &h))
-      x.load((kind == 0   ? static_cast<const T*>(p.q) + t * p.q_stride
-              : kind == 1 ? static_cast<const T*>(p.k) + t * p.k_stride
-                          : static_cast<const T*>(p.v) + t * p.v_stride) + (long long)h * D + 8 * l);
-  };
-  Vec8<T> x[2];
-  load(u.sa, x[0]);
-  load(u.sa + 1, x[1]);
   int pos = 0;
   long long page_row = 0;
   if constexpr (PAGES) {
@@ -300,62 +292,78 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
   Angles ang;
   load_angles(p, pos, l, false, ang);
   const bool on = 8 * l < p.rot;
-  const int ml = mate_lane(p, l), src = sub * LPR + ml;
-  uint64_t wc[4], ws[4];                       // angles times weights, of kind `have`
-  int have = -1;
-  for (int s = u.sa; s < u.sb; s += 2) {
-    Vec8<T> next[2];
-    load(s + 2, next[0]);
-    load(s + 3, next[1]);
+  const int ml = mate_lane(p, l), src_lane = sub * LPR + ml;
+
+  // H heads at src and dst (this token's), sets [from, from + n): two sets a
+  // turn, both loaded before either is used.
+  auto rows = [&](const T* src, T* dst, int H, int from, int n, const float* weight) {
+    const Heads hd = heads_of<RPS>(u, from, n, sub);
+    if (hd.sets == 0) return;
+    uint64_t wc[4], ws[4];                     // angles times weights
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (s + k >= u.sb) break;                // warp-uniform, as is a set's kind
-      int kind, h;
-      const bool live = set_head<RPS>(p, s + k, sub, &kind, &h);
-      if (kind < 2) {
-        if (kind != have) {
-          have = kind;
+    for (int i = 0; i < 4; ++i) {
+      wc[i] = ang.c[i];
+      ws[i] = ang.s[i];
+    }
+    if (weight) {
+      uint64_t a[4], b[4];
+      load_weights(weight, l, a);
+      load_weights(weight, ml, b);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            wc[i] = ang.c[i];
-            ws[i] = ang.s[i];
-          }
-          if (p.q_weight) {
-            const float* w = kind == 0 ? p.q_weight : p.k_weight;
-            uint64_t a[4], b[4];
-            load_weights(w, l, a);
-            load_weights(w, ml, b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              wc[i] = fmul2(wc[i], a[i]);
-              ws[i] = fmul2(ws[i], p.interleaved ? swap_pair(b[i]) : b[i]);
-            }
-          }
-        }
-        float r = 1.f;
-        if (p.q_weight) {
-          uint64_t ss = f2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ss = ffma2(x[k].pair(i), x[k].pair(i), ss);
-          r = rsqrtf(row_sum<LPR>(pair_sum(ss)) * (1.f / D) + p.eps);
-        }
-        const uint64_t r2 = f2(r, r);
-        const Partners<T> y(p, x[k], src, on);
-        Vec8<T> z;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          z.set(i, fmul2(ffma2(x[k].pair(i), wc[i], fmul2(y.pair(i), ws[i])), r2));
-        if (live) {
-          T* dst = kind == 0 ? static_cast<T*>(p.q_out) + t * p.Hq * D
-                             : static_cast<T*>(p.k_out) + (PAGES ? page_row : t) * p.Hkv * D;
-          z.store(dst + (long long)h * D + 8 * l);
-        }
-      } else if (live) {                       // value rows pass as they are
-        x[k].store(static_cast<T*>(p.v_out) + (page_row * p.Hkv + h) * D + 8 * l);
+      for (int i = 0; i < 4; ++i) {
+        wc[i] = fmul2(wc[i], a[i]);
+        ws[i] = fmul2(ws[i], p.interleaved ? swap_pair(b[i]) : b[i]);
       }
     }
-    x[0] = next[0];
-    x[1] = next[1];
+    src += hd.h * D + 8 * l;
+    dst += hd.h * D + 8 * l;
+    const int left0 = H - hd.h;                // the lane's heads: every RPS-th
+    auto one = [&](const Vec8<T>& x, T* at, bool live) {
+      float r = 1.f;
+      if (weight) {
+        uint64_t ss = fmul2(x.pair(0), x.pair(0));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss = ffma2(x.pair(i), x.pair(i), ss);
+        r = rsqrtf(row_sum<LPR>(pair_sum(ss)) * (1.f / D) + p.eps);
+      }
+      const uint64_t r2 = f2(r, r);
+      const Partners<T> y(p, x, src_lane, on);
+      Vec8<T> z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z.set(i, fmul2(ffma2(x.pair(i), wc[i], fmul2(y.pair(i), ws[i])), r2));
+      if (live) z.store(at);
+    };
+    int left = left0;
+    for (int k = 0; k < hd.sets; k += 2) {
+      Vec8<T> x, y;
+      const bool live0 = left > 0, live1 = k + 1 < hd.sets && left > RPS;
+      if (live0) x.load(src);
+      else x.zero();
+      if (live1) y.load(src + RPS * D);
+      else y.zero();
+      one(x, dst, live0);
+      if (k + 1 < hd.sets) one(y, dst + RPS * D, live1);
+      src += 2 * RPS * D;
+      dst += 2 * RPS * D;
+      left -= 2 * RPS;
+    }
+  };
+  const bool norm = p.q_weight != nullptr;
+  rows(static_cast<const T*>(p.q) + t * p.q_stride, static_cast<T*>(p.q_out) + t * p.Hq * D, p.Hq, 0, p.sets_q,
+       norm ? p.q_weight : nullptr);
+  rows(static_cast<const T*>(p.k) + t * p.k_stride, static_cast<T*>(p.k_out) + (PAGES ? page_row : t) * p.Hkv * D, p.Hkv,
+       p.sets_q, p.sets_k, norm ? p.k_weight : nullptr);
+  if constexpr (PAGES) {                       // value rows pass as they are
+    const Heads hd = heads_of<RPS>(u, p.sets_q + p.sets_k, p.sets_v, sub);
+    const T* src = static_cast<const T*>(p.v) + t * p.v_stride + 8 * l;
+    T* dst = static_cast<T*>(p.v_out) + page_row * p.Hkv * D + 8 * l;
+#pragma unroll 2
+    for (int k = 0, h = hd.h; k < hd.sets; ++k, h += RPS)
+      if (h < p.Hkv) {
+        Vec8<T> x;
+        x.load(src + h * D);
+        x.store(dst + h * D);
+      }
   }
 }
 
@@ -373,25 +381,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
   const int l = lane & (LPR - 1), sub = lane / LPR;
   const bool on = 8 * l < p.rot;
   const int src = sub * LPR + mate_lane(p, l);
-  uint64_t dw[2][4];                           // of the query and the key weight
+  uint64_t dwq[4], dwk[4];                     // of the query and the key weight
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = f2(0.f, 0.f);
+  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = f2(0.f, 0.f);
 
   Unit u;
   for (unsigned unit = blockIdx.x * kWarps + warp; unit_at(p, unit, u); unit += gridDim.x * kWarps) {
     const long long t = u.t;
-    auto load = [&](int s, Vec8<T>& x, Vec8<T>& z) {
-      int kind, h;
-      x.zero();
-      z.zero();
-      if (s < u.sb && set_head<RPS>(p, s, sub, &kind, &h)) {
-        const long long at = (long long)h * D + 8 * l;
-        x.load((kind == 0 ? static_cast<const T*>(p.q) + t * p.q_stride : static_cast<const T*>(p.k) + t * p.k_stride) + at);
-        z.load((kind == 0 ? static_cast<const T*>(p.dq_out) + t * p.Hq * D : static_cast<const T*>(p.dk_out) + t * p.Hkv * D) + at);
-      }
-    };
-    Vec8<T> x, z;
-    load(u.sa, x, z);
     const int pos = p.rot ? __ldg(p.positions + t) : 0;
     if (p.rot && (pos < 0 || pos >= p.max_pos)) {
       if (lane == 0) record_status(p.status, FA_ERR_POSITION);
@@ -399,59 +395,83 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
     }
     Angles ang;
     load_angles(p, pos, l, true, ang);
-    uint64_t w[4];
-    int have = -1;
-    for (int s = u.sa; s < u.sb; ++s) {
-      Vec8<T> xn, zn;
-      load(s + 1, xn, zn);
-      int kind, h;
-      const bool live = set_head<RPS>(p, s, sub, &kind, &h);
-      uint64_t dy[4];
-      {
-        const Partners<T> y(p, z, src, on);
+    auto rows = [&](const T* x_at, const T* z_at, T* d_at, int H, int from, int n, const float* weight, uint64_t* dw) {
+      const Heads hd = heads_of<RPS>(u, from, n, sub);
+      if (hd.sets == 0) return;
+      uint64_t w[4];
+      if (weight) load_weights(weight, l, w);
+      x_at += hd.h * D + 8 * l;
+      z_at += hd.h * D + 8 * l;
+      d_at += hd.h * D + 8 * l;
+      auto one = [&](const Vec8<T>& x, const Vec8<T>& z, T* at, bool live) {
+        uint64_t dy[4];
+        {
+          const Partners<T> y(p, z, src, on);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dy[i] = ffma2(z.pair(i), ang.c[i], fmul2(y.pair(i), ang.s[i]));
+          for (int i = 0; i < 4; ++i) dy[i] = ffma2(z.pair(i), ang.c[i], fmul2(y.pair(i), ang.s[i]));
+        }
+        if (weight) {
+          uint64_t g[4], ss = f2(0.f, 0.f), dot = f2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g[i] = fmul2(dy[i], w[i]);
+            ss = ffma2(x.pair(i), x.pair(i), ss);
+            dot = ffma2(g[i], x.pair(i), dot);
+          }
+          float a = pair_sum(ss), b = pair_sum(dot);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+          }
+          const float r = rsqrtf(a * (1.f / D) + p.eps);
+          // xh = x r, dw += dy xh, dx = r (dy w - xh mean(dy w xh)); a row
+          // that is not there has xh = 0, whatever its r
+          const float rl = live ? r : 0.f, m = -(b * r * (1.f / D)) * r;
+          const uint64_t r2 = f2(r, r), m2 = f2(m, m), rl2 = f2(rl, rl);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t xh = fmul2(x.pair(i), rl2);
+            dw[i] = ffma2(dy[i], xh, dw[i]);
+            dy[i] = ffma2(xh, m2, fmul2(g[i], r2));
+          }
+        }
+        if (live) {
+          Vec8<T> d;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d.set(i, dy[i]);
+          d.store(at);
+        }
+      };
+      int left = H - hd.h;                     // the lane's heads: every RPS-th
+      for (int k = 0; k < hd.sets; k += 2) {
+        Vec8<T> x0, z0, x1, z1;
+        const bool live0 = left > 0, live1 = k + 1 < hd.sets && left > RPS;
+        x0.zero();
+        z0.zero();
+        x1.zero();
+        z1.zero();
+        if (live0) {
+          x0.load(x_at);
+          z0.load(z_at);
+        }
+        if (live1) {
+          x1.load(x_at + RPS * D);
+          z1.load(z_at + RPS * D);
+        }
+        one(x0, z0, d_at, live0);
+        if (k + 1 < hd.sets) one(x1, z1, d_at + RPS * D, live1);
+        x_at += 2 * RPS * D;
+        z_at += 2 * RPS * D;
+        d_at += 2 * RPS * D;
+        left -= 2 * RPS;
       }
-      if (p.q_weight) {
-        if (kind != have) {
-          have = kind;
-          load_weights(kind == 0 ? p.q_weight : p.k_weight, l, w);
-        }
-        uint64_t ss = f2(0.f, 0.f), dot = f2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ss = ffma2(x.pair(i), x.pair(i), ss);
-          dot = ffma2(fmul2(dy[i], w[i]), x.pair(i), dot);
-        }
-        float a = pair_sum(ss), b = pair_sum(dot);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        const float r = rsqrtf(a * (1.f / D) + p.eps);
-        // xh = x r, dw += dy xh, dx = r (dy w - xh mean(dy w xh)); a row that
-        // is not there has xh = 0, whatever its r
-        const float rl = live ? r : 0.f, m = -(b * r * (1.f / D)) * r;
-        const uint64_t r2 = f2(r, r), m2 = f2(m, m), rl2 = f2(rl, rl);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t xh = fmul2(x.pair(i), rl2);
-          if (kind == 0) dw[0][i] = ffma2(dy[i], xh, dw[0][i]);
-          else dw[1][i] = ffma2(dy[i], xh, dw[1][i]);
-          dy[i] = ffma2(xh, m2, fmul2(fmul2(dy[i], w[i]), r2));
-        }
-      }
-      if (live) {
-        Vec8<T> d;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d.set(i, dy[i]);
-        d.store((kind == 0 ? static_cast<T*>(p.dq) + t * p.dq_stride : static_cast<T*>(p.dk) + t * p.dk_stride) +
-                (long long)h * D + 8 * l);
-      }
-      x = xn;
-      z = zn;
-    }
+    };
+    const bool norm = p.q_weight != nullptr;
+    rows(static_cast<const T*>(p.q) + t * p.q_stride, static_cast<const T*>(p.dq_out) + t * p.Hq * D,
+         static_cast<T*>(p.dq) + t * p.dq_stride, p.Hq, 0, p.sets_q, norm ? p.q_weight : nullptr, dwq);
+    rows(static_cast<const T*>(p.k) + t * p.k_stride, static_cast<const T*>(p.dk_out) + t * p.Hkv * D,
+         static_cast<T*>(p.dk) + t * p.dk_stride, p.Hkv, p.sets_q, p.sets_k, norm ? p.k_weight : nullptr, dwk);
   }
   if (p.q_weight) {
     // the warp's row groups, then the block's warps, in a fixed order
@@ -460,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a, b;
-        f2split(dw[k][i], a, b);
+        f2split(k ? dwk[i] : dwq[i], a, b);
 #pragma unroll
         for (int o = LPR; o < 32; o <<= 1) {
           a += __shfl_xor_sync(0xffffffffu, a, o);
