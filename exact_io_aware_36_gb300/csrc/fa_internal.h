@@ -157,8 +157,10 @@ struct NormRopeParams {
 
 // Blocks of the gradient kernel: four per SM of GB300 (152).
 constexpr int kNormRopeBwdBlocks = 4 * 152;
-// Warps that a large batch is cut into: two rounds of what 152 SMs hold.
-constexpr int kNormRopeWarps = 2 * 152 * 48;
+// Warps that a large batch is cut into at least: what 152 SMs hold.  More sets
+// per warp share a token's angles (7900 tokens of 48 heads: 54 us with three
+// times as many warps, 47 with these).
+constexpr int kNormRopeWarps = 152 * 32;
 
 // Page copies (fa_cache.cu).
 struct CachePagesCopy {

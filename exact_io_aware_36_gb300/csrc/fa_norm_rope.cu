@@ -15,13 +15,15 @@
 // Bound by HBM: a row is read and written once (two are read in the backward).
 // A lane holds 8 consecutive elements (16 bytes of bf16), so d / 8 lanes share
 // a row and a warp holds a set of 32 * 8 / d rows of one kind (query, key or
-// value heads) of one token.  A warp takes several sets of its token, two at
-// a time and the next two in flight, so that a token's angles, multiplied by
-// the weights, are made once:
+// value heads) of one token.  A warp takes several sets of its token, a few
+// loaded at a time, so that a token's angles, multiplied by the weights, are
+// made once:
 //     z = r (x (w c) + x' (w' s)),   x', w': the pair's other member.
-// With these packed in float32 pairs a set of bf16 rows costs some 70
-// instructions (105 in the backward), which leaves the issue slots half idle
-// at HBM's rate; the first form, at about 400 a set of two, was bound by them.
+// With these packed in float32 pairs a set costs some 120 instructions (160 in
+// the backward), which leaves the issue slots half idle at HBM's rate; the
+// first form, at twice as many, was bound by them.  One GB300, 16384 tokens of
+// 32 + 8 heads of 128 in bf16: 59 us, 85 % of the measured copy rate; backward
+// 102 us, 73 %.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,6 +39,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+// Sets loaded before the first is used, and the blocks per SM that leaves room
+// for (registers).  Both cover HBM's latency: 16384 tokens of 32 + 8 heads of
+// 128 took 67 us with two bf16 sets ahead and 59 with four (six with three
+// blocks: 61), the gradient 114 and 102; float32 sets are twice as large, and
+// with four of them the registers spilled.
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+constexpr int kBlocksPerSm = sizeof(T) == 2 ? 4 : 3;
 // 8 consecutive elements of a row as stored; as 4 float32 pairs; swapped within
 // their pairs; and another lane's.
 template <typename T>
@@ -46,12 +57,12 @@ template <>
 struct Vec8<__nv_bfloat16> {
   uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   }
   __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
   }
   __device__ __forceinline__ uint64_t pair(int i) const {
     return f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
@@ -76,7 +87,7 @@ template <>
 struct Vec8<float> {
   float w[8];
   __device__ __forceinline__ void load(const float* p) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
@@ -270,7 +281,7 @@ __device__ __forceinline__ Heads heads_of(const Unit& u, int from, int n, int su
 }
 
 template <int D, typename T, bool PAGES>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;                // rows per set
   const int lane = threadIdx.x & 31;
@@ -294,8 +305,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
   const bool on = 8 * l < p.rot;
   const int ml = mate_lane(p, l), src_lane = sub * LPR + ml;
 
-  // H heads at src and dst (this token's), sets [from, from + n): two sets a
-  // turn, both loaded before either is used.
+  // H heads at src and dst (this token's), sets [from, from + n)
   auto rows = [&](const T* src, T* dst, int H, int from, int n, const float* weight) {
     const Heads hd = heads_of<RPS>(u, from, n, sub);
     if (hd.sets == 0) return;
@@ -334,18 +344,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
       if (live) z.store(at);
     };
     int left = left0;
-    for (int k = 0; k < hd.sets; k += 2) {
-      Vec8<T> x, y;
-      const bool live0 = left > 0, live1 = k + 1 < hd.sets && left > RPS;
-      if (live0) x.load(src);
-      else x.zero();
-      if (live1) y.load(src + RPS * D);
-      else y.zero();
-      one(x, dst, live0);
-      if (k + 1 < hd.sets) one(y, dst + RPS * D, live1);
-      src += 2 * RPS * D;
-      dst += 2 * RPS * D;
-      left -= 2 * RPS;
+    for (int k = 0; k < hd.sets; k += kAhead<T>) {
+      Vec8<T> x[kAhead<T>];
+#pragma unroll
+      for (int i = 0; i < kAhead<T>; ++i) {
+        if (k + i < hd.sets && left > i * RPS) x[i].load(src + i * RPS * D);
+        else x[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead<T>; ++i) {
+        if (k + i >= hd.sets) break;
+        one(x[i], dst + i * RPS * D, left > i * RPS);
+      }
+      src += kAhead<T> * RPS * D;
+      dst += kAhead<T> * RPS * D;
+      left -= kAhead<T> * RPS;
     }
   };
   const bool norm = p.q_weight != nullptr;
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
 // (float32 [blocks][2][D]) and norm_rope_dw_kernel adds the blocks up, both in
 // a fixed order, so the result is the same from run to run.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;
   __shared__ float red[kWarps][2][D];
@@ -444,27 +457,26 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeP
         }
       };
       int left = H - hd.h;                     // the lane's heads: every RPS-th
-      for (int k = 0; k < hd.sets; k += 2) {
-        Vec8<T> x0, z0, x1, z1;
-        const bool live0 = left > 0, live1 = k + 1 < hd.sets && left > RPS;
-        x0.zero();
-        z0.zero();
-        x1.zero();
-        z1.zero();
-        if (live0) {
-          x0.load(x_at);
-          z0.load(z_at);
+      for (int k = 0; k < hd.sets; k += kAhead<T>) {
+        Vec8<T> x[kAhead<T>], z[kAhead<T>];
+#pragma unroll
+        for (int i = 0; i < kAhead<T>; ++i) {
+          x[i].zero();
+          z[i].zero();
+          if (k + i < hd.sets && left > i * RPS) {
+            x[i].load(x_at + i * RPS * D);
+            z[i].load(z_at + i * RPS * D);
+          }
         }
-        if (live1) {
-          x1.load(x_at + RPS * D);
-          z1.load(z_at + RPS * D);
+#pragma unroll
+        for (int i = 0; i < kAhead<T>; ++i) {
+          if (k + i >= hd.sets) break;
+          one(x[i], z[i], d_at + i * RPS * D, left > i * RPS);
         }
-        one(x0, z0, d_at, live0);
-        if (k + 1 < hd.sets) one(x1, z1, d_at + RPS * D, live1);
-        x_at += 2 * RPS * D;
-        z_at += 2 * RPS * D;
-        d_at += 2 * RPS * D;
-        left -= 2 * RPS;
+        x_at += kAhead<T> * RPS * D;
+        z_at += kAhead<T> * RPS * D;
+        d_at += kAhead<T> * RPS * D;
+        left -= kAhead<T> * RPS;
       }
     };
     const bool norm = p.q_weight != nullptr;
