@@ -469,6 +469,17 @@ def attention_forward_fp8(q, k, v, signs, *, causal: bool, scale: Optional[float
 # before them here is kept lean: devices are compared by index, shapes as
 # tuples, and a message is made only for a call that is refused.
 
+_torch = None
+
+
+def _import_torch():
+    """torch, imported by the first call that needs it."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _refuse(name, t, dtype, index, shape, contiguous=True):
     if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
@@ -512,16 +523,16 @@ def _gpu(t, stream):
 
 def _empty(like, shape, stream, dtype=None):
     """An uninitialised tensor on `like`'s GPU that belongs to `stream` (None: the current one)."""
+    torch = _torch or _import_torch()
     if stream is None:
-        return like.new_empty(shape, dtype=dtype or like.dtype)
-    import torch
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype or like.dtype)
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _run(what, index, stream, check, *args):
     """The library's `what`(*args, stream) with GPU `index` current; raises on a status that is not FA_OK."""
-    import torch
+    torch = _torch or _import_torch()
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _run(what, index, stream, check, *args)
@@ -536,8 +547,7 @@ def _run(what, index, stream, check, *args):
 
 def _angles(q_weight, k_weight, cos, sin, d, index):
     """Pointers of the weights and of the angles, rot_dim and max_pos."""
-    import torch
-    f32 = torch.float32
+    f32 = (_torch or _import_torch()).float32
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     if (cos is None) != (sin is None):
@@ -567,7 +577,7 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos=N
     goes to ``attention_forward`` and ``attention_backward``'s dq, dk to
     ``qk_norm_rope_backward``.
     """
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(q, stream)
     qp, qs = _rows("q", q, q.dtype, index)
     kp, ks = _rows("k", k, q.dtype, index)
@@ -603,7 +613,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
     q and k.  Returns (dq, dk, dq_weight, dk_weight); the weights' gradients are
     float32 [d], or None without norm.  Results do not vary from run to run.
     """
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(q, stream)
     qp, qs = _rows("q", q, q.dtype, index)
     kp, ks = _rows("k", k, q.dtype, index)
@@ -640,7 +650,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
 
 def _pages(k_pages, v_pages, index):
     """(k pointer, v pointer, num_pages, page_size, Hkv, d) of the two pools."""
-    import torch
+    torch = _torch or _import_torch()
     if k_pages.dim() != 4:
         raise ValueError("k_pages: [num_pages, page_size, Hkv, d] expected")
     kp = _checked("k_pages", k_pages, torch.bfloat16, index)
@@ -650,7 +660,7 @@ def _pages(k_pages, v_pages, index):
 
 def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index):
     """(table, cache_seqlens, cu_seqlens pointers, B, N, max_pages)."""
-    import torch
+    torch = _torch or _import_torch()
     if block_table.dim() != 2:
         raise ValueError("block_table: [B, max_pages] expected")
     B, max_pages = block_table.shape
@@ -675,7 +685,7 @@ def cache_append(k, v, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqle
     are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1], with
     ``max_seqlen`` their largest number), or T / B each without it.
     """
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(k, stream)
     kp, ks = _rows("k", k, torch.bfloat16, index)
     vp, vs = _rows("v", v, torch.bfloat16, index, k.shape)
@@ -696,7 +706,7 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, cache_seqlens, *
     one launch (``fa_qk_norm_rope_append``).  A token's position is its place
     in its sequence's cache.  Returns q_out [T, Hq, d], ready for
     ``attention_forward_paged`` over the same pages."""
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(q, stream)
     qp, qs = _rows("q", q, torch.bfloat16, index)
     kp, ks = _rows("k", k, torch.bfloat16, index)
@@ -721,7 +731,7 @@ def cache_copy(k_pages, v_pages, src, dst, *, stream=None, check: bool = False):
     """Copy pages src[i] to dst[i] (int32 [n], on the GPU) of both pools through
     ``fa_cache_copy``: the fork of a sequence's last page, a compaction's moves.
     The copies run in no order; see include/fa.h on pairs that clash."""
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(k_pages, stream)
     kpool, vpool, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages, index)
     n = src.numel()
@@ -744,7 +754,7 @@ def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, 
     (o [T, Hq, d] of ``out_dtype`` (default: ``out``'s dtype, else q's), lse
     float32 [Hq, T]).
     """
-    import torch
+    torch = _torch or _import_torch()
     index = _gpu(q, stream)
     if q.dim() != 3:
         raise ValueError("q: [T, Hq, d] expected")
