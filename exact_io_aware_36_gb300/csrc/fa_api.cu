@@ -765,7 +765,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   if (T == 0 || B == 0 || N == 0) return FA_OK;
   if (num_pages == 0) return FA_ERR_SHAPE;
   if (!q || !k_pages || !v_pages || !block_table || !cache_seqlens || !o || !lse) return FA_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_ALIGN;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(o) & 31u) != 0) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_ALIGN;
   if (!workspace || workspace_bytes < fa_fwd_paged_workspace_size(Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;

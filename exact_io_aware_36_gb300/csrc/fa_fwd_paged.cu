@@ -376,29 +376,23 @@ __device__ __forceinline__ void rescale_row(uint32_t tO, float alpha) {
   }
 }
 
-// 16 columns of a finished row, or of a part (float32, not divided).  A warp's
-// rows lie apart, so each store of it touches 32 lines whatever its width:
-// `wide` (32-byte aligned rows) halves the stores.
-__device__ __forceinline__ void store32(void* at, const uint32_t* v, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(at), FA_W8(v, 0) : "memory");
-  } else {
-    reinterpret_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
+// 16 columns of a row, as float32 or bf16, `at` 32-byte aligned.  A warp's rows
+// lie apart, so each store of it touches 32 lines whatever its width.
+__device__ __forceinline__ void store32(void* at, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" :: "l"(at), FA_W8(v, 0) : "memory");
 }
 
-__device__ __forceinline__ void store_row16(const float* v, bool f32, bool wide, void* base, long long at) {
+__device__ __forceinline__ void store_row16(const float* v, bool f32, char* at) {
   uint32_t w[16];
   if (f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
-    store32(static_cast<float*>(base) + at, w, wide);
-    store32(static_cast<float*>(base) + at + 8, w + 8, wide);
+    store32(at, w);
+    store32(at + 32, w + 8);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    store32(static_cast<__nv_bfloat16*>(base) + at, w, wide);
+    store32(at, w);
   }
 }
 
@@ -1086,7 +1080,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const long long orow = tok * p.Hq + head;
       const int slot = 2 * (int)blockIdx.x + part - 1;
       const long long prow = (long long)slot * p.part_rows + tl * p.group + rh;
-      const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+      const bool f32 = part || p.o_f32;                 // a part is float32, not divided
+      char* out = part ? reinterpret_cast<char*>(p.part_o + prow * D)
+                       : static_cast<char*>(p.o) + orow * D * (f32 ? 4 : 2);
       float sc = 1.f;
       if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
       if (warp_rows) {
@@ -1105,10 +1101,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (use1) v[i] = fmaf(__uint_as_float(b[i]), w1, v[i]);
             v[i] *= sc;
           }
-          if (valid) {
-            if (part) store_row16(v, true, true, p.part_o, prow * D + c);
-            else store_row16(v, p.o_f32, wide, p.o, orow * D + c);
-          }
+          if (valid) store_row16(v, f32, out + c * (f32 ? 4 : 2));
         }
       }
       tc_fence_before();

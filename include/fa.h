@@ -459,8 +459,9 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
  * do not vary from run to run.
  *   q             bf16 [T, Hq, d], contiguous; rows of b as in fa_cache_append
  *                 (cu_seqlens, N = the largest n_b, total_tokens)
- *   o, lse        [T, Hq, d] of o_dtype (FA_FP32 or FA_BF16), float32 [Hq, T]
- *                 (natural log); rows behind the last sequence are left alone
+ *   o, lse        [T, Hq, d] of o_dtype (FA_FP32 or FA_BF16), 32-byte aligned,
+ *                 and float32 [Hq, T] (natural log); rows behind the last
+ *                 sequence are left alone
  *   Hq / Hkv      <= 128;  B <= 8192
  *   workspace     device, >= fa_fwd_paged_workspace_size bytes, 256-byte
  *                 aligned, contents irrelevant on entry; calls that may overlap

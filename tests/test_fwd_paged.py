@@ -34,7 +34,7 @@ def call(**kw):
     (dict(d=96), 3), (dict(P=24), 3), (dict(P=8), 3), (dict(Hq=258, Hkv=2), 3), (dict(B=8193), 3), (dict(scale=0.0), 3),
     (dict(scale=float("inf")), 3), (dict(causal=2), 3), (dict(causal=0, window=5), 3), (dict(causal=0, alibi=A_), 3),
     (dict(odt=5), 3), (dict(np=1 << 27), 3), (dict(q=None), 1), (dict(bt=None), 1), (dict(cs=None), 1), (dict(lse=None), 1),
-    (dict(q=A_ + 8), 4), (dict(o=A_ + 4), 4), (dict(lse=A_ + 2), 4), (dict(ws=A_ + 16), 4), (dict(ws=None), 5),
+    (dict(q=A_ + 8), 4), (dict(o=A_ + 4), 4), (dict(o=A_ + 16), 4), (dict(lse=A_ + 2), 4), (dict(ws=A_ + 16), 4), (dict(ws=None), 5),
     (dict(wsb=1000), 5), (dict(B=0), 0), (dict(N=0), 0), (dict(cu=A_, T=0), 0)])
 def test_refuses_before_launch(kw, code):
     assert call(**kw) == code
