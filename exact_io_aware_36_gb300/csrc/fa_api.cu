@@ -819,7 +819,8 @@ fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const 
                         int n, int num_pages, int page_size, int Hkv, int d, void* stream) {
   if (n < 0 || Hkv <= 0 || d <= 0) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  if (Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  // every block looks through all n pairs
+  if (Hkv > 65535 || n > fa::kCopyMaxPairs) return FA_ERR_UNSUPPORTED;
   fa::NormRopeParams sizes = {};
   const fa_status st = page_args(&sizes, 0, 0, page_size, num_pages, 0);
   if (st != FA_OK) return st;

@@ -163,6 +163,7 @@ constexpr int kNormRopeBwdBlocks = 4 * 152;
 constexpr int kNormRopeWarps = 152 * 32;
 
 // Page copies (fa_cache.cu).
+constexpr int kCopyMaxPairs = 1 << 17;
 struct CachePagesCopy {
   void* k;
   void* v;

@@ -406,7 +406,8 @@ fa_status fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
  * 128).  Sequence b holds L_b = cache_seqlens[b] tokens; its token j is slot
  * j % page_size of page block_table[b * max_pages + j / page_size]
  * (block_table: device int32 [B, max_pages]).  Entries of the table behind a
- * sequence's last page are not read.  Several sequences may share pages.
+ * sequence's last page are not read.  Several sequences may share pages (but
+ * not the slots that a call writes).
  *
  * fa_cache_append writes the new tokens' keys and values: sequence b brings n_b
  * tokens, the last n_b of its L_b (cache_seqlens counts them already).
@@ -488,7 +489,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
  * the moves of a compaction.  The copies run in no order: a pair whose dst is
  * another pair's src or dst, or whose src is another pair's dst (pairs with
  * src == dst, which do nothing, aside), is not copied and sets FA_ERR_PAGE, and so
- * is a pair with a page outside the pool; the other pairs are copied.
+ * is a pair with a page outside the pool; the other pairs are copied.  Every
+ * pair is compared with every other, so n is at most 131072.
  */
 fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
                         int n, int num_pages, int page_size, int Hkv, int d, void* stream);

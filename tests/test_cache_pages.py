@@ -48,7 +48,7 @@ def test_norm_rope_append_refuses(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [(dict(n=-1), 2), (dict(H=0), 2), (dict(np=-1), 2), (dict(P=24), 3), (dict(d=96), 3),
-                                     (dict(k=None), 1), (dict(s=None), 1), (dict(v=A + 4), 4), (dict(n=0, k=None), 0)])
+                                     (dict(n=131073), 3), (dict(k=None), 1), (dict(s=None), 1), (dict(v=A + 4), 4), (dict(n=0, k=None), 0)])
 def test_copy_refuses(kw, code):
     a = dict(k=A, v=A, s=A, d_=A, n=3, np=8, P=16, H=2, d=128)
     a.update(kw)
