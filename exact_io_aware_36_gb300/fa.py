@@ -521,13 +521,16 @@ def _gpu(t, stream):
     return index
 
 
-def _empty(like, shape, stream, dtype=None):
-    """An uninitialised tensor on `like`'s GPU that belongs to `stream` (None: the current one)."""
-    torch = _torch or _import_torch()
+def _out(name, t, like, shape, dtype, index, stream):
+    """(tensor, pointer) of an output: the one given, checked, or a new one that belongs to `stream` (None: the current one)."""
+    if t is not None:
+        return t, _checked(name, t, dtype, index, shape)
     if stream is None:
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+        t = _torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        with _torch.cuda.stream(stream):
+            t = _torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
 
 
 def _run(what, index, stream, check, *args):
@@ -591,13 +594,9 @@ def qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos=N
         if positions is None:
             raise ValueError("positions are required with cos and sin")
         pos = _checked("positions", positions, torch.int32, index, (T,))
-    if q_out is None:
-        q_out = _empty(q, (T, Hq, d), stream)
-    if k_out is None:
-        k_out = _empty(q, (T, Hkv, d), stream)
-    _run("fa_qk_norm_rope", index, stream, check, qp, kp,
-         _checked("q_out", q_out, q.dtype, index, (T, Hq, d)),
-         _checked("k_out", k_out, q.dtype, index, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
+    q_out, qop = _out("q_out", q_out, q, (T, Hq, d), q.dtype, index, stream)
+    k_out, kop = _out("k_out", k_out, q, (T, Hkv, d), q.dtype, index, stream)
+    _run("fa_qk_norm_rope", index, stream, check, qp, kp, qop, kop, qs, ks, ang[0], ang[1], float(eps),
          ang[2], ang[3], pos, T, Hq, Hkv, d, ang[4], ang[5], interleaved, _dtype_code(q.dtype))
     return q_out, k_out
 
@@ -628,24 +627,26 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None,
             raise ValueError("positions are required with cos and sin")
         pos = _checked("positions", positions, torch.int32, index, (T,))
     if dq is None:
-        dq = _empty(q, (T, Hq, d), stream)
+        dqs, (dq, dqp) = Hq * d, _out("dq", None, q, (T, Hq, d), q.dtype, index, stream)
+    else:
+        dqp, dqs = _rows("dq", dq, q.dtype, index, (T, Hq, d))
     if dk is None:
-        dk = _empty(q, (T, Hkv, d), stream)
-    dqp, dqs = _rows("dq", dq, q.dtype, index, (T, Hq, d))
-    dkp, dks = _rows("dk", dk, q.dtype, index, (T, Hkv, d))
-    dw = (None, None)
+        dks, (dk, dkp) = Hkv * d, _out("dk", None, q, (T, Hkv, d), q.dtype, index, stream)
+    else:
+        dkp, dks = _rows("dk", dk, q.dtype, index, (T, Hkv, d))
+    dqw = dkw = dqwp = dkwp = wp = None
+    wbytes = 0
     if q_weight is not None:
-        dw = _empty(q, (2, d), stream, torch.float32).unbind()
-        if workspace is None:
-            workspace = _empty(q, (fa_qk_norm_rope_bwd_workspace_size(d),), stream, torch.uint8)
-        _checked("workspace", workspace, torch.uint8, index)
+        dqw, dqwp = _out("", None, q, (d,), torch.float32, index, stream)
+        dkw, dkwp = _out("", None, q, (d,), torch.float32, index, stream)
+        wbytes = fa_qk_norm_rope_bwd_workspace_size(d) if workspace is None else workspace.numel()
+        workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
     _run("fa_qk_norm_rope_bwd", index, stream, check, qp, kp,
          _checked("dq_out", dq_out, q.dtype, index, (T, Hq, d)),
          _checked("dk_out", dk_out, q.dtype, index, (T, Hkv, d)), qs, ks, ang[0], ang[1], float(eps),
-         ang[2], ang[3], pos, dqp, dkp, dqs, dks, _ptr(dw[0]), _ptr(dw[1]), T, Hq, Hkv, d, ang[4],
-         ang[5], interleaved, _dtype_code(q.dtype), _ptr(workspace),
-         workspace.numel() if workspace is not None else 0)
-    return dq, dk, dw[0], dw[1]
+         ang[2], ang[3], pos, dqp, dkp, dqs, dks, dqwp, dkwp, T, Hq, Hkv, d, ang[4], ang[5],
+         interleaved, _dtype_code(q.dtype), wp, wbytes)
+    return dq, dk, dqw, dkw
 
 
 def _pages(k_pages, v_pages, index):
@@ -718,10 +719,8 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, cache_seqlens, *
         raise ValueError("q, k and the pages must have the same tokens, key heads and head dimension")
     tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
     ang = _angles(q_weight, k_weight, cos, sin, d, index)
-    if q_out is None:
-        q_out = _empty(q, (T, Hq, d), stream)
-    _run("fa_qk_norm_rope_append", index, stream, check, qp, kp, vp,
-         _checked("q_out", q_out, q.dtype, index, (T, Hq, d)), kpool, vpool, qs, ks, vs, ang[0],
+    q_out, qop = _out("q_out", q_out, q, (T, Hq, d), q.dtype, index, stream)
+    _run("fa_qk_norm_rope_append", index, stream, check, qp, kp, vp, qop, kpool, vpool, qs, ks, vs, ang[0],
          ang[1], float(eps), ang[2], ang[3], tp, cp, cup, B, Hq, Hkv, N, d, T, ang[4], ang[5],
          interleaved, page_size, num_pages, max_pages)
     return q_out
@@ -765,16 +764,11 @@ def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, 
         raise ValueError("q and the pages must have the same head dimension")
     tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
     slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, index, (Hq,))
-    if out is None:
-        out = _empty(q, (T, Hq, d), stream, out_dtype)
-    if lse is None:
-        lse = _empty(q, (Hq, T), stream, torch.float32)
-    need = fa_fwd_paged_workspace_size(Hq, Hkv, N, d)
-    if workspace is None:
-        workspace = _empty(q, (max(need, 1),), stream, torch.uint8)
-    _run("fa_fwd_paged", index, stream, check, qp, kpool, vpool, tp, cp, cup,
-         _checked("out", out, out.dtype, index, (T, Hq, d)), _checked("lse", lse, torch.float32, index, (Hq, T)),
-         B, Hq, Hkv, N, d, T, page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale),
-         causal, -1 if window is None else window, slopes, _dtype_code(out.dtype),
-         _checked("workspace", workspace, torch.uint8, index), workspace.numel())
+    out, op = _out("out", out, q, (T, Hq, d), (out_dtype or q.dtype) if out is None else out.dtype, index, stream)
+    lse, lp = _out("lse", lse, q, (Hq, T), torch.float32, index, stream)
+    wbytes = fa_fwd_paged_workspace_size(Hq, Hkv, N, d) if workspace is None else workspace.numel()
+    workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
+    _run("fa_fwd_paged", index, stream, check, qp, kpool, vpool, tp, cp, cup, op, lp, B, Hq, Hkv, N, d, T,
+         page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale), causal,
+         -1 if window is None else window, slopes, _dtype_code(out.dtype), wp, wbytes)
     return out, lse
