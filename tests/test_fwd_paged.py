@@ -112,7 +112,7 @@ def check(out, q, kp, vp, table, lens, cu, page, causal=True, window=None, slope
     e = (d + 8) * 2.0 ** -23 * qn * kn * scale + 2.0 ** -21 * (np.where(seen, np.abs(lref), 0) + 8)
     got = npf(lse).T[:live]
     assert (got[~seen] == -np.inf).all()
-    el = np.abs(got - lref)[seen] - (2 * e + 2.0 ** -22 * np.abs(lref))[seen]
+    el = np.abs(got[seen] - lref[seen]) - (2 * e[seen] + 2.0 ** -22 * np.abs(lref[seen]))
     assert el.size == 0 or el.max() <= 0, float(el.max())
     pp = np.where(two, 2.0 ** -7, 2.0 ** -15)[:live, None, None]
     u = 2.0 ** -8 if O.dtype == t.bfloat16 else 2.0 ** -24
@@ -184,7 +184,57 @@ def test_peaked_scores(gain, new, lens):
 
 
 @pytest.mark.gpu
-def test_rows_behind_the_last_sequence_and_other_strides_of_time():
+@pytest.mark.parametrize("seed", range(12))
+def test_random_mixes(seed):
+    """Sequences that bring nothing, one token, a few or a chunk, in one call, over any cut of the work."""
+    import torch as t
+    g = np.random.default_rng(seed)
+    Hkv = int(g.choice([1, 2, 3, 8]))
+    Hq, d, page = Hkv * int(g.choice([1, 2, 3, 4, 7, 16])), int(g.choice([64, 128])), int(g.choice([16, 32, 128, 256]))
+    B = int(g.integers(1, 24))
+    new = [int(g.choice([0, 1, 1, 1, int(g.integers(2, 40)), int(g.integers(40, 400))])) for _ in range(B)]
+    new[0] = max(new[0], 1)
+    lens = [n + int(g.choice([0, 1, int(g.integers(0, 300)), int(g.integers(0, 2500))])) for n in new]
+    window = int(g.integers(0, 1500)) if seed % 3 == 0 else None
+    slopes = t.tensor(2.0 ** (-8 * (np.arange(Hq) + 1) / Hq), dtype=t.float32, device="cuda") if seed % 4 == 1 else None
+    q, kp, vp, table, cs, cu = state(new, lens, page, Hq, Hkv, d, seed, window=window, gain=float(g.choice([1.0, 4.0])))
+    out = fa.attention_forward_paged(q, kp, vp, table, cs, cu_seqlens=cu, max_seqlen=max(new) + seed % 2, window=window,
+                                     alibi_slopes=slopes, out_dtype=t.float32, check=True)
+    check(out, q, kp, vp, table, lens, cu, page, window=window, slopes=slopes)
+
+
+@pytest.mark.gpu
+def test_thousands_of_sequences():
+    """More sequences than the block that plans has threads, most of them idle."""
+    import torch as t
+    new = [1 if b % 7 == 3 else 0 for b in range(5000)]
+    lens = [1 + (11 * b) % 97 if n else 0 for b, n in enumerate(new)]
+    q, kp, vp, table, cs, cu = state(new, lens, 16, 2, 1, 64, 1)
+    out = fa.attention_forward_paged(q, kp, vp, table, cs, cu_seqlens=cu, max_seqlen=1, out_dtype=t.float32, check=True)
+    check(out, q, kp, vp, table, lens, cu, 16)
+
+
+@pytest.mark.gpu
+def test_pools_past_32_bits():
+    """Pages whose elements lie past 2^31 in the pool give what the same pages give in a small one."""
+    import torch as t
+    page, Hkv, d = 256, 8, 128
+    pages = (1 << 31) // (page * Hkv * d) + 4
+    lens, new = [700, 300], [1, 70]
+    q, kp, vp, table, cs, cu = state(new, lens, page, 16, Hkv, d, 2)
+    kp.nan_to_num_()
+    vp.nan_to_num_()
+    big = [t.empty(pages, page, Hkv, d, dtype=t.bfloat16, device="cuda") for _ in range(2)]
+    n = kp.shape[0]
+    big[0][-n:], big[1][-n:] = kp, vp
+    kw = dict(cu_seqlens=cu, max_seqlen=70, check=True)
+    want = fa.attention_forward_paged(q, kp, vp, table, cs, **kw)
+    got = fa.attention_forward_paged(q, *big, t.where(table < 0, table, table + pages - n), cs, **kw)
+    assert all(t.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.gpu
+def test_rows_behind_the_last_sequence_and_repeats():
     """A padded batch: rows from cu[B] on are left as they were; the same call twice gives the same bits."""
     import torch as t
     new, lens = [1, 40, 1], [2500, 100, 60]
