@@ -798,8 +798,6 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   const int blocks = (N + 2 * p.tpt - 1) / (2 * p.tpt);
   p.plan_lanes = 1;
   while (p.plan_lanes < 32 && p.plan_lanes < blocks) p.plan_lanes *= 2;
-  // one warp is done sooner than the block's barriers for up to kPagedSoloBlocks
-  p.plan_solo = (long long)B * blocks <= fa::kPagedSoloBlocks;
   p.page_size = page_size;
   p.page_shift = sizes.page_shift;
   p.num_pages = num_pages;

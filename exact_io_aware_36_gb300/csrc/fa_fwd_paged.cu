@@ -247,21 +247,14 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
   return false;
 }
 
-// Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  By one
-// warp (SOLO: small batches; no barrier, and the other roles set up meanwhile)
-// or by the whole block; `pre` holds B 64-bit words of shared memory.
-template <bool SOLO>
+// Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
+// threads; `pre` holds B 64-bit words of shared memory.
 __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre, unsigned min_run) {
-  constexpr int NT = SOLO ? 32 : kThreads;
-  const int lane = threadIdx.x & 31, tid = SOLO ? lane : threadIdx.x, warp = SOLO ? 0 : threadIdx.x >> 5;
-  auto sync = [] {
-    if (SOLO) __syncwarp();
-    else __syncthreads();
-  };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // 1. every sequence's weight, nl lanes per sequence
   const int nl = p.plan_lanes;
   const int sub = lane & (nl - 1);
-  for (int b0 = 0; b0 < p.B; b0 += NT / nl) {
+  for (int b0 = 0; b0 < p.B; b0 += kThreads / nl) {
     const int b = b0 + tid / nl;
     long long wsum = 0;
     if (b < p.B) {
@@ -272,9 +265,9 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     for (int o = nl / 2; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
     if (b < p.B && sub == 0) pre[b] = (unsigned long long)wsum;      // of one kv head
   }
-  sync();
+  __syncthreads();
   // 2. exclusive prefix sums: each thread a run of sequences
-  const int per = (p.B + NT - 1) / NT;
+  const int per = (p.B + kThreads - 1) / kThreads;
   const int f = min(tid * per, p.B), e = min(f + per, p.B);
   unsigned long long own = 0;
   for (int b = f; b < e; ++b) own += pre[b] * p.Hkv;
@@ -285,9 +278,9 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     if (lane >= o) inc += x;
   }
   if (lane == 31) bars->warp_sum[warp] = inc;
-  sync();
+  __syncthreads();
   unsigned long long before = 0, total = 0;
-  for (int w = 0; w < NT / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += bars->warp_sum[w];
     total += bars->warp_sum[w];
   }
@@ -308,7 +301,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     bars->base = w1;             // an empty run
     bars->b = bars->g = bars->qb = 0;
   }
-  sync();
+  __syncthreads();
   if (w0 < w1) {
     unsigned long long at = before;
     for (int b = f; b < e; ++b) {
@@ -320,7 +313,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
       at += x;
     }
   }
-  sync();
+  __syncthreads();
   // 4. the kv head and the q block
   if (warp == 0 && w0 < w1) {
     const int b = bars->b;
@@ -358,7 +351,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
       bars->base = base;
     }
   }
-  sync();
+  __syncthreads();
 }
 
 // O row (D columns at tO) *= alpha, in TMEM.  Warp-collective.
@@ -445,11 +438,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int box = i / ((128 - rows_box) * 8), j = i % ((128 - rows_box) * 8);
     reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
   }
-  unsigned long long* pre = reinterpret_cast<unsigned long long*>(smem + C::K_OFF);
-  if (!p.plan_solo) {
-    __syncthreads();
-    make_plan<false>(ps, bars, pre, ONE ? kMinRunOne : kMinRunTwo);
-  }
+  __syncthreads();
+  make_plan(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -785,11 +775,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // -------------------------------------------------------------- walker
     Walk w;
     Seg s;
-    if (p.plan_solo) {
-      make_plan<true>(ps, bars, pre, ONE ? kMinRunOne : kMinRunTwo);
-      fence_proxy_async_smem();                         // the loads come into this memory
-      __syncwarp();
-    }
     walk_begin(p, bars, w);
     // what the parts of this CTA are, for the merge: kind of the part that
     // goes on from the CTA before (2: the item's last), and the item begun here

@@ -196,7 +196,6 @@ struct PagedParams {
   int tpt;                     // tokens per tile of 128 rows: 128 / group
   int part_rows;               // rows of the largest item
   int plan_lanes;              // lanes that add up one sequence's work
-  int plan_solo;               // one warp plans (small batches), else the block
   int page_size, page_shift, num_pages, max_pages;
   int causal, window, o_f32;   // window: kNoWindow when unbanded
   float scale, scale_log2;
@@ -205,7 +204,6 @@ struct PagedParams {
 // CTAs of the paged forward: GB300's SMs; each leaves at most two parts.
 constexpr int kPagedCtas = 152;
 constexpr int kPagedMaxBatch = 8192;
-constexpr int kPagedSoloBlocks = 256;     // q blocks (of all sequences) that one warp plans
 
 // The host-side argument checks of fa_bwd (everything but the workspace), in
 // fa_bwd's order.  On FA_OK, *T is the total token count, or 0 when the call
