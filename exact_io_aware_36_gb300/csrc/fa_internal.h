@@ -155,8 +155,8 @@ struct NormRopeParams {
   int B, N, page_size, page_shift, num_pages, max_pages;
 };
 
-// Blocks of the gradient kernel: four per SM of GB300 (152).
-constexpr int kNormRopeBwdBlocks = 4 * 152;
+// Blocks of the gradient kernel: two per SM of GB300 (152).
+constexpr int kNormRopeBwdBlocks = 2 * 152;
 // Warps that a large batch is cut into at least: what 152 SMs hold.  More sets
 // per warp share a token's angles (7900 tokens of 48 heads: 54 us with three
 // times as many warps, 47 with these).

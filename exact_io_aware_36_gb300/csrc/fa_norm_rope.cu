@@ -19,11 +19,11 @@
 // loaded at a time, so that a token's angles, multiplied by the weights, are
 // made once:
 //     z = r (x (w c) + x' (w' s)),   x', w': the pair's other member.
-// With these packed in float32 pairs a set costs some 120 instructions (160 in
-// the backward), which leaves the issue slots half idle at HBM's rate; the
-// first form, at twice as many, was bound by them.  One GB300, 16384 tokens of
-// 32 + 8 heads of 128 in bf16: 59 us, 85 % of the measured copy rate; backward
-// 102 us, 73 %.
+// With these packed in float32 pairs a set costs some 120 instructions (170 in
+// the backward), which leaves issue slots idle at HBM's rate; the first form,
+// at twice as many, was bound by them.  One GB300, 16384 tokens of 32 + 8 heads
+// of 128 in bf16: 58.7 us, 5.75 TB/s, 85 % of the measured copy rate; backward
+// 94.4 us, 5.35 TB/s, 79 %.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,11 +39,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Sets loaded before the first is used, and the blocks per SM that leaves room
-// for (registers).  Both cover HBM's latency: 16384 tokens of 32 + 8 heads of
-// 128 took 67 us with two bf16 sets ahead and 59 with four (six with three
-// blocks: 61), the gradient 114 and 102; float32 sets are twice as large, and
-// with four of them the registers spilled.
+// Sets that the forward loads before it uses the first, and the blocks per SM
+// that leaves room for (registers).  Both cover HBM's latency: 16384 tokens of
+// 32 + 8 heads of 128 took 67 us with two bf16 sets ahead, 59 with four, 61 with
+// six and three blocks; float32 sets are twice as large (four: 7.9 us for 3001
+// tokens of 16 heads of 64, two: 6.6).
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
@@ -60,6 +60,7 @@ struct Vec8<__nv_bfloat16> {
     const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   }
+  __device__ __forceinline__ void from(const uint4* a) { w[0] = a->x; w[1] = a->y; w[2] = a->z; w[3] = a->w; }
   __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const {
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
@@ -90,6 +91,13 @@ struct Vec8<float> {
     const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+  __device__ __forceinline__ void from(const uint4* a) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[4 * i] = __uint_as_float(a[i].x); w[4 * i + 1] = __uint_as_float(a[i].y);
+      w[4 * i + 2] = __uint_as_float(a[i].z); w[4 * i + 3] = __uint_as_float(a[i].w);
+    }
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -380,43 +388,129 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>) norm_rope_kernel(co
   }
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros where `bytes`
+// is 0 (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Sets of x and of dz that a warp of the gradient has on their way.
+template <typename T>
+constexpr int kDepth = sizeof(T) == 2 ? 6 : 3;
+
+template <typename T>
+constexpr int kBwdSmem = kWarps * kDepth<T> * 2 * 32 * 8 * sizeof(T);
+
 // Gradient.  A warp walks units with a fixed stride and keeps the weights'
 // sums of its columns in registers; a block writes its sum to the workspace
 // (float32 [blocks][2][D]) and norm_rope_dw_kernel adds the blocks up, both in
 // a fixed order, so the result is the same from run to run.
+// The registers this takes leave 16 warps per SM, too few for HBM's latency
+// with loads into registers (102 us for 16384 tokens of 32 + 8 heads of 128,
+// 94 this way).  So the loads go to shared memory, kDepth sets ahead and on
+// into the warp's next units: each lane fetches the 8 elements that it will
+// itself use, so no lane waits for another.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;
+  constexpr int DEPTH = kDepth<T>;
+  constexpr int PARTS = 8 * sizeof(T) / 16;    // 16-byte pieces of a lane's elements
+  extern __shared__ uint4 ring_smem[];         // [warp][DEPTH][x, z][PARTS][lane]
   __shared__ float red[kWarps][2][D];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int l = lane & (LPR - 1), sub = lane / LPR;
   const bool on = 8 * l < p.rot;
   const int src = sub * LPR + mate_lane(p, l);
+  uint4* ring = ring_smem + warp * DEPTH * 2 * PARTS * 32 + lane;
   uint64_t dwq[4], dwk[4];                     // of the query and the key weight
 #pragma unroll
   for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = f2(0.f, 0.f);
+
+  // The set to be fetched next: this lane's place in x and dz, the heads and
+  // the sets left of its kind, whether keys follow; and its place in the ring.
+  Unit lu;
+  unsigned lunit = blockIdx.x * kWarps + warp;
+  const T *lx = nullptr, *lz = nullptr;
+  int lheads = 0, lsets = 0;
+  bool lkeys = false;
+  auto begin_kind = [&](bool keys) {
+    const int H = keys ? p.Hkv : p.Hq;
+    const Heads hd = keys ? heads_of<RPS>(lu, p.sets_q, p.sets_k, sub) : heads_of<RPS>(lu, 0, p.sets_q, sub);
+    lx = (keys ? static_cast<const T*>(p.k) + lu.t * p.k_stride : static_cast<const T*>(p.q) + lu.t * p.q_stride) + hd.h * D + 8 * l;
+    lz = (keys ? static_cast<const T*>(p.dk_out) : static_cast<const T*>(p.dq_out)) + lu.t * H * D + hd.h * D + 8 * l;
+    lheads = H - hd.h;
+    lsets = hd.sets;
+    lkeys = keys;
+  };
+  bool more = unit_at(p, lunit, lu);
+  if (more) begin_kind(false);
+  uint32_t lring = smem_u32(ring);
+  const uint32_t ring_end = lring + DEPTH * 2 * PARTS * 32 * 16;
+  auto fetch = [&] {
+    if (more) {
+      while (lsets == 0) {                     // on to the next kind or unit
+        if (!lkeys) {
+          begin_kind(true);
+        } else {
+          lunit += gridDim.x * kWarps;
+          if (!(more = unit_at(p, lunit, lu))) break;
+          begin_kind(false);
+        }
+      }
+    }
+    if (more) {
+      const uint32_t bytes = lheads > 0 ? 16 : 0;
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        copy16(lring + i * 512, lx + i * (16 / sizeof(T)), bytes);
+        copy16(lring + (PARTS + i) * 512, lz + i * (16 / sizeof(T)), bytes);
+      }
+      lx += RPS * D;
+      lz += RPS * D;
+      lheads -= RPS;
+      --lsets;
+    }
+    lring += 2 * PARTS * 512;
+    if (lring == ring_end) lring = smem_u32(ring);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < DEPTH - 1; ++i) fetch();
+
+  const uint4* oldest = ring;
+  auto take = [&](Vec8<T>& x, Vec8<T>& z) {    // the oldest set of the ring
+    fetch();
+    asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory");
+    uint4 v[2 * PARTS];
+#pragma unroll
+    for (int i = 0; i < 2 * PARTS; ++i) v[i] = oldest[i * 32];
+    x.from(v);
+    z.from(v + PARTS);
+    oldest += 2 * PARTS * 32;
+    if (oldest == ring + DEPTH * 2 * PARTS * 32) oldest = ring;
+  };
 
   Unit u;
   for (unsigned unit = blockIdx.x * kWarps + warp; unit_at(p, unit, u); unit += gridDim.x * kWarps) {
     const long long t = u.t;
     const int pos = p.rot ? __ldg(p.positions + t) : 0;
-    if (p.rot && (pos < 0 || pos >= p.max_pos)) {
-      if (lane == 0) record_status(p.status, FA_ERR_POSITION);
-      continue;
-    }
-    Angles ang;
-    load_angles(p, pos, l, true, ang);
-    auto rows = [&](const T* x_at, const T* z_at, T* d_at, int H, int from, int n, const float* weight, uint64_t* dw) {
+    const bool bad = p.rot && (pos < 0 || pos >= p.max_pos);
+    if (bad && lane == 0) record_status(p.status, FA_ERR_POSITION);
+    Angles ang = {};
+    if (!bad) load_angles(p, pos, l, true, ang);
+    auto rows = [&](T* d_at, int H, int from, int n, const float* weight, uint64_t* dw) {
       const Heads hd = heads_of<RPS>(u, from, n, sub);
-      if (hd.sets == 0) return;
       uint64_t w[4];
-      if (weight) load_weights(weight, l, w);
-      x_at += hd.h * D + 8 * l;
-      z_at += hd.h * D + 8 * l;
+      if (weight && hd.sets) load_weights(weight, l, w);
       d_at += hd.h * D + 8 * l;
-      auto one = [&](const Vec8<T>& x, const Vec8<T>& z, T* at, bool live) {
+      int left = bad ? 0 : H - hd.h;           // the lane's heads: every RPS-th
+#pragma unroll 1
+      for (int k = 0; k < hd.sets; ++k, d_at += RPS * D, left -= RPS) {
+        Vec8<T> x, z;
+        take(x, z);
+        const bool live = left > 0;
         uint64_t dy[4];
         {
           const Partners<T> y(p, z, src, on);
@@ -439,13 +533,13 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
           }
           const float r = rsqrtf(a * (1.f / D) + p.eps);
           // xh = x r, dw += dy xh, dx = r (dy w - xh mean(dy w xh)); a row
-          // that is not there has xh = 0, whatever its r
-          const float rl = live ? r : 0.f, m = -(b * r * (1.f / D)) * r;
-          const uint64_t r2 = f2(r, r), m2 = f2(m, m), rl2 = f2(rl, rl);
+          // that is not there adds nothing, whatever its r
+          const float m = -(b * r * (1.f / D)) * r;
+          const uint64_t r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint64_t xh = fmul2(x.pair(i), rl2);
-            dw[i] = ffma2(dy[i], xh, dw[i]);
+            const uint64_t xh = fmul2(x.pair(i), r2);
+            if (live) dw[i] = ffma2(dy[i], xh, dw[i]);
             dy[i] = ffma2(xh, m2, fmul2(g[i], r2));
           }
         }
@@ -453,38 +547,15 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
           Vec8<T> d;
 #pragma unroll
           for (int i = 0; i < 4; ++i) d.set(i, dy[i]);
-          d.store(at);
+          d.store(d_at);
         }
-      };
-      int left = H - hd.h;                     // the lane's heads: every RPS-th
-      for (int k = 0; k < hd.sets; k += kAhead<T>) {
-        Vec8<T> x[kAhead<T>], z[kAhead<T>];
-#pragma unroll
-        for (int i = 0; i < kAhead<T>; ++i) {
-          x[i].zero();
-          z[i].zero();
-          if (k + i < hd.sets && left > i * RPS) {
-            x[i].load(x_at + i * RPS * D);
-            z[i].load(z_at + i * RPS * D);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead<T>; ++i) {
-          if (k + i >= hd.sets) break;
-          one(x[i], z[i], d_at + i * RPS * D, left > i * RPS);
-        }
-        x_at += kAhead<T> * RPS * D;
-        z_at += kAhead<T> * RPS * D;
-        d_at += kAhead<T> * RPS * D;
-        left -= kAhead<T> * RPS;
       }
     };
     const bool norm = p.q_weight != nullptr;
-    rows(static_cast<const T*>(p.q) + t * p.q_stride, static_cast<const T*>(p.dq_out) + t * p.Hq * D,
-         static_cast<T*>(p.dq) + t * p.dq_stride, p.Hq, 0, p.sets_q, norm ? p.q_weight : nullptr, dwq);
-    rows(static_cast<const T*>(p.k) + t * p.k_stride, static_cast<const T*>(p.dk_out) + t * p.Hkv * D,
-         static_cast<T*>(p.dk) + t * p.dk_stride, p.Hkv, p.sets_q, p.sets_k, norm ? p.k_weight : nullptr, dwk);
+    rows(static_cast<T*>(p.dq) + t * p.dq_stride, p.Hq, 0, p.sets_q, norm ? p.q_weight : nullptr, dwq);
+    rows(static_cast<T*>(p.dk) + t * p.dk_stride, p.Hkv, p.sets_q, p.sets_k, norm ? p.k_weight : nullptr, dwk);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (p.q_weight) {
     // the warp's row groups, then the block's warps, in a fixed order
 #pragma unroll
@@ -558,7 +629,9 @@ template <int D, typename T>
 int launch_bwd(NormRopeParams p, cudaStream_t stream) {
   const long long units = cut_units<D>(p, false, kNormRopeWarps);
   const int grid = (int)std::min<long long>((units + kWarps - 1) / kWarps, kNormRopeBwdBlocks);
-  norm_rope_bwd_kernel<D, T><<<grid, kThreads, 0, stream>>>(p);
+  auto kern = norm_rope_bwd_kernel<D, T>;
+  if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kBwdSmem<T>)) return e;
+  kern<<<grid, kThreads, kBwdSmem<T>, stream>>>(p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
   if (!p.q_weight) return 0;
   return launch_dependent(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(256), 0, stream,
