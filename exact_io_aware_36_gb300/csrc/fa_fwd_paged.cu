@@ -13,24 +13,34 @@
 // two such tiles): up to 256 rows against the keys any of them sees.
 //   two tiles   both run over the same K/V tiles, each with its own S, P, O in
 //               TMEM: one tile's softmax overlaps the other's products.
-//               Bound by the tensor cores and the softmax.
+//               Bound by the products: 32 of them take 2600 of the about 3400
+//               cycles of a step of 128 keys (two chunks of 2048 tokens over
+//               31k keys, 32 heads on 8, d = 128: 1545 us, 1345 TFLOP/s, 71 %
+//               of the measured cuBLAS rate).  What an item costs beside its
+//               steps, 14600 cycles of first loads, first softmax and
+//               epilogue, shows where items are short (8192 tokens from
+//               scratch: 500 us, 1100 TFLOP/s).
 //   one tile    (a token or a few per sequence) the same two streams share the
 //               rows and take the key tiles in turn; their O and (m, l) are
 //               merged at the end.  64 KB of K/V per 128 keys come from HBM
 //               (1.4 us of one SM's share at d = 128) against 0.8 us of
 //               products, so HBM bounds it, and the tensor cores have time to
 //               take P as two bf16 parts (high and low, 16 bits of P instead
-//               of 8): O then carries its own rounding only.
+//               of 8): O then carries its own rounding only.  16 caches of
+//               1k-32k tokens, one new token each: 158 us, 6.35 TB/s, 94 % of
+//               the measured copy rate.
 //
 // Work.  Lengths are known on the device alone (so a captured call can be
 // replayed with others).  Every CTA, one per SM, adds up the key tiles of all
 // items, weighed by their measured times (a tile of a two-tile item 9, of
-// another 8; what an item costs beside its tiles 36 and 16), and takes an equal
-// run of this one line.  A run begins and ends inside
-// items; such parts go to the workspace, two at most per CTA, and
+// another 8; what an item costs beside its tiles 36 and 16: without that the
+// SMs with the short items ended last, 658 us instead of 490 for the 8192
+// tokens), and takes an equal run of this one line.  A run begins and ends
+// inside items; such parts go to the workspace, two at most per CTA, and
 // paged_merge_kernel joins an item's parts in a fixed order.  No SM waits for
 // a long sequence and nothing depends on timing: the result is the same from
-// run to run.
+// run to run.  Plan, first loads and merge are what a short call costs (one
+// sequence of 777 tokens, 16 heads of 64: 16 us).
 //
 // Roles:
 //   warp 10    walker: finds the CTA's items one after the other and passes
@@ -41,7 +51,9 @@
 //              page_size boxes, one lane each, at the pages the table names;
 //              pages with no visible key are not read.  Page numbers of the
 //              next step are loaded before the wait for its slot.
-//   warp 9     MMA issuer (one lane).  Where a V tile reaches past the visible
+//   warp 9     MMA issuer (one lane), not on the scheduler of warps 0 and 4,
+//              which do all the softmax of a few rows (176 instead of 187 us
+//              for the 16 caches).  Where a V tile reaches past the visible
 //              keys, the warp first zeroes those rows: a slot no token filled
 //              may hold NaN, and 0 x NaN would reach O.
 //   warps 0-3  softmax of stream 0 (one TMEM lane = one row), warps 4-7 of
@@ -52,7 +64,10 @@
 // Registers: three warps share a quarter of the SM, so a thread has 168, too
 // few for a row's 128 scores and what is done with them.  The softmax takes a
 // row's scores from TMEM 16 columns at a time, the next 16 in flight, and
-// holds P (64 registers), not S.
+// holds P (64 registers), not S.  (Raised register limits by setmaxnreg would
+// hold S, but a first form with them did not end once in some hundred calls;
+// a dependent launch that may begin early, as the merge does here, could take
+// the registers between the lowering and the raise.)
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D);
 // P overwrites S: 64 columns, or all 128 (each 16 keys' high part, then low).
 #include <cuda.h>
