@@ -1129,56 +1129,78 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
-// following ones, in their order.  One warp per row.
+// following ones, in their order.  One warp per row, D / 32 columns per lane;
+// four parts' loads at a time, so that a row costs two waits for memory: what
+// the parts are, and the parts.
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
   grid_dependency_wait();
   const int c = blockIdx.x;
-  const int4 it = p.part_meta[2 * c + 1];
-  if (it.x == 0) return;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= it.z * p.group) return;
-  // parts: slot 2 c + 1, then slot 2 c' of c' = c + 1 .. until an end
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int4 it = p.part_meta[2 * c + 1];
+  int kind = c + 1 + lane < nctas ? p.part_meta[2 * (c + 1 + lane)].x : 0;
+  if (it.x == 0 || row >= it.z * p.group) return;
+  // parts: slot 2 c + 1, then slot 2 c' of c' = c + 1 .. until an end (kind 2)
   int nparts = 1;
-  for (int c0 = c + 1; c0 < nctas; c0 += 32) {
-    const int kind = c0 + lane < nctas ? p.part_meta[2 * (c0 + lane)].x : 2;
+  for (int c0 = c + 1;; c0 += 32) {
     const unsigned stop = __ballot_sync(0xffffffffu, kind != 1);
     if (stop) {
       const int at = __ffs(stop) - 1;
-      nparts += at + (c0 + at < nctas && __shfl_sync(0xffffffffu, kind, at) == 2 ? 1 : 0);
+      nparts += at + (__shfl_sync(0xffffffffu, kind, at) == 2 ? 1 : 0);
       break;
     }
     nparts += 32;
+    kind = c0 + 32 + lane < nctas ? p.part_meta[2 * (c0 + 32 + lane)].x : 0;
   }
-  auto prow = [&](int s) { return (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row; };
-  float M = -INFINITY;
-  for (int s = lane; s < nparts; s += 32) M = fmaxf(M, p.part_ml[prow(s) * 4]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int PER = D / 32;
-  float o[PER];
+  struct alignas(4 * PER) Cols { float v[PER]; };
+  Cols o;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  float l = 0.f, lr = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < nparts; ++s) {
-    const float4 ml = *reinterpret_cast<const float4*>(p.part_ml + prow(s) * 4);
-    const float wgt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-    l = fmaf(wgt, ml.y, l);
-    lr = fmaf(wgt, ml.z, lr);
-    const float* src = p.part_o + prow(s) * D;
+  for (int i = 0; i < PER; ++i) o.v[i] = 0.f;
+  float M = -INFINITY, l = 0.f, lr = 0.f;
+  for (int s0 = 0; s0 < nparts; s0 += 4) {
+    float4 ml[4];
+    Cols x[4];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = fmaf(wgt, src[lane + 32 * i], o[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int s = min(s0 + i, nparts - 1);
+      const long long at = (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row;
+      ml[i] = *reinterpret_cast<const float4*>(p.part_ml + at * 4);
+      x[i] = *reinterpret_cast<const Cols*>(p.part_o + at * D + lane * PER);
+    }
+    float mx = M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s0 + i < nparts) mx = fmaxf(mx, ml[i].x);
+    const float a = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+    l *= a;
+    lr *= a;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) o.v[k] *= a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i >= nparts || ml[i].x == -INFINITY) continue;
+      const float w = ex2_approx(ml[i].x - mx);
+      l = fmaf(w, ml[i].y, l);
+      lr = fmaf(w, ml[i].z, lr);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x[i].v[k], o.v[k]);
+    }
+    M = mx;
   }
   const float inv = lr > 0.f ? 1.f / lr : 0.f;
   const long long tok = it.y + row / p.group;
   const int h = it.w * p.group + row % p.group;
-  const long long at = (tok * p.Hq + h) * D;
+  const long long at = (tok * p.Hq + h) * D + lane * PER;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (p.o_f32) static_cast<float*>(p.o)[at + lane + 32 * i] = o[i] * inv;
-    else static_cast<__nv_bfloat16*>(p.o)[at + lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
+  for (int k = 0; k < PER; ++k) o.v[k] *= inv;
+  if (p.o_f32) {
+    *reinterpret_cast<Cols*>(static_cast<float*>(p.o) + at) = o;
+  } else {
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at + k) = pack_bf16x2(o.v[k], o.v[k + 1]);
   }
   if (lane == 0) p.lse[(long long)h * p.T + tok] = l > 0.f ? (M + lg2_approx(l)) * kLn2 : -INFINITY;
 }

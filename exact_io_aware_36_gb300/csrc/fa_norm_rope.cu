@@ -23,7 +23,7 @@
 // the backward), which leaves issue slots idle at HBM's rate; the first form,
 // at twice as many, was bound by them.  One GB300, 16384 tokens of 32 + 8 heads
 // of 128 in bf16: 58.7 us, 5.75 TB/s, 85 % of the measured copy rate; backward
-// 94.4 us, 5.35 TB/s, 79 %.
+// 91.5 us, 5.52 TB/s, 81 %.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -582,25 +582,32 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
   grid_launch_dependents();
 }
 
-// Sum of the blocks' parts: one block per 32 of the 2 D columns, 8 strips of
-// blocks per column, added in a fixed order.
-__global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* part, int nblocks, int D, float* dwq, float* dwk) {
-  __shared__ float red[8][32];
+// Sum of the blocks' parts: one block per 32 of the 2 D columns, 32 strips of
+// blocks per column (ten loads each, all on their way at once), added in a
+// fixed order.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int nblocks, int D, float* dwq, float* dwk) {
+  __shared__ float red[32][33];
   grid_dependency_wait();
   const int c = threadIdx.x & 31;
   const int strip = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
+  constexpr int kLoads = (kNormRopeBwdBlocks + 31) / 32;
+  float x[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) x[i] = strip + 32 * i < nblocks ? part[(long long)(strip + 32 * i) * 2 * D + col] : 0.f;
   float s = 0.f;
-#pragma unroll 4
-  for (int b = strip; b < nblocks; b += 8) s += part[(long long)b * 2 * D + col];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) s += x[i];
   red[strip][c] = s;
   __syncthreads();
-  if (strip == 0) {
-    s = 0.f;
+  // warp `strip` adds up column `strip`
+  s = red[c][strip];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += red[i][c];
-    if (col < D) dwq[col] = s;
-    else dwk[col - D] = s;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (c == 0) {
+    const int out = blockIdx.x * 32 + strip;
+    if (out < D) dwq[out] = s;
+    else dwk[out - D] = s;
   }
 }
 
@@ -634,7 +641,7 @@ int launch_bwd(NormRopeParams p, cudaStream_t stream) {
   kern<<<grid, kThreads, kBwdSmem<T>, stream>>>(p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
   if (!p.q_weight) return 0;
-  return launch_dependent(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(256), 0, stream,
+  return launch_dependent(norm_rope_dw_kernel, dim3(2 * D / 32), dim3(1024), 0, stream,
                           (const float*)p.dw_part, grid, D, p.dq_weight, p.dk_weight);
 }
 
