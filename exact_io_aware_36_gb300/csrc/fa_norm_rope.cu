@@ -22,8 +22,9 @@
 // With these packed in float32 pairs a set costs some 120 instructions (170 in
 // the backward), which leaves issue slots idle at HBM's rate; the first form,
 // at twice as many, was bound by them.  One GB300, 16384 tokens of 32 + 8 heads
-// of 128 in bf16: 58.7 us, 5.75 TB/s, 85 % of the measured copy rate; backward
-// 91.5 us, 5.52 TB/s, 81 %.
+// of 128 in bf16: 58.3 us, 5.79 TB/s, 85 % of the measured copy rate; backward
+// 87.6 us, 5.77 TB/s, 85 %.  The order of the rotation's pairs is a template
+// argument: chosen at run time the two cost 58.6 and 91.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,7 +43,8 @@ constexpr int kWarps = kThreads / 32;
 // Sets that the forward loads before it uses the first, and the blocks per SM
 // that leaves room for (registers).  Both cover HBM's latency: 16384 tokens of
 // 32 + 8 heads of 128 took 67 us with two bf16 sets ahead, 59 with four, 61 with
-// six and three blocks; float32 sets are twice as large (four: 7.9 us for 3001
+// six and three blocks; fetching a warp's first rows ahead of its angles cost
+// registers or time (67 by loads, 60 by a prefetch into L2); float32 sets are twice as large (four: 7.9 us for 3001
 // tokens of 16 heads of 64, two: 6.6).
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
@@ -184,17 +186,15 @@ __device__ __forceinline__ void load_angles(const NormRopeParams& p, int pos, in
 
 // The partners of a lane's elements.  Warp-collective; zero where there is no
 // rotation, so that an infinity there meets no 0.
-template <typename T>
+template <typename T, bool INTER>
 struct Partners {
   Vec8<T> v;
-  bool swap;
   __device__ __forceinline__ Partners(const NormRopeParams& p, const Vec8<T>& x, int src, bool on) {
-    swap = p.interleaved;
     v = x;
-    if (!swap && p.rot) v = x.from_lane(src);
+    if (!INTER && p.rot) v = x.from_lane(src);
     if (!on) v.zero();
   }
-  __device__ __forceinline__ uint64_t pair(int i) const { return swap ? v.swapped(i) : v.pair(i); }
+  __device__ __forceinline__ uint64_t pair(int i) const { return INTER ? v.swapped(i) : v.pair(i); }
 };
 
 __device__ __forceinline__ void load_weights(const float* w, int l, uint64_t* f) {
@@ -288,7 +288,8 @@ __device__ __forceinline__ Heads heads_of(const Unit& u, int from, int n, int su
   return Heads{(s0 - from) * RPS + sub, max(s1 - s0, 0)};
 }
 
-template <int D, typename T, bool PAGES>
+// INTER: the pairs of the rotation are neighbours (p.interleaved).
+template <int D, typename T, bool PAGES, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;                // rows per set
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>) norm_rope_kernel(co
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         wc[i] = fmul2(wc[i], a[i]);
-        ws[i] = fmul2(ws[i], p.interleaved ? swap_pair(b[i]) : b[i]);
+        ws[i] = fmul2(ws[i], INTER ? swap_pair(b[i]) : b[i]);
       }
     }
     src += hd.h * D + 8 * l;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>) norm_rope_kernel(co
         r = rsqrtf(row_sum<LPR>(pair_sum(ss)) * (1.f / D) + p.eps);
       }
       const uint64_t r2 = f2(r, r);
-      const Partners<T> y(p, x, src_lane, on);
+      const Partners<T, INTER> y(p, x, src_lane, on);
       Vec8<T> z;
 #pragma unroll
       for (int i = 0; i < 4; ++i) z.set(i, fmul2(ffma2(x.pair(i), wc[i], fmul2(y.pair(i), ws[i])), r2));
@@ -394,7 +395,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Sets of x and of dz that a warp of the gradient has on their way.
+// Sets of x and of dz that a warp of the gradient has on their way (bf16, 16384
+// tokens: four 87.6 us, six 87.6, eight 88.5).
 template <typename T>
 constexpr int kDepth = sizeof(T) == 2 ? 6 : 3;
 
@@ -407,10 +409,10 @@ constexpr int kBwdSmem = kWarps * kDepth<T> * 2 * 32 * 8 * sizeof(T);
 // a fixed order, so the result is the same from run to run.
 // The registers this takes leave 16 warps per SM, too few for HBM's latency
 // with loads into registers (102 us for 16384 tokens of 32 + 8 heads of 128,
-// 94 this way).  So the loads go to shared memory, kDepth sets ahead and on
+// 94 this way, when this was built).  So the loads go to shared memory, kDepth sets ahead and on
 // into the warp's next units: each lane fetches the 8 elements that it will
 // itself use, so no lane waits for another.
-template <int D, typename T>
+template <int D, typename T, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
         const bool live = left > 0;
         uint64_t dy[4];
         {
-          const Partners<T> y(p, z, src, on);
+          const Partners<T, INTER> y(p, z, src, on);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dy[i] = ffma2(z.pair(i), ang.c[i], fmul2(y.pair(i), ang.s[i]));
         }
@@ -628,7 +630,8 @@ long long cut_units(NormRopeParams& p, bool values, int want) {
 template <int D, typename T, bool PAGES>
 int launch_fwd(NormRopeParams p, cudaStream_t stream) {
   const long long units = cut_units<D>(p, PAGES, kNormRopeWarps);
-  norm_rope_kernel<D, T, PAGES><<<(unsigned)((units + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
+  auto kern = p.interleaved ? norm_rope_kernel<D, T, PAGES, true> : norm_rope_kernel<D, T, PAGES, false>;
+  kern<<<(unsigned)((units + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p);
   return (int)cudaGetLastError();
 }
 
@@ -636,7 +639,7 @@ template <int D, typename T>
 int launch_bwd(NormRopeParams p, cudaStream_t stream) {
   const long long units = cut_units<D>(p, false, kNormRopeWarps);
   const int grid = (int)std::min<long long>((units + kWarps - 1) / kWarps, kNormRopeBwdBlocks);
-  auto kern = norm_rope_bwd_kernel<D, T>;
+  auto kern = p.interleaved ? norm_rope_bwd_kernel<D, T, true> : norm_rope_bwd_kernel<D, T, false>;
   if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kBwdSmem<T>)) return e;
   kern<<<grid, kThreads, kBwdSmem<T>, stream>>>(p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
