@@ -1112,7 +1112,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           float* ml = p.part_ml + prow * 4;
           *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, 0.f);
         } else {
-          p.lse[(long long)head * p.T + tok] = l > 0.f ? (m_ref + lg2_approx(l)) * kLn2 : -INFINITY;
+          p.lse[(long long)head * p.T + tok] = l == 0.f ? -INFINITY : (m_ref + lg2_approx(l)) * kLn2;
         }
       }
       ++nseg;
@@ -1180,7 +1180,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
     for (int k = 0; k < PER; ++k) o.v[k] *= a;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (s0 + i >= nparts || ml[i].x == -INFINITY) continue;
+      // no key seen there, or (l not 0) a score that is not a number
+      if (s0 + i >= nparts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
       const float w = ex2_approx(ml[i].x - mx);
       l = fmaf(w, ml[i].y, l);
       lr = fmaf(w, ml[i].z, lr);
@@ -1202,7 +1203,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
     for (int k = 0; k < PER; k += 2)
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at + k) = pack_bf16x2(o.v[k], o.v[k + 1]);
   }
-  if (lane == 0) p.lse[(long long)h * p.T + tok] = l > 0.f ? (M + lg2_approx(l)) * kLn2 : -INFINITY;
+  if (lane == 0) p.lse[(long long)h * p.T + tok] = l == 0.f ? -INFINITY : (M + lg2_approx(l)) * kLn2;
 }
 
 template <int D, bool ALIBI, bool ONE>

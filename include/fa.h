@@ -454,7 +454,10 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
  *             fa_fwd over the whole sequence.  Needs L_b >= n_b.
  *   causal 0: it sees all L_b keys, whatever n_b (an encoder's states, kept
  *             in pages).  A window or ALiBi is FA_ERR_UNSUPPORTED.
- * A row that sees no key (L_b = 0) has o = 0 and lse = -inf.  One token per
+ * A row that sees no key (L_b = 0) has o = 0 and lse = -inf, one with a NaN
+ * score NaN.  A NaN or infinity in a key reaches the rows that see it; in a
+ * value also rows of the same block of up to 256 / (Hq / Hkv) tokens that do
+ * not (0 x NaN).  One token per
  * sequence, long chunks and any mixture of both go in one call; with lengths
  * on the device alone, a captured call can be replayed with others.  Results
  * do not vary from run to run.

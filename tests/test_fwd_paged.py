@@ -184,6 +184,23 @@ def test_peaked_scores(gain, new, lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new,lens,bad", [([1, 2], [20000, 60], [0, 2]), ([1, 5, 1], [300, 900, 1], [0, 3, 6]),
+                                          ([150], [9000], [0, 70, 149])])
+def test_nan_rows_stay_nan_and_alone(new, lens, bad):
+    """A row of q with a NaN gives NaN, in one part or in many, and no other row takes notice."""
+    import torch as t
+    q, kp, vp, table, cs, cu = state(new, lens, 64, 8, 2, 128, 21)
+    run = lambda x: fa.attention_forward_paged(x, kp, vp, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    O, lse = run(q)
+    x = q.clone()
+    x[bad, 3, 5] = float("nan")
+    On, ln = run(x)
+    assert bool(On[bad, 3].isnan().all()) and bool(ln[3, bad].isnan().all())
+    On[bad, 3], ln[3, bad] = O[bad, 3], lse[3, bad]
+    check((On, ln), q, kp, vp, table, lens, cu, 64)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(12))
 def test_random_mixes(seed):
     """Sequences that bring nothing, one token, a few or a chunk, in one call, over any cut of the work."""
