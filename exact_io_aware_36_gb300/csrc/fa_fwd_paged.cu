@@ -795,7 +795,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // goes on from the CTA before (2: the item's last), and the item begun here
     int cont = 0;
     int4 begun = make_int4(0, 0, 0, 0);
-    for (bool more = true; more; ++nitem) {
+    bool more = true;
+    for (; more; ++nitem) {
       more = walk_next(p, w, s);
       if (more) {
         if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
@@ -814,6 +815,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       __syncwarp();
     }
+    // A wait that ran out: the merge must not take what the workspace held.
+    if (more && lane < 2) p.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
