@@ -679,9 +679,9 @@ static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k
   if ((st = check_rows(q_out, (long long)p.Hq * p.d, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(k, k_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(v, v_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
+  if (p.T == 0 || B == 0 || N == 0) return FA_OK;
   if (!k_pages || !v_pages || !block_table || !cache_seqlens) return FA_ERR_NULL;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
-  if (p.T == 0 || B == 0 || N == 0) return FA_OK;
   p.q = q;
   p.k = k;
   p.v = v;

@@ -671,9 +671,10 @@ def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index):
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
         return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, index, (B + 1,)), B, int(max_seqlen), max_pages
-    if B == 0 or T % B:
+    N = T // B if B else 0
+    if T != B * N:
         raise ValueError("without cu_seqlens every sequence brings the same number of tokens")
-    return tp, cp, None, B, T // B, max_pages
+    return tp, cp, None, B, N, max_pages
 
 
 def cache_append(k, v, k_pages, v_pages, block_table, cache_seqlens, *, cu_seqlens=None,

@@ -201,6 +201,19 @@ def test_nan_rows_stay_nan_and_alone(new, lens, bad):
 
 
 @pytest.mark.gpu
+def test_no_sequences():
+    import torch as t
+    e = lambda *s, dtype=t.bfloat16: t.empty(s, dtype=dtype, device="cuda")
+    pools = e(4, 16, 2, 64), e(4, 16, 2, 64)
+    lengths = e(0, 3, dtype=t.int32), e(0, dtype=t.int32)
+    O, lse = fa.attention_forward_paged(e(0, 4, 64), *pools, *lengths, check=True)
+    assert O.shape == (0, 4, 64) and lse.shape == (4, 0)
+    fa.cache_append(e(0, 2, 64), e(0, 2, 64), *pools, *lengths, check=True)
+    with pytest.raises(ValueError):
+        fa.cache_append(e(2, 2, 64), e(2, 2, 64), *pools, *lengths)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(12))
 def test_random_mixes(seed):
     """Sequences that bring nothing, one token, a few or a chunk, in one call, over any cut of the work."""
