@@ -409,9 +409,9 @@ constexpr int kBwdSmem = kWarps * kDepth<T> * 2 * 32 * 8 * sizeof(T);
 // a fixed order, so the result is the same from run to run.
 // The registers this takes leave 16 warps per SM, too few for HBM's latency
 // with loads into registers (102 us for 16384 tokens of 32 + 8 heads of 128,
-// 94 this way, when this was built).  So the loads go to shared memory, kDepth sets ahead and on
-// into the warp's next units: each lane fetches the 8 elements that it will
-// itself use, so no lane waits for another.
+// 94 this way, when this was built).  So the loads go to shared memory, kDepth
+// sets ahead and on into the warp's next units: each lane fetches the 8
+// elements that it will itself use, so no lane waits for another.
 template <int D, typename T, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8;
