@@ -123,6 +123,10 @@ struct Bars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_full[2];
   uint64_t o_done, o_free, drain;
+  uint64_t joined;              // (m, l, l~) of both streams' rows of a one-tile item are there
+#ifdef FA_PAGED_STOP
+  uint64_t never;               // nothing arrives on it
+#endif
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem_base;
   int abort_flag;
@@ -132,6 +136,13 @@ struct Bars {
   int b, g, qb;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+
+#ifdef FA_PAGED_STOP
+// Test build: the wait of warp g_stop[0] of CTA g_stop[1] for its item number
+// g_stop[2] runs out, as if the item's arrival had been lost.
+__device__ int g_stop[3] = {-1, -1, -1};
+constexpr unsigned long long kStopLimitNs = 1000000;
+#endif
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -440,6 +451,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     mbar_init(&bars->o_done, 1);
     mbar_init(&bars->o_free, 8);
     mbar_init(&bars->drain, 1);
+    mbar_init(&bars->joined, 8);
+#ifdef FA_PAGED_STOP
+    mbar_init(&bars->never, 1);
+#endif
     bars->abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -468,6 +483,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const Seg* ring = reinterpret_cast<const Seg*>(smem + C::SEG_OFF);
   int nitem = 0;
   auto next_seg = [&](bool& ok) -> bool {
+#ifdef FA_PAGED_STOP
+    if (warp == g_stop[0] && (int)blockIdx.x == g_stop[1] && nitem == g_stop[2])
+      return ok = wait_warp(&bars->never, 0, WaitCtx{&bars->abort_flag, p.status, kStopLimitNs});
+#endif
     if (!wait(&bars->seg_full[nitem % kSegs], (nitem / kSegs) & 1)) return ok = false;
     return ring[nitem % kSegs].ie >= 0;
   };
@@ -830,19 +849,16 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int cs = 0;                  // S products consumed (s_full phases)
     int nseg = 0, flip = 0;
     int gs = 0;                  // steps before this item
-    // A warp that gives up (a wait ran out) still walks the items: it meets
-    // the others at the barrier of every one-tile item, and they give up too.
+    int njoin = 0;               // one-tile items before this one
+    // A warp whose wait ran out leaves; the others' waits for it run out or
+    // see the abort flag.
     while (true) {
       int n0, steps, diag, low, kend;
       bool valid, dual;
       float slope2 = 0.f;
       int vslot = 0;             // step of this stream's next tile
       {
-        bool got = true;
-        if (!next_seg(got)) {
-          if (!got) ok = false;
-          break;
-        }
+        if (!next_seg(ok)) break;
         const Seg& s = ring[nitem % kSegs];
         const int r = 32 * q4 + lane, rq = r / p.group;  // row of the tile, its token
         dual = ONE || !s.k.two;
@@ -1042,7 +1058,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       // ---------------------------------------------------------- epilogue
-      if (ok) ok = wait(&bars->o_done, nseg & 1);
+      if (!ok || !wait(&bars->o_done, nseg & 1)) break;
       tc_fence_after();
       // A stream without a step in this part has no O: its columns are not
       // used.
@@ -1061,7 +1077,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         own[0] = m_ref;
         own[1] = l;
         own[2] = lr;
-        if (named_bar_any(1, 256, !ok)) ok = false;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->joined);
+        // Only the time limit ends this wait, not the abort flag: a row's two
+        // halves are written by both streams' warps or by neither.
+        const uint32_t par = njoin++ & 1;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->joined, par)) && !wait_warp_drain(&bars->joined, par)) break;
         const float mo = oth[0];
         const float M = fmaxf(m_ref, mo);
         w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
@@ -1071,10 +1092,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         m_ref = M;
         c_from = t * (D / 2);
         c_to = c_from + D / 2;
-      }
-      if (!ok) {
-        seg_done();
-        continue;
       }
       const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
       const int tl = (dual ? 0 : t * p.tpt) + r / p.group;            // token of the item
@@ -1238,6 +1255,13 @@ int launch_d(const PagedParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef FA_PAGED_STOP
+extern "C" int fa_selftest_paged_stop(int warp, int cta, int item) {
+  const int at[3] = {warp, cta, item};
+  return (int)cudaMemcpyToSymbol(g_stop, at, sizeof(at));
+}
+#endif
 
 int launch_fwd_paged(const PagedParams& p, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
