@@ -834,8 +834,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       __syncwarp();
     }
-    // A wait that ran out: the merge must not take what the workspace held.
-    if (more && lane < 2) p.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
@@ -1145,11 +1143,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-
+  // A wait ran out, so parts may be missing, whatever the walker put on record
+  // ahead of them: the merge must not take what the workspace held.
+  if (threadIdx.x < 2 && bars->abort_flag) p.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
-// following ones, in their order.  One warp per row, D / 32 columns per lane;
+// following ones, in their order; an item of which a CTA has no part to show
+// is left alone.  One warp per row, D / 32 columns per lane;
 // four parts' loads at a time, so that a row costs two waits for memory: what
 // the parts are, and the parts.
 template <int D>
@@ -1167,7 +1168,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
     const unsigned stop = __ballot_sync(0xffffffffu, kind != 1);
     if (stop) {
       const int at = __ffs(stop) - 1;
-      nparts += at + (__shfl_sync(0xffffffffu, kind, at) == 2 ? 1 : 0);
+      if (__shfl_sync(0xffffffffu, kind, at) != 2) return;
+      nparts += at + 1;
       break;
     }
     nparts += 32;

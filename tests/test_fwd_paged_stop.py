@@ -66,3 +66,28 @@ def test_a_lost_item_ends_the_call(lib, warp, cta, item, new, lens):
     assert run(lib, *args, again, ws) == 0
     assert all(t.equal(a, b) for a, b in zip(good, again))
     assert status == 7
+
+
+@pytest.mark.parametrize("new,lens", MIXES)
+@pytest.mark.parametrize("cta,item", [(0, 0), (5, 0), (7, 1), (30, 0)])
+@pytest.mark.parametrize("warp", [0, 6, PRODUCER, MMA])
+def test_rows_are_right_or_left_alone(lib, warp, cta, item, new, lens):
+    """What the workspace held (here numbers that would pass for parts) never gets into a row."""
+    import torch as t
+    Hq, Hkv, d = 8, 2, 128
+    q, kp, vp, table, cs, cu = state(new, lens, 16, Hq, Hkv, d, 3)
+    T = sum(new)
+    outs = []
+    for at in ((-1, -1, -1), (warp, cta, item)):
+        ws = t.ones(fa.fa_fwd_paged_workspace_size(Hq, Hkv, max(new), d) // 4, device="cuda").view(t.uint8)
+        out = t.full((T, Hq, d), 5.0, device="cuda"), t.full((Hq, T), 5.0, device="cuda")
+        lib.fa_selftest_paged_stop(*at)
+        status = run(lib, q, kp, vp, table, cs, cu, max(new), out, ws)
+        lib.fa_selftest_paged_stop(-1, -1, -1)
+        assert status == (7 if warp in at else 0)
+        outs.append(out)
+    (good, lgood), (o, lse) = outs
+    right, left = (o == good).all(-1), (o == 5).all(-1)
+    assert bool((right ^ left).all())
+    assert bool(((lse.T == lgood.T) == right).all()) and bool(((lse.T == 5) == left).all())
+    assert bool(left.any()) and bool(right.any())
