@@ -108,7 +108,7 @@ struct Cfg {
   static constexpr int V_OFF = K_OFF + NS * TILE_BYTES;
   static constexpr int ML_OFF = V_OFF + NS * TILE_BYTES;   // (m, l, l~) of both streams' rows
   static constexpr int SEG_OFF = ML_OFF + 2 * 128 * 3 * 4;          // ring of items
-  static constexpr int PAR_OFF = SEG_OFF + kSegs * 80;              // a copy of the parameters
+  static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;              // a copy of the parameters
   static constexpr int BAR_OFF = PAR_OFF + 256;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -130,6 +130,7 @@ struct Bars {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem_base;
   int abort_flag;
+  int part_lost[2];             // the part's item met a page outside the pool
   // the plan: where this CTA's run begins
   unsigned long long warp_sum[kThreads / 32];
   long long w0, w1, base;
@@ -220,8 +221,9 @@ struct Seg {
   Block k;
   int g, tok, ntok;            // kv head; first token (row of q) and tokens of the item
   int b, L, ib, ie;            // sequence, its length
+  int lost;                    // the producer met a page outside the pool
 };
-static_assert(sizeof(Seg) <= 80, "segment ring");
+static_assert(sizeof(Seg) <= 96, "segment ring");
 
 // A CTA's walk over its run [w0, w1) of the line of tiles.
 struct Walk {
@@ -455,7 +457,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #ifdef FA_PAGED_STOP
     mbar_init(&bars->never, 1);
 #endif
-    bars->abort_flag = 0;
+    bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
     fence_mbarrier_init();
   }
   if (warp == kMmaWarp) {
@@ -516,6 +518,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool two = !ONE && s.k.two;
       const int g = s.g, ib = s.ib, ie = s.ie, vlo = s.k.vlo, vhi = s.k.vhi, hi_all = s.k.hi_all;
       const int tok = s.tok, b = s.b;
+      // (the place in the ring stays this item's until its epilogue is done)
+      int* lost = const_cast<int*>(&s.lost);
       seg_done();
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         const int x = two ? t : qsel;
@@ -538,12 +542,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int key0 = (hi_all - i) * 128 + lane * box_rows;
         int krow = -1;
         if (lane < nbox && key0 < vhi && key0 + box_rows > vlo) {
-          int page = __ldg(table + (key0 >> p.page_shift));
-          if (page < 0 || page >= p.num_pages) {
+          const int page = __ldg(table + (key0 >> p.page_shift));
+          if (page >= 0 && page < p.num_pages) {
+            krow = page * p.page_size + (key0 & (p.page_size - 1));
+          } else {
+            // nothing is loaded, and the item's rows are not written
             record_status(p.status, FA_ERR_PAGE);
-            page = 0;
+            *lost = 1;
           }
-          krow = page * p.page_size + (key0 & (p.page_size - 1));
         }
         const int sl = gs % C::NS;
         if (gs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) break;
@@ -809,6 +815,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // -------------------------------------------------------------- walker
     Walk w;
     Seg s;
+    s.lost = 0;
     walk_begin(p, bars, w);
     // what the parts of this CTA are, for the merge: kind of the part that
     // goes on from the CTA before (2: the item's last), and the item begun here
@@ -1065,6 +1072,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // 0: the whole item; else the slot of the part: 1 its continuation from
       // the CTA before, 2 its beginning
       const int part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
+      if (s.lost) {
+        valid = false;
+        if (part) bars->part_lost[part - 1] = 1;
+      }
       const bool use0 = steps > 0, use1 = dual && (steps == 0 || s.ie - s.ib > 1);
       float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
@@ -1144,8 +1155,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tmem_dealloc(tmem, 512);
   }
   // A wait ran out, so parts may be missing, whatever the walker put on record
-  // ahead of them: the merge must not take what the workspace held.
-  if (threadIdx.x < 2 && bars->abort_flag) p.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+  // ahead of them: the merge must not take what the workspace held.  Nor a part
+  // of an item that met a page outside the pool.
+  if (threadIdx.x < 2 && (bars->abort_flag || bars->part_lost[threadIdx.x]))
+    p.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the

@@ -473,6 +473,9 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
  * Pages without a key that some row sees (below the window) are not read, nor
  * their table entries; slots behind a sequence's last token may hold anything.
  * Device errors as fa_cache_append; a sequence with a wrong length is skipped.
+ * With a table entry outside the pool the rows that see a key of that page are
+ * not written, nor are the others of their block of up to 256 / (Hq / Hkv)
+ * tokens.
  * After FA_ERR_DEVICE_TIMEOUT every row is either right or as it was.
  * Scores and sums are float32; P is rounded to bf16 for the P V product, and
  * where an item has at most 128 rows (n_b * Hq / Hkv), to two bf16 parts.

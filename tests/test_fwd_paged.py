@@ -446,3 +446,26 @@ def test_a_training_step():
                 r = rng.standard_normal(b.shape)
                 bound = 8 * 5 * 2.0 ** -8 * np.linalg.norm(b) * np.linalg.norm(r) / np.sqrt(b.size)
                 assert abs(((a - b) * r).sum()) <= bound
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,lens,b,entry,left,causal", [
+    ([2, 3, 1], [200, 300, 100], 1, 3, range(2, 5), True),              # a few rows of one CTA
+    ([1, 1, 1], [20000, 30000, 500], 1, 900, range(1, 2), True),        # parts in many CTAs, one of them meets it
+    ([1, 1, 1], [20000, 30000, 500], 0, 1249, range(0, 1), True),       # ... the first tile of all
+    ([600, 1], [600, 40], 0, 20, range(320, 600), True),                # blocks of 64 tokens before it see nothing of it
+    ([70, 3], [2000, 900], 0, 77, range(0, 70), False),
+])
+@pytest.mark.parametrize("page", [-1, "past"])
+def test_a_page_outside_the_pool_leaves_its_rows_alone(new, lens, b, entry, left, causal, page):
+    import torch as t
+    q, kp, vp, table, cs, cu = state(new, lens, 16, 8, 2, 64, 13, causal=causal)
+    T = sum(new)
+    kw = dict(cu_seqlens=cu, max_seqlen=max(new), causal=causal)
+    good, lgood = fa.attention_forward_paged(q, kp, vp, table, cs, out_dtype=t.float32, check=True, **kw)
+    table[b, entry] = kp.shape[0] if page == "past" else page
+    o, lse = t.full((T, 8, 64), 5.0, device="cuda"), t.full((8, T), 5.0, device="cuda")
+    fa.attention_forward_paged(q, kp, vp, table, cs, out=o, lse=lse, **kw)
+    assert fa.fa_check_device_error(t.cuda.current_stream().cuda_stream) == 9
+    good[left], lgood[:, left] = 5.0, 5.0
+    assert t.equal(o, good) and t.equal(lse, lgood)
