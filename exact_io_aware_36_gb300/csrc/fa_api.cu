@@ -679,7 +679,7 @@ static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k
   if ((st = check_rows(q_out, (long long)p.Hq * p.d, p.T, p.Hq, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(k, k_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
   if ((st = check_rows(v, v_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
-  if (p.T == 0 || B == 0 || N == 0) return FA_OK;
+  if (p.T == 0 || B == 0) return FA_OK;      // N = 0 with tokens: the kernel finds whose they are
   if (!k_pages || !v_pages || !block_table || !cache_seqlens) return FA_ERR_NULL;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
   p.q = q;
@@ -762,7 +762,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   if (o_dtype != FA_FP32 && o_dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
   const long long T = cu_seqlens ? total_tokens : dense;
   if (T >= (1ll << 31) || N >= (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if (T == 0 || B == 0 || N == 0) return FA_OK;
+  if (T == 0 || B == 0) return FA_OK;        // N = 0 with tokens: the kernel finds whose they are
   if (num_pages == 0) return FA_ERR_SHAPE;
   if (!q || !k_pages || !v_pages || !block_table || !cache_seqlens || !o || !lse) return FA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;

@@ -1258,7 +1258,7 @@ int launch_impl(const PagedParams& p, cudaStream_t stream) {
   const int grid = std::min(nsm, kPagedCtas);
   kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
-  return launch_dependent(paged_merge_kernel<D>, dim3(grid, (p.part_rows + 7) / 8), dim3(256), 0, stream, p, grid);
+  return launch_dependent(paged_merge_kernel<D>, dim3(grid, std::max(1, (p.part_rows + 7) / 8)), dim3(256), 0, stream, p, grid);
 }
 
 template <int D>

@@ -469,3 +469,25 @@ def test_a_page_outside_the_pool_leaves_its_rows_alone(new, lens, b, entry, left
     assert fa.fa_check_device_error(t.cuda.current_stream().cuda_stream) == 9
     good[left], lgood[:, left] = 5.0, 5.0
     assert t.equal(o, good) and t.equal(lse, lgood)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[0, 0], [2, 0], [0, 3]])
+def test_tokens_with_a_largest_number_of_zero(new):
+    """max_seqlen 0: a sequence that brings tokens all the same is reported and nothing is written; padding alone is fine."""
+    import torch as t
+    q, kp, vp, table, cs, cu = state([max(n, 1) for n in new], [40, 70], 16, 4, 2, 64, 1)
+    cu.copy_(t.tensor([0, new[0], sum(new)], dtype=t.int32))
+    q = t.randn(6, 4, 64, device="cuda").bfloat16()
+    k = t.randn(6, 2, 64, device="cuda").bfloat16()
+    kw = dict(cu_seqlens=cu, max_seqlen=0)
+    outs = [t.full((6, 4, 64), 5.0, device="cuda"), t.full((4, 6), 5.0, device="cuda"), t.full_like(q, 5.0)]
+    pools = [x.nan_to_num_().clone() for x in (kp, vp)]
+    one = t.ones(100, 16, device="cuda")
+    for call in (lambda: fa.attention_forward_paged(q, kp, vp, table, cs, out=outs[0], lse=outs[1], **kw),
+                 lambda: fa.cache_append(k, k, kp, vp, table, cs, **kw),
+                 lambda: fa.qk_norm_rope_append(q, k, k, kp, vp, table, cs, q_out=outs[2], cos=one, sin=one, **kw)):
+        call()
+        assert fa.fa_check_device_error(t.cuda.current_stream().cuda_stream) == (8 if sum(new) else 0)
+    assert all(bool((x == 5).all()) for x in outs)
+    assert t.equal(kp, pools[0]) and t.equal(vp, pools[1])
