@@ -409,8 +409,9 @@ fa_status fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
  * sequence's last page are not read.  Several sequences may share pages (but
  * not the slots that a call writes).
  *
- * fa_cache_append writes the new tokens' keys and values: sequence b brings n_b
- * tokens, the last n_b of its L_b (cache_seqlens counts them already).
+ * fa_cache_append writes the new tokens' keys and values, bit for bit: sequence
+ * b brings n_b tokens, the last n_b of its L_b (cache_seqlens counts them
+ * already).
  *   k, v          bf16 [T, Hkv, d], token strides k_stride and v_stride
  *                 (elements)
  *   cu_seqlens    device int32 [B + 1]: b's new tokens are rows

@@ -236,3 +236,17 @@ def test_pools_past_32_bits():
     i32 = lambda *x: t.tensor(x, dtype=t.int32, device="cuda")
     fa.cache_copy(kp, vp, i32(pages - 1, pages - 2), i32(0, pages - 3), check=True)
     assert t.equal(kp[0], k[:256]) and t.equal(vp[pages - 3, :44], v[256:]) and not bool(kp[1].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_keeps_every_bit_pattern(d):
+    """Each of the 65536 bf16 patterns, -0 and every NaN among them, as a key and as a value."""
+    import torch as t
+    n = 65536 // (4 * d)
+    kp, vp, table, cs, cu, g = cache([n], [n + 5], 32, 4, d, 9)
+    every = t.arange(65536, dtype=t.int32).to(t.int16)
+    k, v = (x.view(t.bfloat16).view(n, 4, d).cuda() for x in (every, every.flip(0).contiguous()))
+    want = [P.append(bits(p), bits(x), table.cpu().numpy(), [n + 5], [0, n], 32) for p, x in ((kp, k), (vp, v))]
+    fa.cache_append(k, v, kp, vp, table, cs, check=True)
+    assert (bits(kp) == want[0]).all() and (bits(vp) == want[1]).all()
