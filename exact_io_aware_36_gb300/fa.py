@@ -469,6 +469,8 @@ def attention_forward_fp8(q, k, v, signs, *, causal: bool, scale: Optional[float
 # before them here is kept lean: devices are compared by index, shapes as
 # tuples, and a message is made only for a call that is refused.
 
+_INT_MAX = 2**31 - 1    # ctypes cuts a larger int to its low 32 bits without a word
+
 _torch = None
 
 
@@ -670,7 +672,8 @@ def _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index):
     if cu_seqlens is not None:
         if max_seqlen is None:
             raise ValueError("max_seqlen is required with cu_seqlens")
-        return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, index, (B + 1,)), B, int(max_seqlen), max_pages
+        return tp, cp, _checked("cu_seqlens", cu_seqlens, torch.int32, index, (B + 1,)), B, \
+            max(-1, min(int(max_seqlen), _INT_MAX)), max_pages
     N = T // B if B else 0
     if T != B * N:
         raise ValueError("without cu_seqlens every sequence brings the same number of tokens")
@@ -771,5 +774,5 @@ def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, 
     workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
     _run("fa_fwd_paged", index, stream, check, qp, kpool, vpool, tp, cp, cup, op, lp, B, Hq, Hkv, N, d, T,
          page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale), causal,
-         -1 if window is None else window, slopes, _dtype_code(out.dtype), wp, wbytes)
+         -1 if window is None else max(-1, min(window, _INT_MAX)), slopes, _dtype_code(out.dtype), wp, wbytes)
     return out, lse

@@ -491,3 +491,24 @@ def test_tokens_with_a_largest_number_of_zero(new):
         assert fa.fa_check_device_error(t.cuda.current_stream().cuda_stream) == (8 if sum(new) else 0)
     assert all(bool((x == 5).all()) for x in outs)
     assert t.equal(kp, pools[0]) and t.equal(vp, pools[1])
+
+
+@pytest.mark.gpu
+def test_numbers_past_32_bits_are_not_cut():
+    """A window past every length is no window; a largest number of new tokens past 32 bits is refused, or as good as any."""
+    import torch as t
+    q, kp, vp, table, cs, cu = state([2, 1], [300, 40], 16, 4, 2, 64, 1)
+    kw = dict(cu_seqlens=cu, max_seqlen=2)
+    want = fa.attention_forward_paged(q, kp, vp, table, cs, **kw)
+    for window in (2 ** 31 - 1, 2 ** 32, 2 ** 40 + 7):
+        got = fa.attention_forward_paged(q, kp, vp, table, cs, window=window, check=True, **kw)
+        assert all(t.equal(a, b) for a, b in zip(want, got))
+    for most, status in ((2 ** 32 + 2, 3), (2 ** 31, 3), (-2 ** 32 + 2, 2), (-1, 2)):
+        with pytest.raises(fa.FAError) as e:
+            fa.attention_forward_paged(q, kp, vp, table, cs, cu_seqlens=cu, max_seqlen=most)
+        assert e.value.status == status
+    k = t.randn(3, 2, 64, device="cuda").bfloat16()
+    pools = [[x.clone() for x in (kp, vp)] for _ in range(2)]
+    for pool, most in zip(pools, (2, 2 ** 32)):
+        fa.cache_append(k, k, *pool, table, cs, cu_seqlens=cu, max_seqlen=most, check=True)
+    assert all(t.equal(a.view(t.int16), b.view(t.int16)) for a, b in zip(*pools))
