@@ -512,3 +512,72 @@ def test_numbers_past_32_bits_are_not_cut():
     for pool, most in zip(pools, (2, 2 ** 32)):
         fa.cache_append(k, k, *pool, table, cs, cu_seqlens=cu, max_seqlen=most, check=True)
     assert all(t.equal(a.view(t.int16), b.view(t.int16)) for a, b in zip(*pools))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,rot,il", [(64, 32, True), (128, 128, False)])
+def test_a_training_steps_gradients_by_norm(d, rot, il):
+    """The chain of norm + rotation, attention and both backward passes on packed sequences, head by head.
+
+    Roundings to bf16 on the way, each off by at most 2^-8 of its own tensor:
+    z (which enters the scores in the forward and the backward pass, and dS K
+    or dS^T Q once more: three times), P, dS, dz and dx.  Together 7 * 2^-8 =
+    0.027 of the gradient's norm.  A 5 % error in a factor, or the gradient of
+    the norm without its mean, is more than that."""
+    import torch as t
+    from oracle import attention_fp64 as Aor
+    g = t.Generator().manual_seed(d)
+    Hq, Hkv, cu = 6, 2, np.array([0, 150, 151, 260], np.int32)
+    T = int(cu[-1])
+    qkv = t.randn(T, Hq + 2 * Hkv, d, generator=g).bfloat16().cuda()
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:].contiguous()
+    w = (1 + 0.3 * t.randn(2, d, generator=g)).cuda()
+    ang = t.arange(T, dtype=t.float64)[:, None] * 10000.0 ** (-t.arange(0, rot, 2, dtype=t.float64) / rot)
+    pos = np.concatenate([np.arange(b - a) for a, b in zip(cu, cu[1:])]).astype(np.int32)
+    kw = dict(q_weight=w[0], k_weight=w[1], cos=ang.cos().float().cuda(), sin=ang.sin().float().cuda(),
+              positions=t.from_numpy(pos).cuda(), interleaved=il)
+    do = t.randn(T, Hq, d, generator=g).bfloat16().cuda()
+    seqs = dict(causal=True, cu_seqlens=t.from_numpy(cu).cuda(), max_seqlen=150)
+    zq, zk = fa.qk_norm_rope(q, k, **kw)
+    o, lse = fa.attention_forward(zq, zk, v, out_dtype=t.float32, **seqs)
+    dzq, dzk, _ = fa.attention_backward(zq, zk, v, o, do, lse, check=True, **seqs)
+    dq, dk, dwq, dwk = fa.qk_norm_rope_backward(q, k, dzq, dzk, check=True, **kw)
+    args = (1e-6, pos, npf(kw["cos"]), npf(kw["sin"]), il)
+    norm = lambda x, ww: P.norm_rope(npf(x), npf(ww), *args)
+    rz = Aor.attention_backward(norm(q, w[0]), norm(k, w[1]), npf(v), npf(do), d ** -0.5, True, cu, None)[:2]
+    bound = 7 * 2.0 ** -8
+    off = lambda a, b: np.sqrt(((a - b) ** 2).sum() / (b ** 2).sum())
+    for x, ww, z, dx, dw in ((q, w[0], rz[0], dq, dwq), (k, w[1], rz[1], dk, dwk)):
+        want, wantw = P.norm_rope_backward(npf(x), z, npf(ww), *args)
+        per_head = [off(npf(dx)[:, h], want[:, h]) for h in range(want.shape[1])]
+        assert max(per_head) <= bound, per_head
+        assert off(npf(dw), wantw) <= bound
+        # what the bound tells apart: no mean in the norm's gradient, one wrong sign in the rotation's
+        r = 1 / np.sqrt((npf(x) ** 2).mean(-1, keepdims=True) + 1e-6)
+        dy = P.rotate(z, *args[1:], transposed=True)
+        assert off(r * dy * npf(ww), want) > bound
+        assert off(P.norm_rope_backward(npf(x), P.rotate(P.rotate(z, *args[1:]), *args[1:]), npf(ww), *args)[0], want) > bound
+
+
+@pytest.mark.gpu
+def test_two_streams_side_by_side():
+    """Calls in flight on two streams, each with a workspace of its own, give what they give alone."""
+    import torch as t
+    cases = [([1] * 9, [9000, 300, 5000, 1, 128, 7000, 2000, 64, 4000]), ([400, 1, 70], [3000, 6000, 70])]
+    calls, want = [], []
+    for seed, (new, lens) in enumerate(cases):
+        q, kp, vp, table, cs, cu = state(new, lens, 32, 8, 2, 128, seed)
+        ws = t.empty(fa.fa_fwd_paged_workspace_size(8, 2, max(new), 128), dtype=t.uint8, device="cuda")
+        calls.append(lambda stream, a=(q, kp, vp, table, cs), cu=cu, n=max(new), ws=ws: fa.attention_forward_paged(
+            *a, cu_seqlens=cu, max_seqlen=n, workspace=ws, out_dtype=t.float32, stream=stream))
+        want.append(calls[-1](None))
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(20):
+        for i, (call, stream) in enumerate(zip(calls, streams)):
+            got[i].append(call(stream))
+    t.cuda.synchronize()
+    assert fa.fa_check_device_error(None) == 0
+    for outs, (o, lse) in zip(got, want):
+        assert all(t.equal(a, o) and t.equal(b, lse) for a, b in outs)
