@@ -9,8 +9,12 @@
 //
 // The pairs run in no order, so a page written by one pair must not be read
 // or written by another.  Each block looks for such pairs itself, while its
-// loads are in flight: it compares its pair with all n (8 n bytes out of L1
-// and L2, against the chunk's 4 * kChunk).  A pair in such a conflict copies
+// loads are in flight: it compares its pair with all n, 8 n bytes out of L1
+// and L2 beside the 4 * min(page bytes, kChunk) that it moves.  So the check
+// grows with n^2, again for every chunk of a page: with pages of 32 KB it reads
+// as much as the copy moves at 16384 pairs, with pages of 2 KB (16 tokens of
+// one head of 64) at 1024, and at the limit of 131072 pairs 8 and 128 times as
+// much.  A page below kChunk also leaves part of its block idle.  A pair in such a conflict copies
 // nothing and is recorded, and so is one with a page outside the pool.
 #include <cuda_runtime.h>
 

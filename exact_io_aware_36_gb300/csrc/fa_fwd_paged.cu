@@ -15,32 +15,39 @@
 //               TMEM: one tile's softmax overlaps the other's products.
 //               Bound by the products: 32 of them take 2600 of the about 3400
 //               cycles of a step of 128 keys (two chunks of 2048 tokens over
-//               31k keys, 32 heads on 8, d = 128: 1545 us, 1345 TFLOP/s, 71 %
-//               of the measured cuBLAS rate).  What an item costs beside its
-//               steps, 14600 cycles of first loads, first softmax and
-//               epilogue, shows where items are short (8192 tokens from
-//               scratch: 500 us, 1100 TFLOP/s).
+//               31k keys, 32 heads on 8, d = 128: 1535-1575 us on the GPU by
+//               the box, 1320-1350 TFLOP/s, 70 % of the measured cuBLAS rate;
+//               1680-1745 us in a long loop of calls, where the power cap lowers
+//               the clock).  What an item costs beside its steps, 14600 cycles
+//               of first loads, first softmax and epilogue, shows where items
+//               are short (8192 tokens from scratch: 480-510 us, 1110 TFLOP/s).
+//               P is rounded to bf16 once, as in the dense forward: two parts
+//               would be half as many products again.  O is then off by 0.0023
+//               of its norm against 64 bits, of which 0.0017 are O's own bf16.
 //   one tile    (a token or a few per sequence) the same two streams share the
 //               rows and take the key tiles in turn; their O and (m, l) are
 //               merged at the end.  64 KB of K/V per 128 keys come from HBM
 //               (1.4 us of one SM's share at d = 128) against 0.8 us of
 //               products, so HBM bounds it, and the tensor cores have time to
 //               take P as two bf16 parts (high and low, 16 bits of P instead
-//               of 8): O then carries its own rounding only.  16 caches of
-//               1k-32k tokens, one new token each: 158 us, 6.35 TB/s, 94 % of
-//               the measured copy rate.
+//               of 8): O then carries its own rounding only (0.0016).  16 caches
+//               of 1k-32k tokens, one new token each: 161 us, 6.24 TB/s, 92 % of
+//               the measured copy rate.  A chunk's last block of at most one tile
+//               has these rows too, so its rows are closer than those before it.
 //
 // Work.  Lengths are known on the device alone (so a captured call can be
 // replayed with others).  Every CTA, one per SM, adds up the key tiles of all
 // items, weighed by their measured times (a tile of a two-tile item 9, of
 // another 8; what an item costs beside its tiles 36 and 16: without that the
 // SMs with the short items ended last, 658 us instead of 490 for the 8192
-// tokens), and takes an equal run of this one line.  A run begins and ends
+// tokens; measured at d = 128 and with items of one kind at a time, where the
+// other cases took no figures of their own), and takes an equal run of this one line.  A run begins and ends
 // inside items; such parts go to the workspace, two at most per CTA, and
 // paged_merge_kernel joins an item's parts in a fixed order.  No SM waits for
 // a long sequence and nothing depends on timing: the result is the same from
 // run to run.  Plan, first loads and merge are what a short call costs (one
-// sequence of 777 tokens, 16 heads of 64: 16 us).
+// sequence of 777 tokens, 16 heads of 64: 15.5 us on the GPU, where a bare
+// launch takes about 3; some 30 us through the Python call).
 //
 // Roles:
 //   warp 10    walker: finds the CTA's items one after the other and passes
@@ -64,10 +71,14 @@
 // Registers: three warps share a quarter of the SM, so a thread has 168, too
 // few for a row's 128 scores and what is done with them.  The softmax takes a
 // row's scores from TMEM 16 columns at a time, the next 16 in flight, and
-// holds P (64 registers), not S.  (Raised register limits by setmaxnreg would
-// hold S, but a first form with them did not end once in some hundred calls;
-// a dependent launch that may begin early, as the merge does here, could take
-// the registers between the lowering and the raise.)
+// holds P (64 registers), not S; the ALiBi instance with two-tile items still
+// spills 72 bytes.  (Raised register limits by setmaxnreg would hold S, but a
+// first form with them did not end once in some hundred calls.  The cause was
+// not found: the registers come from the CTA's own pool, which no other grid
+// can draw on.)
+// Waits.  Every wait for another role is bounded: a role whose wait runs out
+// sets the abort flag and leaves, the others' waits see it, and the CTA's parts
+// are taken off the record.  Rows are right or as they were.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D);
 // P overwrites S: 64 columns, or all 128 (each 16 keys' high part, then low).
 #include <cuda.h>
@@ -671,8 +682,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const bool inside = !pv_first && !pv_last && i > ib && i < ie - 1 && v_lo <= 0 && v_hi >= 128;
         if (!ONE && two && inside && cur == 3 && pv == 3) {
           // Two tiles: PV0, S0, PV1, S1.  The slot's loads were waited for by
-          // softmax warp 0 (before p_full[0]); P1 is asked for while the
-          // last products of the first batch run.
+          // softmax warp 0 (before p_full[0]), which these products rest on: a
+          // softmax without that wait would let them read a slot that is being
+          // filled.  P1 is asked for while the last products of the first batch
+          // run.
           const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
           auto batch = [&](int t, bool ask) -> bool {
             const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);

@@ -158,8 +158,8 @@ struct NormRopeParams {
 // Blocks of the gradient kernel: two per SM of GB300 (152).
 constexpr int kNormRopeBwdBlocks = 2 * 152;
 // Warps that a large batch is cut into at least: what 152 SMs hold.  More sets
-// per warp share a token's angles (7900 tokens of 48 heads: 54 us with three
-// times as many warps, 47 with these).
+// per warp share a token's angles (7900 tokens of 48 heads, with the kernel of
+// that time: 54 us with three times as many warps, 47 with these; 40.7 now).
 constexpr int kNormRopeWarps = 152 * 32;
 
 // Page copies (fa_cache.cu).

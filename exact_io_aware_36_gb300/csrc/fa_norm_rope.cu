@@ -44,8 +44,10 @@ constexpr int kWarps = kThreads / 32;
 // that leaves room for (registers).  Both cover HBM's latency: 16384 tokens of
 // 32 + 8 heads of 128 took 67 us with two bf16 sets ahead, 59 with four, 61 with
 // six and three blocks; fetching a warp's first rows ahead of its angles cost
-// registers or time (67 by loads, 60 by a prefetch into L2); float32 sets are twice as large (four: 7.9 us for 3001
-// tokens of 16 heads of 64, two: 6.6).
+// registers or time (67 by loads, 60 by a prefetch into L2).  The bf16 forms do
+// not quite fit their 64 registers: they spill 84 bytes (96 into pages, 24-32
+// with neighbouring pairs).  Float32 sets are twice as large (four: 7.9 us for
+// 3001 tokens of 16 heads of 64, two: 6.4, without spills).
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
@@ -441,7 +443,9 @@ constexpr int kBwdSmem = kWarps * kDepth<T> * 2 * 32 * 8 * sizeof(T);
 // Gradient.  A warp walks units with a fixed stride and keeps the weights'
 // sums of its columns in registers; a block writes its sum to the workspace
 // (float32 [blocks][2][D]) and norm_rope_dw_kernel adds the blocks up, both in
-// a fixed order, so the result is the same from run to run.
+// a fixed order, so the result is the same from run to run.  All of it is
+// float32: a weight's sum of N = tokens x heads terms passes through a chain of
+// about 2 N / 4864 + 95 additions at most, each off by 2^-24 of the sum so far.
 // The registers this takes leave 16 warps per SM, too few for HBM's latency
 // with loads into registers (102 us for 16384 tokens of 32 + 8 heads of 128,
 // 94 this way, when this was built).  So the loads go to shared memory, kDepth

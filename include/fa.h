@@ -381,7 +381,8 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out
  * Gradient of fa_qk_norm_rope: from its inputs and the gradients dq_out,
  * dk_out of its outputs (contiguous, of `dtype`), writes dq and dk (token
  * strides dq_stride, dk_stride) and, with norm, dq_weight and dk_weight
- * (float32 [d], summed over all tokens and heads):
+ * (float32 [d], summed over all tokens and heads in float32, in an order that
+ * the sizes alone decide):
  *     dy = R^T dz,   dw = sum dy x r,   dx = r (dy w - xh mean(dy w xh)),  xh = x r.
  * Results do not vary from run to run.  dq, dk may not overlap an input.  A
  * token whose position is out of range gets no dq, dk and adds nothing to the
@@ -478,8 +479,9 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
  * not written, nor are the others of their block of up to 256 / (Hq / Hkv)
  * tokens.
  * After FA_ERR_DEVICE_TIMEOUT every row is either right or as it was.
- * Scores and sums are float32; P is rounded to bf16 for the P V product, and
- * where an item has at most 128 rows (n_b * Hq / Hkv), to two bf16 parts.
+ * Scores and sums are float32; P is rounded to bf16 for the P V product, as in
+ * fa_fwd, and where a block of tokens has at most 128 / (Hq / Hkv) of them (a
+ * token or a few per sequence, the rest of a chunk), to two bf16 parts.
  */
 size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d);
 
