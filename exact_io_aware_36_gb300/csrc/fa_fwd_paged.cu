@@ -552,6 +552,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       for (int i = ib; i < ie; ++i, ++gs) {
         const int key0 = (hi_all - i) * 128 + lane * box_rows;
         int krow = -1;
+        bool bad = false;
         if (lane < nbox && key0 < vhi && key0 + box_rows > vlo) {
           const int page = __ldg(table + (key0 >> p.page_shift));
           if (page >= 0 && page < p.num_pages) {
@@ -559,9 +560,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           } else {
             // nothing is loaded, and the item's rows are not written
             record_status(p.status, FA_ERR_PAGE);
-            *lost = 1;
+            bad = true;
           }
         }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) *lost = 1;      // (the lane whose arrival publishes it)
         const int sl = gs % C::NS;
         if (gs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) break;
         const int boxes = __popc(__ballot_sync(0xffffffffu, krow >= 0)) + __popc(__ballot_sync(0xffffffffu, vrow >= 0));
