@@ -1106,7 +1106,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // Only the time limit ends this wait, not the abort flag: a row's two
         // halves are written by both streams' warps or by neither.
         const uint32_t par = njoin++ & 1;
-        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->joined, par)) && !wait_warp_drain(&bars->joined, par)) break;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->joined, par)) && !wait_warp_drain(&bars->joined, par)) {
+          if (lane == 0) {
+            *wc.abort_flag = 1;
+            record_status(p.status, FA_ERR_DEVICE_TIMEOUT);
+          }
+          break;
+        }
         const float mo = oth[0];
         const float M = fmaxf(m_ref, mo);
         w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
