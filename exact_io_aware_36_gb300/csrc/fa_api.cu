@@ -661,8 +661,9 @@ fa_status fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
   return fa::launch_norm_rope_bwd(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
-// fa_cache_append (no q, no norm, no rotation) and fa_qk_norm_rope_append.
-static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k, const void* v,
+// fa_cache_append (no q, no norm, no rotation) and fa_qk_norm_rope_append; with
+// `scales`, {of the key pages, of the value pages}, into pages of e4m3 codes.
+static fa_status append_impl(fa::NormRopeParams& p, void* const* scales, const void* q, const void* k, const void* v,
                              void* q_out, void* k_pages, void* v_pages, long long q_stride,
                              long long k_stride, long long v_stride, const int32_t* block_table,
                              const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B, int N,
@@ -681,7 +682,9 @@ static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k
   if ((st = check_rows(v, v_stride, p.T, p.Hkv, p.d, 2)) != FA_OK) return st;
   if (p.T == 0 || B == 0) return FA_OK;      // N = 0 with tokens: the kernel finds whose they are
   if (!k_pages || !v_pages || !block_table || !cache_seqlens) return FA_ERR_NULL;
+  if (scales && (!scales[0] || !scales[1])) return FA_ERR_NULL;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if (scales && (!aligned16(scales[0]) || !aligned16(scales[1]))) return FA_ERR_ALIGN;
   p.q = q;
   p.k = k;
   p.v = v;
@@ -696,6 +699,13 @@ static fa_status append_impl(fa::NormRopeParams& p, const void* q, const void* k
   p.cu_seqlens = cu_seqlens;
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
+  if (scales) {
+    fa::QuantAppendParams qp = {};
+    qp.n = p;
+    qp.k_scales = static_cast<uint8_t*>(scales[0]);
+    qp.v_scales = static_cast<uint8_t*>(scales[1]);
+    return fa::launch_append_fp8(qp, p.Hq > 0, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+  }
   return fa::launch_norm_rope_pages(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -707,7 +717,7 @@ fa_status fa_cache_append(const void* k, const void* v, void* k_pages, void* v_p
   fa::NormRopeParams p = {};
   const fa_status st = norm_rope_args(&p, nullptr, nullptr, 0.f, nullptr, nullptr, total_tokens, 0, Hkv, d, 0, 0, 0);
   if (st != FA_OK) return st;
-  return append_impl(p, nullptr, k, v, nullptr, k_pages, v_pages, 0, k_stride, v_stride, block_table,
+  return append_impl(p, nullptr, nullptr, k, v, nullptr, k_pages, v_pages, 0, k_stride, v_stride, block_table,
                      cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
 }
 
@@ -725,7 +735,42 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, vo
   if (st != FA_OK) return st;
   if (Hq == 0) return FA_ERR_SHAPE;
   if (!q_weight && rot_dim == 0) return FA_ERR_UNSUPPORTED;
-  return append_impl(p, q, k, v, q_out, k_pages, v_pages, q_stride, k_stride, v_stride, block_table,
+  return append_impl(p, nullptr, q, k, v, q_out, k_pages, v_pages, q_stride, k_stride, v_stride, block_table,
+                     cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
+}
+
+fa_status fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pages,
+                              void* k_scales, void* v_scales, long long k_stride,
+                              long long v_stride, const int32_t* block_table,
+                              const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B,
+                              int Hkv, int N, int d, long long total_tokens, int page_size,
+                              int num_pages, int max_pages, void* stream) {
+  fa::NormRopeParams p = {};
+  void* const scales[2] = {k_scales, v_scales};
+  const fa_status st = norm_rope_args(&p, nullptr, nullptr, 0.f, nullptr, nullptr, total_tokens, 0, Hkv, d, 0, 0, 0);
+  if (st != FA_OK) return st;
+  return append_impl(p, scales, nullptr, k, v, nullptr, k_pages, v_pages, 0, k_stride, v_stride, block_table,
+                     cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
+}
+
+fa_status fa_qk_norm_rope_append_fp8(const void* q, const void* k, const void* v, void* q_out,
+                                     void* k_pages, void* v_pages, void* k_scales,
+                                     void* v_scales, long long q_stride, long long k_stride,
+                                     long long v_stride, const float* q_weight,
+                                     const float* k_weight, float eps, const float* cos,
+                                     const float* sin, const int32_t* block_table,
+                                     const int32_t* cache_seqlens, const int32_t* cu_seqlens,
+                                     int B, int Hq, int Hkv, int N, int d,
+                                     long long total_tokens, int rot_dim, int max_pos,
+                                     int interleaved, int page_size, int num_pages,
+                                     int max_pages, void* stream) {
+  fa::NormRopeParams p = {};
+  void* const scales[2] = {k_scales, v_scales};
+  const fa_status st = norm_rope_args(&p, q_weight, k_weight, eps, cos, sin, total_tokens, Hq, Hkv, d, rot_dim, max_pos, interleaved);
+  if (st != FA_OK) return st;
+  if (Hq == 0) return FA_ERR_SHAPE;
+  if (!q_weight && rot_dim == 0) return FA_ERR_UNSUPPORTED;
+  return append_impl(p, scales, q, k, v, q_out, k_pages, v_pages, q_stride, k_stride, v_stride, block_table,
                      cache_seqlens, cu_seqlens, B, N, total_tokens, page_size, num_pages, max_pages, stream);
 }
 
@@ -740,13 +785,15 @@ size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d) {
          round256(2 * fa::kPagedCtas * sizeof(int4));
 }
 
-fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
-                       const int32_t* block_table, const int32_t* cache_seqlens,
-                       const int32_t* cu_seqlens, void* o, float* lse, int B, int Hq, int Hkv,
-                       int N, int d, long long total_tokens, int page_size, int num_pages,
-                       int max_pages, float scale, int causal, int window,
-                       const float* alibi_slopes, fa_dtype o_dtype, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+// fa_fwd_paged, and with `scales` ({of the keys, of the values}) fa_fwd_paged_fp8.
+static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pages,
+                            const void* const* scales, const int32_t* block_table,
+                            const int32_t* cache_seqlens, const int32_t* cu_seqlens, void* o,
+                            float* lse, int B, int Hq, int Hkv, int N, int d,
+                            long long total_tokens, int page_size, int num_pages, int max_pages,
+                            float scale, int causal, int window, const float* alibi_slopes,
+                            fa_dtype o_dtype, void* workspace, size_t workspace_bytes,
+                            void* stream) {
   if (Hq <= 0 || Hkv <= 0 || d <= 0 || total_tokens < 0) return FA_ERR_SHAPE;
   if (Hq % Hkv != 0) return FA_ERR_SHAPE;
   fa::NormRopeParams sizes = {};
@@ -765,7 +812,9 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   if (T == 0 || B == 0) return FA_OK;        // N = 0 with tokens: the kernel finds whose they are
   if (num_pages == 0) return FA_ERR_SHAPE;
   if (!q || !k_pages || !v_pages || !block_table || !cache_seqlens || !o || !lse) return FA_ERR_NULL;
+  if (scales && (!scales[0] || !scales[1])) return FA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if (scales && (!aligned16(scales[0]) || !aligned16(scales[1]))) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(o) & 31u) != 0) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_ALIGN;
   if (!workspace || workspace_bytes < fa_fwd_paged_workspace_size(Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
@@ -810,11 +859,48 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   p.scale_log2 = scale * fa::kLog2e;
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
+  if (scales) {
+    p.k_scales = static_cast<const uint8_t*>(scales[0]);
+    p.v_scales = static_cast<const uint8_t*>(scales[1]);
+    return fa::launch_fwd_paged_fp8(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+  }
   return fa::launch_fwd_paged(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
-fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
-                        int n, int num_pages, int page_size, int Hkv, int d, void* stream) {
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                       const int32_t* block_table, const int32_t* cache_seqlens,
+                       const int32_t* cu_seqlens, void* o, float* lse, int B, int Hq, int Hkv,
+                       int N, int d, long long total_tokens, int page_size, int num_pages,
+                       int max_pages, float scale, int causal, int window,
+                       const float* alibi_slopes, fa_dtype o_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return paged_impl(q, k_pages, v_pages, nullptr, block_table, cache_seqlens, cu_seqlens, o, lse, B,
+                    Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages, scale, causal,
+                    window, alibi_slopes, o_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d) {
+  return fa_fwd_paged_workspace_size(Hq, Hkv, N, d);
+}
+
+fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                           const void* k_scales, const void* v_scales, const int32_t* block_table,
+                           const int32_t* cache_seqlens, const int32_t* cu_seqlens, void* o,
+                           float* lse, int B, int Hq, int Hkv, int N, int d,
+                           long long total_tokens, int page_size, int num_pages, int max_pages,
+                           float scale, int causal, int window, const float* alibi_slopes,
+                           fa_dtype o_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const void* const scales[2] = {k_scales, v_scales};
+  return paged_impl(q, k_pages, v_pages, scales, block_table, cache_seqlens, cu_seqlens, o, lse, B,
+                    Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages, scale, causal,
+                    window, alibi_slopes, o_dtype, workspace, workspace_bytes, stream);
+}
+
+// fa_cache_copy, and with `scales` ({of the keys, of the values}) fa_cache_copy_fp8.
+static fa_status copy_impl(void* k_pages, void* v_pages, void* const* scales, const int32_t* src,
+                           const int32_t* dst, int n, int num_pages, int page_size, int Hkv, int d,
+                           void* stream) {
   if (n < 0 || Hkv <= 0 || d <= 0) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   // every block looks through all n pairs
@@ -824,18 +910,37 @@ fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const 
   if (st != FA_OK) return st;
   if (n == 0) return FA_OK;
   if (!k_pages || !v_pages || !src || !dst) return FA_ERR_NULL;
+  if (scales && (!scales[0] || !scales[1])) return FA_ERR_NULL;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if (scales && (!aligned16(scales[0]) || !aligned16(scales[1]))) return FA_ERR_ALIGN;
   fa::CachePagesCopy p = {};
   p.k = k_pages;
   p.v = v_pages;
+  if (scales) {
+    p.k_scales = static_cast<uint8_t*>(scales[0]);
+    p.v_scales = static_cast<uint8_t*>(scales[1]);
+  }
   p.src = src;
   p.dst = dst;
   p.n = n;
   p.num_pages = num_pages;
-  p.page_bytes = (long long)page_size * Hkv * d * 2;
+  p.page_bytes = (long long)page_size * Hkv * d * (scales ? 1 : 2);
+  p.scale_bytes = page_size / 16 * Hkv;
   p.status = status_ptr();
   if (!p.status) return FA_ERR_CUDA;
   return fa::launch_copy_pages(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const int32_t* dst,
+                        int n, int num_pages, int page_size, int Hkv, int d, void* stream) {
+  return copy_impl(k_pages, v_pages, nullptr, src, dst, n, num_pages, page_size, Hkv, d, stream);
+}
+
+fa_status fa_cache_copy_fp8(void* k_pages, void* v_pages, void* k_scales, void* v_scales,
+                            const int32_t* src, const int32_t* dst, int n, int num_pages,
+                            int page_size, int Hkv, int d, void* stream) {
+  void* const scales[2] = {k_scales, v_scales};
+  return copy_impl(k_pages, v_pages, scales, src, dst, n, num_pages, page_size, Hkv, d, stream);
 }
 
 fa_status fa_selftest_wait_timeout(unsigned long long limit_ns, void* stream) {

@@ -28,6 +28,9 @@ constexpr int kThreads = 256;
 constexpr int kPer = 8;                              // 16-byte pieces per thread and pool
 constexpr int kChunk = kThreads * kPer * 16;         // bytes per block and pool
 
+// SCALES: the pages hold codes, and their scales go with them (scale_bytes of
+// each page, a few at a time by the block of the page's first chunk).
+template <bool SCALES>
 __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CachePagesCopy p) {
   const int i = (int)(blockIdx.x / p.chunks);
   const long long off = (long long)(blockIdx.x % p.chunks) * kChunk;
@@ -47,6 +50,12 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CachePagesCo
     for (int u = 0; u < kPer; ++u)
       if (u * kThreads + threadIdx.x < n16) x[v][u] = __ldcs(at + u * kThreads + threadIdx.x);
   }
+  uint8_t sc[2] = {0, 0};
+  const bool scales = SCALES && off == 0;
+  if (scales && threadIdx.x < p.scale_bytes) {
+    sc[0] = p.k_scales[(long long)s * p.scale_bytes + threadIdx.x];
+    sc[1] = p.v_scales[(long long)s * p.scale_bytes + threadIdx.x];
+  }
   bool clash = false;
   for (int j = threadIdx.x; j < p.n; j += kThreads) {
     const int sj = __ldg(p.src + j), dj = __ldg(p.dst + j);
@@ -63,6 +72,15 @@ __global__ void __launch_bounds__(kThreads) copy_pages_kernel(const CachePagesCo
     for (int u = 0; u < kPer; ++u)
       if (u * kThreads + threadIdx.x < n16) __stcs(at + u * kThreads + threadIdx.x, x[v][u]);
   }
+  if (scales)
+    for (int i = threadIdx.x; i < p.scale_bytes; i += kThreads) {
+      if (i >= kThreads) {
+        sc[0] = p.k_scales[(long long)s * p.scale_bytes + i];
+        sc[1] = p.v_scales[(long long)s * p.scale_bytes + i];
+      }
+      p.k_scales[(long long)d * p.scale_bytes + i] = sc[0];
+      p.v_scales[(long long)d * p.scale_bytes + i] = sc[1];
+    }
 }
 
 }  // namespace
@@ -71,7 +89,8 @@ int launch_copy_pages(CachePagesCopy p, void* stream) {
   p.chunks = (unsigned)((p.page_bytes + kChunk - 1) / kChunk);
   const long long grid = (long long)p.n * p.chunks;
   if (grid >= (1ll << 31)) return (int)cudaErrorInvalidConfiguration;
-  copy_pages_kernel<<<(unsigned)grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  auto kern = p.k_scales ? copy_pages_kernel<true> : copy_pages_kernel<false>;
+  kern<<<(unsigned)grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return (int)cudaGetLastError();
 }
 

@@ -155,6 +155,21 @@ struct NormRopeParams {
   int B, N, page_size, page_shift, num_pages, max_pages;
 };
 
+// New tokens' k and v quantized into pages of e4m3 codes (fa_cache_fp8.cu).
+struct QuantAppendParams {
+  NormRopeParams n;
+  uint8_t* k_scales;           // [num_pages, page_size / 16, Hkv]: exponent + 127
+  uint8_t* v_scales;
+  int per_seq, blocks;         // block numbers per sequence (0: by place in cu_seqlens), and of all
+  unsigned block_ctas;
+};
+
+// Exponents that a scale of a cache in 8 bits takes.  Below the least, a
+// block's largest code is a subnormal one or zero; codes times the largest
+// stay below bf16's infinity.
+constexpr int kScaleLow = -100;
+constexpr int kScaleHigh = 119;
+
 // Blocks of the gradient kernel: two per SM of GB300 (152).
 constexpr int kNormRopeBwdBlocks = 2 * 152;
 // Warps that a large batch is cut into at least: what 152 SMs hold.  More sets
@@ -167,10 +182,13 @@ constexpr int kCopyMaxPairs = 1 << 17;
 struct CachePagesCopy {
   void* k;
   void* v;
+  uint8_t* k_scales;           // [num_pages, scale_bytes], or nullptr
+  uint8_t* v_scales;
   const int32_t* src;          // [n]
   const int32_t* dst;          // [n]
   unsigned int* status;
   long long page_bytes;
+  int scale_bytes;             // scales of one page
   int n, num_pages;
   unsigned chunks;
 };
@@ -178,8 +196,10 @@ struct CachePagesCopy {
 // Attention of new tokens over a cache in pages (fa_fwd_paged.cu).
 struct PagedParams {
   const void* q;               // bf16 [T, Hq, d]
-  const void* k;               // bf16 [num_pages, page_size, Hkv, d]
+  const void* k;               // [num_pages, page_size, Hkv, d]: bf16, or e4m3 codes
   const void* v;
+  const uint8_t* k_scales;     // codes: [num_pages, page_size / 16, Hkv], exponent + 127
+  const uint8_t* v_scales;
   void* o;                     // [T, Hq, d], fp32 or bf16
   float* lse;                  // [Hq, T]
   const int32_t* block_table;  // [B, max_pages]
@@ -228,8 +248,10 @@ int launch_fwd_fp8(const AttnParams& p, void* stream);
 int launch_norm_rope(const NormRopeParams& p, void* stream);
 int launch_norm_rope_pages(const NormRopeParams& p, void* stream);    // into cache pages
 int launch_norm_rope_bwd(const NormRopeParams& p, void* stream);      // rows, then the weights' sums
+int launch_append_fp8(const QuantAppendParams& p, bool turn, void* stream);   // turn: with q, norm and rotation
 int launch_copy_pages(CachePagesCopy p, void* stream);
 int launch_fwd_paged(const PagedParams& p, void* stream);             // runs + merge of parts
+int launch_fwd_paged_fp8(const PagedParams& p, void* stream);         // the same over e4m3 codes
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__

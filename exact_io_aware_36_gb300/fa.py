@@ -31,7 +31,8 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_stage", "fa_bwd_workspace_size", "fa_chec
            "fa_fwd_fp8", "fa_host_cache_stats", "fa_bwd_workspace_size_gqa", "fa_bwd_dkdv_split",
            "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
            "fa_qk_norm_rope_append", "fa_cache_append", "fa_cache_copy", "fa_fwd_paged",
-           "fa_fwd_paged_workspace_size")
+           "fa_fwd_paged_workspace_size", "fa_cache_append_fp8", "fa_qk_norm_rope_append_fp8",
+           "fa_cache_copy_fp8", "fa_fwd_paged_fp8", "fa_fwd_paged_fp8_workspace_size")
 FA_BWD_PREPROCESS, FA_BWD_DKDV, FA_BWD_DQ_CONVERT = 0, 1, 2
 
 
@@ -108,6 +109,13 @@ def load(path: Optional[str] = None):
     lib.fa_fwd_paged.restype = i
     lib.fa_cache_copy.argtypes = [vp, vp, vp, vp, i, i, i, i, i, vp]
     lib.fa_cache_copy.restype = i
+    # the calls over a cache in 8 bits: two more pointers, the scales, behind the pages
+    for name, pages in (("fa_cache_append", 4), ("fa_qk_norm_rope_append", 6), ("fa_cache_copy", 2), ("fa_fwd_paged", 3)):
+        a = getattr(lib, name).argtypes
+        getattr(lib, name + "_fp8").argtypes = a[:pages] + [vp, vp] + a[pages:]
+        getattr(lib, name + "_fp8").restype = i
+    lib.fa_fwd_paged_fp8_workspace_size.argtypes = [i, i, i, i]
+    lib.fa_fwd_paged_fp8_workspace_size.restype = sz
     lib.fa_check_device_error.argtypes = [vp]
     lib.fa_check_device_error.restype = i
     lib.fa_status_string.argtypes = [i]
@@ -247,6 +255,44 @@ def fa_fwd_paged(q, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens, o,
                                B, Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages,
                                scale, int(causal), int(window), alibi_slopes, o_dtype, workspace,
                                workspace_bytes, stream)
+
+
+def fa_cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, k_stride, v_stride, block_table,
+                        cache_seqlens, cu_seqlens, B, Hkv, N, d, total_tokens, page_size, num_pages,
+                        max_pages, stream) -> int:
+    return load().fa_cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, k_stride, v_stride,
+                                      block_table, cache_seqlens, cu_seqlens, B, Hkv, N, d,
+                                      total_tokens, page_size, num_pages, max_pages, stream)
+
+
+def fa_qk_norm_rope_append_fp8(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales, q_stride,
+                               k_stride, v_stride, q_weight, k_weight, eps, cos, sin, block_table,
+                               cache_seqlens, cu_seqlens, B, Hq, Hkv, N, d, total_tokens, rot_dim,
+                               max_pos, interleaved, page_size, num_pages, max_pages, stream) -> int:
+    return load().fa_qk_norm_rope_append_fp8(q, k, v, q_out, k_pages, v_pages, k_scales, v_scales,
+                                             q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos,
+                                             sin, block_table, cache_seqlens, cu_seqlens, B, Hq, Hkv, N,
+                                             d, total_tokens, rot_dim, max_pos, int(interleaved),
+                                             page_size, num_pages, max_pages, stream)
+
+
+def fa_cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, n, num_pages, page_size, Hkv, d,
+                      stream) -> int:
+    return load().fa_cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, n, num_pages,
+                                    page_size, Hkv, d, stream)
+
+
+def fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) -> int:
+    return load().fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d)
+
+
+def fa_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens, cu_seqlens, o,
+                     lse, B, Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages, scale, causal,
+                     window, alibi_slopes, o_dtype, workspace, workspace_bytes, stream) -> int:
+    return load().fa_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens,
+                                   cu_seqlens, o, lse, B, Hq, Hkv, N, d, total_tokens, page_size,
+                                   num_pages, max_pages, scale, int(causal), int(window), alibi_slopes,
+                                   o_dtype, workspace, workspace_bytes, stream)
 
 
 def fa_bwd_workspace_size(B, Hq, N, d, total_tokens) -> int:
@@ -773,6 +819,113 @@ def attention_forward_paged(q, k_pages, v_pages, block_table, cache_seqlens, *, 
     wbytes = fa_fwd_paged_workspace_size(Hq, Hkv, N, d) if workspace is None else workspace.numel()
     workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
     _run("fa_fwd_paged", index, stream, check, qp, kpool, vpool, tp, cp, cup, op, lp, B, Hq, Hkv, N, d, T,
+         page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale), causal,
+         -1 if window is None else max(-1, min(window, _INT_MAX)), slopes, _dtype_code(out.dtype), wp, wbytes)
+    return out, lse
+
+
+def _pages_fp8(k_pages, v_pages, k_scales, v_scales, index):
+    """(the four pointers, num_pages, page_size, Hkv, d) of pools of codes and their scales."""
+    torch = _torch or _import_torch()
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages: [num_pages, page_size, Hkv, d] expected")
+    codes = torch.uint8 if k_pages.dtype is torch.uint8 else torch.float8_e4m3fn
+    scale = torch.uint8 if k_scales.dtype is torch.uint8 else torch.float8_e8m0fnu
+    num_pages, page_size, Hkv, d = k_pages.shape
+    shape = (num_pages, page_size // 16, Hkv)
+    return (_checked("k_pages", k_pages, codes, index), _checked("v_pages", v_pages, codes, index, k_pages.shape),
+            _checked("k_scales", k_scales, scale, index, shape), _checked("v_scales", v_scales, scale, index, shape),
+            num_pages, page_size, Hkv, d)
+
+
+def cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens, *,
+                     cu_seqlens=None, max_seqlen: Optional[int] = None, stream=None,
+                     check: bool = False):
+    """Quantize the new tokens' k and v into the pages of a cache in 8 bits
+    through ``fa_cache_append_fp8``.
+
+    k_pages, v_pages: codes, float8_e4m3fn or uint8 [num_pages, page_size, Hkv,
+    d]; k_scales, v_scales: the exponents (plus 127) of the powers of two of every
+    16 slots and head, float8_e8m0fnu or uint8 [num_pages, page_size / 16, Hkv].
+    The other arguments as ``cache_append``.  A block of 16 slots that gets
+    tokens takes the least scale that holds them and the older tokens before
+    them (see include/fa.h).
+    """
+    torch = _torch or _import_torch()
+    index = _gpu(k, stream)
+    kp, ks = _rows("k", k, torch.bfloat16, index)
+    vp, vs = _rows("v", v, torch.bfloat16, index, k.shape)
+    T, Hkv, d = k.shape
+    *pools, num_pages, page_size, Hp, dp = _pages_fp8(k_pages, v_pages, k_scales, v_scales, index)
+    if (Hp, dp) != (Hkv, d):
+        raise ValueError("the pages have other heads than k")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    _run("fa_cache_append_fp8", index, stream, check, kp, vp, *pools, ks, vs, tp, cp, cup, B, Hkv, N, d, T,
+         page_size, num_pages, max_pages)
+
+
+def qk_norm_rope_append_fp8(q, k, v, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens, *,
+                            cu_seqlens=None, max_seqlen: Optional[int] = None, q_weight=None,
+                            k_weight=None, eps: float = 1e-6, cos=None, sin=None,
+                            interleaved: bool = False, q_out=None, stream=None, check: bool = False):
+    """``qk_norm_rope`` of new tokens and ``cache_append_fp8`` of their k and v in
+    one launch (``fa_qk_norm_rope_append_fp8``); k is quantized from float32.
+    Returns q_out [T, Hq, d] in bf16, ready for ``attention_forward_paged_fp8``
+    over the same pages."""
+    torch = _torch or _import_torch()
+    index = _gpu(q, stream)
+    qp, qs = _rows("q", q, torch.bfloat16, index)
+    kp, ks = _rows("k", k, torch.bfloat16, index)
+    vp, vs = _rows("v", v, torch.bfloat16, index, k.shape)
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    *pools, num_pages, page_size, Hp, dp = _pages_fp8(k_pages, v_pages, k_scales, v_scales, index)
+    if k.shape[0] != T or k.shape[2] != d or (Hp, dp) != (Hkv, d):
+        raise ValueError("q, k and the pages must have the same tokens, key heads and head dimension")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    ang = _angles(q_weight, k_weight, cos, sin, d, index)
+    q_out, qop = _out("q_out", q_out, q, (T, Hq, d), q.dtype, index, stream)
+    _run("fa_qk_norm_rope_append_fp8", index, stream, check, qp, kp, vp, qop, *pools, qs, ks, vs, ang[0],
+         ang[1], float(eps), ang[2], ang[3], tp, cp, cup, B, Hq, Hkv, N, d, T, ang[4], ang[5],
+         interleaved, page_size, num_pages, max_pages)
+    return q_out
+
+
+def cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, *, stream=None, check: bool = False):
+    """``cache_copy`` of pages of codes and their scales through ``fa_cache_copy_fp8``."""
+    torch = _torch or _import_torch()
+    index = _gpu(k_pages, stream)
+    *pools, num_pages, page_size, Hkv, d = _pages_fp8(k_pages, v_pages, k_scales, v_scales, index)
+    n = src.numel()
+    _run("fa_cache_copy_fp8", index, stream, check, *pools,
+         _checked("src", src, torch.int32, index, (n,)), _checked("dst", dst, torch.int32, index, (n,)),
+         n, num_pages, page_size, Hkv, d)
+
+
+def attention_forward_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens, *,
+                                cu_seqlens=None, max_seqlen: Optional[int] = None, causal: bool = True,
+                                scale: Optional[float] = None, alibi_slopes=None,
+                                window: Optional[int] = None, out=None, lse=None, out_dtype=None,
+                                workspace=None, stream=None, check: bool = False):
+    """``attention_forward_paged`` over a cache in 8 bits (pools and scales as
+    ``cache_append_fp8``) through ``fa_fwd_paged_fp8``.  q: bf16 [T, Hq, d].
+    Returns (o, lse) as ``attention_forward_paged``."""
+    torch = _torch or _import_torch()
+    index = _gpu(q, stream)
+    if q.dim() != 3:
+        raise ValueError("q: [T, Hq, d] expected")
+    T, Hq, d = q.shape
+    qp = _checked("q", q, torch.bfloat16, index)
+    *pools, num_pages, page_size, Hkv, dp = _pages_fp8(k_pages, v_pages, k_scales, v_scales, index)
+    if dp != d:
+        raise ValueError("q and the pages must have the same head dimension")
+    tp, cp, cup, B, N, max_pages = _table(block_table, cache_seqlens, cu_seqlens, max_seqlen, T, index)
+    slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, index, (Hq,))
+    out, op = _out("out", out, q, (T, Hq, d), (out_dtype or q.dtype) if out is None else out.dtype, index, stream)
+    lse, lp = _out("lse", lse, q, (Hq, T), torch.float32, index, stream)
+    wbytes = fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) if workspace is None else workspace.numel()
+    workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
+    _run("fa_fwd_paged_fp8", index, stream, check, qp, *pools, tp, cp, cup, op, lp, B, Hq, Hkv, N, d, T,
          page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale), causal,
          -1 if window is None else max(-1, min(window, _INT_MAX)), slopes, _dtype_code(out.dtype), wp, wbytes)
     return out, lse

@@ -506,6 +506,73 @@ fa_status fa_cache_copy(void* k_pages, void* v_pages, const int32_t* src, const 
                         int n, int num_pages, int page_size, int Hkv, int d, void* stream);
 
 /*
+ * A cache in 8 bits.  The pools hold e4m3 codes, uint8 [num_pages, page_size,
+ * Hkv, d], and every block of 16 slots of a page has one power of two per
+ * head, uint8 [num_pages, page_size / 16, Hkv]: the byte s stands for
+ * 2^(s - 127), and a code c for the value c 2^(s - 127).  Bytes above 246 count
+ * as 246.  Pages, tables and lengths are otherwise those of the cache in bf16,
+ * and so are the checks and device errors of the calls.  Scales start on a
+ * 16-byte boundary.
+ *
+ * fa_cache_append_fp8 writes the new tokens' keys and values.  A block that gets
+ * tokens takes the least 2^e, -100 <= e <= 119, with max|x| <= 448 2^e over the
+ * finite elements written there (e = -100 without any), and the codes are
+ * e4m3(x 2^-e): nearest, ties to even, at most 448; an infinity or NaN becomes
+ * NaN.  Where older tokens lie before the new ones in the block, e does not
+ * fall below the block's own; if it rises, their codes are rounded to the new
+ * scale (exact but for codes that become subnormal).  So, unlike in bf16, a
+ * call may rewrite the older tokens of the block that a sequence's first new
+ * token falls into: sequences that share a page which is still written to must
+ * share it up to a whole block, and blocks that a call writes belong to one
+ * sequence of the batch.  Slots behind the new tokens are left as they are.
+ *
+ * fa_qk_norm_rope_append_fp8 is fa_qk_norm_rope_append into such pages: q_out is
+ * bf16, k is quantized from its float32 values, without a rounding to bf16 in
+ * between.  One launch.
+ *
+ * fa_cache_copy_fp8 copies whole pages with their scales.
+ */
+fa_status fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pages,
+                              void* k_scales, void* v_scales, long long k_stride,
+                              long long v_stride, const int32_t* block_table,
+                              const int32_t* cache_seqlens, const int32_t* cu_seqlens, int B,
+                              int Hkv, int N, int d, long long total_tokens, int page_size,
+                              int num_pages, int max_pages, void* stream);
+
+fa_status fa_qk_norm_rope_append_fp8(const void* q, const void* k, const void* v, void* q_out,
+                                     void* k_pages, void* v_pages, void* k_scales,
+                                     void* v_scales, long long q_stride, long long k_stride,
+                                     long long v_stride, const float* q_weight,
+                                     const float* k_weight, float eps, const float* cos,
+                                     const float* sin, const int32_t* block_table,
+                                     const int32_t* cache_seqlens, const int32_t* cu_seqlens,
+                                     int B, int Hq, int Hkv, int N, int d,
+                                     long long total_tokens, int rot_dim, int max_pos,
+                                     int interleaved, int page_size, int num_pages,
+                                     int max_pages, void* stream);
+
+fa_status fa_cache_copy_fp8(void* k_pages, void* v_pages, void* k_scales, void* v_scales,
+                            const int32_t* src, const int32_t* dst, int n, int num_pages,
+                            int page_size, int Hkv, int d, void* stream);
+
+/*
+ * fa_fwd_paged over a cache in 8 bits: the attention of the values that the
+ * codes stand for, with fa_fwd_paged's arguments, masks, rows and errors and a
+ * workspace of fa_fwd_paged_fp8_workspace_size bytes.  Only q, P and O are in
+ * 16 bits beside the codes.
+ */
+size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d);
+
+fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                           const void* k_scales, const void* v_scales,
+                           const int32_t* block_table, const int32_t* cache_seqlens,
+                           const int32_t* cu_seqlens, void* o, float* lse, int B, int Hq,
+                           int Hkv, int N, int d, long long total_tokens, int page_size,
+                           int num_pages, int max_pages, float scale, int causal, int window,
+                           const float* alibi_slopes, fa_dtype o_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Error reporting of this library (the pages have no counterpart; their
  * usage contract only names the inputs a call takes).
  * Synchronises `stream`, then reads and clears the current device's status
