@@ -778,11 +778,42 @@ fa_status fa_qk_norm_rope_append_fp8(const void* q, const void* k, const void* v
 // tokens, times the group's heads.
 static long long paged_part_rows(int group, int N) { return (long long)std::min(2 * (128 / group), N) * group; }
 
+// Workspace for parts of up to `part_rows` rows, and its places in p.
+static size_t paged_parts(fa::PagedParams* p, char* ws, long long part_rows, int d) {
+  const size_t rows = 2 * (size_t)fa::kPagedCtas * part_rows;
+  const size_t o = round256(rows * d * sizeof(float)), ml = round256(rows * 4 * sizeof(float));
+  if (p) {
+    p->part_rows = (int)part_rows;
+    p->part_o = reinterpret_cast<float*>(ws);
+    p->part_ml = reinterpret_cast<float*>(ws + o);
+    p->part_meta = reinterpret_cast<int4*>(ws + o + ml);
+  }
+  return o + ml + round256(2 * fa::kPagedCtas * sizeof(int4));
+}
+
 size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d) {
   if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || N < 0 || d <= 0) return 0;
-  const size_t rows = 2 * (size_t)fa::kPagedCtas * paged_part_rows(Hq / Hkv, N);
-  return round256(rows * d * sizeof(float)) + round256(rows * 4 * sizeof(float)) +
-         round256(2 * fa::kPagedCtas * sizeof(int4));
+  return paged_parts(nullptr, nullptr, paged_part_rows(Hq / Hkv, N), d);
+}
+
+// Over codes, sequences of up to this many rows per kv head go to the kernel for
+// few rows: 32 where no sequence brings more (then it is the call's only one),
+// else what one token of each brings, in 16 or 32; 0 with larger groups.
+static int paged_few_rows(int group, int N) {
+  const long long rows = (long long)N * group;
+  if (rows <= 32) return rows <= 16 ? 16 : 32;
+  return group <= 16 ? 16 : group <= 32 ? 32 : 0;
+}
+
+static long long paged_few_part_rows(int group, int N) { return (long long)std::min(paged_few_rows(group, N) / group, N) * group; }
+
+size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || N < 0 || d <= 0) return 0;
+  const int group = Hq / Hkv, few = paged_few_rows(group, N);
+  size_t n = 0;
+  if (few) n += paged_parts(nullptr, nullptr, paged_few_part_rows(group, N), d);
+  if ((long long)N * group > few) n += paged_parts(nullptr, nullptr, paged_part_rows(group, N), d);
+  return n;
 }
 
 // fa_fwd_paged, and with `scales` ({of the keys, of the values}) fa_fwd_paged_fp8.
@@ -817,7 +848,8 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
   if (scales && (!aligned16(scales[0]) || !aligned16(scales[1]))) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(o) & 31u) != 0) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_ALIGN;
-  if (!workspace || workspace_bytes < fa_fwd_paged_workspace_size(Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
+  const size_t need = scales ? fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) : fa_fwd_paged_workspace_size(Hq, Hkv, N, d);
+  if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
   fa::PagedParams p = {};
   p.q = q;
@@ -837,12 +869,8 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
   p.d = d;
   p.group = Hq / Hkv;
   p.tpt = 128 / p.group;
-  p.part_rows = (int)paged_part_rows(p.group, N);
-  const size_t rows = 2 * (size_t)fa::kPagedCtas * p.part_rows;
   char* ws = static_cast<char*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + round256(rows * d * sizeof(float)));
-  p.part_meta = reinterpret_cast<int4*>(ws + round256(rows * d * sizeof(float)) + round256(rows * 4 * sizeof(float)));
+  if (!scales) paged_parts(&p, ws, paged_part_rows(p.group, N), d);
   // lanes that add up a sequence's q blocks: enough for the longest chunk
   const int blocks = (N + 2 * p.tpt - 1) / (2 * p.tpt);
   p.plan_lanes = 1;
@@ -862,7 +890,19 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
   if (scales) {
     p.k_scales = static_cast<const uint8_t*>(scales[0]);
     p.v_scales = static_cast<const uint8_t*>(scales[1]);
-    return fa::launch_fwd_paged_fp8(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
+    p.few_rows = paged_few_rows(p.group, N);
+    fa::PagedParams few = p;
+    few.few = 1;
+    if (p.few_rows) {
+      few.tpt = p.few_rows / p.group;
+      few.plan_lanes = 1;
+      ws += paged_parts(&few, ws, paged_few_part_rows(p.group, N), d);
+    } else {
+      few.B = 0;
+    }
+    if ((long long)N * p.group > p.few_rows) paged_parts(&p, ws, paged_part_rows(p.group, N), d);
+    else p.B = 0;
+    return fa::launch_fwd_paged_fp8(few, p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
   }
   return fa::launch_fwd_paged(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
 }
@@ -877,10 +917,6 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
   return paged_impl(q, k_pages, v_pages, nullptr, block_table, cache_seqlens, cu_seqlens, o, lse, B,
                     Hq, Hkv, N, d, total_tokens, page_size, num_pages, max_pages, scale, causal,
                     window, alibi_slopes, o_dtype, workspace, workspace_bytes, stream);
-}
-
-size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d) {
-  return fa_fwd_paged_workspace_size(Hq, Hkv, N, d);
 }
 
 fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,

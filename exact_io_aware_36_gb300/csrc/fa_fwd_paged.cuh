@@ -155,7 +155,7 @@ struct Bars {
   int abort_flag;
   int part_lost[2];             // the part's item met a page outside the pool
   // the plan: where this CTA's run begins
-  unsigned long long warp_sum[kThreads<true> / 32];
+  unsigned long long warp_sum[16];
   long long w0, w1, base;
   int b, g, qb;
 };
@@ -173,7 +173,9 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 }
 
 // New tokens [c0, c0 + n) of sequence b and its cached length L; n = 0 where
-// there is nothing to do.  False: malformed (n is 0 then).
+// there is nothing to do.  False: malformed (n is 0 then).  PICK: of the kernels
+// that share a call, one has the sequences of up to few_rows rows per kv head.
+template <bool PICK>
 __device__ __forceinline__ bool load_seq(const PagedParams& p, int b, int* c0, int* n, int* L) {
   int c1;
   if (p.cu_seqlens) {
@@ -188,6 +190,7 @@ __device__ __forceinline__ bool load_seq(const PagedParams& p, int b, int* c0, i
   if (*c0 < 0 || (b == 0 && *c0 != 0) || c1 < *c0 || (long long)c1 > p.T || c1 - *c0 > p.N) return false;
   if (c1 == *c0) return true;
   if (*L < (p.causal ? c1 - *c0 : 0) || (long long)*L > (long long)p.max_pages * p.page_size) return false;
+  if (PICK && ((long long)(c1 - *c0) * p.group <= p.few_rows) != (p.few != 0)) return true;
   *n = c1 - *c0;
   return true;
 }
@@ -254,6 +257,7 @@ struct Walk {
   int b, g, qb, c0, n, L;
 };
 
+template <bool PICK>
 __device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bars, Walk& w) {
   w.w0 = bars->w0;
   w.w1 = bars->w1;
@@ -262,10 +266,11 @@ __device__ __forceinline__ void walk_begin(const PagedParams& p, const Bars* bar
   w.g = bars->g;
   w.qb = bars->qb;
   w.c0 = w.n = w.L = 0;
-  if (w.w0 < w.w1) load_seq(p, w.b, &w.c0, &w.n, &w.L);
+  if (w.w0 < w.w1) load_seq<PICK>(p, w.b, &w.c0, &w.n, &w.L);
 }
 
 // The next part of an item in the run; false at its end.
+template <bool PICK>
 __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s) {
   while (w.base < w.w1) {
     if (w.qb * 2 * p.tpt >= w.n) {
@@ -274,7 +279,7 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
         w.g = 0;
         do {
           if (++w.b >= p.B) return false;              // not reached: the run ends with an item
-          load_seq(p, w.b, &w.c0, &w.n, &w.L);
+          load_seq<PICK>(p, w.b, &w.c0, &w.n, &w.L);
         } while (w.n == 0);
       }
     }
@@ -300,7 +305,7 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
 
 // Cuts the line of tiles: fills bars->w0, w1 and the place they begin.  All
 // threads; `pre` holds B 64-bit words of shared memory.
-template <int NT>
+template <int NT, bool PICK>
 __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsigned long long* pre, unsigned min_run) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // 1. every sequence's weight, nl lanes per sequence
@@ -311,7 +316,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     long long wsum = 0;
     if (b < p.B) {
       int c0, n, L;
-      if (!load_seq(p, b, &c0, &n, &L) && blockIdx.x == 0 && sub == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
+      if (!load_seq<PICK>(p, b, &c0, &n, &L) && blockIdx.x == 0 && sub == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
       for (int tok0 = sub * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) wsum += block_weight(p, n, L, tok0);
     }
     for (int o = nl / 2; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
@@ -371,7 +376,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     const int b = bars->b;
     const long long sw = (long long)pre[b];
     int c0, n, L;
-    load_seq(p, b, &c0, &n, &L);
+    load_seq<PICK>(p, b, &c0, &n, &L);
     // the head: a float quotient, put right by at most a step
     int g = min((int)((float)(w0 - bars->base) / (float)sw), p.Hkv - 1);
     while (g > 0 && bars->base + g * sw > w0) --g;
@@ -483,6 +488,20 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" :: "r"(at), "r"(v) : "memory");
+}
+
 // ONE: no item has two tiles (the host knows from N).  KV8: the pages hold
 // codes.
 template <int D, bool ALIBI, bool ONE, bool KV8>
@@ -539,7 +558,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-  make_plan<kThreads<KV8>>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
+  make_plan<kThreads<KV8>, KV8>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -914,14 +933,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     Walk w;
     Seg s;
     s.lost = 0;
-    walk_begin(p, bars, w);
+    walk_begin<KV8>(p, bars, w);
     // what the parts of this CTA are, for the merge: kind of the part that
     // goes on from the CTA before (2: the item's last), and the item begun here
     int cont = 0;
     int4 begun = make_int4(0, 0, 0, 0);
     bool more = true;
     for (; more; ++nitem) {
-      more = walk_next(p, w, s);
+      more = walk_next<KV8>(p, w, s);
       if (more) {
         if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
         else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
@@ -964,38 +983,38 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     constexpr int RPU = 32 / LPR;                       // rows per load
     const int cw = warp - kConvWarp;
     const int rl = lane / LPR, jj = lane % LPR;
-    uint8_t* stage = smem + C::STG_OFF + cw * C::RD * C::GROUP_BYTES;
     const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
     enum { kValues = 1, kSecond = 2, kFirstOfStep = 4, kLastOfStep = 8 };
     bool ok = true;
     int fg = 0, cg = 0;                                 // groups fetched, turned
     int cs = 0;                                         // steps turned
+    const uint32_t ring0 = smem_u32(smem + C::STG_OFF + cw * C::RD * C::GROUP_BYTES);
     auto turn = [&] {
-      const uint8_t* at = stage + cg % C::RD * C::GROUP_BYTES;
+      const uint32_t at = ring0 + cg % C::RD * C::GROUP_BYTES;
       ++cg;
       __syncwarp();                                     // lane 0's header and scale
-      const uint2 hd = *reinterpret_cast<const uint2*>(at + 16 * D);
+      const uint4 hd = lds128(at + 16 * D);
+      uint4 c[UNITS];
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) c[u] = lds128(at + u * 512 + lane * 16);
       const int sl = cs % C::NS;
       if ((hd.y & kFirstOfStep) && cs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((cs / C::NS) - 1) & 1))) return;
       const uint32_t s = min(hd.x >> (hd.y >> 8 & 24u) & 0xffu, (uint32_t)kScaleHigh + 127);
       const uint32_t s1 = min(s, 134u);                 // 2^120 2^(s1 - 127) in bf16
       const uint32_t mul = (s1 + 120) * 0x00800080u, mul2 = s > s1 ? (127 + s - s1) * 0x00800080u : 0;
-      uint8_t* tile = smem + (hd.y & kValues ? C::V_OFF : C::K_OFF) + sl * C::TILE_BYTES;
-      const int row0 = 32 * cw + (hd.y & kSecond ? 16 : 0);
+      const int row0 = 32 * cw + (hd.y & kSecond ? 16 : 0) + rl;
       // the second box's lanes write their odd half first, so that eight lanes'
       // stores take eight different places of a line
-      const int odd = jj >> 2;
+      const int odd = jj >> 2, j0 = 2 * (jj & 3) + odd;
+      uint32_t box = smem_u32(smem) + (hd.y & kValues ? C::V_OFF : C::K_OFF) + sl * C::TILE_BYTES + odd * C::BOX_BYTES + row0 * 128;
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        const uint4 c = *reinterpret_cast<const uint4*>(at + u * 512 + lane * 16);
         uint32_t x[8];
-        codes_to_bf16(c, mul, mul2, x);
-        const int r = row0 + u * RPU + rl;
-        uint8_t* box = tile + (jj >> 2) * C::BOX_BYTES + r * 128;
-        const int j0 = 2 * (jj & 3);
+        codes_to_bf16(c[u], mul, mul2, x);
         const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), b = make_uint4(x[4], x[5], x[6], x[7]);
-        *reinterpret_cast<uint4*>(box + (((j0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-        *reinterpret_cast<uint4*>(box + (((j0 + (odd ^ 1)) ^ (r & 7)) << 4)) = odd ? a : b;
+        const int r7 = (rl + u * RPU) & 7;
+        sts128(box + u * RPU * 128 + ((j0 ^ r7) << 4), odd ? b : a);
+        sts128(box + u * RPU * 128 + ((j0 ^ 1 ^ r7) << 4), odd ? a : b);
       }
       if (hd.y & kLastOfStep) {
         fence_proxy_async_smem();
@@ -1004,93 +1023,118 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ++cs;
       }
     };
-    // `row`: the pool's row of the group's first slot, whose key is key0; none: < 0
-    auto fetch = [&](unsigned flags, long long row, int key0, int head, int vlo, int vhi) {
-      if (fg - cg == C::RD) {
-        asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
-        turn();
-        if (!ok) return;
-      }
-      __syncwarp();
-      uint8_t* at = stage + fg % C::RD * C::GROUP_BYTES;
-      ++fg;
-      const uint8_t* src = static_cast<const uint8_t*>(flags & kValues ? p.v : p.k);
-      if (row >= 0) src += (row * p.Hkv + head) * D + jj * 16;
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int r = u * RPU + rl, key = key0 + r;
-        const bool seen = row >= 0 && key >= vlo && key < vhi;
-        copy_async16(smem_u32(at) + u * 512 + lane * 16, seen ? src + (long long)r * p.Hkv * D : src, seen ? 16 : 0);
-      }
-      if (lane == 0) {
-        const long long i = row >= 0 ? (row >> 4) * p.Hkv + head : 0;
-        const uint8_t* scales = flags & kValues ? p.v_scales : p.k_scales;
-        copy_async4(smem_u32(at) + 16 * D, scales + (i & ~3ll), row >= 0 ? (int)min(4ll, scale_bytes - (i & ~3ll)) : 0);
-        reinterpret_cast<uint32_t*>(at + 16 * D)[1] = flags | (uint32_t)(i & 3) << 11;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    constexpr int kNoPage = -0x7fffffff - 1;            // no row sees these keys
+    const int32_t* table = nullptr;
+    int* lost = nullptr;
+    int i = 0, ie = 0, own = 0, page[2] = {kNoPage, kNoPage}, steps = 0;
+    // the step being fetched [0] and the one before [1]: pool's rows of the
+    // groups' first slots (none: < 0), first key, keys that are seen, kv head
+    long long row[2][2] = {{-1, -1}, {-1, -1}};
+    int key0[2] = {0, 0}, vlo[2] = {0, 0}, vhi[2] = {0, 0}, g[2] = {0, 0};
+    auto page_of = [&](int step, int half) {
+      const int k = own - step * 128 + 16 * half;
+      return step < ie && k < vhi[0] && k + 16 > vlo[0] ? __ldg(table + (k >> p.page_shift)) : kNoPage;
     };
-    long long prow[2] = {-1, -1};                       // the step before
-    int pkey = 0, pg = 0, pvlo = 0, pvhi = 0, steps = 0;
-    auto values = [&](unsigned first) {
-      fetch(kValues | first, prow[0], pkey, pg, pvlo, pvhi);
-      if (ok) fetch(kValues | kSecond | kLastOfStep, prow[1], pkey + 16, pg, pvlo, pvhi);
-    };
-    auto next_item = [&]() -> bool {
+    // A step's groups in turn: keys 0, 1, values of the step before 2, 3.  One
+    // loop with one copy of each part: four copies of `turn`, one for each group,
+    // do not stay in the instruction caches (6800 cycles per step, 1300 so).
+    int part = 0;
+    bool ended = false, done = false;
+#pragma unroll 1
+    while (true) {
+      const bool new_item = part == 0 && i >= ie && !ended;
       // Nobody else's progress waits for the groups that are still in the ring
       // while this warp waits for the walker.
-      if (!__all_sync(0xffffffffu, mbar_try_wait(&bars->seg_full[nitem % kSegs], (nitem / kSegs) & 1))) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        while (ok && cg < fg) turn();
+      const bool drain = done || (new_item && !__all_sync(0xffffffffu, mbar_try_wait(&bars->seg_full[nitem % kSegs], (nitem / kSegs) & 1)));
+#pragma unroll 1
+      while (ok && fg - cg > (drain ? 0 : C::RD - 1)) {
+        if (drain) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
+        turn();
       }
-      return ok && next_seg(ok);
-    };
-    while (next_item()) {
-      const Seg& s = ring[nitem % kSegs];
-      const int g = s.g, ib = s.ib, ie = s.ie, vlo = s.k.vlo, vhi = s.k.vhi, hi_all = s.k.hi_all;
-      // (the place in the ring stays this item's until its epilogue is done)
-      int* lost = const_cast<int*>(&s.lost);
-      const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
-      seg_done();
-      const int own = hi_all * 128 + 32 * cw;           // first key of this warp's rows at step 0
-      constexpr int kNoPage = -0x7fffffff - 1;          // no row sees these keys
-      auto page_of = [&](int i, int half) {
-        const int key0 = own - i * 128 + 16 * half;
-        return i < ie && key0 < vhi && key0 + 16 > vlo ? __ldg(table + (key0 >> p.page_shift)) : kNoPage;
-      };
-      int page[2] = {page_of(ib, 0), page_of(ib, 1)};
-      for (int i = ib; ok && i < ie; ++i, ++steps) {
-        const int next[2] = {page_of(i + 1, 0), page_of(i + 1, 1)};
-        const int key0 = own - i * 128;
-        long long row[2];
+      if (!ok || done) break;
+      if (new_item) {
+        if (next_seg(ok)) {
+          const Seg& s = ring[nitem % kSegs];
+          g[0] = s.g;
+          i = s.ib;
+          ie = s.ie;
+          vlo[0] = s.k.vlo;
+          vhi[0] = s.k.vhi;
+          own = s.k.hi_all * 128 + 32 * cw;             // first key of this warp's rows at step 0
+          // (the place in the ring stays this item's until its epilogue is done)
+          lost = const_cast<int*>(&s.lost);
+          table = p.block_table + (long long)s.b * p.max_pages;
+          seg_done();
+          page[0] = page_of(i, 0);
+          page[1] = page_of(i, 1);
+        } else {
+          ended = true;
+          part = 2;                                     // the last step's values
+          if (!ok || steps == 0) {
+            done = true;
+            continue;
+          }
+        }
+      }
+      if (part == 0) {
+        key0[0] = own - i * 128;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          row[h] = -1;
+          row[0][h] = -1;
           if (page[h] >= 0 && page[h] < p.num_pages) {
-            row[h] = (long long)page[h] * p.page_size + ((key0 + 16 * h) & (p.page_size - 1));
-          } else if (page[h] != kNoPage) {
+            row[0][h] = (long long)page[h] * p.page_size + ((key0[0] + 16 * h) & (p.page_size - 1));
+          } else if (page[h] != kNoPage && lane == 0) {
             // nothing is read, and the item's rows are not written
-            if (lane == 0) {
-              record_status(p.status, FA_ERR_PAGE);
-              *lost = 1;                                // (the lane whose arrival publishes it)
-            }
+            record_status(p.status, FA_ERR_PAGE);
+            *lost = 1;                                  // (the lane whose arrival publishes it)
           }
-          page[h] = next[h];
+          page[h] = page_of(i + 1, h);
         }
-        fetch(kFirstOfStep, row[0], key0, g, vlo, vhi);
-        if (ok) fetch(kSecond | (steps == 0 ? kLastOfStep : 0), row[1], key0 + 16, g, vlo, vhi);
-        if (ok && steps > 0) values(0);
-        prow[0] = row[0];
-        prow[1] = row[1];
-        pkey = key0;
-        pg = g;
-        pvlo = vlo;
-        pvhi = vhi;
+      }
+      {
+        // this group of 16 slots on its way
+        const int x = part >> 1, h = part & 1;
+        const long long rw = x ? (h ? row[1][1] : row[1][0]) : (h ? row[0][1] : row[0][0]);
+        const int k = (x ? key0[1] : key0[0]) + 16 * h + rl, head = x ? g[1] : g[0];
+        const int lo = rw >= 0 ? (x ? vlo[1] : vlo[0]) : 1, hi = rw >= 0 ? (x ? vhi[1] : vhi[0]) : 0;
+        const uint32_t at = ring0 + fg % C::RD * C::GROUP_BYTES;
+        ++fg;
+        __syncwarp();                                   // the place's header has been read
+        const uint8_t* src = static_cast<const uint8_t*>(x ? p.v : p.k) + (rw >= 0 ? ((rw + rl) * p.Hkv + head) * D : 0) + jj * 16;
+        const long long step = (long long)RPU * p.Hkv * D;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const bool seen = k + u * RPU >= lo && k + u * RPU < hi;
+          copy_async16(at + u * 512 + lane * 16, seen ? src + u * step : static_cast<const uint8_t*>(p.k), seen ? 16 : 0);
+        }
+        if (lane == 0) {
+          const long long j = rw >= 0 ? (rw >> 4) * p.Hkv + head : 0;
+          copy_async4(at + 16 * D, (x ? p.v_scales : p.k_scales) + (j & ~3ll), rw >= 0 ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
+          const bool first = part == 0 || (ended && part == 2), last = part == 3 || (steps == 0 && part == 1);
+          sts32(at + 16 * D + 4, (x ? kValues : 0) | (h ? kSecond : 0) | (first ? kFirstOfStep : 0) | (last ? kLastOfStep : 0) |
+                                     (uint32_t)(j & 3) << 11);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      ++part;
+      if (part == 4 || (part == 2 && steps == 0)) {
+        if (ended) {
+          done = true;
+          continue;
+        }
+        part = 0;
+        ++steps;
+        ++i;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) row[1][h] = row[0][h];
+        key0[1] = key0[0];
+        vlo[1] = vlo[0];
+        vhi[1] = vhi[0];
+        g[1] = g[0];
       }
     }
-    if (ok && steps > 0) values(kFirstOfStep);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (ok && cg < fg) turn();
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
@@ -1410,6 +1454,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // The call's other kernel may still run; what follows this one must find both
+  // at their end.
+  if (KV8) grid_dependency_wait();
   // A wait ran out, so parts may be missing, whatever the walker put on record
   // ahead of them: the merge must not take what the workspace held.  Nor a part
   // of an item that met a page outside the pool.
@@ -1423,8 +1470,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 // four parts' loads at a time, so that a row costs two waits for memory: what
 // the parts are, and the parts.
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
-  grid_dependency_wait();
+__device__ __forceinline__ void merge_parts(const PagedParams& p, const int nctas) {
   const int c = blockIdx.x;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -1497,8 +1543,23 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
   if (lane == 0) p.lse[(long long)h * p.T + tok] = l == 0.f ? -INFINITY : (M + lg2_approx(l)) * kLn2;
 }
 
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
+  grid_dependency_wait();
+  merge_parts<D>(p, nctas);
+}
+
+// Those of the two kernels of a call over codes.
+template <int D>
+__global__ void __launch_bounds__(256) paged_merge_two_kernel(const PagedParams p, const PagedParams q, const int nctas) {
+  grid_dependency_wait();
+  merge_parts<D>(blockIdx.z ? q : p, nctas);
+}
+
+// `after`: another kernel of the call runs before this one, and the merge is
+// the caller's.
 template <int D, bool ALIBI, bool ONE, bool KV8>
-int launch_impl(const PagedParams& p, cudaStream_t stream) {
+int launch_impl(const PagedParams& p, cudaStream_t stream, bool after = false) {
   using C = Cfg<D, ONE, KV8>;
   auto kern = fwd_paged_kernel<D, ALIBI, ONE, KV8>;
   if (const int ea = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ea;
@@ -1516,17 +1577,18 @@ int launch_impl(const PagedParams& p, cudaStream_t stream) {
   int nsm = 0;
   if (const int es = sm_count(&nsm)) return es;
   const int grid = std::min(nsm, kPagedCtas);
+  if (KV8 && after) return launch_dependent(kern, dim3(grid), dim3(kThreads<KV8>), C::SMEM_BYTES, stream, tq, tk, tv, p);
   kern<<<grid, kThreads<KV8>, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
   return launch_dependent(paged_merge_kernel<D>, dim3(grid, std::max(1, (p.part_rows + 7) / 8)), dim3(256), 0, stream, p, grid);
 }
 
 template <int D, bool KV8>
-int launch_d(const PagedParams& p, cudaStream_t stream) {
+int launch_d(const PagedParams& p, cudaStream_t stream, bool after = false) {
   // no sequence brings more tokens than one tile holds
   const bool one = p.N <= p.tpt;
-  if (p.alibi) return one ? launch_impl<D, true, true, KV8>(p, stream) : launch_impl<D, true, false, KV8>(p, stream);
-  return one ? launch_impl<D, false, true, KV8>(p, stream) : launch_impl<D, false, false, KV8>(p, stream);
+  if (p.alibi) return one ? launch_impl<D, true, true, KV8>(p, stream, after) : launch_impl<D, true, false, KV8>(p, stream, after);
+  return one ? launch_impl<D, false, true, KV8>(p, stream, after) : launch_impl<D, false, false, KV8>(p, stream, after);
 }
 
 }  // namespace

@@ -219,6 +219,8 @@ struct PagedParams {
   int page_size, page_shift, num_pages, max_pages;
   int causal, window, o_f32;   // window: kNoWindow when unbanded
   float scale, scale_log2;
+  int few_rows, few;           // codes: sequences of up to few_rows rows per kv head
+                               // are another kernel's (few: the others are)
 };
 
 // CTAs of the paged forward: GB300's SMs; each leaves at most two parts.
@@ -251,7 +253,10 @@ int launch_norm_rope_bwd(const NormRopeParams& p, void* stream);      // rows, t
 int launch_append_fp8(const QuantAppendParams& p, bool turn, void* stream);   // turn: with q, norm and rotation
 int launch_copy_pages(CachePagesCopy p, void* stream);
 int launch_fwd_paged(const PagedParams& p, void* stream);             // runs + merge of parts
-int launch_fwd_paged_fp8(const PagedParams& p, void* stream);         // the same over e4m3 codes
+// The same over e4m3 codes: `few` with the sequences of up to few.few_rows rows
+// per kv head, `many` with the others; either may be absent (B = 0).
+int launch_fwd_paged_fp8(const PagedParams& few, const PagedParams& many, void* stream);
+int launch_fwd_paged_few(const PagedParams& p, int grid, void* stream);   // its first part: runs
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__
