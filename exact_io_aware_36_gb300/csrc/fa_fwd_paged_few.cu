@@ -5,14 +5,17 @@
 //     S = scale Q K^T (+ ALiBi),   O = softmax(S) V,   k = 2^ek ck,  v = 2^ev cv
 // with codes c and one pair of exponents for every 16 slots of a kv head.
 //
-// A warp takes such a block of 16 keys by itself: its codes come from HBM by
-// cp.async into a ring of its own, several blocks ahead and on into the next
-// items, and no warp waits for another until an item ends.  The codes become
-// fp16 in registers (exact) and go straight into matrix instructions of 16 rows:
-// their order along d (and along the keys, for P V) is free as long as both
-// operands agree, so each lane's operands are whole 16-byte reads.  The
-// exponents stay out of the products: 2^ek multiplies a block's scores, and
-// 2^(ev - eref) its P, with O held in units of 2^eref.
+// A warp takes such a block of 16 keys by itself: TMA brings its codes into a
+// ring of the warp's own, several blocks ahead and on into the next items, and
+// no warp waits for another until an item ends.  The products are matrix
+// instructions of 16 rows whose operands go straight from shared memory into
+// registers: the order of the elements along d (and of the keys, for P V) is
+// free as long as both operands agree, so each lane's operands are whole 16-byte
+// reads.  The exponents stay out of the products: 2^ek multiplies a block's
+// scores, and 2^(ev - eref) its P, with O held in units of 2^eref.
+// Codes become fp16 (exact) in registers: two instructions for four of them.
+// (mma.sync with e4m3 operands is no way around that: it is taken apart into the
+// same conversions and fp16 products, and took 1.4 times as long.)
 //   Q  is scaled by a power of two per row to at most 2^15 and rounded to fp16:
 //      exact for elements down to 2^-22 of the row's largest, and what the
 //      others lose is below 2^-39 of that one.
@@ -20,11 +23,11 @@
 //      exceed by at most 2^8, and 2^7 P at most 2^15, so that P's normal range
 //      reaches down to 2^-21 and its smallest step is 2^-31.
 // What a 16-row instruction leaves unused does not matter: 128 keys cost an SM
-// some 130 cycles of the matrix pipe and 1500 of its share of HBM at d = 128.
+// some 400 cycles of the matrix pipe and 1500 of its share of HBM at d = 128.
 //
 // The work is cut as in fa_fwd_paged.cuh (equal runs of the line of key tiles,
-// parts joined in a fixed order), so nothing depends on timing.  There is no
-// wait that could run out.
+// parts joined in a fixed order), so nothing depends on timing.  A warp whose
+// wait for its copies runs out gives its items up: their rows are left alone.
 #include <cuda_fp16.h>
 
 #include "fa_fwd_paged.cuh"
@@ -35,36 +38,45 @@ namespace {
 template <int D, int MT>
 struct Few {
   static constexpr int ROWS = 16 * MT;
-  // Warps: as many as the registers of O (D MT / 2 of a lane), Q and the codes
-  // leave room for.
+  // Warps: as many as the registers of O (D MT / 2 of a lane) and Q leave room for.
   static constexpr int W = D == 128 ? (MT == 1 ? 12 : 8) : (MT == 1 ? 16 : 12);
   static constexpr int NT = 32 * W;
   static constexpr int RD = D == 128 && MT == 1 ? 3 : 4;    // blocks of a warp's ring
   static constexpr int POOL = 16 * D;                       // codes of a block in one pool
-  static constexpr int BLOCK_BYTES = 2 * POOL + 16;
+  static constexpr int BLOCK_BYTES = 2 * POOL;
   static constexpr int RED_STRIDE = 68;                     // floats per row of 64 columns
   static constexpr int RING_OFF = 0;
-  static constexpr int RED_OFF = RING_OFF + W * RD * BLOCK_BYTES;
+  static constexpr int HEAD_OFF = RING_OFF + W * RD * BLOCK_BYTES;   // scales of the ring's blocks
+  static constexpr int RED_OFF = HEAD_OFF + W * RD * 16;
   static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
   static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
-  static constexpr int SEG_OFF = STAT_OFF + ROWS * 8;
-  static constexpr int PAR_OFF = SEG_OFF + 4 * 96;
-  static constexpr int BAR_OFF = PAR_OFF + 256;
+  // Q of an item and of the next, as fragments, and the rows' exponents
+  static constexpr int Q_FRAGS = MT * (D / 16) * 512;
+  static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
+  static constexpr int Q_OFF = STAT_OFF + ROWS * 8;
+  static constexpr int SEG_OFF = Q_OFF + 2 * Q_BYTES;
+  static constexpr int WALK_OFF = SEG_OFF + 4 * 96;
+  static constexpr int PAR_OFF = WALK_OFF + 128;
+  static constexpr int FULL_OFF = PAR_OFF + 256;            // barriers of the ring's blocks
+  static constexpr int BAR_OFF = FULL_OFF + W * RD * 8;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(kPagedMaxBatch * 8 <= W * RD * BLOCK_BYTES, "plan");
-  static_assert(SEG_OFF % 16 == 0 && RED_OFF % 16 == 0, "alignment");
+  static_assert(Q_OFF % 16 == 0 && Q_BYTES % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
-__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+// D += A B: 16 rows x 8 columns over 16.
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two codes (four) as fp16.
+// Four codes as fp16: the low two, the high two.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
+  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 t;\n\t"
+      "shr.u32 t, %2, 16;\n\t"
+      "cvt.u16.u32 a, %2;\n\t"
+      "cvt.u16.u32 b, t;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(w));
@@ -85,8 +97,47 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 
+// What finds the run's items, in shared memory, and what the run's parts are
+// for the merge: `cont` the part that goes on from the CTA before (2: the item's
+// last), `begun` the item begun here.
+struct Finder {
+  Walk walk;
+  int more, cont;
+  int4 begun;
+};
+static_assert(sizeof(Finder) <= 128, "finder");
+
+// Item n of the run into segs[n % 4] (ie < 0: the end).  By warp 0, once per
+// item; out of line, and with its state in shared memory, so that the loop over
+// blocks has the registers: what it spills does not even stay in L1, of which
+// shared memory leaves little (16 caches, one token each: 305 us with the queries'
+// fragments and this state in registers).
+static __device__ __noinline__ void find_item(const PagedParams& p, Finder& f, Seg* segs, int n) {
+  if (!f.more) return;
+  Walk w = f.walk;
+  Seg s;
+  s.lost = 0;
+  const bool more = walk_next<true>(p, w, s);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    if (!more) {
+      s.ie = -1;
+    } else if (s.ib > 0) {
+      f.cont = s.ie == s.k.kt ? 2 : 1;
+    } else if (s.ie < s.k.kt) {
+      f.begun = make_int4(1, s.tok, s.ntok, s.g);
+    }
+    f.walk = w;
+    f.more = more;
+    segs[n & 3] = s;
+  }
+  __syncwarp();
+}
+
 template <int D, int MT, bool ALIBI>
-__global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(Few<D, MT>::NT, 1)
+fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PagedParams p) {
   using C = Few<D, MT>;
   constexpr int W = C::W;
   extern __shared__ uint8_t smem_raw[];
@@ -96,164 +147,196 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
   const PagedParams& ps = *reinterpret_cast<const PagedParams*>(smem + C::PAR_OFF);
   if (threadIdx.x < sizeof(PagedParams) / 4)
     reinterpret_cast<uint32_t*>(smem + C::PAR_OFF)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&p)[threadIdx.x];
-  if (threadIdx.x == 0) bars->part_lost[0] = bars->part_lost[1] = 0;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::FULL_OFF) + warp * C::RD;
+  if (lane < C::RD) mbar_init(&full[lane], 1);
+  if (threadIdx.x == 0) {
+    bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  fence_mbarrier_init();
   __syncthreads();
   make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kMinRunOne);
+  fence_proxy_async_smem();                            // (the plan's sums lay where TMA will write)
   grid_launch_dependents();
 
   // The run's items: segs[n % 4] is item n (ie < 0: the end).  Warp 0 finds them,
-  // two ahead; each is published by the barrier of an item's end.
+  // two ahead; each is published by the barriers of an item's end.
   Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
-  Walk walk;
-  int cont = 0;
-  int4 begun = make_int4(0, 0, 0, 0);
-  bool more = true;
-  auto find = [&](int n) {
-    if (!more) return;
-    Seg s;
-    s.lost = 0;
-    more = walk_next<true>(p, walk, s);
-    if (more) {
-      if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
-      else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
-    } else {
-      s.ie = -1;
-    }
-    if (lane == 0) segs[n & 3] = s;
-  };
+  Finder& finder = *reinterpret_cast<Finder*>(smem + C::WALK_OFF);
   if (warp == 0) {
-    walk_begin<true>(p, bars, walk);
-    find(0);
-    find(1);
+    if (lane == 0) {
+      Walk w;
+      walk_begin<true>(p, bars, w);
+      finder.walk = w;
+      finder.more = 1;
+      finder.cont = 0;
+      finder.begun = make_int4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    find_item(ps, finder, segs, 0);
+    find_item(ps, finder, segs, 1);
   }
   __syncthreads();
 
-  // ---- this warp's blocks on their way: block kb of item it is the next
-  const uint32_t ring = smem_u32(smem + C::RING_OFF + warp * C::RD * C::BLOCK_BYTES);
-  constexpr int CPR = D / 16;                          // 16-byte pieces of a row
-  constexpr int RPL = 32 / CPR;                        // rows per load
-  constexpr int LOADS = 16 / RPL;
-  const int lr = lane / CPR, lc = lane % CPR;
+  // ---- this warp's blocks on their way: block kb of item `it` is the next
+  const uint32_t ring = smem_u32(smem + C::RING_OFF) + warp * C::RD * C::BLOCK_BYTES;
+  const uint32_t heads = smem_u32(smem + C::HEAD_OFF) + warp * C::RD * 16;
   const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
+  const uint8_t* const scales = lane == 0 ? p.k_scales : p.v_scales;
   auto first_block = [&](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 8, s.k.vlo >> 4); };
   auto end_block = [&](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 8, (s.k.vhi + 15) >> 4); };
-  int it = 0, kb = 0, kb_end = 0, page = 0, fetched = 0;
+  int it = 0, kb = 0, kb_end = 0, page = 0, head = 0;
+  int fly = 0;                                         // blocks in the ring
+  int to = 0, from = 0;                                // places of the next block to fetch, to take
+  unsigned par = 0;                                    // parity of place `from`
+  const int32_t* table = p.block_table;
   bool any = false;                                    // block kb exists, its page is in `page`
+  bool dead = false;                                   // a wait ran out
   int cur = 0;                                         // the item being worked on
+  auto enter = [&](int n) {
+    const Seg& s = segs[n & 3];
+    it = n;
+    kb = first_block(s) + warp;
+    kb_end = end_block(s);
+    table = p.block_table + (long long)s.b * p.max_pages;
+    head = s.g;
+  };
+  auto look_up = [&] { page = __ldg(table + ((kb << 4) >> p.page_shift)); };
   auto settle = [&] {                                  // on to the next block that exists
-    any = true;
-    while (kb >= kb_end) {
+    any = !dead;
+    while (any && kb >= kb_end) {
       // (items behind the next one are not known yet)
       if (it > cur || segs[(it + 1) & 3].ie < 0) {
         any = false;
-        break;
+        return;
       }
-      ++it;
-      kb = first_block(segs[it & 3]) + warp;
-      kb_end = end_block(segs[it & 3]);
+      enter(it + 1);
     }
-    if (any) page = __ldg(p.block_table + (long long)segs[it & 3].b * p.max_pages + ((kb << 4) >> p.page_shift));
+    if (any) look_up();
   };
   auto fetch = [&] {
-    const uint32_t at = ring + fetched % C::RD * C::BLOCK_BYTES;
-    ++fetched;
-    const Seg& s = segs[it & 3];
-    const bool good = page >= 0 && page < p.num_pages;
-    if (!good && lane == 0) {
-      // nothing is read, and the item's rows are not written
-      record_status(p.status, FA_ERR_PAGE);
-      segs[it & 3].lost = 1;
-    }
-    const long long row = good ? (long long)page * p.page_size + ((kb << 4) & (p.page_size - 1)) : 0;
-    const long long off = ((row + lr) * p.Hkv + s.g) * D + lc * 16;
-    const long long step = (long long)RPL * p.Hkv * D;
-    const int lo = good ? s.k.vlo - (kb << 4) : 16, hi = s.k.vhi - (kb << 4);
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int r = u * RPL + lr;
-      const bool seen = r >= lo && r < hi;
-      const long long from = seen ? off + u * step : 0;
-      const int kc = D == 128 ? lc ^ (r & 7) : lc, vc = D == 128 ? lc ^ 2 * (r & 3) : lc ^ 2 * (r >> 1 & 1);
-      copy_async16(at + r * D + kc * 16, static_cast<const uint8_t*>(p.k) + from, seen ? 16 : 0);
-      copy_async16(at + C::POOL + r * D + vc * 16, static_cast<const uint8_t*>(p.v) + from, seen ? 16 : 0);
-    }
-    if (lane == 0) {
-      const long long j = good ? (row >> 4) * p.Hkv + s.g : 0;
-      const int n = good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0;
-      copy_async4(at + 2 * C::POOL, p.k_scales + (j & ~3ll), n);
-      copy_async4(at + 2 * C::POOL + 4, p.v_scales + (j & ~3ll), n);
-      sts32(at + 2 * C::POOL + 8, (uint32_t)(j & 3) * 8);
-    }
+    const bool good = (unsigned)page < (unsigned)p.num_pages;
+    const uint32_t row = good ? (uint32_t)page * p.page_size + ((kb << 4) & (p.page_size - 1)) : 0;
+    const long long j = good ? (long long)(row >> 4) * p.Hkv + head : 0;
+    const uint32_t hd = heads + to * 16;
+    if (lane < 2)                                      // the scales: of the keys, of the values
+      copy_async4(hd + 4 * lane, scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
+    if (lane == 0) {
+      sts32(hd + 8, (uint32_t)(j & 3) * 8);
+      uint64_t* bar = &full[to];
+      if (good) {
+        uint8_t* at = smem + C::RING_OFF + (warp * C::RD + to) * C::BLOCK_BYTES;
+        mbar_arrive_expect_tx(bar, C::BLOCK_BYTES);
+        tma_load_3d(at, &tmK, 0, head, (int)row, bar);
+        tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row, bar);
+      } else {
+        // nothing is read, and the item's rows are not written
+        record_status(p.status, FA_ERR_PAGE);
+        segs[it & 3].lost = 1;
+        mbar_arrive(bar);
+      }
+    }
+    to = to + 1 == C::RD ? 0 : to + 1;
+    ++fly;
     kb += W;
-    settle();
+    if (kb < kb_end) look_up();
+    else settle();
+  };
+  if (segs[0].ie >= 0) enter(0);
+
+  // ---- Q: a warp prepares rows warp, warp + W, .. of the next item, a lane D /
+  // 32 elements, while it works on this one
+  constexpr int QP = (C::ROWS + W - 1) / W;
+  constexpr int QE = D / 32;
+  uint32_t xq[QP][QE / 2];
+  auto load_q = [&](const Seg& s) {
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int r = warp + i * W;
+#pragma unroll
+      for (int j = 0; j < QE / 2; ++j) xq[i][j] = 0;
+      if (r < s.ntok * p.group) {
+        const int tok = r / p.group, hq = s.g * p.group + r - tok * p.group;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                                ((long long)(s.tok + tok) * p.Hq + hq) * D + QE * lane);
+        if (D == 128) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+          xq[i][0] = v.x;
+          xq[i][QE / 2 - 1] = v.y;
+        } else {
+          xq[i][0] = __ldg(src);
+        }
+      }
+    }
+  };
+  // Fragment k of 16 rows is 16 bytes of every lane: elements (D / 4) c4 + 4 k ..
+  // + 1 and .. + 2, + 3 of rows g8 and g8 + 8 (g8 = lane / 4, c4 = lane % 4).
+  auto store_q = [&](int n) {
+    uint8_t* at = smem + C::Q_OFF + (n & 1) * C::Q_BYTES;
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int r = warp + i * W;
+      if (r >= C::ROWS) break;
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < QE / 2; ++j) top = max(top, max(xq[i][j] << 16 & 0x7fff0000u, xq[i][j] & 0x7fff0000u));
+      top = __reduce_max_sync(0xffffffffu, top);
+      // the largest element to [2^14, 2^15)
+      const int up = min(14 - (max((int)(top >> 23), 1) - 127), 127);
+      const float mul = pow2_cut(up);
+      const int k = D == 128 ? lane & 7 : (lane & 7) >> 1, to_lane = (r & 7) * 4 + (lane >> 3);
+      uint32_t* frag = reinterpret_cast<uint32_t*>(at + ((r >> 4) * (D / 16) + k) * 512 + to_lane * 16) + (r >> 3 & 1);
+#pragma unroll
+      for (int j = 0; j < QE / 2; ++j)
+        frag[2 * (D == 128 ? j : lane & 1)] =
+            pack_f16x2(__uint_as_float(xq[i][j] << 16) * mul, __uint_as_float(xq[i][j] & 0xFFFF0000u) * mul);
+      if (lane == 0) reinterpret_cast<int*>(at + C::Q_FRAGS)[r] = up;
+    }
   };
   if (segs[0].ie >= 0) {
-    kb = first_block(segs[0]) + warp;
-    kb_end = end_block(segs[0]);
+    settle();
+#pragma unroll 1
+    while (any && fly < C::RD) fetch();
+    load_q(segs[0]);
+    store_q(0);
   }
+  __syncthreads();
 
   const int g8 = lane >> 2, c4 = lane & 3;
-  constexpr int X = D == 64 ? 1 : 0;
-  // the keys of a lane's columns 2 c4 and 2 c4 + 1 of eight (even columns: rows
-  // 0 .. 3 of the block's half, odd ones 4 .. 7; so that eight lanes' reads of
-  // keys and of values take eight different places of a line)
-  const int key_even = c4, key_odd = 4 + (c4 ^ X);
-  const int krow = g8 & 1 ? 4 + ((g8 >> 1) ^ X) : g8 >> 1;    // the key of column g8
-  int used = 0;                                        // blocks taken from the ring
   float* red = reinterpret_cast<float*>(smem + C::RED_OFF);
   float2* mls = reinterpret_cast<float2*>(smem + C::ML_OFF);
   float2* stat = reinterpret_cast<float2*>(smem + C::STAT_OFF);
+  const WaitCtx wc{&bars->abort_flag, p.status};
 
 #pragma unroll 1
   for (;; ++cur) {
     const Seg& s = segs[cur & 3];
     if (s.ie < 0) break;
     if (!any) settle();
-    while (any && fetched - used < C::RD) fetch();
-    if (warp == 0) find(cur + 2);
+#pragma unroll 1
+    while (any && fly < C::RD) fetch();
+    if (warp == 0) find_item(ps, finder, segs, cur + 2);
+    const bool next = segs[(cur + 1) & 3].ie >= 0;
+    if (next) load_q(segs[(cur + 1) & 3]);
     const int rows = s.ntok * p.group;
     const int f = s.k.f[0];
-    // rows beyond `diag` or below `low`: keys that some row does not see
+    // blocks beyond `diag` or below `low` hold keys that some row does not see
     const int diag = p.causal ? f : s.L - 1, low = f + s.ntok - 1 - p.window;
-    // ------------------------------------------------- Q, as fp16 fragments
-    uint32_t qf[MT][D / 16][4];
+    const uint32_t qat = smem_u32(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES) + lane * 16;
     float slope2[MT][2];
     int kend[MT][2], qup[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = 16 * m + 8 * h + g8, tok = r / p.group, head = s.g * p.group + r % p.group;
+        const int r = 16 * m + 8 * h + g8;
         const bool valid = r < rows;
-        uint4 x[D / 32];                               // 16 elements of each 64: two pieces
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + ((long long)(s.tok + tok) * p.Hq + head) * D + 16 * c4;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          x[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src + 64 * (i >> 1)) + (i & 1)) : make_uint4(0, 0, 0, 0);
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest element to [2^14, 2^15)
-        const int up = min(14 - (max((int)(top >> 23), 1) - 127), 127);
-        const float mul = pow2_cut(up);
-        qup[m][h] = up;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            qf[m][2 * i + (j >> 1)][h + 2 * (j & 1)] =
-                pack_f16x2(__uint_as_float(w[j] << 16) * mul, __uint_as_float(w[j] & 0xFFFF0000u) * mul);
-        }
+        const int tok = r / p.group;
+        qup[m][h] = reinterpret_cast<const int*>(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES + C::Q_FRAGS)[r];
         kend[m][h] = !valid ? -1 : p.causal ? f + tok : s.L - 1;
-        slope2[m][h] = ALIBI && valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
+        slope2[m][h] = ALIBI && valid ? __ldg(p.alibi + s.g * p.group + r - tok * p.group) * kLog2e : 0.f;
       }
     float mref[MT][2], l[MT][2];
     float o[MT][D / 8][4];
@@ -268,70 +351,103 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
     }
     int eref = -1000, etop = -1000;                    // O's unit, the largest it had
     // ------------------------------------------------------------- blocks
-    const int kb1 = end_block(s);
+    const int kb1 = end_block(s), vlo = s.k.vlo, vhi = s.k.vhi;
 #pragma unroll 1
     for (int b = first_block(s) + warp; b < kb1; b += W) {
-      if (fetched - used == C::RD) asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
+      if (dead || !wait_warp_inl(&full[from], par, wc)) {
+        // this item's rows and those of all that follow are left alone
+        dead = true;
+        any = false;
+        if (lane == 0) segs[cur & 3].lost = 1;
+        break;
+      }
+      if (fly == C::RD) asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
-      const uint32_t at = ring + used % C::RD * C::BLOCK_BYTES;
-      ++used;
-      const uint4 hd = lds128(at + 2 * C::POOL);
+      const uint32_t at = ring + from * C::BLOCK_BYTES;
+      const uint4 hd = lds128(heads + from * 16);
+      --fly;
+      if (++from == C::RD) {
+        from = 0;
+        par ^= 1;
+      }
       const int ek = (int)min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
       const int ev = (int)min(hd.y >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
-      // S of 16 rows x 8 keys, twice
+      // S of 16 rows x 8 keys, twice; column n of half t is key 8 t + n
       float sc[MT][2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int r = 8 * t + krow;
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[m][t][i] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 kw = lds128(at + r * D + (D == 128 ? ((c4 + 4 * h) ^ (r & 7)) : c4) * 16);
-          const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+      for (int i = 0; i < D / 64; ++i) {
+        uint4 kw[2];
+        // (d = 128: pieces 2 c4 and 2 c4 + 1 of a row, swizzled by it, so that the
+        // rows of eight lanes take different places of a line)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            codes_f16(w[i], b0, b1);
+        for (int t = 0; t < 2; ++t)
+          kw[t] = lds128(at + (8 * t + g8) * D + (D == 128 ? (2 * c4 + i) ^ g8 : c4 ^ (g8 >> 1)) * 16);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(sc[m][t], qf[m][4 * h + i], b0, b1);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t b0[2], b1[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) codes_f16(reinterpret_cast<const uint32_t*>(&kw[t])[k], b0[t], b1[t]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint4 q = lds128(qat + (m * (D / 16) + 4 * i + k) * 512);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma_f16(sc[m][t], reinterpret_cast<const uint32_t*>(&q), b0[t], b1[t]);
           }
         }
       }
-      // scores in log2 units; -inf where a row does not see a key
+      // Scores in log2 units are x cs (+ the bias); -inf where a row does not see
+      // a key.  With a bias, or where a row does not see all, they are made here.
       const int k0 = b << 4;
       const bool masked = k0 + 15 > diag || k0 < low;
+      float cs[MT][2];
       bool raise = false;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
+        for (int h = 0; h < 2; ++h) cs[m][h] = p.scale_log2 * pow2_cut(ek - qup[m][h]);
+      if (ALIBI || masked) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float& x = sc[m][t][2 * h + j];
+                const int key = k0 + 8 * t + 2 * c4 + j;
+                x = ALIBI ? fmaf(x, cs[m][h], slope2[m][h] * (float)(key - kend[m][h])) : x * cs[m][h];
+                if (masked && (key > kend[m][h] || (p.causal && key < kend[m][h] - p.window))) x = -INFINITY;
+              }
+            cs[m][h] = 1.f;
+          }
+      }
+      float mx[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float cs = p.scale_log2 * pow2_cut(ek - qup[m][h]);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float& x = sc[m][t][2 * h + j];
-              const int key = k0 + 8 * t + (j ? key_odd : key_even);
-              x = ALIBI ? fmaf(x, cs, slope2[m][h] * (float)(key - kend[m][h])) : x * cs;
-              if (masked && (key > kend[m][h] || (p.causal && key < kend[m][h] - p.window))) x = -INFINITY;
-              raise |= x > mref[m][h] + kTau;
-            }
+          mx[m][h] = fmaxf(fmax3(sc[m][0][2 * h], sc[m][0][2 * h + 1], sc[m][1][2 * h]), sc[m][1][2 * h + 1]) * cs[m][h];
+          raise |= mx[m][h] > mref[m][h] + kTau;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float mx = fmaxf(fmaxf(sc[m][0][2 * h], sc[m][0][2 * h + 1]), fmaxf(sc[m][1][2 * h], sc[m][1][2 * h + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const bool up = mx > mref[m][h] + kTau;
-            const float alpha = up ? ex2_approx(mref[m][h] - mx) : 1.f;
-            if (up) mref[m][h] = mx;
+            float x = mx[m][h];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            const bool up = x > mref[m][h] + kTau;
+            const float alpha = up ? ex2_approx(mref[m][h] - x) : 1.f;
+            if (up) mref[m][h] = x;
             l[m][h] *= alpha;
 #pragma unroll
             for (int t = 0; t < D / 8; ++t) {
@@ -354,19 +470,21 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[m][t][i] *= alpha;
       }
-      const float sv = pow2_cut(ev - eref + 7);
+      // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
+      const int up = max(ev - eref + 7, -126);
+      const float lsv = (float)up, back = pow2_cut(-up);
       uint32_t pf[MT][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mb = mref[m][h] == -INFINITY ? 0.f : mref[m][h];
+          const float mb = lsv - (mref[m][h] == -INFINITY ? 0.f : mref[m][h]);
+          float e[4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float p0 = ex2_approx(sc[m][t][2 * h] - mb), p1 = ex2_approx(sc[m][t][2 * h + 1] - mb);
-            l[m][h] += p0 + p1;
-            pf[m][2 * t + h] = pack_f16x2(p0 * sv, p1 * sv);
-          }
+          for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(sc[m][i >> 1][2 * h + (i & 1)], cs[m][h], mb));
+          l[m][h] = fmaf((e[0] + e[1]) + (e[2] + e[3]), back, l[m][h]);
+          pf[m][h] = pack_f16x2(e[0], e[1]);
+          pf[m][2 + h] = pack_f16x2(e[2], e[3]);
         }
       // O of 16 rows x 8 columns, D / 8 times: column g8 of product t is element
       // g8 D / 8 + t
@@ -375,17 +493,27 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
         uint32_t w[4][D / 32];                         // of the keys 2 c4, 2 c4 + 1, 8 + 2 c4, 9 + 2 c4
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 8 * (i >> 1) + (i & 1 ? key_odd : key_even);
+          const int r = 8 * (i >> 1) + 2 * c4 + (i & 1);
           if (D == 128) {
-            const uint4 v = lds128(vat + r * 128 + (g8 ^ 2 * (r & 3)) * 16);
+            const uint4 v = lds128(vat + r * 128 + (g8 ^ (r & 7)) * 16);
             w[i][0] = v.x;
             w[i][1] = v.y;
             w[i][D / 32 - 2] = v.z;
             w[i][D / 32 - 1] = v.w;
           } else {
-            const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ 2 * (r >> 1 & 1)) * 16 + (g8 & 1) * 8);
+            const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ (r >> 1 & 3)) * 16 + (g8 & 1) * 8);
             w[i][0] = v.x;
             w[i][1] = v.y;
+          }
+        }
+        // a slot that no row sees may hold NaN, and 0 x NaN would reach O
+        if (masked && (k0 < vlo || k0 + 16 > vhi)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = k0 + 8 * (i >> 1) + 2 * c4 + (i & 1);
+            if (key < vlo || key >= vhi)
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
           }
         }
 #pragma unroll
@@ -398,12 +526,13 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(o[m][4 * i + j], pf[m], b0[j], b1[j]);
+            for (int m = 0; m < MT; ++m) mma_f16(o[m][4 * i + j], pf[m], b0[j], b1[j]);
         }
       }
       __syncwarp();
       if (any) fetch();
     }
+    if (next) store_q(cur + 1);
     // ------------------------------------------------- join the warps' parts
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -448,12 +577,12 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
         for (int h = 0; h < 2; ++h) {
           const int r = 16 * m + 8 * h + g8;
           if (r < rows) {
-            float* to = red + (warp * C::ROWS + r) * C::RED_STRIDE + 16 * c4;
+            float* at = red + (warp * C::ROWS + r) * C::RED_STRIDE + 16 * c4;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<float4*>(to + 8 * j + 4 * q) =
+                *reinterpret_cast<float4*>(at + 8 * j + 4 * q) =
                     make_float4(o[m][8 * c + 4 * q][2 * h + j], o[m][8 * c + 4 * q + 1][2 * h + j],
                                 o[m][8 * c + 4 * q + 2][2 * h + j], o[m][8 * c + 4 * q + 3][2 * h + j]);
           }
@@ -472,7 +601,7 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
           v.w += y.w;
         }
         const float2 ml = stat[r];
-        const int tok = r / p.group, head = s.g * p.group + r % p.group;
+        const int tok = r / p.group, hq = s.g * p.group + r % p.group;
         const int col = (x >> 3) * (D / 8) + 8 * c + (x & 7);
         if (part == 0) {
           const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
@@ -481,7 +610,7 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
           v.z *= inv;
           v.w *= inv;
         }
-        const long long at = part ? (prow + r) * D + col : ((long long)(s.tok + tok) * p.Hq + head) * D + col;
+        const long long at = part ? (prow + r) * D + col : ((long long)(s.tok + tok) * p.Hq + hq) * D + col;
         if (f32) {
           *reinterpret_cast<float4*>((part ? p.part_o : static_cast<float*>(p.o)) + at) = v;
         } else {
@@ -491,16 +620,25 @@ __global__ void __launch_bounds__(Few<D, MT>::NT, 1) fwd_paged_few_kernel(const 
           if (part)
             *reinterpret_cast<float4*>(p.part_ml + (prow + r) * 4) = make_float4(ml.x, ml.y, ml.y, 0.f);
           else
-            p.lse[(long long)head * p.T + s.tok + tok] = ml.y == 0.f ? -INFINITY : (ml.x + lg2_approx(ml.y)) * kLn2;
+            p.lse[(long long)hq * p.T + s.tok + tok] = ml.y == 0.f ? -INFINITY : (ml.x + lg2_approx(ml.y)) * kLn2;
         }
       }
       __syncthreads();
     }
   }
+  // Copies in flight must land before this CTA's shared memory goes away.
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+  for (; fly > 0; --fly) {
+    wait_warp_drain(&full[from], par);
+    if (++from == C::RD) {
+      from = 0;
+      par ^= 1;
+    }
+  }
   if (threadIdx.x == 0) {
-    p.part_meta[2 * blockIdx.x] = bars->part_lost[0] ? make_int4(0, 0, 0, 0) : make_int4(cont, 0, 0, 0);
-    p.part_meta[2 * blockIdx.x + 1] = bars->part_lost[1] ? make_int4(0, 0, 0, 0) : begun;
+    p.part_meta[2 * blockIdx.x] = bars->part_lost[0] ? make_int4(0, 0, 0, 0) : make_int4(finder.cont, 0, 0, 0);
+    p.part_meta[2 * blockIdx.x + 1] = bars->part_lost[1] ? make_int4(0, 0, 0, 0) : finder.begun;
   }
 }
 
@@ -509,7 +647,11 @@ int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
   using C = Few<D, MT>;
   auto kern = p.alibi ? fwd_paged_few_kernel<D, MT, true> : fwd_paged_few_kernel<D, MT, false>;
   if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return e;
-  kern<<<grid, C::NT, C::SMEM_BYTES, stream>>>(p);
+  CUtensorMap tk, tv;
+  const long long slots = (long long)p.num_pages * p.page_size;
+  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, 16)) return e;
+  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, 16)) return e;
+  kern<<<grid, C::NT, C::SMEM_BYTES, stream>>>(tk, tv, p);
   return (int)cudaGetLastError();
 }
 

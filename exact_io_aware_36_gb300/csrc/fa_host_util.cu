@@ -38,7 +38,7 @@ struct TmapKey {
   uint64_t dims[3];
   uint64_t strides[2];
   uint32_t box[3];
-  int dtype;
+  int dtype, swizzle, promotion;
   bool operator==(const TmapKey& o) const { return std::memcmp(this, &o, sizeof(*this)) == 0; }
 };
 
@@ -62,7 +62,8 @@ size_t hash_key(const TmapKey& k) {
 }
 
 int encode(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t dims[3],
-           const uint64_t strides[2], const uint32_t box[3]) {
+           const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+           CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   TmapKey key;
   std::memset(&key, 0, sizeof(key));                 // padding bytes take part in ==
   key.base = base;
@@ -70,6 +71,8 @@ int encode(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const 
   std::memcpy(key.strides, strides, sizeof(key.strides));
   std::memcpy(key.box, box, sizeof(key.box));
   key.dtype = (int)dtype;
+  key.swizzle = (int)swizzle;
+  key.promotion = (int)promotion;
   const size_t slot = hash_key(key);
   {
     std::lock_guard<std::mutex> lock(g_cache_mu);
@@ -86,8 +89,7 @@ int encode(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const 
   cuuint32_t b[3] = {box[0], box[1], box[2]};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, dtype, 3, const_cast<void*>(base), d, s, b, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return (int)cudaErrorInvalidValue;
   g_encoded.fetch_add(1, std::memory_order_relaxed);
   std::lock_guard<std::mutex> lock(g_cache_mu);
@@ -131,6 +133,15 @@ int make_tmap_u8_3d(CUtensorMap* map, const void* base, long long n0, long long 
   const uint64_t strides[2] = {(uint64_t)s1, (uint64_t)s2};
   const uint32_t box[3] = {(uint32_t)b0, (uint32_t)b1, (uint32_t)b2};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, box);
+}
+
+int make_tmap_codes_3d(CUtensorMap* map, const void* base, int d, int H, long long slots, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)d, (uint64_t)H, (uint64_t)slots};
+  const uint64_t strides[2] = {(uint64_t)d, (uint64_t)d * H};
+  const uint32_t box[3] = {(uint32_t)d, 1, (uint32_t)box_rows};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, box,
+                d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 int set_max_dynamic_smem(const void* kernel, int bytes) {
