@@ -1033,7 +1033,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int key0[2] = {0, 0}, vlo[2] = {0, 0}, vhi[2] = {0, 0}, g[2] = {0, 0};
     auto page_of = [&](int step, int half) {
       const int k = own - step * 128 + 16 * half;
-      return step < ie && k < vhi[0] && k + 16 > vlo[0] ? __ldg(table + (k >> p.page_shift)) : kNoPage;
+      return step < ie && k < vhi[0] && k + 16 > vlo[0] ? max(__ldg(table + (k >> p.page_shift)), -1) : kNoPage;
     };
     // A step's groups in turn: keys 0, 1, values of the step before 2, 3.  One
     // loop with one copy of each part: four copies of `turn`, one for each group,

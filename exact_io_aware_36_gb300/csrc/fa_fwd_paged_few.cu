@@ -5,9 +5,9 @@
 //     S = scale Q K^T (+ ALiBi),   O = softmax(S) V,   k = 2^ek ck,  v = 2^ev cv
 // with codes c and one pair of exponents for every 16 slots of a kv head.
 //
-// A warp takes such a block of 16 keys by itself: TMA brings its codes into a
-// ring of the warp's own, several blocks ahead and on into the next items, and
-// no warp waits for another until an item ends.  The products are matrix
+// A warp takes 32 keys (two such blocks) at a time by itself: TMA brings their
+// codes into a ring of the warp's own, ahead and on into the next items, and no
+// warp waits for another until an item ends.  The products are matrix
 // instructions of 16 rows whose operands go straight from shared memory into
 // registers: the order of the elements along d (and of the keys, for P V) is
 // free as long as both operands agree, so each lane's operands are whole 16-byte
@@ -22,8 +22,10 @@
 //   P  is rounded to fp16 once (11 bits); m is a reference that a row's scores
 //      exceed by at most 2^8, and 2^7 P at most 2^15, so that P's normal range
 //      reaches down to 2^-21 and its smallest step is 2^-31.
-// What a 16-row instruction leaves unused does not matter: 128 keys cost an SM
-// some 400 cycles of the matrix pipe and 1500 of its share of HBM at d = 128.
+// Both products are taken transposed (S^T = K Q^T, O^T = V^T P^T): keys and
+// elements of V fill the 16 rows of an instruction, and up to 8 rows of Q its
+// columns, so that eight rows cost half of what 16 x 8 the other way round would
+// (registers of O, products, exponentials).
 //
 // The work is cut as in fa_fwd_paged.cuh (equal runs of the line of key tiles,
 // parts joined in a fixed order), so nothing depends on timing.  A warp whose
@@ -35,37 +37,38 @@
 namespace fa {
 namespace {
 
-template <int D, int MT>
+template <int D, int NR>
 struct Few {
-  static constexpr int ROWS = 16 * MT;
-  // Warps: as many as the registers of O (D MT / 2 of a lane) and Q leave room for.
-  static constexpr int W = D == 128 ? (MT == 1 ? 12 : 8) : (MT == 1 ? 16 : 12);
+  static constexpr int ROWS = 8 * NR;
+  // Warps: as many as the registers of O (D NR / 4 of a lane) and shared memory
+  // leave room for.
+  static constexpr int W = D == 128 ? (NR == 1 ? 12 : NR == 2 ? 10 : 8) : (NR == 4 ? 12 : 16);
   static constexpr int NT = 32 * W;
-  static constexpr int RD = D == 128 && MT == 1 ? 3 : 4;    // blocks of a warp's ring
-  static constexpr int POOL = 16 * D;                       // codes of a block in one pool
-  static constexpr int BLOCK_BYTES = 2 * POOL;
+  static constexpr int RD = 2;                              // steps of a warp's ring
+  static constexpr int POOL = 32 * D;                       // codes of a step in one pool
+  static constexpr int STEP_BYTES = 2 * POOL;
   static constexpr int RED_STRIDE = 68;                     // floats per row of 64 columns
   static constexpr int RING_OFF = 0;
-  static constexpr int HEAD_OFF = RING_OFF + W * RD * BLOCK_BYTES;   // scales of the ring's blocks
-  static constexpr int RED_OFF = HEAD_OFF + W * RD * 16;
+  static constexpr int HEAD_OFF = RING_OFF + W * RD * STEP_BYTES;    // scales of the ring's steps
+  static constexpr int RED_OFF = HEAD_OFF + W * RD * 32;
   static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
   static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
   // Q of an item and of the next, as fragments, and the rows' exponents
-  static constexpr int Q_FRAGS = MT * (D / 16) * 512;
+  static constexpr int Q_FRAGS = NR * (D / 16) * 256;
   static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
   static constexpr int Q_OFF = STAT_OFF + ROWS * 8;
   static constexpr int SEG_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int WALK_OFF = SEG_OFF + 4 * 96;
   static constexpr int PAR_OFF = WALK_OFF + 128;
-  static constexpr int FULL_OFF = PAR_OFF + 256;            // barriers of the ring's blocks
+  static constexpr int FULL_OFF = PAR_OFF + 256;            // barriers of the ring's steps
   static constexpr int BAR_OFF = FULL_OFF + W * RD * 8;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(kPagedMaxBatch * 8 <= W * RD * BLOCK_BYTES, "plan");
+  static_assert(kPagedMaxBatch * 8 <= W * RD * STEP_BYTES, "plan");
   static_assert(Q_OFF % 16 == 0 && Q_BYTES % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
-// D += A B: 16 rows x 8 columns over 16.
+// D += A B: 16 x 8, over 16.
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -73,10 +76,8 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 
 // Four codes as fp16: the low two, the high two.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 t;\n\t"
-      "shr.u32 t, %2, 16;\n\t"
-      "cvt.u16.u32 a, %2;\n\t"
-      "cvt.u16.u32 b, t;\n\t"
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(w));
@@ -90,6 +91,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // 2^e, the exponent cut to what a float holds.
 __device__ __forceinline__ float pow2_cut(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+
+// An 8 x 8 matrix of 16-bit elements, transposed: row lane / 4, columns 2 (lane %
+// 4) and the next.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
   uint2 v;
@@ -109,7 +118,7 @@ static_assert(sizeof(Finder) <= 128, "finder");
 
 // Item n of the run into segs[n % 4] (ie < 0: the end).  By warp 0, once per
 // item; out of line, and with its state in shared memory, so that the loop over
-// blocks has the registers: what it spills does not even stay in L1, of which
+// keys has the registers: what it spills does not even stay in L1, of which
 // shared memory leaves little (16 caches, one token each: 305 us with the queries'
 // fragments and this state in registers).
 static __device__ __noinline__ void find_item(const PagedParams& p, Finder& f, Seg* segs, int n) {
@@ -134,11 +143,11 @@ static __device__ __noinline__ void find_item(const PagedParams& p, Finder& f, S
   __syncwarp();
 }
 
-template <int D, int MT, bool ALIBI>
-__global__ void __launch_bounds__(Few<D, MT>::NT, 1)
+template <int D, int NR, bool ALIBI>
+__global__ void __launch_bounds__(Few<D, NR>::NT, 1)
 fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PagedParams p) {
-  using C = Few<D, MT>;
+  using C = Few<D, NR>;
   constexpr int W = C::W;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -179,31 +188,41 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   __syncthreads();
 
-  // ---- this warp's blocks on their way: block kb of item `it` is the next
-  const uint32_t ring = smem_u32(smem + C::RING_OFF) + warp * C::RD * C::BLOCK_BYTES;
-  const uint32_t heads = smem_u32(smem + C::HEAD_OFF) + warp * C::RD * 16;
+  // ---- this warp's steps of 32 keys on their way: step kb of item `it` is the next
+  const uint32_t ring = smem_u32(smem + C::RING_OFF) + warp * C::RD * C::STEP_BYTES;
+  const uint32_t heads = smem_u32(smem + C::HEAD_OFF) + warp * C::RD * 32;
   const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
-  const uint8_t* const scales = lane == 0 ? p.k_scales : p.v_scales;
-  auto first_block = [&](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 8, s.k.vlo >> 4); };
-  auto end_block = [&](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 8, (s.k.vhi + 15) >> 4); };
-  int it = 0, kb = 0, kb_end = 0, page = 0, head = 0;
-  int fly = 0;                                         // blocks in the ring
-  int to = 0, from = 0;                                // places of the next block to fetch, to take
+  const bool small = p.page_shift == 4;                // a step lies in two pages
+  auto first_step = [&](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 4, s.k.vlo >> 5); };
+  auto end_step = [&](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 4, (s.k.vhi + 31) >> 5); };
+  int it = 0, kb = 0, kb_end = 0, head = 0;
+  int page[2] = {0, 0};                                // of the step's halves
+  int fly = 0;                                         // steps in the ring
+  int to = 0, from = 0;                                // places of the next step to fetch, to take
   unsigned par = 0;                                    // parity of place `from`
   const int32_t* table = p.block_table;
-  bool any = false;                                    // block kb exists, its page is in `page`
+  bool any = false;                                    // step kb exists, its pages are in `page`
   bool dead = false;                                   // a wait ran out
   int cur = 0;                                         // the item being worked on
   auto enter = [&](int n) {
     const Seg& s = segs[n & 3];
     it = n;
-    kb = first_block(s) + warp;
-    kb_end = end_block(s);
+    kb = first_step(s) + warp;
+    kb_end = end_step(s);
     table = p.block_table + (long long)s.b * p.max_pages;
     head = s.g;
   };
-  auto look_up = [&] { page = __ldg(table + ((kb << 4) >> p.page_shift)); };
-  auto settle = [&] {                                  // on to the next block that exists
+  constexpr int kNoPage = -0x7fffffff - 1;             // no row sees these keys
+  auto look_up = [&] {
+    if (small) {
+      const Seg& s = segs[it & 3];
+      page[0] = (kb << 5) + 16 > s.k.vlo ? max(__ldg(table + 2 * kb), -1) : kNoPage;
+      page[1] = (kb << 5) + 16 < s.k.vhi ? max(__ldg(table + 2 * kb + 1), -1) : kNoPage;
+    } else {
+      page[0] = max(__ldg(table + ((kb << 5) >> p.page_shift)), -1);
+    }
+  };
+  auto settle = [&] {                                  // on to the next step that exists
     any = !dead;
     while (any && kb >= kb_end) {
       // (items behind the next one are not known yet)
@@ -216,26 +235,42 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     if (any) look_up();
   };
   auto fetch = [&] {
-    const bool good = (unsigned)page < (unsigned)p.num_pages;
-    const uint32_t row = good ? (uint32_t)page * p.page_size + ((kb << 4) & (p.page_size - 1)) : 0;
-    const long long j = good ? (long long)(row >> 4) * p.Hkv + head : 0;
-    const uint32_t hd = heads + to * 16;
-    if (lane < 2)                                      // the scales: of the keys, of the values
-      copy_async4(hd + 4 * lane, scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
+    const uint32_t hd = heads + to * 32;
+    const bool good0 = (unsigned)page[0] < (unsigned)p.num_pages;
+    const bool good1 = small ? (unsigned)page[1] < (unsigned)p.num_pages : good0;
+    const uint32_t row0 = good0 ? (uint32_t)page[0] * p.page_size + ((kb << 5) & (p.page_size - 1)) : 0;
+    const uint32_t row1 = !small ? row0 + 16 : good1 ? (uint32_t)page[1] * 16 : 0;
+    if (lane < 4) {                                    // the scales: of the halves' keys, of their values
+      const bool good = lane >> 1 ? good1 : good0;
+      const long long j = good ? (long long)((lane >> 1 ? row1 : row0) >> 4) * p.Hkv + head : 0;
+      copy_async4(hd + 4 * lane, (lane & 1 ? p.v_scales : p.k_scales) + (j & ~3ll),
+                  good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
+      if (!(lane & 1)) sts32(hd + 16 + 2 * lane, (uint32_t)(j & 3) * 8);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (lane == 0) {
-      sts32(hd + 8, (uint32_t)(j & 3) * 8);
       uint64_t* bar = &full[to];
-      if (good) {
-        uint8_t* at = smem + C::RING_OFF + (warp * C::RD + to) * C::BLOCK_BYTES;
-        mbar_arrive_expect_tx(bar, C::BLOCK_BYTES);
-        tma_load_3d(at, &tmK, 0, head, (int)row, bar);
-        tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row, bar);
+      uint8_t* at = smem + C::RING_OFF + (warp * C::RD + to) * C::STEP_BYTES;
+      if (!small && good0) {
+        mbar_arrive_expect_tx(bar, C::STEP_BYTES);
+        tma_load_3d(at, &tmK, 0, head, (int)row0, bar);
+        tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row0, bar);
       } else {
-        // nothing is read, and the item's rows are not written
-        record_status(p.status, FA_ERR_PAGE);
-        segs[it & 3].lost = 1;
-        mbar_arrive(bar);
+        // pages of 16 slots one by one; one that is not there is not read, and
+        // if a row sees its keys, the item's rows are not written
+        mbar_arrive_expect_tx(bar, small ? (good0 + good1) * (C::STEP_BYTES / 2) : 0);
+        if (small && good0) {
+          tma_load_3d(at, &tmK, 0, head, (int)row0, bar);
+          tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row0, bar);
+        }
+        if (small && good1) {
+          tma_load_3d(at + C::POOL / 2, &tmK, 0, head, (int)row1, bar);
+          tma_load_3d(at + C::POOL + C::POOL / 2, &tmV, 0, head, (int)row1, bar);
+        }
+        if ((!good0 && page[0] != kNoPage) || (small && !good1 && page[1] != kNoPage)) {
+          record_status(p.status, FA_ERR_PAGE);
+          segs[it & 3].lost = 1;
+        }
       }
     }
     to = to + 1 == C::RD ? 0 : to + 1;
@@ -271,8 +306,8 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       }
     }
   };
-  // Fragment k of 16 rows is 16 bytes of every lane: elements (D / 4) c4 + 4 k ..
-  // + 1 and .. + 2, + 3 of rows g8 and g8 + 8 (g8 = lane / 4, c4 = lane % 4).
+  // Fragment k of 8 rows is 8 bytes of every lane: elements (D / 4) c4 + 4 k .. + 3
+  // of row g8 (g8 = lane / 4, c4 = lane % 4); two of them lie side by side.
   auto store_q = [&](int n) {
     uint8_t* at = smem + C::Q_OFF + (n & 1) * C::Q_BYTES;
 #pragma unroll
@@ -287,10 +322,10 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const int up = min(14 - (max((int)(top >> 23), 1) - 127), 127);
       const float mul = pow2_cut(up);
       const int k = D == 128 ? lane & 7 : (lane & 7) >> 1, to_lane = (r & 7) * 4 + (lane >> 3);
-      uint32_t* frag = reinterpret_cast<uint32_t*>(at + ((r >> 4) * (D / 16) + k) * 512 + to_lane * 16) + (r >> 3 & 1);
+      uint32_t* frag = reinterpret_cast<uint32_t*>(at + ((r >> 3) * (D / 32) + (k >> 1)) * 512 + to_lane * 16 + (k & 1) * 8);
 #pragma unroll
       for (int j = 0; j < QE / 2; ++j)
-        frag[2 * (D == 128 ? j : lane & 1)] =
+        frag[D == 128 ? j : lane & 1] =
             pack_f16x2(__uint_as_float(xq[i][j] << 16) * mul, __uint_as_float(xq[i][j] & 0xFFFF0000u) * mul);
       if (lane == 0) reinterpret_cast<int*>(at + C::Q_FRAGS)[r] = up;
     }
@@ -325,35 +360,47 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     // blocks beyond `diag` or below `low` hold keys that some row does not see
     const int diag = p.causal ? f : s.L - 1, low = f + s.ntok - 1 - p.window;
     const uint32_t qat = smem_u32(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES) + lane * 16;
-    float slope2[MT][2];
-    int kend[MT][2], qup[MT][2];
+    uint32_t qf[NR == 1 ? D / 16 : 1][2];              // of 8 rows they stay in registers
+    if (NR == 1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int k = 0; k < D / 16; k += 2) {
+        const uint4 v = lds128(qat + (k >> 1) * 512);
+        qf[NR == 1 ? k : 0][0] = v.x;
+        qf[NR == 1 ? k : 0][1] = v.y;
+        qf[NR == 1 ? k + 1 : 0][0] = v.z;
+        qf[NR == 1 ? k + 1 : 0][1] = v.w;
+      }
+    }
+    // a lane's rows are 8 n + 2 c4 and the next
+    float slope2[NR][2];
+    int kend[NR][2], qup[NR][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * m + 8 * h + g8;
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * n + 2 * c4 + j;
         const bool valid = r < rows;
         const int tok = r / p.group;
-        qup[m][h] = reinterpret_cast<const int*>(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES + C::Q_FRAGS)[r];
-        kend[m][h] = !valid ? -1 : p.causal ? f + tok : s.L - 1;
-        slope2[m][h] = ALIBI && valid ? __ldg(p.alibi + s.g * p.group + r - tok * p.group) * kLog2e : 0.f;
+        qup[n][j] = reinterpret_cast<const int*>(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES + C::Q_FRAGS)[r];
+        kend[n][j] = !valid ? -1 : p.causal ? f + tok : s.L - 1;
+        slope2[n][j] = ALIBI && valid ? __ldg(p.alibi + s.g * p.group + r - tok * p.group) * kLog2e : 0.f;
       }
-    float mref[MT][2], l[MT][2];
-    float o[MT][D / 8][4];
+    float mref[NR][2], l[NR][2];
+    float o[NR][D / 16][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mref[m][0] = mref[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
+    for (int n = 0; n < NR; ++n) {
+      mref[n][0] = mref[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
+      for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[m][t][i] = 0.f;
+        for (int i = 0; i < 4; ++i) o[n][t][i] = 0.f;
     }
     int eref = -1000, etop = -1000;                    // O's unit, the largest it had
-    // ------------------------------------------------------------- blocks
-    const int kb1 = end_block(s), vlo = s.k.vlo, vhi = s.k.vhi;
+    // ------------------------------------------------- steps of two blocks
+    const int kb1 = end_step(s), vlo = s.k.vlo, vhi = s.k.vhi;
 #pragma unroll 1
-    for (int b = first_block(s) + warp; b < kb1; b += W) {
+    for (int b = first_step(s) + warp; b < kb1; b += W) {
       if (dead || !wait_warp_inl(&full[from], par, wc)) {
         // this item's rows and those of all that follow are left alone
         dead = true;
@@ -364,169 +411,204 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       if (fly == C::RD) asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
-      const uint32_t at = ring + from * C::BLOCK_BYTES;
-      const uint4 hd = lds128(heads + from * 16);
+      const uint32_t at = ring + from * C::STEP_BYTES;
+      const uint4 hd = lds128(heads + from * 32);
+      const uint2 sh = lds64(heads + from * 32 + 16);
       --fly;
       if (++from == C::RD) {
         from = 0;
         par ^= 1;
       }
-      const int ek = (int)min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
-      const int ev = (int)min(hd.y >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
-      // S of 16 rows x 8 keys, twice; column n of half t is key 8 t + n
-      float sc[MT][2][4];
+      // S transposed, 16 keys x 8 rows: row g8 and g8 + 8 of a block, columns 2 c4 and
+      // the next
+      float sc[NR][2][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[m][t][i] = 0.f;
+          for (int i = 0; i < 4; ++i) sc[n][x][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        uint4 kw[2];
+        uint4 kw[4];
         // (d = 128: pieces 2 c4 and 2 c4 + 1 of a row, swizzled by it, so that the
         // rows of eight lanes take different places of a line)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 4; ++t)
           kw[t] = lds128(at + (8 * t + g8) * D + (D == 128 ? (2 * c4 + i) ^ g8 : c4 ^ (g8 >> 1)) * 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t b0[2], b1[2];
+        for (int k = 0; k < 4; k += 2) {
+          uint4 q[NR];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) codes_f16(reinterpret_cast<const uint32_t*>(&kw[t])[k], b0[t], b1[t]);
+          for (int n = 0; n < NR; ++n)
+            q[n] = NR > 1 ? lds128(qat + (n * (D / 32) + 2 * i + (k >> 1)) * 512)
+                          : make_uint4(qf[NR == 1 ? 4 * i + k : 0][0], qf[NR == 1 ? 4 * i + k : 0][1],
+                                       qf[NR == 1 ? 4 * i + k + 1 : 0][0], qf[NR == 1 ? 4 * i + k + 1 : 0][1]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint4 q = lds128(qat + (m * (D / 16) + 4 * i + k) * 512);
+          for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) mma_f16(sc[m][t], reinterpret_cast<const uint32_t*>(&q), b0[t], b1[t]);
-          }
+            for (int x = 0; x < 2; ++x) {
+              uint32_t a[4];
+              codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x])[k + kk], a[0], a[2]);
+              codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x + 1])[k + kk], a[1], a[3]);
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_f16(sc[n][x], a, kk ? q[n].z : q[n].x, kk ? q[n].w : q[n].y);
+            }
         }
       }
       // Scores in log2 units are x cs (+ the bias); -inf where a row does not see
       // a key.  With a bias, or where a row does not see all, they are made here.
-      const int k0 = b << 4;
-      const bool masked = k0 + 15 > diag || k0 < low;
-      float cs[MT][2];
+      const int k0 = b << 5;
+      const bool masked = k0 + 31 > diag || k0 < low;
+      const bool live0 = k0 + 16 > vlo, live1 = k0 + 16 < vhi;      // (a block that no row sees has no scale)
+      const int ek[2] = {(int)min(hd.x >> sh.x & 0xffu, (uint32_t)kScaleHigh + 127) - 127,
+                         (int)min(hd.z >> sh.y & 0xffu, (uint32_t)kScaleHigh + 127) - 127};
+      int ev[2] = {(int)min(hd.y >> sh.x & 0xffu, (uint32_t)kScaleHigh + 127) - 127,
+                   (int)min(hd.w >> sh.y & 0xffu, (uint32_t)kScaleHigh + 127) - 127};
+      if (!live0) ev[0] = ev[1];
+      if (!live1) ev[1] = ev[0];
+      float cs[NR][2][2];                              // of a row's two blocks
       bool raise = false;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) cs[m][h] = p.scale_log2 * pow2_cut(ek - qup[m][h]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) cs[n][j][x] = p.scale_log2 * pow2_cut(ek[x] - qup[n][j]);
       if (ALIBI || masked) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float& x = sc[m][t][2 * h + j];
-                const int key = k0 + 8 * t + 2 * c4 + j;
-                x = ALIBI ? fmaf(x, cs[m][h], slope2[m][h] * (float)(key - kend[m][h])) : x * cs[m][h];
-                if (masked && (key > kend[m][h] || (p.causal && key < kend[m][h] - p.window))) x = -INFINITY;
+              for (int h = 0; h < 2; ++h) {
+                float& y = sc[n][x][2 * h + j];
+                const int key = k0 + 16 * x + 8 * h + g8;
+                const float c = cs[n][j][x];
+                y = ALIBI ? fmaf(y, c, slope2[n][j] * (float)(key - kend[n][j])) : y * c;
+                if (masked && (key > kend[n][j] || (p.causal && key < kend[n][j] - p.window))) y = -INFINITY;
               }
-            cs[m][h] = 1.f;
+            cs[n][j][0] = cs[n][j][1] = 1.f;
           }
       }
-      float mx[MT][2];
+      float mx[NR][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[m][h] = fmaxf(fmax3(sc[m][0][2 * h], sc[m][0][2 * h + 1], sc[m][1][2 * h]), sc[m][1][2 * h + 1]) * cs[m][h];
-          raise |= mx[m][h] > mref[m][h] + kTau;
+        for (int j = 0; j < 2; ++j) {
+          mx[n][j] = fmaxf(fmaxf(sc[n][0][j], sc[n][0][2 + j]) * cs[n][j][0], fmaxf(sc[n][1][j], sc[n][1][2 + j]) * cs[n][j][1]);
+          raise |= mx[n][j] > mref[n][j] + kTau;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = mx[m][h];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            const bool up = x > mref[m][h] + kTau;
-            const float alpha = up ? ex2_approx(mref[m][h] - x) : 1.f;
-            if (up) mref[m][h] = x;
-            l[m][h] *= alpha;
+          for (int j = 0; j < 2; ++j) {
+            float x = mx[n][j];
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-              o[m][t][2 * h] *= alpha;
-              o[m][t][2 * h + 1] *= alpha;
+            for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
+            const bool up = x > mref[n][j] + kTau;
+            const float alpha = up ? ex2_approx(mref[n][j] - x) : 1.f;
+            if (up) mref[n][j] = x;
+            l[n][j] *= alpha;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[n][t][j] *= alpha;
+              o[n][t][2 + j] *= alpha;
             }
           }
       }
-      if (ev > eref || ev < eref - 8) {
-        // O's unit follows the values' exponent, at most 2^80 below the largest
-        // so far (which O's float32 holds)
-        etop = max(etop, ev);
-        const int e = max(ev, etop - 80);
-        const float alpha = pow2_cut(eref - e);
-        eref = e;
+      // O's unit follows the values' exponents, at most 2^80 below the largest so
+      // far (which O's float32 holds).  Two blocks further apart than 2^8 take the
+      // products one after the other (the other's P is 0).
+      const int top = max(ev[0], ev[1]), bottom = min(ev[0], ev[1]);
+      const int passes = top - bottom > 8 ? 2 : 1;
+#pragma unroll 1
+      for (int pass = 0; pass < passes; ++pass) {
+        const int hi = passes == 1 ? top : ev[pass], lo = passes == 1 ? bottom : ev[pass];
+        if (hi > eref || lo < eref - 8) {
+          etop = max(etop, hi);
+          const int e = max(hi, etop - 80);
+          const float alpha = pow2_cut(eref - e);
+          eref = e;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int t = 0; t < D / 8; ++t)
+            for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[m][t][i] *= alpha;
-      }
-      // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
-      const int up = max(ev - eref + 7, -126);
-      const float lsv = (float)up, back = pow2_cut(-up);
-      uint32_t pf[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float mb = lsv - (mref[m][h] == -INFINITY ? 0.f : mref[m][h]);
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(sc[m][i >> 1][2 * h + (i & 1)], cs[m][h], mb));
-          l[m][h] = fmaf((e[0] + e[1]) + (e[2] + e[3]), back, l[m][h]);
-          pf[m][h] = pack_f16x2(e[0], e[1]);
-          pf[m][2 + h] = pack_f16x2(e[2], e[3]);
+              for (int i = 0; i < 4; ++i) o[n][t][i] *= alpha;
         }
-      // O of 16 rows x 8 columns, D / 8 times: column g8 of product t is element
-      // g8 D / 8 + t
-      {
-        const uint32_t vat = at + C::POOL;
-        uint32_t w[4][D / 32];                         // of the keys 2 c4, 2 c4 + 1, 8 + 2 c4, 9 + 2 c4
+        // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
+        float lsv[2], back[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * (i >> 1) + 2 * c4 + (i & 1);
-          if (D == 128) {
-            const uint4 v = lds128(vat + r * 128 + (g8 ^ (r & 7)) * 16);
-            w[i][0] = v.x;
-            w[i][1] = v.y;
-            w[i][D / 32 - 2] = v.z;
-            w[i][D / 32 - 1] = v.w;
-          } else {
-            const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ (r >> 1 & 3)) * 16 + (g8 & 1) * 8);
-            w[i][0] = v.x;
-            w[i][1] = v.y;
+        for (int x = 0; x < 2; ++x) {
+          const int up = max(ev[x] - eref + 7, -126);
+          const bool on = passes == 1 || pass == x;
+          lsv[x] = on ? (float)up : -1e6f;
+          back[x] = pow2_cut(-up);
+        }
+        uint32_t pf[NR][2][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const float mr[2] = {mref[n][0] == -INFINITY ? 0.f : mref[n][0], mref[n][1] == -INFINITY ? 0.f : mref[n][1]};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(sc[n][x][i], cs[n][i & 1][x], lsv[x] - mr[i & 1]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) l[n][j] = fmaf(e[j] + e[2 + j], back[x], l[n][j]);
+            pf[n][x][0] = transposed(pack_f16x2(e[0], e[1]));
+            pf[n][x][1] = transposed(pack_f16x2(e[2], e[3]));
           }
         }
-        // a slot that no row sees may hold NaN, and 0 x NaN would reach O
-        if (masked && (k0 < vlo || k0 + 16 > vhi)) {
+        // O transposed, 16 elements x 8 rows, D / 16 times: row g8 of product t is
+        // element g8 D / 8 + 2 t, row g8 + 8 the next
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t vat = at + C::POOL + x * 16 * D;
+          uint32_t w[4][D / 32];                       // of the block's keys 2 c4, 2 c4 + 1, 8 + 2 c4, 9 + 2 c4
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = k0 + 8 * (i >> 1) + 2 * c4 + (i & 1);
-            if (key < vlo || key >= vhi)
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
+            const int r = 8 * (i >> 1) + 2 * c4 + (i & 1);
+            if (D == 128) {
+              const uint4 v = lds128(vat + r * 128 + (g8 ^ (r & 7)) * 16);
+              w[i][0] = v.x;
+              w[i][1] = v.y;
+              w[i][D / 32 - 2] = v.z;
+              w[i][D / 32 - 1] = v.w;
+            } else {
+              const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ (r >> 1 & 3)) * 16 + (g8 & 1) * 8);
+              w[i][0] = v.x;
+              w[i][1] = v.y;
+            }
           }
-        }
+          // a slot that no row sees may hold NaN, and 0 x NaN would reach O
+          if (masked && (k0 < vlo || k0 + 32 > vhi)) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t b0[4], b1[4];
-          codes_f16(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
-          codes_f16(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
-          codes_f16(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
-          codes_f16(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+            for (int i = 0; i < 4; ++i) {
+              const int key = k0 + 16 * x + 8 * (i >> 1) + 2 * c4 + (i & 1);
+              if (key < vlo || key >= vhi)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
+            }
+          }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma_f16(o[m][4 * i + j], pf[m], b0[j], b1[j]);
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t b0[4], b1[4];
+            codes_f16(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
+            codes_f16(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
+            codes_f16(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
+            codes_f16(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_f16(o[n][2 * i + j], a, pf[n][x][0], pf[n][x][1]);
+            }
+          }
         }
       }
       __syncwarp();
@@ -535,13 +617,13 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     if (next) store_q(cur + 1);
     // ------------------------------------------------- join the warps' parts
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = l[m][h];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (c4 == 0) mls[warp * C::ROWS + 16 * m + 8 * h + g8] = make_float2(mref[m][h], x);
+      for (int j = 0; j < 2; ++j) {
+        float x = l[n][j];
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
+        if (g8 == 0) mls[warp * C::ROWS + 8 * n + 2 * c4 + j] = make_float2(mref[n][j], x);
       }
     __syncthreads();
     if (threadIdx.x < rows) {
@@ -554,16 +636,16 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       stat[threadIdx.x] = make_float2(M, L);
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int j = 0; j < 2; ++j) {
         float M = -INFINITY;
-        for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + 16 * m + 8 * h + g8].x);
-        const float a = (mref[m][h] == M ? 1.f : ex2_approx(mref[m][h] - M)) * pow2_cut(eref - 7);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + 8 * n + 2 * c4 + j].x);
+        const float a = (mref[n][j] == M ? 1.f : ex2_approx(mref[n][j] - M)) * pow2_cut(eref - 7);
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          o[m][t][2 * h] *= a;
-          o[m][t][2 * h + 1] *= a;
+        for (int t = 0; t < D / 16; ++t) {
+          o[n][t][j] *= a;
+          o[n][t][2 + j] *= a;
         }
       }
     const int part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
@@ -572,19 +654,16 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {                 // 64 columns at a time
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * m + 8 * h + g8;
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * n + 2 * c4 + j;
           if (r < rows) {
-            float* at = red + (warp * C::ROWS + r) * C::RED_STRIDE + 16 * c4;
+            float* at = red + (warp * C::ROWS + r) * C::RED_STRIDE + 8 * g8;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<float4*>(at + 8 * j + 4 * q) =
-                    make_float4(o[m][8 * c + 4 * q][2 * h + j], o[m][8 * c + 4 * q + 1][2 * h + j],
-                                o[m][8 * c + 4 * q + 2][2 * h + j], o[m][8 * c + 4 * q + 3][2 * h + j]);
+            for (int q = 0; q < 2; ++q)
+              *reinterpret_cast<float4*>(at + 4 * q) = make_float4(o[n][4 * c + 2 * q][j], o[n][4 * c + 2 * q][2 + j],
+                                                                   o[n][4 * c + 2 * q + 1][j], o[n][4 * c + 2 * q + 1][2 + j]);
           }
         }
       __syncthreads();
@@ -642,15 +721,15 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
 }
 
-template <int D, int MT>
+template <int D, int NR>
 int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
-  using C = Few<D, MT>;
-  auto kern = p.alibi ? fwd_paged_few_kernel<D, MT, true> : fwd_paged_few_kernel<D, MT, false>;
+  using C = Few<D, NR>;
+  auto kern = p.alibi ? fwd_paged_few_kernel<D, NR, true> : fwd_paged_few_kernel<D, NR, false>;
   if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return e;
   CUtensorMap tk, tv;
   const long long slots = (long long)p.num_pages * p.page_size;
-  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, 16)) return e;
-  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, 16)) return e;
+  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, std::min(p.page_size, 32))) return e;
+  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, std::min(p.page_size, 32))) return e;
   kern<<<grid, C::NT, C::SMEM_BYTES, stream>>>(tk, tv, p);
   return (int)cudaGetLastError();
 }
@@ -659,8 +738,9 @@ int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
 
 int launch_fwd_paged_few(const PagedParams& p, int grid, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 1>(p, grid, stream) : launch_few<64, 1>(p, grid, stream);
-  return p.d == 128 ? launch_few<128, 2>(p, grid, stream) : launch_few<64, 2>(p, grid, stream);
+  if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, stream) : launch_few<64, 1>(p, grid, stream);
+  if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, stream) : launch_few<64, 2>(p, grid, stream);
+  return p.d == 128 ? launch_few<128, 4>(p, grid, stream) : launch_few<64, 4>(p, grid, stream);
 }
 
 }  // namespace fa

@@ -413,7 +413,8 @@ def parts(new, Hq, Hkv):
     """What P loses by its rounding, of each row: relative to P, and of each key."""
     G = Hq // Hkv
     tpt = 128 // G
-    few = 32 if max(new) * G <= 32 else 16 if G <= 16 else 32 if G <= 32 else 0
+    most = max(new) * G if max(new) * G <= 32 else G
+    few = next((r for r in (8, 16, 32) if most <= r), 0)
     out = []
     for n in new:
         if n * G <= few:
