@@ -5,14 +5,10 @@
 //     S = scale Q K^T (+ ALiBi),   O = softmax(S) V,   k = 2^ek ck,  v = 2^ev cv
 // with codes c and one pair of exponents for every 16 slots of a kv head.
 //
-// A warp takes 32 keys (two such blocks) at a time by itself: TMA brings their
-// codes into a ring of the warp's own, ahead and on into the next items, and no
-// warp waits for another until an item ends.  The products are matrix
-// instructions of 16 rows whose operands go straight from shared memory into
-// registers: the order of the elements along d (and of the keys, for P V) is
-// free as long as both operands agree, so each lane's operands are whole 16-byte
-// reads.  The exponents stay out of the products: 2^ek multiplies a block's
-// scores, and 2^(ev - eref) its P, with O held in units of 2^eref.
+// One warp brings the codes: TMA into a ring of steps of 32 keys (two such
+// blocks), cp.async for their exponents, ahead and on into the next items.  The
+// others take the steps in turn, each by itself (its own m, l and O), and meet
+// when an item ends.
 // Codes become fp16 (exact) in registers: two instructions for four of them.
 // (mma.sync with e4m3 operands is no way around that: it is taken apart into the
 // same conversions and fp16 products, and took 1.4 times as long.)
@@ -40,31 +36,36 @@ namespace {
 template <int D, int NR>
 struct Few {
   static constexpr int ROWS = 8 * NR;
-  // Warps: as many as the registers of O (D NR / 4 of a lane) and shared memory
-  // leave room for.
-  static constexpr int W = D == 128 ? (NR == 1 ? 12 : NR == 2 ? 10 : 8) : (NR == 4 ? 12 : 16);
-  static constexpr int NT = 32 * W;
-  static constexpr int RD = 2;                              // steps of a warp's ring
+  // Warps that take steps: as many as the registers of O (D NR / 4 of a lane)
+  // leave room for beside the one that brings the codes.
+  static constexpr int W = NR * D <= 128 ? 15 : NR * D <= 256 ? 11 : 7;
+  static constexpr int NT = 32 * (W + 1);
+  // Blocks of a step that are taken together.
+  static constexpr int XB = NR <= 2 ? 2 : 1;
   static constexpr int POOL = 32 * D;                       // codes of a step in one pool
   static constexpr int STEP_BYTES = 2 * POOL;
   static constexpr int RED_STRIDE = 68;                     // floats per row of 64 columns
-  static constexpr int RING_OFF = 0;
-  static constexpr int HEAD_OFF = RING_OFF + W * RD * STEP_BYTES;    // scales of the ring's steps
-  static constexpr int RED_OFF = HEAD_OFF + W * RD * 32;
-  static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
-  static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
   // Q of an item and of the next, as fragments, and the rows' exponents
   static constexpr int Q_FRAGS = NR * (D / 16) * 256;
   static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
+  // Steps of the ring: what the rest leaves of shared memory, at most 160 KB (what
+  // HBM's latency asks for is about 60).
+  static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 8 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
+  static constexpr int FIT = (227 * 1024 - REST) / (STEP_BYTES + 48);
+  static constexpr int NS = FIT < 163840 / STEP_BYTES ? FIT : 163840 / STEP_BYTES;
+  static constexpr int RING_OFF = 0;
+  static constexpr int HEAD_OFF = RING_OFF + NS * STEP_BYTES;        // exponents of the ring's steps
+  static constexpr int RED_OFF = HEAD_OFF + NS * 32;
+  static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
+  static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
   static constexpr int Q_OFF = STAT_OFF + ROWS * 8;
   static constexpr int SEG_OFF = Q_OFF + 2 * Q_BYTES;
-  static constexpr int WALK_OFF = SEG_OFF + 4 * 96;
-  static constexpr int PAR_OFF = WALK_OFF + 128;
-  static constexpr int FULL_OFF = PAR_OFF + 256;            // barriers of the ring's steps
-  static constexpr int BAR_OFF = FULL_OFF + W * RD * 8;
+  static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;
+  static constexpr int RINGBAR_OFF = PAR_OFF + 256;         // full and empty of the ring's steps
+  static constexpr int BAR_OFF = RINGBAR_OFF + NS * 16;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(kPagedMaxBatch * 8 <= W * RD * STEP_BYTES, "plan");
+  static_assert(kPagedMaxBatch * 8 <= NS * STEP_BYTES, "plan");
   static_assert(Q_OFF % 16 == 0 && Q_BYTES % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
@@ -106,41 +107,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 
-// What finds the run's items, in shared memory, and what the run's parts are
-// for the merge: `cont` the part that goes on from the CTA before (2: the item's
-// last), `begun` the item begun here.
-struct Finder {
-  Walk walk;
-  int more, cont;
-  int4 begun;
-};
-static_assert(sizeof(Finder) <= 128, "finder");
-
-// Item n of the run into segs[n % 4] (ie < 0: the end).  By warp 0, once per
-// item; out of line, and with its state in shared memory, so that the loop over
-// keys has the registers: what it spills does not even stay in L1, of which
-// shared memory leaves little (16 caches, one token each: 305 us with the queries'
-// fragments and this state in registers).
-static __device__ __noinline__ void find_item(const PagedParams& p, Finder& f, Seg* segs, int n) {
-  if (!f.more) return;
-  Walk w = f.walk;
-  Seg s;
-  s.lost = 0;
-  const bool more = walk_next<true>(p, w, s);
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    if (!more) {
-      s.ie = -1;
-    } else if (s.ib > 0) {
-      f.cont = s.ie == s.k.kt ? 2 : 1;
-    } else if (s.ie < s.k.kt) {
-      f.begun = make_int4(1, s.tok, s.ntok, s.g);
-    }
-    f.walk = w;
-    f.more = more;
-    segs[n & 3] = s;
-  }
-  __syncwarp();
+// Completes one of the arrivals that `bar` waits for when this thread's copies
+// so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
 template <int D, int NR, bool ALIBI>
@@ -148,7 +118,7 @@ __global__ void __launch_bounds__(Few<D, NR>::NT, 1)
 fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PagedParams p) {
   using C = Few<D, NR>;
-  constexpr int W = C::W;
+  constexpr int W = C::W, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::BAR_OFF);
@@ -156,9 +126,17 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const PagedParams& ps = *reinterpret_cast<const PagedParams*>(smem + C::PAR_OFF);
   if (threadIdx.x < sizeof(PagedParams) / 4)
     reinterpret_cast<uint32_t*>(smem + C::PAR_OFF)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&p)[threadIdx.x];
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::FULL_OFF) + warp * C::RD;
-  if (lane < C::RD) mbar_init(&full[lane], 1);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::RINGBAR_OFF);
+  uint64_t* const empty = full + NS;
+  if (threadIdx.x < NS) {
+    mbar_init(&full[threadIdx.x], 5);                  // the codes, four exponents
+    mbar_init(&empty[threadIdx.x], 1);
+  }
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], W);
+    }
     bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -167,120 +145,134 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   __syncthreads();
   make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kMinRunOne);
   fence_proxy_async_smem();                            // (the plan's sums lay where TMA will write)
-  grid_launch_dependents();
-
-  // The run's items: segs[n % 4] is item n (ie < 0: the end).  Warp 0 finds them,
-  // two ahead; each is published by the barriers of an item's end.
-  Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
-  Finder& finder = *reinterpret_cast<Finder*>(smem + C::WALK_OFF);
-  if (warp == 0) {
-    if (lane == 0) {
-      Walk w;
-      walk_begin<true>(p, bars, w);
-      finder.walk = w;
-      finder.more = 1;
-      finder.cont = 0;
-      finder.begun = make_int4(0, 0, 0, 0);
-    }
-    __syncwarp();
-    find_item(ps, finder, segs, 0);
-    find_item(ps, finder, segs, 1);
-  }
   __syncthreads();
+  grid_launch_dependents();
+  const WaitCtx wc{&bars->abort_flag, p.status};
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp_inl(bar, parity, wc); };
+  // The run's items: segs[n % kSegs] is item n (ie < 0: the end).
+  Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
+  auto first_step = [](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 4, s.k.vlo >> 5); };
+  auto end_step = [](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 4, (s.k.vhi + 31) >> 5); };
 
-  // ---- this warp's steps of 32 keys on their way: step kb of item `it` is the next
-  const uint32_t ring = smem_u32(smem + C::RING_OFF) + warp * C::RD * C::STEP_BYTES;
-  const uint32_t heads = smem_u32(smem + C::HEAD_OFF) + warp * C::RD * 32;
-  const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
-  const bool small = p.page_shift == 4;                // a step lies in two pages
-  auto first_step = [&](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 4, s.k.vlo >> 5); };
-  auto end_step = [&](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 4, (s.k.vhi + 31) >> 5); };
-  int it = 0, kb = 0, kb_end = 0, head = 0;
-  int page[2] = {0, 0};                                // of the step's halves
-  int fly = 0;                                         // steps in the ring
-  int to = 0, from = 0;                                // places of the next step to fetch, to take
-  unsigned par = 0;                                    // parity of place `from`
-  const int32_t* table = p.block_table;
-  bool any = false;                                    // step kb exists, its pages are in `page`
-  bool dead = false;                                   // a wait ran out
-  int cur = 0;                                         // the item being worked on
-  auto enter = [&](int n) {
-    const Seg& s = segs[n & 3];
-    it = n;
-    kb = first_step(s) + warp;
-    kb_end = end_step(s);
-    table = p.block_table + (long long)s.b * p.max_pages;
-    head = s.g;
-  };
-  constexpr int kNoPage = -0x7fffffff - 1;             // no row sees these keys
-  auto look_up = [&] {
-    if (small) {
-      const Seg& s = segs[it & 3];
-      page[0] = (kb << 5) + 16 > s.k.vlo ? max(__ldg(table + 2 * kb), -1) : kNoPage;
-      page[1] = (kb << 5) + 16 < s.k.vhi ? max(__ldg(table + 2 * kb + 1), -1) : kNoPage;
-    } else {
-      page[0] = max(__ldg(table + ((kb << 5) >> p.page_shift)), -1);
-    }
-  };
-  auto settle = [&] {                                  // on to the next step that exists
-    any = !dead;
-    while (any && kb >= kb_end) {
-      // (items behind the next one are not known yet)
-      if (it > cur || segs[(it + 1) & 3].ie < 0) {
-        any = false;
-        return;
-      }
-      enter(it + 1);
-    }
-    if (any) look_up();
-  };
-  auto fetch = [&] {
-    const uint32_t hd = heads + to * 32;
-    const bool good0 = (unsigned)page[0] < (unsigned)p.num_pages;
-    const bool good1 = small ? (unsigned)page[1] < (unsigned)p.num_pages : good0;
-    const uint32_t row0 = good0 ? (uint32_t)page[0] * p.page_size + ((kb << 5) & (p.page_size - 1)) : 0;
-    const uint32_t row1 = !small ? row0 + 16 : good1 ? (uint32_t)page[1] * 16 : 0;
-    if (lane < 4) {                                    // the scales: of the halves' keys, of their values
-      const bool good = lane >> 1 ? good1 : good0;
-      const long long j = good ? (long long)((lane >> 1 ? row1 : row0) >> 4) * p.Hkv + head : 0;
-      copy_async4(hd + 4 * lane, (lane & 1 ? p.v_scales : p.k_scales) + (j & ~3ll),
-                  good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
-      if (!(lane & 1)) sts32(hd + 16 + 2 * lane, (uint32_t)(j & 3) * 8);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (lane == 0) {
-      uint64_t* bar = &full[to];
-      uint8_t* at = smem + C::RING_OFF + (warp * C::RD + to) * C::STEP_BYTES;
-      if (!small && good0) {
-        mbar_arrive_expect_tx(bar, C::STEP_BYTES);
-        tma_load_3d(at, &tmK, 0, head, (int)row0, bar);
-        tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row0, bar);
+  if (warp == W) {
+    // ------------------------------------------------------------ producer
+    // Finds the run's items, one ahead of the steps it fetches, and fetches four
+    // steps at a time: lane 4 i + j brings exponent j of step i (of its two blocks'
+    // keys and values), lane 4 i its codes.
+    Walk w;
+    Seg s;
+    s.lost = 0;
+    walk_begin<true>(p, bars, w);
+    // what the parts of this CTA are, for the merge: kind of the part that goes on
+    // from the CTA before (2: the item's last), and the item begun here
+    int cont = 0;
+    int4 begun = make_int4(0, 0, 0, 0);
+    bool more = true, ok = true;
+    auto publish = [&](int n) {
+      if (n >= kSegs && !wait(&bars->seg_empty[n % kSegs], (n / kSegs - 1) & 1)) return false;
+      more = walk_next<true>(p, w, s);
+      if (more) {
+        if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
+        else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
       } else {
-        // pages of 16 slots one by one; one that is not there is not read, and
-        // if a row sees its keys, the item's rows are not written
-        mbar_arrive_expect_tx(bar, small ? (good0 + good1) * (C::STEP_BYTES / 2) : 0);
-        if (small && good0) {
-          tma_load_3d(at, &tmK, 0, head, (int)row0, bar);
-          tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row0, bar);
+        s.ie = -1;
+      }
+      if (lane == 0) {
+        segs[n % kSegs] = s;
+        mbar_arrive(&bars->seg_full[n % kSegs]);
+      }
+      __syncwarp();
+      return true;
+    };
+    const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
+    const bool small = p.page_shift == 4;              // a step lies in two pages
+    const int step_of = lane >> 2 & 3, half = lane >> 1 & 1;
+    const uint8_t* const scales = lane & 1 ? p.v_scales : p.k_scales;
+    constexpr int kNoPage = -0x7fffffff - 1;           // no row sees these keys
+    int place = 0;                                     // of the next step in the ring
+    unsigned par = 1;                                  // parity of its last emptying (the first: none to wait for)
+    ok = publish(0);
+    for (int n = 0; ok && more; ++n) {
+      const int b1 = end_step(s), head = s.g, vlo = s.k.vlo, vhi = s.k.vhi;
+      int b = first_step(s);
+      const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
+      int* const lost = &segs[n % kSegs].lost;
+      auto look_up = [&](int b0) {
+        const int key = ((b0 + step_of) << 5) + 16 * half;
+        const bool in = b0 + step_of < b1 && (!small || (key < vhi && key + 16 > vlo));
+        return in ? max(__ldg(table + (min(key, vhi - 1) >> p.page_shift)), -1) : kNoPage;
+      };
+      int page = look_up(b);
+      if (!(ok = publish(n + 1))) break;
+      for (; b < b1; b += 4) {
+        const int next_page = look_up(b + 4);
+        const int steps = min(4, b1 - b);
+        const int mine = place + step_of >= NS ? place + step_of - NS : place + step_of;
+        const unsigned mine_par = place + step_of >= NS ? par ^ 1 : par;
+        // (lanes without a step ask for the first one's place)
+        const bool in = lane < 4 * steps;
+        if (!(ok = wait(&empty[in ? mine : place], in ? mine_par : par))) break;
+        const bool good = (unsigned)page < (unsigned)p.num_pages;
+        const int key = ((b + step_of) << 5) + 16 * half;
+        const uint32_t row = good ? (uint32_t)page * p.page_size + (key & (p.page_size - 1)) : 0;
+        const int other = __shfl_xor_sync(0xffffffffu, page, 2);
+        const uint32_t row1 = __shfl_xor_sync(0xffffffffu, row, 2);
+        if (in) {
+          const uint32_t hd = smem_u32(smem + C::HEAD_OFF) + mine * 32;
+          const long long j = good ? (long long)(row >> 4) * p.Hkv + head : 0;
+          copy_async4(hd + 4 * (lane & 3), scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
+          if (!(lane & 1)) sts32(hd + 16 + 4 * half, (uint32_t)(j & 3) * 8);
         }
-        if (small && good1) {
-          tma_load_3d(at + C::POOL / 2, &tmK, 0, head, (int)row1, bar);
-          tma_load_3d(at + C::POOL + C::POOL / 2, &tmV, 0, head, (int)row1, bar);
+        __syncwarp();
+        if (in && (lane & 3) == 0) {
+          const bool good1 = (unsigned)other < (unsigned)p.num_pages;
+          uint8_t* at = smem + C::RING_OFF + mine * C::STEP_BYTES;
+          // a page that is not there is not read, and if a row sees its keys, the
+          // item's rows are not written
+          if ((!good && page != kNoPage) || (!good1 && other != kNoPage)) {
+            record_status(p.status, FA_ERR_PAGE);
+            *lost = 1;
+          }
+          // a step's 32 slots at once, or those of each of its two pages
+          const bool first = good, second = small && good1;
+          mbar_arrive_expect_tx(&full[mine], small ? (first + second) * (C::STEP_BYTES / 2) : first ? C::STEP_BYTES : 0);
+          if (first) {
+            tma_load_3d(at, &tmK, 0, head, (int)row, &full[mine]);
+            tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row, &full[mine]);
+          }
+          if (second) {
+            tma_load_3d(at + C::POOL / 2, &tmK, 0, head, (int)row1, &full[mine]);
+            tma_load_3d(at + C::POOL + C::POOL / 2, &tmV, 0, head, (int)row1, &full[mine]);
+          }
         }
-        if ((!good0 && page[0] != kNoPage) || (small && !good1 && page[1] != kNoPage)) {
-          record_status(p.status, FA_ERR_PAGE);
-          segs[it & 3].lost = 1;
+        if (in) copies_arrive(&full[mine]);
+        __syncwarp();
+        place += steps;
+        if (place >= NS) {
+          place -= NS;
+          par ^= 1;
         }
+        page = next_page;
       }
     }
-    to = to + 1 == C::RD ? 0 : to + 1;
-    ++fly;
-    kb += W;
-    if (kb < kb_end) look_up();
-    else settle();
-  };
-  if (segs[0].ie >= 0) enter(0);
+    // Copies in flight must land before this CTA's shared memory goes away: of
+    // every place that was filled (its parity: the emptying it waited for, turned).
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int i = 0; i < NS; ++i) {
+      const unsigned last = (i < place ? par : par ^ 1) ^ 1;      // parity of the place's last fill
+      wait_warp_drain(&full[i], last);
+    }
+    __syncthreads();
+    // A wait ran out, so parts may be missing: the merge must not take what the
+    // workspace held.  Nor a part of an item that met a page outside the pool.
+    if (lane < 2)
+      p.part_meta[2 * blockIdx.x + lane] = bars->abort_flag || bars->part_lost[lane] ? make_int4(0, 0, 0, 0)
+                                           : lane ? begun : make_int4(cont, 0, 0, 0);
+    return;
+  }
 
+  // -------------------------------------------------------- the other warps
+  auto meet = [] { named_bar_sync(1, 32 * W); };       // barrier of these warps
   // ---- Q: a warp prepares rows warp, warp + W, .. of the next item, a lane D /
   // 32 elements, while it works on this one
   constexpr int QP = (C::ROWS + W - 1) / W;
@@ -330,31 +322,33 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       if (lane == 0) reinterpret_cast<int*>(at + C::Q_FRAGS)[r] = up;
     }
   };
-  if (segs[0].ie >= 0) {
-    settle();
-#pragma unroll 1
-    while (any && fly < C::RD) fetch();
+  // Items n and n + 1 are known; the same answer for every warp.
+  auto known = [&](int n) {
+    bool ok = wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1);
+    if (ok && segs[n % kSegs].ie >= 0) ok = wait(&bars->seg_full[(n + 1) % kSegs], ((n + 1) / kSegs) & 1);
+    return !named_bar_any(1, 32 * W, !ok);
+  };
+  bool go = known(0) && segs[0].ie >= 0;
+  if (go) {
     load_q(segs[0]);
     store_q(0);
+    meet();
   }
-  __syncthreads();
 
   const int g8 = lane >> 2, c4 = lane & 3;
   float* red = reinterpret_cast<float*>(smem + C::RED_OFF);
   float2* mls = reinterpret_cast<float2*>(smem + C::ML_OFF);
   float2* stat = reinterpret_cast<float2*>(smem + C::STAT_OFF);
-  const WaitCtx wc{&bars->abort_flag, p.status};
+  bool dead = false;                                   // a wait for a step ran out
+  int turn = warp;                                     // this warp's first step of the item
+  int from = 0;                                        // place of the item's first step in the ring
+  unsigned par = 0;                                    // parity of its filling
 
 #pragma unroll 1
-  for (;; ++cur) {
-    const Seg& s = segs[cur & 3];
-    if (s.ie < 0) break;
-    if (!any) settle();
-#pragma unroll 1
-    while (any && fly < C::RD) fetch();
-    if (warp == 0) find_item(ps, finder, segs, cur + 2);
-    const bool next = segs[(cur + 1) & 3].ie >= 0;
-    if (next) load_q(segs[(cur + 1) & 3]);
+  for (int cur = 0; go; ++cur) {
+    const Seg& s = segs[cur % kSegs];
+    const bool next = segs[(cur + 1) % kSegs].ie >= 0;
+    if (next) load_q(segs[(cur + 1) % kSegs]);
     const int rows = s.ntok * p.group;
     const int f = s.k.f[0];
     // blocks beyond `diag` or below `low` hold keys that some row does not see
@@ -397,222 +391,243 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         for (int i = 0; i < 4; ++i) o[n][t][i] = 0.f;
     }
     int eref = -1000, etop = -1000;                    // O's unit, the largest it had
-    // ------------------------------------------------- steps of two blocks
-    const int kb1 = end_step(s), vlo = s.k.vlo, vhi = s.k.vhi;
+    // ------------------------------------------------------------- steps
+    const int b0 = first_step(s), steps = max(end_step(s) - b0, 0), vlo = s.k.vlo, vhi = s.k.vhi;
+    int place = from + turn, lap = par;
+    while (place >= NS) {
+      place -= NS;
+      lap ^= 1;
+    }
+    int step = turn;
 #pragma unroll 1
-    for (int b = first_step(s) + warp; b < kb1; b += W) {
-      if (dead || !wait_warp_inl(&full[from], par, wc)) {
+    for (; step < steps; step += W) {
+      const int b = b0 + step;
+      if (dead || !wait(&full[place], lap)) {
         // this item's rows and those of all that follow are left alone
         dead = true;
-        any = false;
-        if (lane == 0) segs[cur & 3].lost = 1;
+        if (lane == 0) segs[cur % kSegs].lost = 1;
         break;
       }
-      if (fly == C::RD) asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
-      else asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncwarp();
-      const uint32_t at = ring + from * C::STEP_BYTES;
-      const uint4 hd = lds128(heads + from * 32);
-      const uint2 sh = lds64(heads + from * 32 + 16);
-      --fly;
-      if (++from == C::RD) {
-        from = 0;
-        par ^= 1;
-      }
-      // S transposed, 16 keys x 8 rows: row g8 and g8 + 8 of a block, columns 2 c4 and
-      // the next
-      float sc[NR][2][4];
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[n][x][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        uint4 kw[4];
-        // (d = 128: pieces 2 c4 and 2 c4 + 1 of a row, swizzled by it, so that the
-        // rows of eight lanes take different places of a line)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          kw[t] = lds128(at + (8 * t + g8) * D + (D == 128 ? (2 * c4 + i) ^ g8 : c4 ^ (g8 >> 1)) * 16);
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          uint4 q[NR];
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-            q[n] = NR > 1 ? lds128(qat + (n * (D / 32) + 2 * i + (k >> 1)) * 512)
-                          : make_uint4(qf[NR == 1 ? 4 * i + k : 0][0], qf[NR == 1 ? 4 * i + k : 0][1],
-                                       qf[NR == 1 ? 4 * i + k + 1 : 0][0], qf[NR == 1 ? 4 * i + k + 1 : 0][1]);
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t a[4];
-              codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x])[k + kk], a[0], a[2]);
-              codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x + 1])[k + kk], a[1], a[3]);
-#pragma unroll
-              for (int n = 0; n < NR; ++n) mma_f16(sc[n][x], a, kk ? q[n].z : q[n].x, kk ? q[n].w : q[n].y);
-            }
-        }
-      }
-      // Scores in log2 units are x cs (+ the bias); -inf where a row does not see
-      // a key.  With a bias, or where a row does not see all, they are made here.
+      const uint32_t at = smem_u32(smem + C::RING_OFF) + place * C::STEP_BYTES;
+      const uint4 hd = lds128(smem_u32(smem + C::HEAD_OFF) + place * 32);
+      const uint2 sh = lds64(smem_u32(smem + C::HEAD_OFF) + place * 32 + 16);
       const int k0 = b << 5;
       const bool masked = k0 + 31 > diag || k0 < low;
-      const bool live0 = k0 + 16 > vlo, live1 = k0 + 16 < vhi;      // (a block that no row sees has no scale)
-      const int ek[2] = {(int)min(hd.x >> sh.x & 0xffu, (uint32_t)kScaleHigh + 127) - 127,
-                         (int)min(hd.z >> sh.y & 0xffu, (uint32_t)kScaleHigh + 127) - 127};
-      int ev[2] = {(int)min(hd.y >> sh.x & 0xffu, (uint32_t)kScaleHigh + 127) - 127,
-                   (int)min(hd.w >> sh.y & 0xffu, (uint32_t)kScaleHigh + 127) - 127};
-      if (!live0) ev[0] = ev[1];
-      if (!live1) ev[1] = ev[0];
-      float cs[NR][2][2];                              // of a row's two blocks
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) cs[n][j][x] = p.scale_log2 * pow2_cut(ek[x] - qup[n][j]);
-      if (ALIBI || masked) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float& y = sc[n][x][2 * h + j];
-                const int key = k0 + 16 * x + 8 * h + g8;
-                const float c = cs[n][j][x];
-                y = ALIBI ? fmaf(y, c, slope2[n][j] * (float)(key - kend[n][j])) : y * c;
-                if (masked && (key > kend[n][j] || (p.causal && key < kend[n][j] - p.window))) y = -INFINITY;
-              }
-            cs[n][j][0] = cs[n][j][1] = 1.f;
-          }
-      }
-      float mx[NR][2];
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mx[n][j] = fmaxf(fmaxf(sc[n][0][j], sc[n][0][2 + j]) * cs[n][j][0], fmaxf(sc[n][1][j], sc[n][1][2 + j]) * cs[n][j][1]);
-          raise |= mx[n][j] > mref[n][j] + kTau;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float x = mx[n][j];
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
-            const bool up = x > mref[n][j] + kTau;
-            const float alpha = up ? ex2_approx(mref[n][j] - x) : 1.f;
-            if (up) mref[n][j] = x;
-            l[n][j] *= alpha;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-              o[n][t][j] *= alpha;
-              o[n][t][2 + j] *= alpha;
-            }
-          }
-      }
-      // O's unit follows the values' exponents, at most 2^80 below the largest so
-      // far (which O's float32 holds).  Two blocks further apart than 2^8 take the
-      // products one after the other (the other's P is 0).
-      const int top = max(ev[0], ev[1]), bottom = min(ev[0], ev[1]);
-      const int passes = top - bottom > 8 ? 2 : 1;
 #pragma unroll 1
-      for (int pass = 0; pass < passes; ++pass) {
-        const int hi = passes == 1 ? top : ev[pass], lo = passes == 1 ? bottom : ev[pass];
-        if (hi > eref || lo < eref - 8) {
-          etop = max(etop, hi);
-          const int e = max(hi, etop - 80);
-          const float alpha = pow2_cut(eref - e);
-          eref = e;
+      for (int y = 0; y < 2; y += C::XB) {             // blocks y .. y + XB - 1
+        if (C::XB == 1 && !(y ? k0 + 16 < vhi : k0 + 16 > vlo)) continue;
+        constexpr int XB = C::XB;
+        // S transposed, 16 keys x 8 rows: row g8 and g8 + 8 of a block, columns 2 c4 and
+        // the next
+        float sc[NR][XB][4];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int x = 0; x < XB; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[n][x][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint4 kw[2 * XB];
+          // (d = 128: pieces 2 c4 and 2 c4 + 1 of a row, swizzled by it, so that the
+          // rows of eight lanes take different places of a line)
+#pragma unroll
+          for (int t = 0; t < 2 * XB; ++t)
+            kw[t] = lds128(at + (16 * y + 8 * t + g8) * D + (D == 128 ? (2 * c4 + i) ^ g8 : c4 ^ (g8 >> 1)) * 16);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            uint4 q[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              q[n] = NR > 1 ? lds128(qat + (n * (D / 32) + 2 * i + (k >> 1)) * 512)
+                            : make_uint4(qf[NR == 1 ? 4 * i + k : 0][0], qf[NR == 1 ? 4 * i + k : 0][1],
+                                         qf[NR == 1 ? 4 * i + k + 1 : 0][0], qf[NR == 1 ? 4 * i + k + 1 : 0][1]);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+              for (int x = 0; x < XB; ++x) {
+                uint32_t a[4];
+                codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x])[k + kk], a[0], a[2]);
+                codes_f16(reinterpret_cast<const uint32_t*>(&kw[2 * x + 1])[k + kk], a[1], a[3]);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma_f16(sc[n][x], a, kk ? q[n].z : q[n].x, kk ? q[n].w : q[n].y);
+              }
+          }
+        }
+        // Scores in log2 units are x cs (+ the bias); -inf where a row does not see
+        // a key.  With a bias, or where a row does not see all, they are made here.
+        int ek[XB], ev[XB];
+#pragma unroll
+        for (int x = 0; x < XB; ++x) {
+          const uint32_t at_byte = y + x ? sh.y : sh.x;
+          ek[x] = (int)min((y + x ? hd.z : hd.x) >> at_byte & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+          ev[x] = (int)min((y + x ? hd.w : hd.y) >> at_byte & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+        }
+        if (XB == 2) {                                   // (a block that no row sees has no exponents)
+          if (k0 + 16 <= vlo) ev[0] = ev[XB - 1];
+          if (k0 + 16 >= vhi) ev[XB - 1] = ev[0];
+        }
+        float cs[NR][2][XB];                             // of a row's blocks
+        bool raise = false;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int x = 0; x < XB; ++x) cs[n][j][x] = p.scale_log2 * pow2_cut(ek[x] - qup[n][j]);
+        if (ALIBI || masked) {
 #pragma unroll
           for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t)
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[n][t][i] *= alpha;
-        }
-        // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
-        float lsv[2], back[2];
+              for (int x = 0; x < XB; ++x)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int up = max(ev[x] - eref + 7, -126);
-          const bool on = passes == 1 || pass == x;
-          lsv[x] = on ? (float)up : -1e6f;
-          back[x] = pow2_cut(-up);
-        }
-        uint32_t pf[NR][2][2];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          const float mr[2] = {mref[n][0] == -INFINITY ? 0.f : mref[n][0], mref[n][1] == -INFINITY ? 0.f : mref[n][1]};
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(sc[n][x][i], cs[n][i & 1][x], lsv[x] - mr[i & 1]));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) l[n][j] = fmaf(e[j] + e[2 + j], back[x], l[n][j]);
-            pf[n][x][0] = transposed(pack_f16x2(e[0], e[1]));
-            pf[n][x][1] = transposed(pack_f16x2(e[2], e[3]));
-          }
-        }
-        // O transposed, 16 elements x 8 rows, D / 16 times: row g8 of product t is
-        // element g8 D / 8 + 2 t, row g8 + 8 the next
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t vat = at + C::POOL + x * 16 * D;
-          uint32_t w[4][D / 32];                       // of the block's keys 2 c4, 2 c4 + 1, 8 + 2 c4, 9 + 2 c4
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * (i >> 1) + 2 * c4 + (i & 1);
-            if (D == 128) {
-              const uint4 v = lds128(vat + r * 128 + (g8 ^ (r & 7)) * 16);
-              w[i][0] = v.x;
-              w[i][1] = v.y;
-              w[i][D / 32 - 2] = v.z;
-              w[i][D / 32 - 1] = v.w;
-            } else {
-              const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ (r >> 1 & 3)) * 16 + (g8 & 1) * 8);
-              w[i][0] = v.x;
-              w[i][1] = v.y;
+                for (int h = 0; h < 2; ++h) {
+                  float& v = sc[n][x][2 * h + j];
+                  const int key = k0 + 16 * (y + x) + 8 * h + g8;
+                  const float c = cs[n][j][x];
+                  v = ALIBI ? fmaf(v, c, slope2[n][j] * (float)(key - kend[n][j])) : v * c;
+                  if (masked && (key > kend[n][j] || (p.causal && key < kend[n][j] - p.window))) v = -INFINITY;
+                }
+              cs[n][j][0] = cs[n][j][XB - 1] = 1.f;
             }
+        }
+        float mx[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mx[n][j] = fmaxf(sc[n][0][j], sc[n][0][2 + j]) * cs[n][j][0];
+            if (XB == 2) mx[n][j] = fmaxf(mx[n][j], fmaxf(sc[n][XB - 1][j], sc[n][XB - 1][2 + j]) * cs[n][j][XB - 1]);
+            raise |= mx[n][j] > mref[n][j] + kTau;
           }
-          // a slot that no row sees may hold NaN, and 0 x NaN would reach O
-          if (masked && (k0 < vlo || k0 + 32 > vhi)) {
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = k0 + 16 * x + 8 * (i >> 1) + 2 * c4 + (i & 1);
-              if (key < vlo || key >= vhi)
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t b0[4], b1[4];
-            codes_f16(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
-            codes_f16(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
-            codes_f16(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
-            codes_f16(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t a[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+              float x = mx[n][j];
 #pragma unroll
-              for (int n = 0; n < NR; ++n) mma_f16(o[n][2 * i + j], a, pf[n][x][0], pf[n][x][1]);
+              for (int q = 4; q < 32; q <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, q));
+              const bool up = x > mref[n][j] + kTau;
+              const float alpha = up ? ex2_approx(mref[n][j] - x) : 1.f;
+              if (up) mref[n][j] = x;
+              l[n][j] *= alpha;
+#pragma unroll
+              for (int t = 0; t < D / 16; ++t) {
+                o[n][t][j] *= alpha;
+                o[n][t][2 + j] *= alpha;
+              }
+            }
+        }
+        // O's unit follows the values' exponents, at most 2^80 below the largest so
+        // far (which O's float32 holds).  Two blocks further apart than 2^8 take the
+        // products one after the other (the other's P is 0).
+        const int top = max(ev[0], ev[XB - 1]), bottom = min(ev[0], ev[XB - 1]);
+        const int passes = XB == 2 && top - bottom > 8 ? 2 : 1;
+#pragma unroll 1
+        for (int pass = 0; pass < passes; ++pass) {
+          const int own = pass ? ev[XB - 1] : ev[0], hi = passes == 1 ? top : own, lo = passes == 1 ? bottom : own;
+          if (hi > eref || lo < eref - 8) {
+            etop = max(etop, hi);
+            const int e = max(hi, etop - 80);
+            const float alpha = pow2_cut(eref - e);
+            eref = e;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][t][i] *= alpha;
+          }
+          // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
+          float lsv[XB], back[XB];
+#pragma unroll
+          for (int x = 0; x < XB; ++x) {
+            const int up = max(ev[x] - eref + 7, -126);
+            const bool on = passes == 1 || pass == x;
+            lsv[x] = on ? (float)up : -1e6f;
+            back[x] = pow2_cut(-up);
+          }
+          uint32_t pf[NR][XB][2];
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float mr[2] = {mref[n][0] == -INFINITY ? 0.f : mref[n][0], mref[n][1] == -INFINITY ? 0.f : mref[n][1]};
+#pragma unroll
+            for (int x = 0; x < XB; ++x) {
+              float e[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(sc[n][x][i], cs[n][i & 1][x], lsv[x] - mr[i & 1]));
+#pragma unroll
+              for (int j = 0; j < 2; ++j) l[n][j] = fmaf(e[j] + e[2 + j], back[x], l[n][j]);
+              pf[n][x][0] = transposed(pack_f16x2(e[0], e[1]));
+              pf[n][x][1] = transposed(pack_f16x2(e[2], e[3]));
+            }
+          }
+          // O transposed, 16 elements x 8 rows, D / 16 times: row g8 of product t is
+          // element g8 D / 8 + 2 t, row g8 + 8 the next
+#pragma unroll
+          for (int x = 0; x < XB; ++x) {
+            const uint32_t vat = at + C::POOL + (y + x) * 16 * D;
+            uint32_t w[4][D / 32];                       // of the block's keys 2 c4, 2 c4 + 1, 8 + 2 c4, 9 + 2 c4
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * (i >> 1) + 2 * c4 + (i & 1);
+              if (D == 128) {
+                const uint4 v = lds128(vat + r * 128 + (g8 ^ (r & 7)) * 16);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+                w[i][D / 32 - 2] = v.z;
+                w[i][D / 32 - 1] = v.w;
+              } else {
+                const uint2 v = lds64(vat + r * 64 + ((g8 >> 1) ^ (r >> 1 & 3)) * 16 + (g8 & 1) * 8);
+                w[i][0] = v.x;
+                w[i][1] = v.y;
+              }
+            }
+            // a slot that no row sees may hold NaN, and 0 x NaN would reach O
+            if (masked && (k0 < vlo || k0 + 32 > vhi)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = k0 + 16 * (y + x) + 8 * (i >> 1) + 2 * c4 + (i & 1);
+                if (key < vlo || key >= vhi)
+#pragma unroll
+                  for (int j = 0; j < D / 32; ++j) w[i][j] = 0;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t b0[4], b1[4];
+              codes_f16(__byte_perm(w[0][i], w[1][i], 0x5140), b0[0], b0[1]);
+              codes_f16(__byte_perm(w[0][i], w[1][i], 0x7362), b0[2], b0[3]);
+              codes_f16(__byte_perm(w[2][i], w[3][i], 0x5140), b1[0], b1[1]);
+              codes_f16(__byte_perm(w[2][i], w[3][i], 0x7362), b1[2], b1[3]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma_f16(o[n][2 * i + j], a, pf[n][x][0], pf[n][x][1]);
+              }
             }
           }
         }
       }
       __syncwarp();
-      if (any) fetch();
+      if (lane == 0) mbar_arrive(&empty[place]);
+      place += W;
+      if (place >= NS) {
+        place -= NS;
+        lap ^= 1;
+      }
+    }
+    // the next item's first step and place
+    turn -= steps % W;
+    if (turn < 0) turn += W;
+    from += steps;
+    while (from >= NS) {
+      from -= NS;
+      par ^= 1;
     }
     if (next) store_q(cur + 1);
     // ------------------------------------------------- join the warps' parts
@@ -625,7 +640,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
         if (g8 == 0) mls[warp * C::ROWS + 8 * n + 2 * c4 + j] = make_float2(mref[n][j], x);
       }
-    __syncthreads();
+    meet();
     if (threadIdx.x < rows) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + threadIdx.x].x);
@@ -666,10 +681,10 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                                                                    o[n][4 * c + 2 * q + 1][j], o[n][4 * c + 2 * q + 1][2 + j]);
           }
         }
-      __syncthreads();
+      meet();
       const bool lost = s.lost != 0;
       if (lost && part && threadIdx.x == 0) bars->part_lost[part - 1] = 1;
-      for (int i = threadIdx.x; i < rows * 16 && !lost; i += C::NT) {
+      for (int i = threadIdx.x; i < rows * 16 && !lost; i += 32 * W) {
         const int r = i >> 4, x = (i & 15) * 4;        // four columns of row r
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < W; ++w) {
@@ -702,23 +717,12 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             p.lse[(long long)hq * p.T + s.tok + tok] = ml.y == 0.f ? -INFINITY : (ml.x + lg2_approx(ml.y)) * kLn2;
         }
       }
-      __syncthreads();
+      meet();
     }
+    if (lane == 0) mbar_arrive(&bars->seg_empty[cur % kSegs]);
+    go = next && known(cur + 1);
   }
-  // Copies in flight must land before this CTA's shared memory goes away.
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll 1
-  for (; fly > 0; --fly) {
-    wait_warp_drain(&full[from], par);
-    if (++from == C::RD) {
-      from = 0;
-      par ^= 1;
-    }
-  }
-  if (threadIdx.x == 0) {
-    p.part_meta[2 * blockIdx.x] = bars->part_lost[0] ? make_int4(0, 0, 0, 0) : make_int4(finder.cont, 0, 0, 0);
-    p.part_meta[2 * blockIdx.x + 1] = bars->part_lost[1] ? make_int4(0, 0, 0, 0) : finder.begun;
-  }
+  __syncthreads();
 }
 
 template <int D, int NR>
