@@ -5,9 +5,11 @@
 //     S = scale Q K^T (+ ALiBi),   O = softmax(S) V,   k = 2^ek ck,  v = 2^ev cv
 // with codes c and one pair of exponents for every 16 slots of a kv head.
 //
-// One warp brings the codes: TMA into a ring of steps of 32 keys (two such
-// blocks), cp.async for their exponents, ahead and on into the next items.  The
-// others take the steps in turn, each by itself (its own m, l and O), and meet
+// Two warps bring the codes, one the keys' and one the values': TMA into a ring of
+// tiles of 128 keys and cp.async for their exponents, ahead and on into the next
+// items.  (One warp is not enough: a TMA takes it about 140 cycles, and a tile in
+// pages of 32 slots 8 of them, where HBM takes 1400 for the tile.)  The others
+// take steps of 32 keys in turn, each by itself (its own m, l and O), and meet
 // when an item ends.
 // Codes become fp16 (exact) in registers: two instructions for four of them.
 // (mma.sync with e4m3 operands is no way around that: it is taken apart into the
@@ -37,35 +39,38 @@ template <int D, int NR>
 struct Few {
   static constexpr int ROWS = 8 * NR;
   // Warps that take steps: as many as the registers of O (D NR / 4 of a lane)
-  // leave room for beside the one that brings the codes.
-  static constexpr int W = NR * D <= 128 ? 15 : NR * D <= 256 ? 11 : 7;
-  static constexpr int NT = 32 * (W + 1);
+  // leave room for beside the two that bring the codes.
+  static constexpr int W = NR * D <= 128 ? 14 : NR * D <= 256 ? 10 : 6;
+  static constexpr int NT = 32 * (W + 2);
   // Blocks of a step that are taken together.
   static constexpr int XB = NR <= 2 ? 2 : 1;
-  static constexpr int POOL = 32 * D;                       // codes of a step in one pool
-  static constexpr int STEP_BYTES = 2 * POOL;
+  static constexpr int POOL = 128 * D;                      // codes of a tile in one pool
+  static constexpr int TILE_BYTES = 2 * POOL;
   static constexpr int RED_STRIDE = 68;                     // floats per row of 64 columns
   // Q of an item and of the next, as fragments, and the rows' exponents
   static constexpr int Q_FRAGS = NR * (D / 16) * 256;
   static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
-  // Steps of the ring: what the rest leaves of shared memory, at most 160 KB (what
+  // Tiles of the ring: what the rest leaves of shared memory, at most 160 KB (what
   // HBM's latency asks for is about 60).
   static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 8 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
-  static constexpr int FIT = (227 * 1024 - REST) / (STEP_BYTES + 48);
-  static constexpr int NS = FIT < 163840 / STEP_BYTES ? FIT : 163840 / STEP_BYTES;
+  static constexpr int FIT = (227 * 1024 - REST) / (TILE_BYTES + 128 + 16);
+  static constexpr int NS = FIT < 163840 / TILE_BYTES ? FIT : 163840 / TILE_BYTES;
   static constexpr int RING_OFF = 0;
-  static constexpr int HEAD_OFF = RING_OFF + NS * STEP_BYTES;        // exponents of the ring's steps
-  static constexpr int RED_OFF = HEAD_OFF + NS * 32;
+  static constexpr int HEAD_OFF = RING_OFF + NS * TILE_BYTES;        // exponents of the tiles' blocks
+  static constexpr int RED_OFF = HEAD_OFF + NS * 128;
   static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
   static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
   static constexpr int Q_OFF = STAT_OFF + ROWS * 8;
   static constexpr int SEG_OFF = Q_OFF + 2 * Q_BYTES;
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;
-  static constexpr int RINGBAR_OFF = PAR_OFF + 256;         // full and empty of the ring's steps
+  static constexpr int RINGBAR_OFF = PAR_OFF + 256;         // full and empty of the ring's tiles
   static constexpr int BAR_OFF = RINGBAR_OFF + NS * 16;
   static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(kPagedMaxBatch * 8 <= NS * STEP_BYTES, "plan");
+  // Each tile's steps belong to different warps, and a warp's next step lies at
+  // most NS - 1 tiles on.
+  static_assert(W >= 4 && (W + 3) / 4 <= NS - 1, "ring");
+  static_assert(kPagedMaxBatch * 8 <= NS * TILE_BYTES && NS >= 3, "plan");
   static_assert(Q_OFF % 16 == 0 && Q_BYTES % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
 };
 
@@ -107,6 +112,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // Completes one of the arrivals that `bar` waits for when this thread's copies
 // so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
@@ -129,13 +138,13 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::RINGBAR_OFF);
   uint64_t* const empty = full + NS;
   if (threadIdx.x < NS) {
-    mbar_init(&full[threadIdx.x], 5);                  // the codes, four exponents
-    mbar_init(&empty[threadIdx.x], 1);
+    mbar_init(&full[threadIdx.x], 2 * (1 + 8));        // of each pool the codes and eight exponents
+    mbar_init(&empty[threadIdx.x], 4);                 // the tile's steps
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      mbar_init(&bars->seg_empty[i], W);
+      mbar_init(&bars->seg_empty[i], W + 1);           // these and the warp of the values
     }
     bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
     tma_prefetch_desc(&tmK);
@@ -154,15 +163,16 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   auto first_step = [](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 4, s.k.vlo >> 5); };
   auto end_step = [](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 4, (s.k.vhi + 31) >> 5); };
 
-  if (warp == W) {
-    // ------------------------------------------------------------ producer
-    // Finds the run's items, one ahead of the steps it fetches, and fetches four
-    // steps at a time: lane 4 i + j brings exponent j of step i (of its two blocks'
-    // keys and values), lane 4 i its codes.
+  if (warp >= W) {
+    // ----------------------------------------------------------- producers
+    // Warp W brings the keys' codes and finds the run's items, one ahead of the
+    // tiles it fetches; warp W + 1 brings the values'.  A tile is 128 / page_size
+    // boxes, one lane each (one of them for larger pages), and lane i brings the
+    // exponents of block i.
+    const bool values = warp > W;
     Walk w;
     Seg s;
     s.lost = 0;
-    walk_begin<true>(p, bars, w);
     // what the parts of this CTA are, for the merge: kind of the part that goes on
     // from the CTA before (2: the item's last), and the item begun here
     int cont = 0;
@@ -185,87 +195,91 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       return true;
     };
     const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
-    const bool small = p.page_shift == 4;              // a step lies in two pages
-    const int step_of = lane >> 2 & 3, half = lane >> 1 & 1;
-    const uint8_t* const scales = lane & 1 ? p.v_scales : p.k_scales;
+    const uint8_t* const scales = values ? p.v_scales : p.k_scales;
+    const CUtensorMap* const tm = values ? &tmV : &tmK;
+    const int box_rows = min(p.page_size, 128), boxes = 128 / box_rows;
     constexpr int kNoPage = -0x7fffffff - 1;           // no row sees these keys
-    int place = 0;                                     // of the next step in the ring
-    unsigned par = 1;                                  // parity of its last emptying (the first: none to wait for)
-    ok = publish(0);
-    for (int n = 0; ok && more; ++n) {
-      const int b1 = end_step(s), head = s.g, vlo = s.k.vlo, vhi = s.k.vhi;
-      int b = first_step(s);
+    int place = 0;                                     // of the next tile in the ring
+    unsigned par = 1;                                  // parity of its last emptying (at first none is waited for)
+    if (!values) {
+      walk_begin<true>(p, bars, w);
+      ok = publish(0);
+    }
+    for (int n = 0; ok; ++n) {
+      if (values) {
+        if (!(ok = wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1))) break;
+        s = segs[n % kSegs];
+        more = s.ie >= 0;
+      }
+      if (!more) break;
+      const int b0 = first_step(s), b1 = end_step(s), head = s.g, vlo = s.k.vlo, vhi = s.k.vhi;
       const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
       int* const lost = &segs[n % kSegs].lost;
-      auto look_up = [&](int b0) {
-        const int key = ((b0 + step_of) << 5) + 16 * half;
-        const bool in = b0 + step_of < b1 && (!small || (key < vhi && key + 16 > vlo));
-        return in ? max(__ldg(table + (min(key, vhi - 1) >> p.page_shift)), -1) : kNoPage;
+      // page of the lane's 16 slots of a tile (lanes 0 .. 7)
+      auto look_up = [&](int tile) {
+        const int key = (tile << 7) + 16 * lane;
+        const bool in = lane < 8 && key < vhi && key + 16 > vlo;
+        return in ? max(__ldg(table + (key >> p.page_shift)), -1) : kNoPage;
       };
-      int page = look_up(b);
-      if (!(ok = publish(n + 1))) break;
-      for (; b < b1; b += 4) {
-        const int next_page = look_up(b + 4);
-        const int steps = min(4, b1 - b);
-        const int mine = place + step_of >= NS ? place + step_of - NS : place + step_of;
-        const unsigned mine_par = place + step_of >= NS ? par ^ 1 : par;
-        // (lanes without a step ask for the first one's place)
-        const bool in = lane < 4 * steps;
-        if (!(ok = wait(&empty[in ? mine : place], in ? mine_par : par))) break;
+      int tile = b0 >> 2;
+      const int end = b0 < b1 ? (b1 + 3) >> 2 : tile;
+      int page = tile < end ? look_up(tile) : kNoPage;
+      if (!values && !(ok = publish(n + 1))) break;
+      for (; tile < end; ++tile) {
+        const int next_page = tile + 1 < end ? look_up(tile + 1) : kNoPage;
+        if (!(ok = wait(&empty[place], par))) break;
         const bool good = (unsigned)page < (unsigned)p.num_pages;
-        const int key = ((b + step_of) << 5) + 16 * half;
+        // a page that is not there is not read, and the item's rows are not written
+        const bool bad = __any_sync(0xffffffffu, !good && page != kNoPage);
+        const int key = (tile << 7) + 16 * lane;
         const uint32_t row = good ? (uint32_t)page * p.page_size + (key & (p.page_size - 1)) : 0;
-        const int other = __shfl_xor_sync(0xffffffffu, page, 2);
-        const uint32_t row1 = __shfl_xor_sync(0xffffffffu, row, 2);
-        if (in) {
-          const uint32_t hd = smem_u32(smem + C::HEAD_OFF) + mine * 32;
+        if (lane < 8) {
+          const uint32_t hd = smem_u32(smem + C::HEAD_OFF) + place * 128 + lane * 16;
           const long long j = good ? (long long)(row >> 4) * p.Hkv + head : 0;
-          copy_async4(hd + 4 * (lane & 3), scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
-          if (!(lane & 1)) sts32(hd + 16 + 4 * half, (uint32_t)(j & 3) * 8);
+          copy_async4(hd + 4 * values, scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
+          if (!values) sts32(hd + 8, (uint32_t)(j & 3) * 8);
         }
-        __syncwarp();
-        if (in && (lane & 3) == 0) {
-          const bool good1 = (unsigned)other < (unsigned)p.num_pages;
-          uint8_t* at = smem + C::RING_OFF + mine * C::STEP_BYTES;
-          // a page that is not there is not read, and if a row sees its keys, the
-          // item's rows are not written
-          if ((!good && page != kNoPage) || (!good1 && other != kNoPage)) {
+        // the box of lane i begins at block i box_rows / 16, whose lane knows its
+        // page if a row sees those keys; else the lane of one that it sees
+        const int blocks = box_rows >> 4;              // of a box
+        const unsigned there = __ballot_sync(0xffffffffu, good);
+        const unsigned mine = lane < boxes ? there >> (lane * blocks) & ((1u << blocks) - 1) : 0;
+        const int from_lane = mine ? lane * blocks + __ffs(mine) - 1 : 0;
+        const uint32_t row_of = __shfl_sync(0xffffffffu, row, from_lane);
+        const int fetched = __popc(__ballot_sync(0xffffffffu, mine != 0));
+        __syncwarp();                                  // lane 0 publishes what the others wrote
+        if (lane == 0) {
+          if (bad) {
             record_status(p.status, FA_ERR_PAGE);
             *lost = 1;
           }
-          // a step's 32 slots at once, or those of each of its two pages
-          const bool first = good, second = small && good1;
-          mbar_arrive_expect_tx(&full[mine], small ? (first + second) * (C::STEP_BYTES / 2) : first ? C::STEP_BYTES : 0);
-          if (first) {
-            tma_load_3d(at, &tmK, 0, head, (int)row, &full[mine]);
-            tma_load_3d(at + C::POOL, &tmV, 0, head, (int)row, &full[mine]);
-          }
-          if (second) {
-            tma_load_3d(at + C::POOL / 2, &tmK, 0, head, (int)row1, &full[mine]);
-            tma_load_3d(at + C::POOL + C::POOL / 2, &tmV, 0, head, (int)row1, &full[mine]);
-          }
+          mbar_arrive_expect_tx(&full[place], fetched * box_rows * D);
         }
-        if (in) copies_arrive(&full[mine]);
         __syncwarp();
-        place += steps;
-        if (place >= NS) {
-          place -= NS;
+        if (mine)
+          tma_load_3d(smem + C::RING_OFF + place * C::TILE_BYTES + (values ? C::POOL : 0) + lane * box_rows * D, tm, 0, head,
+                      (int)row_of & ~(box_rows - 1), &full[place]);
+        if (lane < 8) copies_arrive(&full[place]);
+        __syncwarp();
+        if (++place == NS) {
+          place = 0;
           par ^= 1;
         }
         page = next_page;
+      }
+      if (values) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
       }
     }
     // Copies in flight must land before this CTA's shared memory goes away: of
     // every place that was filled (its parity: the emptying it waited for, turned).
     asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int i = 0; i < NS; ++i) {
-      const unsigned last = (i < place ? par : par ^ 1) ^ 1;      // parity of the place's last fill
-      wait_warp_drain(&full[i], last);
-    }
+    for (int i = 0; i < NS; ++i) wait_warp_drain(&full[i], (i < place ? par : par ^ 1) ^ 1);
     __syncthreads();
     // A wait ran out, so parts may be missing: the merge must not take what the
     // workspace held.  Nor a part of an item that met a page outside the pool.
-    if (lane < 2)
+    if (!values && lane < 2)
       p.part_meta[2 * blockIdx.x + lane] = bars->abort_flag || bars->part_lost[lane] ? make_int4(0, 0, 0, 0)
                                            : lane ? begun : make_int4(cont, 0, 0, 0);
     return;
@@ -341,7 +355,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   float2* stat = reinterpret_cast<float2*>(smem + C::STAT_OFF);
   bool dead = false;                                   // a wait for a step ran out
   int turn = warp;                                     // this warp's first step of the item
-  int from = 0;                                        // place of the item's first step in the ring
+  int from = 0;                                        // place of the item's first tile in the ring
   unsigned par = 0;                                    // parity of its filling
 
 #pragma unroll 1
@@ -392,25 +406,25 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     }
     int eref = -1000, etop = -1000;                    // O's unit, the largest it had
     // ------------------------------------------------------------- steps
-    const int b0 = first_step(s), steps = max(end_step(s) - b0, 0), vlo = s.k.vlo, vhi = s.k.vhi;
-    int place = from + turn, lap = par;
-    while (place >= NS) {
-      place -= NS;
-      lap ^= 1;
-    }
-    int step = turn;
+    const int b0 = first_step(s), b1 = max(end_step(s), b0), vlo = s.k.vlo, vhi = s.k.vhi;
+    const int tile0 = b0 >> 2;
 #pragma unroll 1
-    for (; step < steps; step += W) {
-      const int b = b0 + step;
-      if (dead || !wait(&full[place], lap)) {
+    for (int b = b0 + turn; b < b1; b += W) {
+      const int nth = from + (b >> 2) - tile0, place = nth % NS;
+      const unsigned lap = par ^ (nth / NS & 1);
+      // A wait for one parity of a barrier says that the last phase of that parity
+      // is over, so it must not be asked two phases ahead.  This warp's tile is at
+      // most NS - 1 behind one that it saw full (or behind the last item's, which
+      // all saw), so that the fill before the last of this place is used up: then
+      // first the last one's being used up, then this one.
+      if (dead || !wait(&empty[place], lap ^ 1) || !wait(&full[place], lap)) {
         // this item's rows and those of all that follow are left alone
         dead = true;
         if (lane == 0) segs[cur % kSegs].lost = 1;
         break;
       }
-      const uint32_t at = smem_u32(smem + C::RING_OFF) + place * C::STEP_BYTES;
-      const uint4 hd = lds128(smem_u32(smem + C::HEAD_OFF) + place * 32);
-      const uint2 sh = lds64(smem_u32(smem + C::HEAD_OFF) + place * 32 + 16);
+      const uint32_t at = smem_u32(smem + C::RING_OFF) + place * C::TILE_BYTES + (b & 3) * 32 * D;
+      const uint32_t heads = smem_u32(smem + C::HEAD_OFF) + place * 128 + (b & 3) * 32;
       const int k0 = b << 5;
       const bool masked = k0 + 31 > diag || k0 < low;
 #pragma unroll 1
@@ -459,9 +473,9 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         int ek[XB], ev[XB];
 #pragma unroll
         for (int x = 0; x < XB; ++x) {
-          const uint32_t at_byte = y + x ? sh.y : sh.x;
-          ek[x] = (int)min((y + x ? hd.z : hd.x) >> at_byte & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
-          ev[x] = (int)min((y + x ? hd.w : hd.y) >> at_byte & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+          const uint4 hd = lds128(heads + (y + x) * 16);
+          ek[x] = (int)min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+          ev[x] = (int)min(hd.y >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
         }
         if (XB == 2) {                                   // (a block that no row sees has no exponents)
           if (k0 + 16 <= vlo) ev[0] = ev[XB - 1];
@@ -614,21 +628,18 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[place]);
-      place += W;
-      if (place >= NS) {
-        place -= NS;
-        lap ^= 1;
+      // (the first step of a tile that has fewer than four arrives for the others)
+      if (lane == 0) {
+        const int lo = max(b & ~3, b0), hi = min((b & ~3) + 4, b1);
+        mbar_arrive_n(&empty[place], b == lo ? 5 - (hi - lo) : 1);
       }
     }
-    // the next item's first step and place
-    turn -= steps % W;
+    // the next item's first step and tile
+    turn -= (b1 - b0) % W;
     if (turn < 0) turn += W;
-    from += steps;
-    while (from >= NS) {
-      from -= NS;
-      par ^= 1;
-    }
+    from += b0 < b1 ? ((b1 + 3) >> 2) - tile0 : 0;
+    par ^= from / NS & 1;
+    from %= NS;
     if (next) store_q(cur + 1);
     // ------------------------------------------------- join the warps' parts
 #pragma unroll
@@ -732,8 +743,8 @@ int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
   if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return e;
   CUtensorMap tk, tv;
   const long long slots = (long long)p.num_pages * p.page_size;
-  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, std::min(p.page_size, 32))) return e;
-  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, std::min(p.page_size, 32))) return e;
+  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, std::min(p.page_size, 128))) return e;
+  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, std::min(p.page_size, 128))) return e;
   kern<<<grid, C::NT, C::SMEM_BYTES, stream>>>(tk, tv, p);
   return (int)cudaGetLastError();
 }
