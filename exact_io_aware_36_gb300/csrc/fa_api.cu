@@ -798,10 +798,10 @@ size_t fa_fwd_paged_workspace_size(int Hq, int Hkv, int N, int d) {
 
 // Over codes, sequences of up to this many rows per kv head go to the kernel for
 // few rows: 32 where no sequence brings more (then it is the call's only one),
-// else what one token of each brings, in 8, 16 or 32; 0 with larger groups.
+// else what one token of each brings, in eights; 0 with larger groups.
 static int paged_few_rows(int group, int N) {
   const long long rows = (long long)N * group <= 32 ? (long long)N * group : group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+  return rows <= 32 ? (int)std::max(1ll, (rows + 7) / 8) * 8 : 0;
 }
 
 static long long paged_few_part_rows(int group, int N) { return (long long)std::min(paged_few_rows(group, N) / group, N) * group; }

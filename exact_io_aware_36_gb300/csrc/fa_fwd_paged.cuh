@@ -110,9 +110,13 @@ constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
+// Of an item of the kernel for few rows: an item more costs a CTA 7000 cycles, a
+// tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands for.
+constexpr int kHeadFew = 44;
 // A CTA's run is at least this long, so that none lies between the beginnings
 // of an item's first two tiles: an item's parts are in CTAs next to each other.
 constexpr int kMinRunTwo = kHeadTwo + kWeightTwo + 2, kMinRunOne = kHeadOne + kWeightOne + 2;
+constexpr int kMinRunFew = kHeadFew + kWeightOne + 2;
 
 template <int D, bool ONE, bool KV8>
 struct Cfg {
@@ -229,16 +233,20 @@ __device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int 
 }
 
 __device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
-__device__ __forceinline__ int head_weight(const Block& k) { return k.two ? kHeadTwo : kHeadOne; }
+template <bool PICK>
+__device__ __forceinline__ int head_weight(const PagedParams& p, const Block& k) {
+  return k.two ? kHeadTwo : PICK && p.few ? kHeadFew : kHeadOne;
+}
 
 // Weight of the block of query tokens from tok0 on (0 behind the last).  Not
 // inlined: a short call runs through code that no SM has cached yet, so each
 // copy of this would cost more than the calls.
+template <bool PICK>
 static __device__ __noinline__ int block_weight(const PagedParams& p, int n, int L, int tok0) {
   if (tok0 >= n) return 0;
   Block k;
   block_geometry(p, n, L, tok0, k);
-  return head_weight(k) + k.kt * tile_weight(k);
+  return head_weight<PICK>(p, k) + k.kt * tile_weight(k);
 }
 
 // A part of an item, as the walker passes it on: steps [ib, ie) of the item's
@@ -287,7 +295,7 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
     block_geometry(p, w.n, w.L, tok0, s.k);
     // On the line an item is its head and then its tiles; the first tile
     // begins with the head.  A CTA has the tiles that begin in its run.
-    const int wt = tile_weight(s.k), head = head_weight(s.k);
+    const int wt = tile_weight(s.k), head = head_weight<PICK>(p, s.k);
     const long long len = head + (long long)s.k.kt * wt;
     s.ib = w.base >= w.w0 ? 0 : max(1, ((int)(w.w0 - w.base) - head + wt - 1) / wt);
     s.ie = w.w1 - w.base >= len ? s.k.kt : min(s.k.kt, max(1, ((int)(w.w1 - w.base) - head + wt - 1) / wt));
@@ -317,7 +325,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     if (b < p.B) {
       int c0, n, L;
       if (!load_seq<PICK>(p, b, &c0, &n, &L) && blockIdx.x == 0 && sub == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
-      for (int tok0 = sub * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) wsum += block_weight(p, n, L, tok0);
+      for (int tok0 = sub * 2 * p.tpt; tok0 < n; tok0 += nl * 2 * p.tpt) wsum += block_weight<PICK>(p, n, L, tok0);
     }
     for (int o = nl / 2; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
     if (b < p.B && sub == 0) pre[b] = (unsigned long long)wsum;      // of one kv head
@@ -384,7 +392,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Bars* bars, unsi
     long long base = bars->base + g * sw;
     int qb = 0;
     for (int q0 = 0;; q0 += 32) {
-      const int x = block_weight(p, n, L, (q0 + lane) * 2 * p.tpt);
+      const int x = block_weight<PICK>(p, n, L, (q0 + lane) * 2 * p.tpt);
       long long run = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

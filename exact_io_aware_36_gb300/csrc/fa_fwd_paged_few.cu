@@ -7,9 +7,9 @@
 //
 // Two warps bring the codes, one the keys' and one the values': TMA into a ring of
 // tiles of 128 keys and cp.async for their exponents, ahead and on into the next
-// items.  (One warp is not enough: a TMA takes it about 140 cycles, and a tile in
-// pages of 32 slots 8 of them, where HBM takes 1400 for the tile.)  The others
-// take steps of 32 keys in turn, each by itself (its own m, l and O), and meet
+// items.  (One warp is not enough: a TMA takes it about 140 cycles, a tile in
+// pages of 32 slots takes 8 of them, and HBM 1400 for the tile.)  The others take
+// steps of 32 keys in turn, each by itself (its own m, l and O), and meet
 // when an item ends.
 // Codes become fp16 (exact) in registers: two instructions for four of them.
 // (mma.sync with e4m3 operands is no way around that: it is taken apart into the
@@ -40,7 +40,7 @@ struct Few {
   static constexpr int ROWS = 8 * NR;
   // Warps that take steps: as many as the registers of O (D NR / 4 of a lane)
   // leave room for beside the two that bring the codes.
-  static constexpr int W = NR * D <= 128 ? 14 : NR * D <= 256 ? 10 : 6;
+  static constexpr int W = (NR * D <= 128 ? 16 : NR * D <= 384 ? 12 : 8) - 2;
   static constexpr int NT = 32 * (W + 2);
   // Blocks of a step that are taken together.
   static constexpr int XB = NR <= 2 ? 2 : 1;
@@ -50,11 +50,11 @@ struct Few {
   // Q of an item and of the next, as fragments, and the rows' exponents
   static constexpr int Q_FRAGS = NR * (D / 16) * 256;
   static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
-  // Tiles of the ring: what the rest leaves of shared memory, at most 160 KB (what
+  // Tiles of the ring: what the rest leaves of shared memory, at most 192 KB (what
   // HBM's latency asks for is about 60).
   static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 8 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
   static constexpr int FIT = (227 * 1024 - REST) / (TILE_BYTES + 128 + 16);
-  static constexpr int NS = FIT < 163840 / TILE_BYTES ? FIT : 163840 / TILE_BYTES;
+  static constexpr int NS = FIT < 196608 / TILE_BYTES ? FIT : 196608 / TILE_BYTES;
   static constexpr int RING_OFF = 0;
   static constexpr int HEAD_OFF = RING_OFF + NS * TILE_BYTES;        // exponents of the tiles' blocks
   static constexpr int RED_OFF = HEAD_OFF + NS * 128;
@@ -144,7 +144,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      mbar_init(&bars->seg_empty[i], W + 1);           // these and the warp of the values
+      mbar_init(&bars->seg_empty[i], W + 1);           // all but the warp that finds them
     }
     bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
     tma_prefetch_desc(&tmK);
@@ -152,7 +152,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   fence_mbarrier_init();
   __syncthreads();
-  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kMinRunOne);
+  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kMinRunFew);
   fence_proxy_async_smem();                            // (the plan's sums lay where TMA will write)
   __syncthreads();
   grid_launch_dependents();
@@ -166,10 +166,13 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   if (warp >= W) {
     // ----------------------------------------------------------- producers
     // Warp W brings the keys' codes and finds the run's items, one ahead of the
-    // tiles it fetches; warp W + 1 brings the values'.  A tile is 128 / page_size
-    // boxes, one lane each (one of them for larger pages), and lane i brings the
+    // tiles it fetches; warp W + 1 brings the values'.  Two tiles at a time, as most
+    // of what a tile costs them does not depend on how many there are (1200 cycles
+    // one by one, of 1400 that HBM takes).  A tile is 128 / page_size boxes, one lane
+    // each (one of them for larger pages), and lane i of its eight brings the
     // exponents of block i.
     const bool values = warp > W;
+    const int second = lane >> 3 & 1, blk = lane & 7;  // (lanes 16 .. 31: as 0 .. 15, but without a copy)
     Walk w;
     Seg s;
     s.lost = 0;
@@ -215,54 +218,60 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const int b0 = first_step(s), b1 = end_step(s), head = s.g, vlo = s.k.vlo, vhi = s.k.vhi;
       const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
       int* const lost = &segs[n % kSegs].lost;
-      // page of the lane's 16 slots of a tile (lanes 0 .. 7)
+      // page of the lane's 16 slots of its tile
       auto look_up = [&](int tile) {
-        const int key = (tile << 7) + 16 * lane;
-        const bool in = lane < 8 && key < vhi && key + 16 > vlo;
-        return in ? max(__ldg(table + (key >> p.page_shift)), -1) : kNoPage;
+        const int key = ((tile + second) << 7) + 16 * blk;
+        return key < vhi && key + 16 > vlo ? max(__ldg(table + (key >> p.page_shift)), -1) : kNoPage;
       };
       int tile = b0 >> 2;
       const int end = b0 < b1 ? (b1 + 3) >> 2 : tile;
       int page = tile < end ? look_up(tile) : kNoPage;
       if (!values && !(ok = publish(n + 1))) break;
-      for (; tile < end; ++tile) {
-        const int next_page = tile + 1 < end ? look_up(tile + 1) : kNoPage;
-        if (!(ok = wait(&empty[place], par))) break;
+      for (; tile < end; tile += 2) {
+        const int next_page = tile + 2 < end ? look_up(tile + 2) : kNoPage;
+        // this lane's tile and its place; the second may be missing
+        const bool there = tile + second < end;
+        int at_place = place + second;
+        const bool over = at_place >= NS;
+        if (over) at_place -= NS;
+        if (!(ok = wait(&empty[there ? at_place : place], there && over ? par ^ 1 : par))) break;
+        if (!there) page = kNoPage;
         const bool good = (unsigned)page < (unsigned)p.num_pages;
         // a page that is not there is not read, and the item's rows are not written
         const bool bad = __any_sync(0xffffffffu, !good && page != kNoPage);
-        const int key = (tile << 7) + 16 * lane;
+        const int key = ((tile + second) << 7) + 16 * blk;
         const uint32_t row = good ? (uint32_t)page * p.page_size + (key & (p.page_size - 1)) : 0;
-        if (lane < 8) {
-          const uint32_t hd = smem_u32(smem + C::HEAD_OFF) + place * 128 + lane * 16;
+        const bool copies = lane < 16 && there;
+        if (copies) {
+          const uint32_t hd = smem_u32(smem + C::HEAD_OFF) + at_place * 128 + blk * 16;
           const long long j = good ? (long long)(row >> 4) * p.Hkv + head : 0;
           copy_async4(hd + 4 * values, scales + (j & ~3ll), good ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
           if (!values) sts32(hd + 8, (uint32_t)(j & 3) * 8);
         }
-        // the box of lane i begins at block i box_rows / 16, whose lane knows its
-        // page if a row sees those keys; else the lane of one that it sees
+        // The box of the tile's lane i begins at block i box_rows / 16.  Its page is
+        // known to the lane of any of its blocks that a row sees.
         const int blocks = box_rows >> 4;              // of a box
-        const unsigned there = __ballot_sync(0xffffffffu, good);
-        const unsigned mine = lane < boxes ? there >> (lane * blocks) & ((1u << blocks) - 1) : 0;
-        const int from_lane = mine ? lane * blocks + __ffs(mine) - 1 : 0;
-        const uint32_t row_of = __shfl_sync(0xffffffffu, row, from_lane);
-        const int fetched = __popc(__ballot_sync(0xffffffffu, mine != 0));
-        __syncwarp();                                  // lane 0 publishes what the others wrote
-        if (lane == 0) {
+        const unsigned seen = __ballot_sync(0xffffffffu, good) >> (8 * second) & 0xffu;
+        const unsigned mine = blk < boxes ? seen >> (blk * blocks) & ((1u << blocks) - 1) : 0;
+        const uint32_t row_of = __shfl_sync(0xffffffffu, row, 8 * second + (mine ? blk * blocks + __ffs(mine) - 1 : 0));
+        const int fetched = __popc(__ballot_sync(0xffffffffu, mine != 0) >> (8 * second) & 0xffu);
+        __syncwarp();                                  // lanes 0 and 8 publish what the others wrote
+        if (copies && blk == 0) {
           if (bad) {
             record_status(p.status, FA_ERR_PAGE);
             *lost = 1;
           }
-          mbar_arrive_expect_tx(&full[place], fetched * box_rows * D);
+          mbar_arrive_expect_tx(&full[at_place], fetched * box_rows * D);
         }
         __syncwarp();
-        if (mine)
-          tma_load_3d(smem + C::RING_OFF + place * C::TILE_BYTES + (values ? C::POOL : 0) + lane * box_rows * D, tm, 0, head,
-                      (int)row_of & ~(box_rows - 1), &full[place]);
-        if (lane < 8) copies_arrive(&full[place]);
+        if (copies && mine)
+          tma_load_3d(smem + C::RING_OFF + at_place * C::TILE_BYTES + (values ? C::POOL : 0) + blk * box_rows * D, tm, 0, head,
+                      (int)row_of & ~(box_rows - 1), &full[at_place]);
+        if (copies) copies_arrive(&full[at_place]);
         __syncwarp();
-        if (++place == NS) {
-          place = 0;
+        place += min(2, end - tile);
+        if (place >= NS) {
+          place -= NS;
           par ^= 1;
         }
         page = next_page;
@@ -415,8 +424,9 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       // A wait for one parity of a barrier says that the last phase of that parity
       // is over, so it must not be asked two phases ahead.  This warp's tile is at
       // most NS - 1 behind one that it saw full (or behind the last item's, which
-      // all saw), so that the fill before the last of this place is used up: then
-      // first the last one's being used up, then this one.
+      // all saw), and tiles are filled in order: when that one was, the fill of this
+      // place before the last had been used up.  So first the wait for the last
+      // one's being used up, then that for this fill.
       if (dead || !wait(&empty[place], lap ^ 1) || !wait(&full[place], lap)) {
         // this item's rows and those of all that follow are left alone
         dead = true;
@@ -755,6 +765,7 @@ int launch_fwd_paged_few(const PagedParams& p, int grid, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, stream) : launch_few<64, 1>(p, grid, stream);
   if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, stream) : launch_few<64, 2>(p, grid, stream);
+  if (p.few_rows <= 24) return p.d == 128 ? launch_few<128, 3>(p, grid, stream) : launch_few<64, 3>(p, grid, stream);
   return p.d == 128 ? launch_few<128, 4>(p, grid, stream) : launch_few<64, 4>(p, grid, stream);
 }
 

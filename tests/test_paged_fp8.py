@@ -414,7 +414,7 @@ def parts(new, Hq, Hkv):
     G = Hq // Hkv
     tpt = 128 // G
     most = max(new) * G if max(new) * G <= 32 else G
-    few = next((r for r in (8, 16, 32) if most <= r), 0)
+    few = next((r for r in (8, 16, 24, 32) if most <= r), 0)
     out = []
     for n in new:
         if n * G <= few:
