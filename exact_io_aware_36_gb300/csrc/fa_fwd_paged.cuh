@@ -110,13 +110,16 @@ constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
-// Of an item of the kernel for few rows: an item more costs a CTA 7000 cycles, a
-// tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands for.
+// Of an item of the kernel for few rows (p.head_few): an item more costs a CTA
+// 7000 cycles, a tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands
+// for.  Counted in full where there are about as many items as SMs or more (16
+// caches of 8 heads: 132 us with 16, 125 with 44); of fewer the runs, which must be
+// longer than a head, would leave SMs idle (16 items of 7 tiles: 15.9 us with 44,
+// 13.7 with 16).
 constexpr int kHeadFew = 44;
 // A CTA's run is at least this long, so that none lies between the beginnings
 // of an item's first two tiles: an item's parts are in CTAs next to each other.
 constexpr int kMinRunTwo = kHeadTwo + kWeightTwo + 2, kMinRunOne = kHeadOne + kWeightOne + 2;
-constexpr int kMinRunFew = kHeadFew + kWeightOne + 2;
 
 template <int D, bool ONE, bool KV8>
 struct Cfg {
@@ -235,7 +238,7 @@ __device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int 
 __device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
 template <bool PICK>
 __device__ __forceinline__ int head_weight(const PagedParams& p, const Block& k) {
-  return k.two ? kHeadTwo : PICK && p.few ? kHeadFew : kHeadOne;
+  return k.two ? kHeadTwo : PICK && p.few ? p.head_few : kHeadOne;
 }
 
 // Weight of the block of query tokens from tok0 on (0 behind the last).  Not

@@ -40,19 +40,21 @@ struct Few {
   static constexpr int ROWS = 8 * NR;
   // Warps that take steps: as many as the registers of O (D NR / 4 of a lane)
   // leave room for beside the two that bring the codes.
-  static constexpr int W = (NR * D <= 128 ? 16 : NR * D <= 384 ? 12 : 8) - 2;
+  static constexpr int W = (NR * D <= 128 ? 16 : NR * D <= 256 ? 12 : 8) - 2;
   static constexpr int NT = 32 * (W + 2);
-  // Blocks of a step that are taken together.
-  static constexpr int XB = NR <= 2 ? 2 : 1;
+  // Blocks of a step that are taken together: both, unless that spills (32 rows).
+  // 24 rows, d = 128 (five tokens of 32 sequences, 32 heads on 8): 123 us, with one
+  // 131; with 10 warps of 168 registers, which spill, 153.
+  static constexpr int XB = NR <= 3 ? 2 : 1;
   static constexpr int POOL = 128 * D;                      // codes of a tile in one pool
   static constexpr int TILE_BYTES = 2 * POOL;
   static constexpr int RED_STRIDE = 68;                     // floats per row of 64 columns
-  // Q of an item and of the next, as fragments, and the rows' exponents
+  // Q of an item and of the next, as fragments, the rows' exponents, their slopes
   static constexpr int Q_FRAGS = NR * (D / 16) * 256;
-  static constexpr int Q_BYTES = Q_FRAGS + ROWS * 4;
+  static constexpr int Q_BYTES = Q_FRAGS + ROWS * 8;
   // Tiles of the ring: what the rest leaves of shared memory, at most 192 KB (what
   // HBM's latency asks for is about 60).
-  static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 8 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
+  static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 12 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
   static constexpr int FIT = (227 * 1024 - REST) / (TILE_BYTES + 128 + 16);
   static constexpr int NS = FIT < 196608 / TILE_BYTES ? FIT : 196608 / TILE_BYTES;
   static constexpr int RING_OFF = 0;
@@ -61,7 +63,8 @@ struct Few {
   static constexpr int ML_OFF = RED_OFF + W * ROWS * RED_STRIDE * 4;
   static constexpr int STAT_OFF = ML_OFF + W * ROWS * 8;
   static constexpr int Q_OFF = STAT_OFF + ROWS * 8;
-  static constexpr int SEG_OFF = Q_OFF + 2 * Q_BYTES;
+  static constexpr int TOK_OFF = Q_OFF + 2 * Q_BYTES;       // each row's token
+  static constexpr int SEG_OFF = TOK_OFF + ROWS * 4;
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;
   static constexpr int RINGBAR_OFF = PAR_OFF + 256;         // full and empty of the ring's tiles
   static constexpr int BAR_OFF = RINGBAR_OFF + NS * 16;
@@ -152,7 +155,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   fence_mbarrier_init();
   __syncthreads();
-  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kMinRunFew);
+  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), p.head_few + kWeightOne + 2);
   fence_proxy_async_smem();                            // (the plan's sums lay where TMA will write)
   __syncthreads();
   grid_launch_dependents();
@@ -295,18 +298,21 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
 
   // -------------------------------------------------------- the other warps
+  if (threadIdx.x < C::ROWS) reinterpret_cast<int*>(smem + C::TOK_OFF)[threadIdx.x] = (int)threadIdx.x / p.group;
   auto meet = [] { named_bar_sync(1, 32 * W); };       // barrier of these warps
   // ---- Q: a warp prepares rows warp, warp + W, .. of the next item, a lane D /
   // 32 elements, while it works on this one
   constexpr int QP = (C::ROWS + W - 1) / W;
   constexpr int QE = D / 32;
   uint32_t xq[QP][QE / 2];
+  float xslope[QP];
   auto load_q = [&](const Seg& s) {
 #pragma unroll
     for (int i = 0; i < QP; ++i) {
       const int r = warp + i * W;
 #pragma unroll
       for (int j = 0; j < QE / 2; ++j) xq[i][j] = 0;
+      xslope[i] = 0.f;
       if (r < s.ntok * p.group) {
         const int tok = r / p.group, hq = s.g * p.group + r - tok * p.group;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
@@ -318,6 +324,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         } else {
           xq[i][0] = __ldg(src);
         }
+        if (ALIBI) xslope[i] = __ldg(p.alibi + hq) * kLog2e;
       }
     }
   };
@@ -342,7 +349,10 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       for (int j = 0; j < QE / 2; ++j)
         frag[D == 128 ? j : lane & 1] =
             pack_f16x2(__uint_as_float(xq[i][j] << 16) * mul, __uint_as_float(xq[i][j] & 0xFFFF0000u) * mul);
-      if (lane == 0) reinterpret_cast<int*>(at + C::Q_FRAGS)[r] = up;
+      if (lane == 0) {
+        reinterpret_cast<int*>(at + C::Q_FRAGS)[r] = up;
+        reinterpret_cast<float*>(at + C::Q_FRAGS)[C::ROWS + r] = xslope[i];
+      }
     }
   };
   // Items n and n + 1 are known; the same answer for every warp.
@@ -388,20 +398,10 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         qf[NR == 1 ? k + 1 : 0][1] = v.w;
       }
     }
-    // a lane's rows are 8 n + 2 c4 and the next
-    float slope2[NR][2];
-    int kend[NR][2], qup[NR][2];
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 8 * n + 2 * c4 + j;
-        const bool valid = r < rows;
-        const int tok = r / p.group;
-        qup[n][j] = reinterpret_cast<const int*>(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES + C::Q_FRAGS)[r];
-        kend[n][j] = !valid ? -1 : p.causal ? f + tok : s.L - 1;
-        slope2[n][j] = ALIBI && valid ? __ldg(p.alibi + s.g * p.group + r - tok * p.group) * kLog2e : 0.f;
-      }
+    // A lane's rows are 8 n + 2 c4 and the next; what is kept of each beside m and l
+    // lies in shared memory.
+    const uint32_t row_at = smem_u32(smem + C::Q_OFF + (cur & 1) * C::Q_BYTES + C::Q_FRAGS) + 8 * c4;
+    const uint32_t tok_at = smem_u32(smem + C::TOK_OFF) + 8 * c4;
     float mref[NR][2], l[NR][2];
     float o[NR][D / 16][4];
 #pragma unroll
@@ -494,28 +494,35 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         float cs[NR][2][XB];                             // of a row's blocks
         bool raise = false;
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NR; ++n) {
+          const uint2 up = lds64(row_at + 32 * n);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int x = 0; x < XB; ++x) cs[n][j][x] = p.scale_log2 * pow2_cut(ek[x] - qup[n][j]);
+            for (int x = 0; x < XB; ++x) cs[n][j][x] = p.scale_log2 * pow2_cut(ek[x] - (int)(j ? up.y : up.x));
+        }
         if (ALIBI || masked) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+          for (int n = 0; n < NR; ++n) {
+            const uint2 slopes = lds64(row_at + 32 * n + 4 * C::ROWS), toks = lds64(tok_at + 32 * n);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+              // the last key that the row sees; a row without a token sees none
+              const int r = 8 * n + 2 * c4 + j;
+              const int kend = r >= rows ? -1 : p.causal ? f + (int)(j ? toks.y : toks.x) : s.L - 1;
+              const float slope2 = __uint_as_float(j ? slopes.y : slopes.x);
 #pragma unroll
               for (int x = 0; x < XB; ++x)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   float& v = sc[n][x][2 * h + j];
                   const int key = k0 + 16 * (y + x) + 8 * h + g8;
-                  const float c = cs[n][j][x];
-                  v = ALIBI ? fmaf(v, c, slope2[n][j] * (float)(key - kend[n][j])) : v * c;
-                  if (masked && (key > kend[n][j] || (p.causal && key < kend[n][j] - p.window))) v = -INFINITY;
+                  v = ALIBI ? fmaf(v, cs[n][j][x], slope2 * (float)(key - kend)) : v * cs[n][j][x];
+                  if (masked && (key > kend || (p.causal && key < kend - p.window))) v = -INFINITY;
                 }
               cs[n][j][0] = cs[n][j][XB - 1] = 1.f;
             }
+          }
         }
         float mx[NR][2];
 #pragma unroll
@@ -761,8 +768,9 @@ int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_fwd_paged_few(const PagedParams& p, int grid, void* stream_) {
+int launch_fwd_paged_few(PagedParams p, int grid, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  p.head_few = (long long)p.B * p.Hkv * 2 >= grid ? kHeadFew : kHeadOne;
   if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, stream) : launch_few<64, 1>(p, grid, stream);
   if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, stream) : launch_few<64, 2>(p, grid, stream);
   if (p.few_rows <= 24) return p.d == 128 ? launch_few<128, 3>(p, grid, stream) : launch_few<64, 3>(p, grid, stream);

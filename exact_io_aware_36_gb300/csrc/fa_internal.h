@@ -221,6 +221,7 @@ struct PagedParams {
   float scale, scale_log2;
   int few_rows, few;           // codes: sequences of up to few_rows rows per kv head
                                // are another kernel's (few: the others are)
+  int head_few;                // that kernel's weight of an item beside its tiles
 };
 
 // CTAs of the paged forward: GB300's SMs; each leaves at most two parts.
@@ -256,7 +257,7 @@ int launch_fwd_paged(const PagedParams& p, void* stream);             // runs + 
 // The same over e4m3 codes: `few` with the sequences of up to few.few_rows rows
 // per kv head, `many` with the others; either may be absent (B = 0).
 int launch_fwd_paged_fp8(const PagedParams& few, const PagedParams& many, void* stream);
-int launch_fwd_paged_few(const PagedParams& p, int grid, void* stream);   // its first part: runs
+int launch_fwd_paged_few(PagedParams p, int grid, void* stream);   // its first part: runs
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__
