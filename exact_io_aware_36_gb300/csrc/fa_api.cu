@@ -806,12 +806,23 @@ static int paged_few_rows(int group, int N) {
 
 static long long paged_few_part_rows(int group, int N) { return (long long)std::min(paged_few_rows(group, N) / group, N) * group; }
 
-size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d) {
-  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || N < 0 || d <= 0) return 0;
+// q as codes: both parts, and the rows' exponents.
+static size_t paged_codes(fa::PagedParams* p, char* ws, long long T, int Hq, int d) {
+  const size_t codes = round256((size_t)2 * T * Hq * d);
+  if (p) {
+    p->q_codes = reinterpret_cast<uint8_t*>(ws);
+    p->q_exps = reinterpret_cast<int*>(ws + codes);
+  }
+  return codes + round256((size_t)T * Hq * sizeof(int));
+}
+
+size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d, long long total_tokens) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || N < 0 || d <= 0 || total_tokens < 0) return 0;
   const int group = Hq / Hkv, few = paged_few_rows(group, N);
   size_t n = 0;
   if (few) n += paged_parts(nullptr, nullptr, paged_few_part_rows(group, N), d);
-  if ((long long)N * group > few) n += paged_parts(nullptr, nullptr, paged_part_rows(group, N), d);
+  if ((long long)N * group > few)
+    n += paged_parts(nullptr, nullptr, paged_part_rows(group, N), d) + paged_codes(nullptr, nullptr, total_tokens, Hq, d);
   return n;
 }
 
@@ -838,7 +849,7 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
   if (!causal && (window >= 0 || alibi_slopes)) return FA_ERR_UNSUPPORTED;
   if (o_dtype != FA_FP32 && o_dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
   const long long T = cu_seqlens ? total_tokens : dense;
-  if (T >= (1ll << 31) || N >= (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (T >= (1ll << (scales ? 30 : 31)) || N >= (1 << 30)) return FA_ERR_UNSUPPORTED;   // (codes: q twice)
   if (T == 0 || B == 0) return FA_OK;        // N = 0 with tokens: the kernel finds whose they are
   if (num_pages == 0) return FA_ERR_SHAPE;
   if (!q || !k_pages || !v_pages || !block_table || !cache_seqlens || !o || !lse) return FA_ERR_NULL;
@@ -847,7 +858,7 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
   if (scales && (!aligned16(scales[0]) || !aligned16(scales[1]))) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(o) & 31u) != 0) return FA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return FA_ERR_ALIGN;
-  const size_t need = scales ? fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) : fa_fwd_paged_workspace_size(Hq, Hkv, N, d);
+  const size_t need = scales ? fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d, T) : fa_fwd_paged_workspace_size(Hq, Hkv, N, d);
   if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_ALIGN;
   fa::PagedParams p = {};
@@ -899,8 +910,12 @@ static fa_status paged_impl(const void* q, const void* k_pages, const void* v_pa
     } else {
       few.B = 0;
     }
-    if ((long long)N * p.group > p.few_rows) paged_parts(&p, ws, paged_part_rows(p.group, N), d);
-    else p.B = 0;
+    if ((long long)N * p.group > p.few_rows) {
+      ws += paged_parts(&p, ws, paged_part_rows(p.group, N), d);
+      paged_codes(&p, ws, T, Hq, d);
+    } else {
+      p.B = 0;
+    }
     return fa::launch_fwd_paged_fp8(few, p, stream) == 0 ? FA_OK : FA_ERR_CUDA;
   }
   return fa::launch_fwd_paged(p, stream) == 0 ? FA_OK : FA_ERR_CUDA;

@@ -96,14 +96,12 @@
 namespace fa {
 namespace {
 
-template <bool KV8>
-constexpr int kThreads = KV8 ? 448 : 384;         // bf16: warp 11 has no role
+constexpr int kThreads = 384;         // bf16 pages: warp 11 has no role
 constexpr int kMmaWarp = 9;
-constexpr int kLoadWarp = 8;           // bf16 alone
-template <bool KV8>
-constexpr int kWalkWarp = KV8 ? 8 : 10;           // codes: also loads Q
+constexpr int kLoadWarp = 8;           // codes: also the walker
+constexpr int kWalkWarp = 10;          // bf16 pages alone
 constexpr int kConvWarp = 10;          // codes alone: the first of kConvWarps
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 2;
 constexpr int kSegs = 4;               // items that the walker may be ahead
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
@@ -121,39 +119,40 @@ constexpr int kHeadFew = 44;
 // of an item's first two tiles: an item's parts are in CTAs next to each other.
 constexpr int kMinRunTwo = kHeadTwo + kWeightTwo + 2, kMinRunOne = kHeadOne + kWeightOne + 2;
 
-template <int D, bool ONE, bool KV8>
+template <int D, bool KV8>
 struct Cfg {
   static constexpr int NB = D / 64;                 // 64-column boxes per row
   static constexpr int BOX_BYTES = 128 * 64 * 2;
   static constexpr int TILE_BYTES = NB * BOX_BYTES;
-  static constexpr int NS = D == 128 ? 2 : 5;       // slots (K of a step, V of the one before)
-  static constexpr int QB = ONE && KV8 ? 1 : 2;     // Q buffers
+  // slots: K of a step, V of the one before
+  static constexpr int NS = D == 128 ? 2 : KV8 ? 4 : 5;
+  static constexpr int K_SLOT = KV8 ? 128 * D : TILE_BYTES;   // codes: K as it is, V in bf16
+  static constexpr int NV = D == 128 ? 3 : 4;       // codes: tiles of V's codes on their way
+  static constexpr int NH = 8;                      // codes: steps whose keys' exponents are kept
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = Q_OFF + QB * TILE_BYTES;
-  static constexpr int V_OFF = K_OFF + NS * TILE_BYTES;
-  static constexpr int ML_OFF = V_OFF + NS * TILE_BYTES;   // (m, l, l~) of both streams' rows
+  static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
+  static constexpr int V_OFF = K_OFF + NS * K_SLOT;
+  static constexpr int STG_OFF = V_OFF + NS * TILE_BYTES;
+  static constexpr int HEAD_OFF = STG_OFF + (KV8 ? NV * 128 * D : 0);     // exponents: of keys, of values
+  static constexpr int ML_OFF = HEAD_OFF + (KV8 ? (NH + NV) * 128 + NV * 16 : 0);   // (m, l, l~) of both streams' rows
   static constexpr int SEG_OFF = ML_OFF + 2 * 128 * 3 * 4;          // ring of items
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;              // a copy of the parameters
   static constexpr int BAR_OFF = PAR_OFF + 256;
-  // Codes on their way, a ring for each warp that turns them into bf16: groups
-  // of 16 slots (one scale) and a header.
-  static constexpr int STG_OFF = BAR_OFF + 512;
-  static constexpr int GROUP_BYTES = 16 * D + 16;
-  static constexpr int RD = D == 128 ? (ONE ? 7 : 3) : (ONE ? 11 : 7);
-  static constexpr int SMEM_BYTES = STG_OFF + (KV8 ? kConvWarps * RD * GROUP_BYTES : 0) + 1024;
+  static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   // the work plan's prefix sums borrow the K/V slots before the first load
-  static_assert(kPagedMaxBatch * 8 <= 2 * NS * TILE_BYTES, "plan");
+  static_assert(kPagedMaxBatch * 8 <= NS * (K_SLOT + TILE_BYTES), "plan");
   static constexpr uint32_t S_COL0 = 0, S_COL1 = 128;
   static constexpr uint32_t O_COL0 = 256, O_COL1 = 256 + D;
 };
 
 struct Bars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t kv_full[5], kv_empty[5];
   uint64_t s_full[2], p_full[2];
   uint64_t o_done, o_free, drain;
   uint64_t joined;              // (m, l, l~) of both streams' rows of a one-tile item are there
+  uint64_t stage_full[4], stage_empty[4];   // codes: V's on their way
 #ifdef FA_PAGED_STOP
   uint64_t never;               // nothing arrives on it
 #endif
@@ -489,12 +488,8 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& c, uint32_t mul, uint
   }
 }
 
-// 16 (4) bytes from global to shared memory, asynchronously; only the first
-// `bytes` are read, zeros for the others.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
+// 4 bytes from global to shared memory, asynchronously; only the first `bytes` are
+// read, zeros for the others.
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -513,13 +508,43 @@ __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" :: "r"(at), "r"(v) : "memory");
 }
 
+// A descriptor as smem_desc_sw128 of rows of 64 bytes, swizzled over them (layout
+// type 4), `sbo_bytes` from one eight of them to the next.
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t sbo_bytes) {
+  return (smem_desc_sw128(saddr, 16, sbo_bytes) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
+// D[tmem] (+)= A[smem] * B[smem], 128 x 128 over 32: e4m3, both K-major, float32.
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
+  constexpr uint32_t idesc = (1u << 4) | (128u >> 3 << 17) | (128u >> 4 << 24);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Completes one of the arrivals that `bar` waits for when this thread's copies
+// so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+
+// 2^e, the exponent cut to what a float holds.
+__device__ __forceinline__ float pow2_cut(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+
+// The exponent that a block's header holds: a word of the scales, the byte's place.
+__device__ __forceinline__ int exponent_of(uint32_t word, uint32_t shift) {
+  return (int)min(word >> shift & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+}
+
 // ONE: no item has two tiles (the host knows from N).  KV8: the pages hold
 // codes.
 template <int D, bool ALIBI, bool ONE, bool KV8>
-__global__ void __launch_bounds__(kThreads<KV8>, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
-  using C = Cfg<D, ONE, KV8>;
+  using C = Cfg<D, KV8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::BAR_OFF);
@@ -539,14 +564,19 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
     }
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&bars->kv_full[s], KV8 ? kConvWarps : 1);
+    for (int s = 0; s < C::NS; ++s) {
+      // codes: K, its blocks' exponents, V in bf16
+      mbar_init(&bars->kv_full[s], KV8 ? 1 + 8 + kConvWarps : 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      // producer (or the warps that bring codes), MMA issuer, 8 softmax warps
+      // producer (or the warps that turn V's codes), MMA issuer, 8 softmax warps
       mbar_init(&bars->seg_empty[i], KV8 ? kConvWarps + 9 : 10);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->stage_full[i], 1 + 8);
+      mbar_init(&bars->stage_empty[i], kConvWarps);
     }
     mbar_init(&bars->o_done, 1);
     mbar_init(&bars->o_free, 8);
@@ -564,17 +594,24 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
   // Q rows past the box (128 % group of them) are zero for good.
   const int rows_box = p.tpt * p.group;
-  for (int i = threadIdx.x; i < C::QB * C::NB * (128 - rows_box) * 8; i += kThreads<KV8>) {
-    const int box = i / ((128 - rows_box) * 8), j = i % ((128 - rows_box) * 8);
-    reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
+  if (!KV8) {
+    for (int i = threadIdx.x; i < 2 * C::NB * (128 - rows_box) * 8; i += kThreads) {
+      const int box = i / ((128 - rows_box) * 8), j = i % ((128 - rows_box) * 8);
+      reinterpret_cast<uint4*>(smem + C::Q_OFF + box * C::BOX_BYTES + rows_box * 128)[j] = make_uint4(0, 0, 0, 0);
+    }
+  } else {                             // both parts of both tiles
+    const int per = (128 - rows_box) * (D / 16);
+    for (int i = threadIdx.x; i < 4 * per; i += kThreads)
+      reinterpret_cast<uint4*>(smem + C::Q_OFF + i / per * (C::TILE_BYTES / 2) + rows_box * D)[i % per] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-  make_plan<kThreads<KV8>, KV8>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
+  make_plan<kThreads, KV8>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_launch_dependents();
+  if (KV8) grid_dependency_wait();     // q's parts are made by the kernel before this one
   const uint32_t tmem = bars->tmem_base;
   const WaitCtx wc{&bars->abort_flag, p.status};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp(bar, parity, wc); };
@@ -690,8 +727,20 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, 0, 1);
-    const uint64_t qdesc0 = smem_desc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024);
-    const uint64_t kdesc0 = smem_desc_sw128(smem_u32(smem + C::K_OFF), 16, 1024);
+    // Product kk of S's D / 16.  Codes: D / 32 of Q's first part, then of its second.
+    auto s_product = [&](uint32_t colS, uint64_t qd, uint64_t kd, int kk) {
+      if (KV8) {
+        const uint32_t off = kk % (D / 32) * 32;
+        mma_ss_e4m3(colS, desc_add(qd, kk / (D / 32) * (C::TILE_BYTES / 2) + off), desc_add(kd, off), kk > 0 ? 1u : 0u);
+      } else {
+        const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
+        mma_ss(colS, desc_add(qd, off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+      }
+    };
+    const uint64_t qdesc0 = KV8 && D == 64 ? smem_desc_sw64(smem_u32(smem + C::Q_OFF), 512)
+                                           : smem_desc_sw128(smem_u32(smem + C::Q_OFF), 16, 1024);
+    const uint64_t kdesc0 = KV8 && D == 64 ? smem_desc_sw64(smem_u32(smem + C::K_OFF), 512)
+                                           : smem_desc_sw128(smem_u32(smem + C::K_OFF), 16, 1024);
     const uint64_t vdesc0 = smem_desc_sw128(smem_u32(smem + C::V_OFF), C::BOX_BYTES, 1024);
     bool ok = true;
     int gs = 0, nseg = 0;
@@ -705,12 +754,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     bool pv_dual = false, pv_last = false;
     auto issue_s = [&](int t, int x, int sl) {
       if (lane == 0) {
-        const uint64_t qd = desc_add(qdesc0, x * C::TILE_BYTES), kd = desc_add(kdesc0, sl * C::TILE_BYTES);
+        const uint64_t qd = desc_add(qdesc0, x * C::TILE_BYTES), kd = desc_add(kdesc0, sl * C::K_SLOT);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
-          mma_ss(tmem + (t ? C::S_COL1 : C::S_COL0), desc_add(qd, off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk) s_product(tmem + (t ? C::S_COL1 : C::S_COL0), qd, kd, kk);
         mma_commit(&bars->s_full[t]);
       }
       __syncwarp();
@@ -777,7 +823,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // softmax without that wait would let them read a slot that is being
           // filled.  P1 is asked for while the last products of the first batch
           // run.
-          const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+          const uint64_t kd = desc_add(kdesc0, sl * C::K_SLOT), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
           auto batch = [&](int t, bool ask) -> bool {
             const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
             bool there = false;
@@ -785,9 +831,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             for (int kk = 0; kk < 8; ++kk) mma_ts(colO, colS + kk * 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
               if (ask && kk == D / 16 - 2) there = mbar_try_wait(&bars->p_full[1], p_par >> 1 & 1);
-              mma_ss(colS, desc_add(qdesc0, t * C::TILE_BYTES + off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
+              s_product(colS, desc_add(qdesc0, t * C::TILE_BYTES), kd, kk);
             }
             mma_commit(&bars->s_full[t]);
             if (t) mma_commit(&bars->kv_empty[sl]);
@@ -821,13 +866,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // One tile: S of this step's stream, PV of the other's.
           const int t = cur >> 1, u = t ^ 1;
           if (lane == 0) {
-            const uint64_t kd = desc_add(kdesc0, sl * C::TILE_BYTES), qd = desc_add(qdesc0, qsel * C::TILE_BYTES);
+            const uint64_t kd = desc_add(kdesc0, sl * C::K_SLOT), qd = desc_add(qdesc0, qsel * C::TILE_BYTES);
             const uint32_t colS = tmem + C::S_COL0 + t * (C::S_COL1 - C::S_COL0);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::BOX_BYTES + (kk & 3) * 32;
-              mma_ss(colS, desc_add(qd, off), desc_add(kd, off), IDESC_S, kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < D / 16; ++kk) s_product(colS, qd, kd, kk);
             mma_commit(&bars->s_full[t]);
           }
           __syncwarp();
@@ -896,7 +938,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         q_par ^= 3u;
       } else {
         q_par ^= 1u << qsel;
-        if (C::QB == 2) qsel ^= 1;
+        qsel ^= 1;
         flip = (flip + ie - ib) & 1;
       }
     }
@@ -915,32 +957,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (lane == 0) mma_commit(&bars->drain);
     __syncwarp();
     wait_warp_drain(&bars->drain, 0);
-  } else if (warp == kWalkWarp<KV8>) {
+  } else if (!KV8 && warp == kWalkWarp) {
     // -------------------------------------------------------------- walker
-    // Codes: Q, as the producer of bf16 pages loads it; one item behind the walk
-    // (the first aside), so that a wait for a Q buffer holds up nobody else.
-    bool ok = true, q_due = false;
-    unsigned q_any = 0, q_par = 0;
-    int qsel = 0, q_g = 0, q_tok = 0;
-    bool q_two = false;
-    auto load_q = [&]() -> bool {
-      for (int t = 0; t < (q_two ? 2 : 1); ++t) {
-        const int x = q_two ? t : qsel;
-        if ((q_any >> x & 1) && !wait(&bars->q_empty[x], q_par >> x & 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full[x], C::NB * rows_box * 128);
-#pragma unroll
-          for (int bx = 0; bx < C::NB; ++bx)
-            tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bx * 64, q_g * p.group,
-                        q_tok + t * p.tpt, &bars->q_full[x]);
-        }
-        __syncwarp();
-        if (q_any >> x & 1) q_par ^= 1u << x;
-        q_any |= 1u << x;
-      }
-      if (!q_two && C::QB == 2) qsel ^= 1;
-      return true;
-    };
     Walk w;
     Seg s;
     s.lost = 0;
@@ -968,184 +986,203 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         mbar_arrive(&bars->seg_full[nitem % kSegs]);
       }
       __syncwarp();
-      if (KV8) {
-        if (q_due && !(ok = load_q())) break;
-        q_due = more;
-        q_two = !ONE && s.k.two;
-        q_g = s.g;
-        q_tok = s.tok;
-        if (nitem == 0 && more) {
-          if (!(ok = load_q())) break;
-          q_due = false;
+    }
+  } else if (KV8 && warp == kLoadWarp) {
+    // -------------------------------------------- codes: walker and producer
+    // Finds the items, one ahead of the steps it fetches.  Per step: K's codes into
+    // a slot, V's codes into a stage (128 / page_size boxes of each, one lane each,
+    // one box for larger pages), and lane i the exponents of the tile's block i.
+    Walk w;
+    Seg s;
+    s.lost = 0;
+    walk_begin<KV8>(p, bars, w);
+    int cont = 0;
+    int4 begun = make_int4(0, 0, 0, 0);
+    bool more = true, ok = true;
+    auto publish = [&](int n) {
+      if (n >= kSegs && !wait(&bars->seg_empty[n % kSegs], (n / kSegs - 1) & 1)) return false;
+      more = walk_next<KV8>(p, w, s);
+      if (more) {
+        if (s.ib > 0) cont = s.ie == s.k.kt ? 2 : 1;
+        else if (s.ie < s.k.kt) begun = make_int4(1, s.tok, s.ntok, s.g);
+      } else {
+        s.ie = -1;
+        if (lane == 0) {
+          p.part_meta[2 * blockIdx.x] = make_int4(cont, 0, 0, 0);
+          p.part_meta[2 * blockIdx.x + 1] = begun;
         }
       }
+      if (lane == 0) {
+        const_cast<Seg*>(ring)[n % kSegs] = s;
+        mbar_arrive(&bars->seg_full[n % kSegs]);
+      }
+      __syncwarp();
+      return true;
+    };
+    const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
+    const int box_rows = min(p.page_size, 128), boxes = 128 / box_rows, blocks = box_rows >> 4;
+    constexpr int kNoPage = -0x7fffffff - 1;            // no row sees these keys
+    unsigned q_any = 0, q_par = 0;   // bit x: Q buffer x was loaded; its last load's parity
+    int qsel = 0;              // buffer of the next one-tile item
+    int gs = 0, ks = 0;        // steps over all items: V's loads, K's
+    // a block's exponents in 16 bytes: the word of the scales that holds its byte, -, the byte's place
+    const uint32_t khead = smem_u32(smem + C::HEAD_OFF), vhead = khead + C::NH * 128;
+    uint32_t* const limits = reinterpret_cast<uint32_t*>(smem + C::HEAD_OFF + (C::NH + C::NV) * 128);
+    ok = publish(0);
+    for (int n = 0; ok && more; ++n) {
+      const bool two = !ONE && s.k.two;
+      const int g = s.g, ib = s.ib, ie = s.ie, vlo = s.k.vlo, vhi = s.k.vhi, hi_all = s.k.hi_all, tok = s.tok;
+      const int32_t* table = p.block_table + (long long)s.b * p.max_pages;
+      int* const lost = &const_cast<Seg*>(ring)[n % kSegs].lost;
+      auto look_up = [&](int i) {                       // page of this lane's block
+        const int key = (hi_all - i) * 128 + 16 * lane;
+        return lane < 8 && i < ie && key < vhi && key + 16 > vlo ? max(__ldg(table + (key >> p.page_shift)), -1) : kNoPage;
+      };
+      int page = look_up(ib);
+      if (!(ok = publish(n + 1))) break;
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        const int x = two ? t : qsel;
+        if ((q_any >> x & 1) && !(ok = wait(&bars->q_empty[x], q_par >> x & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[x], 2 * D * rows_box);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+            tma_load_3d(smem + C::Q_OFF + x * C::TILE_BYTES + part * (C::TILE_BYTES / 2), &tmQ, 0, g * p.group,
+                        (part ? (int)p.T : 0) + tok + t * p.tpt, &bars->q_full[x]);
+        }
+        __syncwarp();
+        if (q_any >> x & 1) q_par ^= 1u << x;
+        q_any |= 1u << x;
+      }
+      if (!ok) break;
+      if (!two) qsel ^= 1;
+      for (int i = ib; i < ie; ++i, ++gs) {
+        const int next_page = look_up(i + 1);
+        const int key = (hi_all - i) * 128 + 16 * lane;
+        const bool good = (unsigned)page < (unsigned)p.num_pages;
+        const uint32_t row = good ? (uint32_t)page * p.page_size + (key & (p.page_size - 1)) : 0;
+        // a page that is not there is not read, and the item's rows are not written
+        const bool bad = __any_sync(0xffffffffu, !good && page != kNoPage);
+        const unsigned seen = __ballot_sync(0xffffffffu, good) & 0xffu;
+        const unsigned mine = lane < boxes ? seen >> (lane * blocks) & ((1u << blocks) - 1) : 0;
+        const int row_of = (int)__shfl_sync(0xffffffffu, row, mine ? lane * blocks + __ffs(mine) - 1 : 0) & ~(box_rows - 1);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine != 0)) * box_rows * D;
+        const long long j = good ? (long long)(row >> 4) * p.Hkv + g : 0;
+        const uint32_t few = good ? (uint32_t)min(4ll, scale_bytes - (j & ~3ll)) : 0;
+        const int sl = gs % C::NS, st = gs % C::NV;
+        if (gs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) break;
+        if (lane < 8) {
+          const uint32_t at = khead + (gs % C::NH) * 128 + lane * 16;
+          copy_async4(at, p.k_scales + (j & ~3ll), few);
+          sts32(at + 8, (uint32_t)(j & 3) * 8);
+        }
+        __syncwarp();                                   // lane 0 publishes what the others wrote
+        if (lane == 0) {
+          if (bad) {
+            record_status(p.status, FA_ERR_PAGE);
+            *lost = 1;
+          }
+          mbar_arrive_expect_tx(&bars->kv_full[sl], bytes);
+        }
+        __syncwarp();
+        if (mine) tma_load_3d(smem + C::K_OFF + sl * C::K_SLOT + lane * box_rows * D, &tmK, 0, g, row_of, &bars->kv_full[sl]);
+        if (lane < 8) copies_arrive(&bars->kv_full[sl]);
+        __syncwarp();
+        ++ks;
+        if (gs >= C::NV && !(ok = wait(&bars->stage_empty[st], ((gs / C::NV) - 1) & 1))) break;
+        if (lane < 8) {
+          const uint32_t at = vhead + st * 128 + lane * 16;
+          copy_async4(at, p.v_scales + (j & ~3ll), few);
+          sts32(at + 8, (uint32_t)(j & 3) * 8);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          limits[4 * st] = vlo - (hi_all - i) * 128;    // rows that some row of the item sees
+          limits[4 * st + 1] = vhi - (hi_all - i) * 128;
+          mbar_arrive_expect_tx(&bars->stage_full[st], bytes);
+        }
+        __syncwarp();
+        if (mine) tma_load_3d(smem + C::STG_OFF + st * 128 * D + lane * box_rows * D, &tmV, 0, g, row_of, &bars->stage_full[st]);
+        if (lane < 8) copies_arrive(&bars->stage_full[st]);
+        __syncwarp();
+        page = next_page;
+      }
     }
-    if (KV8)
-      for (int x = 0; x < 2; ++x)
-        if (q_any >> x & 1) wait_warp_drain(&bars->q_full[x], q_par >> x & 1);
+    if (ok && gs > 0) {                                 // the last step's V: a slot without K
+      const int sl = gs % C::NS;
+      if (gs < C::NS || (ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) {
+        if (lane == 0) mbar_arrive(&bars->kv_full[sl]);
+        __syncwarp();
+        if (lane < 8) copies_arrive(&bars->kv_full[sl]);
+        __syncwarp();
+        ++ks;
+      }
+    }
+    // Copies in flight must land before this CTA's shared memory goes away.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int x = 0; x < 2; ++x)
+      if (q_any >> x & 1) wait_warp_drain(&bars->q_full[x], q_par >> x & 1);
+    for (int i = max(0, ks - C::NS); i < ks; ++i) wait_warp_drain(&bars->kv_full[i % C::NS], (i / C::NS) & 1);
+    for (int i = max(0, gs - C::NV); i < gs; ++i) wait_warp_drain(&bars->stage_full[i % C::NV], (i / C::NV) & 1);
   } else if (KV8 && warp >= kConvWarp) {
-    // ---------------------------------------- codes to bf16, 32 rows per warp
-    // The warp fetches its rows' codes, RD groups of 16 slots ahead, each lane
-    // the 16 bytes that it will itself turn into bf16, and writes these where
-    // TMA puts bf16 pages: 64 columns per box, swizzled over 128 bytes.  Rows
-    // that no row of the item sees arrive as zeros.
-    constexpr int UNITS = 16 * D / 512;                 // loads of a group
-    constexpr int LPR = D / 16;                         // lanes per row
+    // ------------------------------- codes: V's to bf16, 64 rows of a tile per warp
+    // Written where TMA puts bf16 pages: 64 columns per box, swizzled over 128
+    // bytes.  Rows that no row of the item sees become zeros.
+    constexpr int LPR = D / 16;                         // lanes per row, 16 codes each
     constexpr int RPU = 32 / LPR;                       // rows per load
+    constexpr int UNITS = 16 / RPU;                     // loads of a block
     const int cw = warp - kConvWarp;
     const int rl = lane / LPR, jj = lane % LPR;
-    const long long scale_bytes = (long long)p.num_pages * (p.page_size >> 4) * p.Hkv;
-    enum { kValues = 1, kSecond = 2, kFirstOfStep = 4, kLastOfStep = 8 };
+    // the second box's lanes write their odd half first, so that eight lanes'
+    // stores take eight different places of a line
+    const int odd = jj >> 2, j0 = 2 * (jj & 3) + odd;
+    const uint32_t vhead = smem_u32(smem + C::HEAD_OFF) + C::NH * 128;
+    const uint32_t* const limits = reinterpret_cast<const uint32_t*>(smem + C::HEAD_OFF + (C::NH + C::NV) * 128);
     bool ok = true;
-    int fg = 0, cg = 0;                                 // groups fetched, turned
-    int cs = 0;                                         // steps turned
-    const uint32_t ring0 = smem_u32(smem + C::STG_OFF + cw * C::RD * C::GROUP_BYTES);
-    auto turn = [&] {
-      const uint32_t at = ring0 + cg % C::RD * C::GROUP_BYTES;
-      ++cg;
-      __syncwarp();                                     // lane 0's header and scale
-      const uint4 hd = lds128(at + 16 * D);
-      uint4 c[UNITS];
+    int cs = 0;                                         // steps turned: V of step cs goes to slot cs + 1
+    while (ok && next_seg(ok)) {
+      const Seg& s = ring[nitem % kSegs];
+      const int steps = s.ie - s.ib;
+      seg_done();
+      if (cs == 0 && lane == 0) mbar_arrive(&bars->kv_full[0]);      // the first slot has no V
+      for (int i = 0; i < steps; ++i, ++cs) {
+        const int st = cs % C::NV, to = cs + 1, sl = to % C::NS;
+        if (!(ok = wait(&bars->stage_full[st], (cs / C::NV) & 1))) break;
+        if (to >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((to / C::NS) - 1) & 1))) break;
+        const int lo = (int)limits[4 * st], hi = (int)limits[4 * st + 1];
+        const uint32_t from = smem_u32(smem + C::STG_OFF) + st * 128 * D;
+        const uint32_t box = smem_u32(smem + C::V_OFF) + sl * C::TILE_BYTES + odd * C::BOX_BYTES;
+#pragma unroll 1
+        for (int b = 4 * cw; b < 4 * cw + 4; ++b) {
+          const uint4 hd = lds128(vhead + st * 128 + b * 16);
+          const uint32_t e = min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127);
+          const uint32_t e1 = min(e, 134u);             // 2^120 2^(e1 - 127) in bf16
+          const uint32_t mul = (e1 + 120) * 0x00800080u, mul2 = e > e1 ? (127 + e - e1) * 0x00800080u : 0;
+          uint4 c[UNITS];
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) c[u] = lds128(at + u * 512 + lane * 16);
-      const int sl = cs % C::NS;
-      if ((hd.y & kFirstOfStep) && cs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((cs / C::NS) - 1) & 1))) return;
-      const uint32_t s = min(hd.x >> (hd.y >> 8 & 24u) & 0xffu, (uint32_t)kScaleHigh + 127);
-      const uint32_t s1 = min(s, 134u);                 // 2^120 2^(s1 - 127) in bf16
-      const uint32_t mul = (s1 + 120) * 0x00800080u, mul2 = s > s1 ? (127 + s - s1) * 0x00800080u : 0;
-      const int row0 = 32 * cw + (hd.y & kSecond ? 16 : 0) + rl;
-      // the second box's lanes write their odd half first, so that eight lanes'
-      // stores take eight different places of a line
-      const int odd = jj >> 2, j0 = 2 * (jj & 3) + odd;
-      uint32_t box = smem_u32(smem) + (hd.y & kValues ? C::V_OFF : C::K_OFF) + sl * C::TILE_BYTES + odd * C::BOX_BYTES + row0 * 128;
+          for (int u = 0; u < UNITS; ++u) {
+            const int r = 16 * b + u * RPU + rl;
+            c[u] = lds128(from + r * D + (jj ^ (D == 128 ? r & 7 : r >> 1 & 3)) * 16);
+            if (r < lo || r >= hi) c[u] = make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        uint32_t x[8];
-        codes_to_bf16(c[u], mul, mul2, x);
-        const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), b = make_uint4(x[4], x[5], x[6], x[7]);
-        const int r7 = (rl + u * RPU) & 7;
-        sts128(box + u * RPU * 128 + ((j0 ^ r7) << 4), odd ? b : a);
-        sts128(box + u * RPU * 128 + ((j0 ^ 1 ^ r7) << 4), odd ? a : b);
-      }
-      if (hd.y & kLastOfStep) {
+          for (int u = 0; u < UNITS; ++u) {
+            uint32_t x[8];
+            codes_to_bf16(c[u], mul, mul2, x);
+            const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), z = make_uint4(x[4], x[5], x[6], x[7]);
+            const int r = 16 * b + u * RPU + rl;
+            sts128(box + r * 128 + ((j0 ^ (r & 7)) << 4), odd ? z : a);
+            sts128(box + r * 128 + ((j0 ^ 1 ^ (r & 7)) << 4), odd ? a : z);
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->kv_full[sl]);
-        ++cs;
-      }
-    };
-    constexpr int kNoPage = -0x7fffffff - 1;            // no row sees these keys
-    const int32_t* table = nullptr;
-    int* lost = nullptr;
-    int i = 0, ie = 0, own = 0, page[2] = {kNoPage, kNoPage}, steps = 0;
-    // the step being fetched [0] and the one before [1]: pool's rows of the
-    // groups' first slots (none: < 0), first key, keys that are seen, kv head
-    long long row[2][2] = {{-1, -1}, {-1, -1}};
-    int key0[2] = {0, 0}, vlo[2] = {0, 0}, vhi[2] = {0, 0}, g[2] = {0, 0};
-    auto page_of = [&](int step, int half) {
-      const int k = own - step * 128 + 16 * half;
-      return step < ie && k < vhi[0] && k + 16 > vlo[0] ? max(__ldg(table + (k >> p.page_shift)), -1) : kNoPage;
-    };
-    // A step's groups in turn: keys 0, 1, values of the step before 2, 3.  One
-    // loop with one copy of each part: four copies of `turn`, one for each group,
-    // do not stay in the instruction caches (6800 cycles per step, 1300 so).
-    int part = 0;
-    bool ended = false, done = false;
-#pragma unroll 1
-    while (true) {
-      const bool new_item = part == 0 && i >= ie && !ended;
-      // Nobody else's progress waits for the groups that are still in the ring
-      // while this warp waits for the walker.
-      const bool drain = done || (new_item && !__all_sync(0xffffffffu, mbar_try_wait(&bars->seg_full[nitem % kSegs], (nitem / kSegs) & 1)));
-#pragma unroll 1
-      while (ok && fg - cg > (drain ? 0 : C::RD - 1)) {
-        if (drain) asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else asm volatile("cp.async.wait_group %0;" :: "n"(C::RD - 1) : "memory");
-        turn();
-      }
-      if (!ok || done) break;
-      if (new_item) {
-        if (next_seg(ok)) {
-          const Seg& s = ring[nitem % kSegs];
-          g[0] = s.g;
-          i = s.ib;
-          ie = s.ie;
-          vlo[0] = s.k.vlo;
-          vhi[0] = s.k.vhi;
-          own = s.k.hi_all * 128 + 32 * cw;             // first key of this warp's rows at step 0
-          // (the place in the ring stays this item's until its epilogue is done)
-          lost = const_cast<int*>(&s.lost);
-          table = p.block_table + (long long)s.b * p.max_pages;
-          seg_done();
-          page[0] = page_of(i, 0);
-          page[1] = page_of(i, 1);
-        } else {
-          ended = true;
-          part = 2;                                     // the last step's values
-          if (!ok || steps == 0) {
-            done = true;
-            continue;
-          }
-        }
-      }
-      if (part == 0) {
-        key0[0] = own - i * 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          row[0][h] = -1;
-          if (page[h] >= 0 && page[h] < p.num_pages) {
-            row[0][h] = (long long)page[h] * p.page_size + ((key0[0] + 16 * h) & (p.page_size - 1));
-          } else if (page[h] != kNoPage && lane == 0) {
-            // nothing is read, and the item's rows are not written
-            record_status(p.status, FA_ERR_PAGE);
-            *lost = 1;                                  // (the lane whose arrival publishes it)
-          }
-          page[h] = page_of(i + 1, h);
-        }
-      }
-      {
-        // this group of 16 slots on its way
-        const int x = part >> 1, h = part & 1;
-        const long long rw = x ? (h ? row[1][1] : row[1][0]) : (h ? row[0][1] : row[0][0]);
-        const int k = (x ? key0[1] : key0[0]) + 16 * h + rl, head = x ? g[1] : g[0];
-        const int lo = rw >= 0 ? (x ? vlo[1] : vlo[0]) : 1, hi = rw >= 0 ? (x ? vhi[1] : vhi[0]) : 0;
-        const uint32_t at = ring0 + fg % C::RD * C::GROUP_BYTES;
-        ++fg;
-        __syncwarp();                                   // the place's header has been read
-        const uint8_t* src = static_cast<const uint8_t*>(x ? p.v : p.k) + (rw >= 0 ? ((rw + rl) * p.Hkv + head) * D : 0) + jj * 16;
-        const long long step = (long long)RPU * p.Hkv * D;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const bool seen = k + u * RPU >= lo && k + u * RPU < hi;
-          copy_async16(at + u * 512 + lane * 16, seen ? src + u * step : static_cast<const uint8_t*>(p.k), seen ? 16 : 0);
-        }
         if (lane == 0) {
-          const long long j = rw >= 0 ? (rw >> 4) * p.Hkv + head : 0;
-          copy_async4(at + 16 * D, (x ? p.v_scales : p.k_scales) + (j & ~3ll), rw >= 0 ? (int)min(4ll, scale_bytes - (j & ~3ll)) : 0);
-          const bool first = part == 0 || (ended && part == 2), last = part == 3 || (steps == 0 && part == 1);
-          sts32(at + 16 * D + 4, (x ? kValues : 0) | (h ? kSecond : 0) | (first ? kFirstOfStep : 0) | (last ? kLastOfStep : 0) |
-                                     (uint32_t)(j & 3) << 11);
+          mbar_arrive(&bars->stage_empty[st]);
+          mbar_arrive(&bars->kv_full[sl]);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-      ++part;
-      if (part == 4 || (part == 2 && steps == 0)) {
-        if (ended) {
-          done = true;
-          continue;
-        }
-        part = 0;
-        ++steps;
-        ++i;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) row[1][h] = row[0][h];
-        key0[1] = key0[0];
-        vlo[1] = vlo[0];
-        vhi[1] = vhi[0];
-        g[1] = g[0];
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
@@ -1167,6 +1204,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       bool valid, dual;
       float slope2 = 0.f;
       int vslot = 0;             // step of this stream's next tile
+      int hs0 = 0;               // codes: that step, whose keys' exponents it is
+      int qup = 0;               // codes: Q's row is times 2^qup
       {
         if (!next_seg(ok)) break;
         const Seg& s = ring[nitem % kSegs];
@@ -1192,7 +1231,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         diag = p.causal ? f : s.L - 1;
         low = f + nt - 1 - p.window;
         if (ALIBI) slope2 = valid ? __ldg(p.alibi + s.g * p.group + r % p.group) * kLog2e : 0.f;
-        vslot = gs + s.k.hi_all - s.ib - kt0;
+        if (KV8 && valid) qup = p.q_exps[(long long)(s.tok + (second ? p.tpt : 0) + rq) * p.Hq + s.g * p.group + r % p.group];
+        vslot = hs0 = gs + s.k.hi_all - s.ib - kt0;
         gs += s.ie - s.ib;
       }
       const bool warp_rows = __any_sync(0xffffffffu, valid);
@@ -1207,6 +1247,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           continue;
         }
         tc_fence_after();
+        // Codes: lane i has the exponent of the tile's block i; a score of column c is
+        // S scale 2^(that - qup).  Below 2^-100 a score is 0 beside any other.
+        int kexp = 0;
+        if (KV8) {
+          const uint4 hd = lds128(smem_u32(smem + C::HEAD_OFF) + ((hs0 + (dual ? 2 : 1) * j) % C::NH) * 128 + (lane & 7) * 16);
+          kexp = exponent_of(hd.x, hd.z);
+        }
+        auto c2_of = [&](int c) { return KV8 ? c2 * pow2_cut(max(__shfl_sync(0xffffffffu, kexp, c >> 4) - qup, -100)) : c2; };
         // The commit that published S_t also covers this stream's last PV, so
         // O may be rescaled now.
         if (!ONE && __any_sync(0xffffffffu, grow > 0.f)) {
@@ -1230,7 +1278,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const float b0 = fmaf(slope2, (float)c, base - mb);
             bm = f2(b0, b0 + slope2);
           }
-          const uint64_t step = f2(2.f * slope2, 2.f * slope2), c2p = f2(c2, c2);
+          const float c2c = c2_of(c);
+          const uint64_t step = f2(2.f * slope2, 2.f * slope2), c2p = f2(c2c, c2c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint64_t ex = ffma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2p, bm);
@@ -1308,20 +1357,28 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                   if (c + i < lb) x[i] = __float_as_uint(-INFINITY);
               tmem_st32(tS + c, x);
             }
-            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+            const float ca = c2_of(c), cb = c2_of(c + 16);
+            float m4[4] = {KV8 ? -INFINITY : mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
               if (ALIBI) {
-                x0 = fmaf(x0, c2, fmaf(slope2, (float)(c + i), base));
-                x1 = fmaf(x1, c2, fmaf(slope2, (float)(c + i + 1), base));
+                x0 = fmaf(x0, i < 16 ? ca : cb, fmaf(slope2, (float)(c + i), base));
+                x1 = fmaf(x1, i < 16 ? ca : cb, fmaf(slope2, (float)(c + i + 1), base));
               }
-              m4[i / 2 & 3] = fmax3(m4[i / 2 & 3], x0, x1);
+              // codes: columns 0 .. 15 and 16 .. 31 apart, as their scales are
+              const int k = KV8 ? i / 16 * 2 + (i / 2 & 1) : i / 2 & 3;
+              m4[k] = fmax3(m4[k], x0, x1);
             }
-            mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+            if (KV8) {
+              const float a = fmaxf(m4[0], m4[1]), b = fmaxf(m4[2], m4[3]);
+              mx = fmax3(mx, ALIBI ? a : a * ca, ALIBI ? b : b * cb);
+            } else {
+              mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+            }
           }
           if (masked) tmem_wait_st();
-          if (!ALIBI) mx *= c2;
+          if (!ALIBI && !KV8) mx *= c2;
           // Any reference gives the same result: it stays until the max has
           // grown by more than tau.
           const bool raise = mx > m_ref + kTau;
@@ -1465,9 +1522,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // The call's other kernel may still run; what follows this one must find both
-  // at their end.
-  if (KV8) grid_dependency_wait();
   // A wait ran out, so parts may be missing, whatever the walker put on record
   // ahead of them: the merge must not take what the workspace held.  Nor a part
   // of an item that met a page outside the pool.
@@ -1567,39 +1621,36 @@ __global__ void __launch_bounds__(256) paged_merge_two_kernel(const PagedParams 
   merge_parts<D>(blockIdx.z ? q : p, nctas);
 }
 
-// `after`: another kernel of the call runs before this one, and the merge is
-// the caller's.
+// Codes: begins while the kernel that makes q's parts runs; the merge is the
+// caller's.
 template <int D, bool ALIBI, bool ONE, bool KV8>
-int launch_impl(const PagedParams& p, cudaStream_t stream, bool after = false) {
-  using C = Cfg<D, ONE, KV8>;
+int launch_impl(const PagedParams& p, cudaStream_t stream) {
+  using C = Cfg<D, KV8>;
   auto kern = fwd_paged_kernel<D, ALIBI, ONE, KV8>;
   if (const int ea = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return ea;
   CUtensorMap tq, tk, tv;
   const long long slots = (long long)p.num_pages * p.page_size;
   const int box = std::min(p.page_size, 128);
-  int r = make_tmap_bf16_3d_box(&tq, p.q, D, p.Hq, p.T, p.group, p.tpt);
-  if (KV8) {
-    tk = tv = tq;                                   // not used
-  } else {
-    if (!r) r = make_tmap_bf16_3d(&tk, p.k, D, p.Hkv, slots, box);
-    if (!r) r = make_tmap_bf16_3d(&tv, p.v, D, p.Hkv, slots, box);
-  }
+  int r = KV8 ? make_tmap_codes_3d(&tq, p.q_codes, D, p.Hq, 2 * p.T, p.group, p.tpt)
+              : make_tmap_bf16_3d_box(&tq, p.q, D, p.Hq, p.T, p.group, p.tpt);
+  if (!r) r = KV8 ? make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, 1, box) : make_tmap_bf16_3d(&tk, p.k, D, p.Hkv, slots, box);
+  if (!r) r = KV8 ? make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, 1, box) : make_tmap_bf16_3d(&tv, p.v, D, p.Hkv, slots, box);
   if (r) return r;
   int nsm = 0;
   if (const int es = sm_count(&nsm)) return es;
   const int grid = std::min(nsm, kPagedCtas);
-  if (KV8 && after) return launch_dependent(kern, dim3(grid), dim3(kThreads<KV8>), C::SMEM_BYTES, stream, tq, tk, tv, p);
-  kern<<<grid, kThreads<KV8>, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+  if (KV8) return launch_dependent(kern, dim3(grid), dim3(kThreads), C::SMEM_BYTES, stream, tq, tk, tv, p);
+  kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
   if (const cudaError_t e = cudaGetLastError()) return (int)e;
   return launch_dependent(paged_merge_kernel<D>, dim3(grid, std::max(1, (p.part_rows + 7) / 8)), dim3(256), 0, stream, p, grid);
 }
 
 template <int D, bool KV8>
-int launch_d(const PagedParams& p, cudaStream_t stream, bool after = false) {
+int launch_d(const PagedParams& p, cudaStream_t stream) {
   // no sequence brings more tokens than one tile holds
   const bool one = p.N <= p.tpt;
-  if (p.alibi) return one ? launch_impl<D, true, true, KV8>(p, stream, after) : launch_impl<D, true, false, KV8>(p, stream, after);
-  return one ? launch_impl<D, false, true, KV8>(p, stream, after) : launch_impl<D, false, false, KV8>(p, stream, after);
+  if (p.alibi) return one ? launch_impl<D, true, true, KV8>(p, stream) : launch_impl<D, true, false, KV8>(p, stream);
+  return one ? launch_impl<D, false, true, KV8>(p, stream) : launch_impl<D, false, false, KV8>(p, stream);
 }
 
 }  // namespace

@@ -98,9 +98,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// 2^e, the exponent cut to what a float holds.
-__device__ __forceinline__ float pow2_cut(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
-
 // An 8 x 8 matrix of 16-bit elements, transposed: row lane / 4, columns 2 (lane %
 // 4) and the next.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -117,12 +114,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
-}
-
-// Completes one of the arrivals that `bar` waits for when this thread's copies
-// so far have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
 template <int D, int NR, bool ALIBI>
@@ -291,6 +282,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     __syncthreads();
     // A wait ran out, so parts may be missing: the merge must not take what the
     // workspace held.  Nor a part of an item that met a page outside the pool.
+    grid_dependency_wait();                            // (see the end of the kernel)
     if (!values && lane < 2)
       p.part_meta[2 * blockIdx.x + lane] = bars->abort_flag || bars->part_lost[lane] ? make_int4(0, 0, 0, 0)
                                            : lane ? begun : make_int4(cont, 0, 0, 0);
@@ -484,8 +476,8 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
         for (int x = 0; x < XB; ++x) {
           const uint4 hd = lds128(heads + (y + x) * 16);
-          ek[x] = (int)min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
-          ev[x] = (int)min(hd.y >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
+          ek[x] = exponent_of(hd.x, hd.z);
+          ev[x] = exponent_of(hd.y, hd.z);
         }
         if (XB == 2) {                                   // (a block that no row sees has no exponents)
           if (k0 + 16 <= vlo) ev[0] = ev[XB - 1];
@@ -751,30 +743,34 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     go = next && known(cur + 1);
   }
   __syncthreads();
+  // The call's other kernel may still run; what follows this one must find both
+  // at their end.
+  grid_dependency_wait();
 }
 
 template <int D, int NR>
-int launch_few(const PagedParams& p, int grid, cudaStream_t stream) {
+int launch_few(const PagedParams& p, int grid, bool after, cudaStream_t stream) {
   using C = Few<D, NR>;
   auto kern = p.alibi ? fwd_paged_few_kernel<D, NR, true> : fwd_paged_few_kernel<D, NR, false>;
   if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES)) return e;
   CUtensorMap tk, tv;
   const long long slots = (long long)p.num_pages * p.page_size;
-  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, std::min(p.page_size, 128))) return e;
-  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, std::min(p.page_size, 128))) return e;
+  if (const int e = make_tmap_codes_3d(&tk, p.k, D, p.Hkv, slots, 1, std::min(p.page_size, 128))) return e;
+  if (const int e = make_tmap_codes_3d(&tv, p.v, D, p.Hkv, slots, 1, std::min(p.page_size, 128))) return e;
+  if (after) return launch_dependent(kern, dim3(grid), dim3(C::NT), C::SMEM_BYTES, stream, tk, tv, p);
   kern<<<grid, C::NT, C::SMEM_BYTES, stream>>>(tk, tv, p);
   return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_fwd_paged_few(PagedParams p, int grid, void* stream_) {
+int launch_fwd_paged_few(PagedParams p, int grid, bool after, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   p.head_few = (long long)p.B * p.Hkv * 2 >= grid ? kHeadFew : kHeadOne;
-  if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, stream) : launch_few<64, 1>(p, grid, stream);
-  if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, stream) : launch_few<64, 2>(p, grid, stream);
-  if (p.few_rows <= 24) return p.d == 128 ? launch_few<128, 3>(p, grid, stream) : launch_few<64, 3>(p, grid, stream);
-  return p.d == 128 ? launch_few<128, 4>(p, grid, stream) : launch_few<64, 4>(p, grid, stream);
+  if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, after, stream) : launch_few<64, 1>(p, grid, after, stream);
+  if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, after, stream) : launch_few<64, 2>(p, grid, after, stream);
+  if (p.few_rows <= 24) return p.d == 128 ? launch_few<128, 3>(p, grid, after, stream) : launch_few<64, 3>(p, grid, after, stream);
+  return p.d == 128 ? launch_few<128, 4>(p, grid, after, stream) : launch_few<64, 4>(p, grid, after, stream);
 }
 
 }  // namespace fa

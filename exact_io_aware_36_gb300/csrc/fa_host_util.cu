@@ -135,10 +135,10 @@ int make_tmap_u8_3d(CUtensorMap* map, const void* base, long long n0, long long 
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, box);
 }
 
-int make_tmap_codes_3d(CUtensorMap* map, const void* base, int d, int H, long long slots, int box_rows) {
+int make_tmap_codes_3d(CUtensorMap* map, const void* base, int d, int H, long long slots, int box_h, int box_rows) {
   const uint64_t dims[3] = {(uint64_t)d, (uint64_t)H, (uint64_t)slots};
   const uint64_t strides[2] = {(uint64_t)d, (uint64_t)d * H};
-  const uint32_t box[3] = {(uint32_t)d, 1, (uint32_t)box_rows};
+  const uint32_t box[3] = {(uint32_t)d, (uint32_t)box_h, (uint32_t)box_rows};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, box,
                 d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                 d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);

@@ -36,10 +36,10 @@ int make_tmap_u8_3d(CUtensorMap* map, const void* base, long long n0, long long 
                     long long s1, long long s2, int b0, int b1, int b2);
 
 // Encodes a 3-D tiled TMA descriptor over a contiguous byte tensor [slots, H,
-// d] (e4m3 codes; d 64 or 128) with a box of d columns x 1 head x box_rows
+// d] (e4m3 codes; d 64 or 128) with a box of d columns x box_h heads x box_rows
 // slots, swizzled over its d bytes.  A row of one head is all that a box wants of
 // a line, so L2 fetches no more than it.  Returns 0 or a cudaError_t value.
-int make_tmap_codes_3d(CUtensorMap* map, const void* base, int d, int H, long long slots, int box_rows);
+int make_tmap_codes_3d(CUtensorMap* map, const void* base, int d, int H, long long slots, int box_h, int box_rows);
 
 // cudaFuncAttributeMaxDynamicSharedMemorySize of `kernel` in the current
 // device's context, set on the first call per (device, kernel) only.

@@ -222,6 +222,10 @@ struct PagedParams {
   int few_rows, few;           // codes: sequences of up to few_rows rows per kv head
                                // are another kernel's (few: the others are)
   int head_few;                // that kernel's weight of an item beside its tiles
+  // codes: workspace, q 2^q_exps as the sum of two e4m3 parts, [2][T, Hq, d], and
+  // its rows' exponents [T, Hq]
+  uint8_t* q_codes;
+  int* q_exps;
 };
 
 // CTAs of the paged forward: GB300's SMs; each leaves at most two parts.
@@ -255,9 +259,10 @@ int launch_append_fp8(const QuantAppendParams& p, bool turn, void* stream);   //
 int launch_copy_pages(CachePagesCopy p, void* stream);
 int launch_fwd_paged(const PagedParams& p, void* stream);             // runs + merge of parts
 // The same over e4m3 codes: `few` with the sequences of up to few.few_rows rows
-// per kv head, `many` with the others; either may be absent (B = 0).
+// per kv head, `many` with the others; either may be absent (B = 0).  Runs and
+// the merge of parts.
 int launch_fwd_paged_fp8(const PagedParams& few, const PagedParams& many, void* stream);
-int launch_fwd_paged_few(PagedParams p, int grid, void* stream);   // its first part: runs
+int launch_fwd_paged_few(PagedParams p, int grid, bool after, void* stream);   // runs, after another kernel of the call
 int launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, void* stream);
 
 #ifdef __CUDACC__

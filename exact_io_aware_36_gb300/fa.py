@@ -114,7 +114,7 @@ def load(path: Optional[str] = None):
         a = getattr(lib, name).argtypes
         getattr(lib, name + "_fp8").argtypes = a[:pages] + [vp, vp] + a[pages:]
         getattr(lib, name + "_fp8").restype = i
-    lib.fa_fwd_paged_fp8_workspace_size.argtypes = [i, i, i, i]
+    lib.fa_fwd_paged_fp8_workspace_size.argtypes = [i, i, i, i, ll]
     lib.fa_fwd_paged_fp8_workspace_size.restype = sz
     lib.fa_check_device_error.argtypes = [vp]
     lib.fa_check_device_error.restype = i
@@ -282,8 +282,8 @@ def fa_cache_copy_fp8(k_pages, v_pages, k_scales, v_scales, src, dst, n, num_pag
                                     page_size, Hkv, d, stream)
 
 
-def fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) -> int:
-    return load().fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d)
+def fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d, total_tokens) -> int:
+    return load().fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d, total_tokens)
 
 
 def fa_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, cache_seqlens, cu_seqlens, o,
@@ -923,7 +923,7 @@ def attention_forward_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
     slopes = None if alibi_slopes is None else _checked("alibi_slopes", alibi_slopes, torch.float32, index, (Hq,))
     out, op = _out("out", out, q, (T, Hq, d), (out_dtype or q.dtype) if out is None else out.dtype, index, stream)
     lse, lp = _out("lse", lse, q, (Hq, T), torch.float32, index, stream)
-    wbytes = fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d) if workspace is None else workspace.numel()
+    wbytes = fa_fwd_paged_fp8_workspace_size(Hq, Hkv, N, d, T) if workspace is None else workspace.numel()
     workspace, wp = _out("workspace", workspace, q, (wbytes,), torch.uint8, index, stream)
     _run("fa_fwd_paged_fp8", index, stream, check, qp, *pools, tp, cp, cup, op, lp, B, Hq, Hkv, N, d, T,
          page_size, num_pages, max_pages, float(d ** -0.5 if scale is None else scale), causal,

@@ -558,10 +558,14 @@ fa_status fa_cache_copy_fp8(void* k_pages, void* v_pages, void* k_scales, void* 
 /*
  * fa_fwd_paged over a cache in 8 bits: the attention of the values that the
  * codes stand for, with fa_fwd_paged's arguments, masks, rows and errors and a
- * workspace of fa_fwd_paged_fp8_workspace_size bytes.  Only q, P and O are in
- * 16 bits beside the codes.
+ * workspace of fa_fwd_paged_fp8_workspace_size bytes (total_tokens: the rows of
+ * q).  Products with the keys are exact but for elements of q below 2^-9 of its
+ * row's largest, which are off by at most 2^-17 of that one.  P is rounded as in
+ * fa_fwd_paged; for sequences that bring few rows (new tokens times Hq / Hkv: at
+ * most 32 where no sequence of the call brings more, else what one token brings,
+ * rounded up to a multiple of 8) once to fp16.
  */
-size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d);
+size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d, long long total_tokens);
 
 fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                            const void* k_scales, const void* v_scales,
