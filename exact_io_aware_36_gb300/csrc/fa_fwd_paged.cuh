@@ -84,6 +84,7 @@
 // P overwrites S: 64 columns, or all 128 (each 16 keys' high part, then low).
 #pragma once
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -106,6 +107,8 @@ constexpr int kSegs = 4;               // items that the walker may be ahead
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
 constexpr float kMaxSum = 1.0995116e12f;   // 2^40
+constexpr int kUpP = 6;                // codes: P in f16 is times 2^6, ..
+constexpr float kMaxSumF16 = 1000.0f;  // .. and no more than 2^16
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
 // Of an item of the kernel for few rows (p.head_few): an item more costs a CTA
@@ -128,13 +131,13 @@ struct Cfg {
   static constexpr int NS = D == 128 ? 2 : KV8 ? 4 : 5;
   static constexpr int K_SLOT = KV8 ? 128 * D : TILE_BYTES;   // codes: K as it is, V in bf16
   static constexpr int NV = D == 128 ? 3 : 4;       // codes: tiles of V's codes on their way
-  static constexpr int NH = 8;                      // codes: steps whose keys' exponents are kept
+  static constexpr int NH = 8;                      // codes: steps whose exponents are kept
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
   static constexpr int V_OFF = K_OFF + NS * K_SLOT;
   static constexpr int STG_OFF = V_OFF + NS * TILE_BYTES;
-  static constexpr int HEAD_OFF = STG_OFF + (KV8 ? NV * 128 * D : 0);     // exponents: of keys, of values
-  static constexpr int ML_OFF = HEAD_OFF + (KV8 ? (NH + NV) * 128 + NV * 16 : 0);   // (m, l, l~) of both streams' rows
+  static constexpr int HEAD_OFF = STG_OFF + (KV8 ? NV * 128 * D : 0);     // exponents, then the rows of V's tiles that count
+  static constexpr int ML_OFF = HEAD_OFF + (KV8 ? NH * 128 + NV * 16 : 0);   // (m, l, l~ or O's power of two) of both streams' rows
   static constexpr int SEG_OFF = ML_OFF + 2 * 128 * 3 * 4;          // ring of items
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;              // a copy of the parameters
   static constexpr int BAR_OFF = PAR_OFF + 256;
@@ -456,36 +459,18 @@ __device__ __forceinline__ void store_row16(const float* v, bool f32, char* at) 
   }
 }
 
-// 16 codes as bf16 times a scale: a code's bits, moved to a bf16's place, are
-// the value times 2^-120 (subnormal codes too), so one multiplication by 2^120
-// times the scale (mul; a scale above 2^7 takes two) gives the value exactly.
-__device__ __forceinline__ void codes_to_bf16(const uint4& c, uint32_t mul, uint32_t mul2, uint32_t* out) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t nan = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // two codes, each with its sign over the byte above
-      uint32_t t;
-      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w[i]), "r"(j ? 0xB3A2 : 0x9180));
-      t = t << 4 & 0x87f087f0u;
-      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(out[2 * i + j]) : "r"(t), "r"(mul), "r"(0x80008000u));
-    }
-  }
-  if (mul2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(out[i]) : "r"(mul2), "r"(0x80008000u));
-  }
-  if (nan & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = w[i / 2] >> (16 * (i & 1));
-      if ((b & 0x7fu) == 0x7fu) out[i] |= 0x7fffu;
-      if ((b & 0x7f00u) == 0x7f00u) out[i] |= 0x7fff0000u;
-    }
-  }
+// 4 codes as f16.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
+  uint2 r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"((uint16_t)w));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"((uint16_t)(w >> 16)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // 4 bytes from global to shared memory, asynchronously; only the first `bytes` are
@@ -538,6 +523,9 @@ __device__ __forceinline__ int exponent_of(uint32_t word, uint32_t shift) {
   return (int)min(word >> shift & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
 }
 
+// 2^e for e from -127 to 127.
+__device__ __forceinline__ float pow2_of(int e) { return __int_as_float(e > -127 ? (e + 127) << 23 : 0x00400000); }
+
 // ONE: no item has two tiles (the host knows from N).  KV8: the pages hold
 // codes.
 template <int D, bool ALIBI, bool ONE, bool KV8>
@@ -565,7 +553,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bars->p_full[t], 4);
     }
     for (int s = 0; s < C::NS; ++s) {
-      // codes: K, its blocks' exponents, V in bf16
+      // codes: K, the exponents, V in f16
       mbar_init(&bars->kv_full[s], KV8 ? 1 + 8 + kConvWarps : 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
@@ -575,7 +563,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bars->seg_empty[i], KV8 ? kConvWarps + 9 : 10);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->stage_full[i], 1 + 8);
+      mbar_init(&bars->stage_full[i], 1);
       mbar_init(&bars->stage_empty[i], kConvWarps);
     }
     mbar_init(&bars->o_done, 1);
@@ -726,7 +714,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, 0, 0);
-    constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, 0, 1);
+    // (codes: f16 where the others have bf16)
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, 0, 1) & ~(KV8 ? 1u << 7 | 1u << 10 : 0u);
     // Product kk of S's D / 16.  Codes: D / 32 of Q's first part, then of its second.
     auto s_product = [&](uint32_t colS, uint64_t qd, uint64_t kd, int kk) {
       if (KV8) {
@@ -772,7 +761,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (lane == 0) {
         const uint64_t vd = desc_add(vdesc0, sl * C::TILE_BYTES);
         const uint32_t colP = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
-        if (ONE || pv_dual) {                             // 16 keys of P: high part, low part
+        if (!KV8 && (ONE || pv_dual)) {                   // 16 keys of P: high part, low part
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             mma_ts(colO, colP + kk * 16, desc_add(vd, kk * 2048), IDESC_O, (!first || kk > 0) ? 1u : 0u);
@@ -881,8 +870,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const uint32_t colO = tmem + C::O_COL0 + u * (C::O_COL1 - C::O_COL0);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              mma_ts(colO, colP + kk * 16, desc_add(vd, kk * 2048), IDESC_O, 1u);
-              mma_ts(colO, colP + kk * 16 + 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
+              mma_ts(colO, colP + kk * (KV8 ? 8 : 16), desc_add(vd, kk * 2048), IDESC_O, 1u);
+              if (!KV8) mma_ts(colO, colP + kk * 16 + 8, desc_add(vd, kk * 2048), IDESC_O, 1u);
             }
             mma_commit(&bars->kv_empty[sl]);
           }
@@ -989,9 +978,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
   } else if (KV8 && warp == kLoadWarp) {
     // -------------------------------------------- codes: walker and producer
-    // Finds the items, one ahead of the steps it fetches.  Per step: K's codes into
-    // a slot, V's codes into a stage (128 / page_size boxes of each, one lane each,
-    // one box for larger pages), and lane i the exponents of the tile's block i.
+    // Finds the items, one ahead of the steps it fetches.  Per step: K's codes and
+    // lane i the exponents of the tile's block i into a slot, V's codes into a stage
+    // (128 / page_size boxes of each, one lane each, one box for larger pages).
     Walk w;
     Seg s;
     s.lost = 0;
@@ -1025,9 +1014,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     unsigned q_any = 0, q_par = 0;   // bit x: Q buffer x was loaded; its last load's parity
     int qsel = 0;              // buffer of the next one-tile item
     int gs = 0, ks = 0;        // steps over all items: V's loads, K's
-    // a block's exponents in 16 bytes: the word of the scales that holds its byte, -, the byte's place
-    const uint32_t khead = smem_u32(smem + C::HEAD_OFF), vhead = khead + C::NH * 128;
-    uint32_t* const limits = reinterpret_cast<uint32_t*>(smem + C::HEAD_OFF + (C::NH + C::NV) * 128);
+    // a block's exponents in 16 bytes: the words of the scales that hold its byte, the byte's place
+    const uint32_t heads = smem_u32(smem + C::HEAD_OFF);
+    uint32_t* const limits = reinterpret_cast<uint32_t*>(smem + C::HEAD_OFF + C::NH * 128);
     ok = publish(0);
     for (int n = 0; ok && more; ++n) {
       const bool two = !ONE && s.k.two;
@@ -1072,8 +1061,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int sl = gs % C::NS, st = gs % C::NV;
         if (gs >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((gs / C::NS) - 1) & 1))) break;
         if (lane < 8) {
-          const uint32_t at = khead + (gs % C::NH) * 128 + lane * 16;
+          const uint32_t at = heads + (gs % C::NH) * 128 + lane * 16;
           copy_async4(at, p.k_scales + (j & ~3ll), few);
+          copy_async4(at + 4, p.v_scales + (j & ~3ll), few);
           sts32(at + 8, (uint32_t)(j & 3) * 8);
         }
         __syncwarp();                                   // lane 0 publishes what the others wrote
@@ -1090,12 +1080,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         __syncwarp();
         ++ks;
         if (gs >= C::NV && !(ok = wait(&bars->stage_empty[st], ((gs / C::NV) - 1) & 1))) break;
-        if (lane < 8) {
-          const uint32_t at = vhead + st * 128 + lane * 16;
-          copy_async4(at, p.v_scales + (j & ~3ll), few);
-          sts32(at + 8, (uint32_t)(j & 3) * 8);
-        }
-        __syncwarp();
         if (lane == 0) {
           limits[4 * st] = vlo - (hi_all - i) * 128;    // rows that some row of the item sees
           limits[4 * st + 1] = vhi - (hi_all - i) * 128;
@@ -1103,7 +1087,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         __syncwarp();
         if (mine) tma_load_3d(smem + C::STG_OFF + st * 128 * D + lane * box_rows * D, &tmV, 0, g, row_of, &bars->stage_full[st]);
-        if (lane < 8) copies_arrive(&bars->stage_full[st]);
         __syncwarp();
         page = next_page;
       }
@@ -1125,19 +1108,18 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int i = max(0, ks - C::NS); i < ks; ++i) wait_warp_drain(&bars->kv_full[i % C::NS], (i / C::NS) & 1);
     for (int i = max(0, gs - C::NV); i < gs; ++i) wait_warp_drain(&bars->stage_full[i % C::NV], (i / C::NV) & 1);
   } else if (KV8 && warp >= kConvWarp) {
-    // ------------------------------- codes: V's to bf16, 64 rows of a tile per warp
+    // ------------------------------- codes: V's to f16, 64 rows of a tile per warp
     // Written where TMA puts bf16 pages: 64 columns per box, swizzled over 128
     // bytes.  Rows that no row of the item sees become zeros.
-    constexpr int LPR = D / 16;                         // lanes per row, 16 codes each
-    constexpr int RPU = 32 / LPR;                       // rows per load
-    constexpr int UNITS = 16 / RPU;                     // loads of a block
+    // A lane has 16 codes of a row.  Eight lanes' loads and their stores each take
+    // eight different places of 128 bytes: at d = 128 four lanes of row r and four
+    // of row r ^ 5.
+    constexpr int RPU = 512 / D;                        // rows per load
     const int cw = warp - kConvWarp;
-    const int rl = lane / LPR, jj = lane % LPR;
-    // the second box's lanes write their odd half first, so that eight lanes'
-    // stores take eight different places of a line
-    const int odd = jj >> 2, j0 = 2 * (jj & 3) + odd;
-    const uint32_t vhead = smem_u32(smem + C::HEAD_OFF) + C::NH * 128;
-    const uint32_t* const limits = reinterpret_cast<const uint32_t*>(smem + C::HEAD_OFF + (C::NH + C::NV) * 128);
+    const int rl = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    const int jj = D == 128 ? (lane >> 1 & 4) | (lane & 3) : lane & 3, j0 = 2 * (jj & 3);
+    auto row_of = [&](int u) { return D == 128 ? (u >> 1) * 8 + ((u & 1) * 2 ^ rl) : u * RPU + rl; };
+    const uint32_t* const limits = reinterpret_cast<const uint32_t*>(smem + C::HEAD_OFF + C::NH * 128);
     bool ok = true;
     int cs = 0;                                         // steps turned: V of step cs goes to slot cs + 1
     while (ok && next_seg(ok)) {
@@ -1150,29 +1132,31 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (!(ok = wait(&bars->stage_full[st], (cs / C::NV) & 1))) break;
         if (to >= C::NS && !(ok = wait(&bars->kv_empty[sl], ((to / C::NS) - 1) & 1))) break;
         const int lo = (int)limits[4 * st], hi = (int)limits[4 * st + 1];
+        const bool all = lo <= 0 && hi >= 128;
         const uint32_t from = smem_u32(smem + C::STG_OFF) + st * 128 * D;
-        const uint32_t box = smem_u32(smem + C::V_OFF) + sl * C::TILE_BYTES + odd * C::BOX_BYTES;
+        const uint32_t box = smem_u32(smem + C::V_OFF) + sl * C::TILE_BYTES + (jj >> 2) * C::BOX_BYTES;
 #pragma unroll 1
-        for (int b = 4 * cw; b < 4 * cw + 4; ++b) {
-          const uint4 hd = lds128(vhead + st * 128 + b * 16);
-          const uint32_t e = min(hd.x >> hd.z & 0xffu, (uint32_t)kScaleHigh + 127);
-          const uint32_t e1 = min(e, 134u);             // 2^120 2^(e1 - 127) in bf16
-          const uint32_t mul = (e1 + 120) * 0x00800080u, mul2 = e > e1 ? (127 + e - e1) * 0x00800080u : 0;
-          uint4 c[UNITS];
+        for (int r0 = 64 * cw; r0 < 64 * cw + 64; r0 += 16) {
+          uint4 c[16 / RPU];
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u) {
-            const int r = 16 * b + u * RPU + rl;
-            c[u] = lds128(from + r * D + (jj ^ (D == 128 ? r & 7 : r >> 1 & 3)) * 16);
-            if (r < lo || r >= hi) c[u] = make_uint4(0, 0, 0, 0);
+          for (int u = 0; u < 16 / RPU; ++u) {
+            const int r = row_of(u);
+            c[u] = lds128(from + r0 * D + r * D + (jj ^ (D == 128 ? r & 7 : r >> 1 & 3)) * 16);
+          }
+          if (!all) {
+#pragma unroll
+            for (int u = 0; u < 16 / RPU; ++u) {
+              const int r = r0 + row_of(u);
+              if (r < lo || r >= hi) c[u] = make_uint4(0, 0, 0, 0);
+            }
           }
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u) {
-            uint32_t x[8];
-            codes_to_bf16(c[u], mul, mul2, x);
-            const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), z = make_uint4(x[4], x[5], x[6], x[7]);
-            const int r = 16 * b + u * RPU + rl;
-            sts128(box + r * 128 + ((j0 ^ (r & 7)) << 4), odd ? z : a);
-            sts128(box + r * 128 + ((j0 ^ 1 ^ (r & 7)) << 4), odd ? a : z);
+          for (int u = 0; u < 16 / RPU; ++u) {
+            const uint2 x0 = codes_to_f16(c[u].x), x1 = codes_to_f16(c[u].y);
+            const uint2 x2 = codes_to_f16(c[u].z), x3 = codes_to_f16(c[u].w);
+            const uint32_t at = box + r0 * 128 + row_of(u) * 128, sw = row_of(u) & 7;
+            sts128(at + ((j0 ^ sw) << 4), make_uint4(x0.x, x0.y, x1.x, x1.y));
+            sts128(at + ((j0 ^ 1 ^ sw) << 4), make_uint4(x2.x, x2.y, x3.x, x3.y));
           }
         }
         fence_proxy_async_smem();
@@ -1204,8 +1188,9 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       bool valid, dual;
       float slope2 = 0.f;
       int vslot = 0;             // step of this stream's next tile
-      int hs0 = 0;               // codes: that step, whose keys' exponents it is
-      int qup = 0;               // codes: Q's row is times 2^qup
+      int hs0 = 0;               // codes: that step, whose exponents are its keys'
+      float c2q = c2;            // codes: over the power of two that Q's row is times
+      int eref = -127;           // codes: O is over 2^eref
       {
         if (!next_seg(ok)) break;
         const Seg& s = ring[nitem % kSegs];
@@ -1231,7 +1216,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         diag = p.causal ? f : s.L - 1;
         low = f + nt - 1 - p.window;
         if (ALIBI) slope2 = valid ? __ldg(p.alibi + s.g * p.group + r % p.group) * kLog2e : 0.f;
-        if (KV8 && valid) qup = p.q_exps[(long long)(s.tok + (second ? p.tpt : 0) + rq) * p.Hq + s.g * p.group + r % p.group];
+        if (KV8 && valid) c2q = c2 * pow2_of(-p.q_exps[(long long)(s.tok + (second ? p.tpt : 0) + rq) * p.Hq + s.g * p.group + r % p.group]);
         vslot = hs0 = gs + s.k.hi_all - s.ib - kt0;
         gs += s.ie - s.ib;
       }
@@ -1247,14 +1232,26 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           continue;
         }
         tc_fence_after();
-        // Codes: lane i has the exponent of the tile's block i; a score of column c is
-        // S scale 2^(that - qup).  Below 2^-100 a score is 0 beside any other.
-        int kexp = 0;
+        // Codes: lane i has the exponents of the tile's block i, of its keys and, over
+        // the reference, of its values.  A score of column c is S c2q 2^(its keys').
+        // P takes the power of two of its values, so that the products take the
+        // values' codes: O is over 2^eref, the largest so far.
+        float kpow = 1.f, vlog = 0.f, vinv = 1.f;
         if (KV8) {
           const uint4 hd = lds128(smem_u32(smem + C::HEAD_OFF) + ((hs0 + (dual ? 2 : 1) * j) % C::NH) * 128 + (lane & 7) * 16);
-          kexp = exponent_of(hd.x, hd.z);
+          kpow = pow2_of(exponent_of(hd.x, hd.z));
+          const int ev = exponent_of(hd.y, hd.z), top = __reduce_max_sync(0xffffffffu, ev);
+          if (top > eref) {
+            if (j > 0) rescale_row<D>(tO, pow2_cut(eref - top));
+            eref = top;
+          }
+          // 2^-60 and less of a P below 2^10 is 0 in f16
+          const int up = max(ev - eref, -60) + kUpP;
+          vlog = (float)up;
+          vinv = pow2_of(-up);
         }
-        auto c2_of = [&](int c) { return KV8 ? c2 * pow2_cut(max(__shfl_sync(0xffffffffu, kexp, c >> 4) - qup, -100)) : c2; };
+        // (a scale below 2^-100 makes 0 of any score, and must not make NaN of -inf)
+        auto c2_of = [&](int c) { return KV8 ? fmaxf(c2q * __shfl_sync(0xffffffffu, kpow, c >> 4), 7.8886091e-31f) : c2; };
         // The commit that published S_t also covers this stream's last PV, so
         // O may be rescaled now.
         if (!ONE && __any_sync(0xffffffffu, grow > 0.f)) {
@@ -1273,13 +1270,15 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         uint64_t acc[2], accr[2];
         auto exp16 = [&](auto low_part, int c, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
           constexpr bool LOW = decltype(low_part)::value;
-          uint64_t bm = f2(-mb, -mb);
+          const float mv = KV8 ? mb - __shfl_sync(0xffffffffu, vlog, c >> 4) : mb;
+          uint64_t bm = f2(-mv, -mv);
           if (ALIBI) {
-            const float b0 = fmaf(slope2, (float)c, base - mb);
+            const float b0 = fmaf(slope2, (float)c, base - mv);
             bm = f2(b0, b0 + slope2);
           }
           const float c2c = c2_of(c);
           const uint64_t step = f2(2.f * slope2, 2.f * slope2), c2p = f2(c2c, c2c);
+          uint64_t sum[2] = {0, 0};                     // codes: of these 16
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint64_t ex = ffma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2p, bm);
@@ -1289,6 +1288,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const float p0 = ex2_approx(e0);
             const float p1 = ex2_approx(e1);
             const uint64_t pp = f2(p0, p1);
+            if (KV8) {
+              sum[i & 1] = i < 2 ? pp : fadd2(sum[i & 1], pp);
+              hi[i] = pack_f16x2(p0, p1);
+              continue;
+            }
             acc[i & 1] = fadd2(acc[i & 1], pp);
             hi[i] = pack_bf16x2(p0, p1);
             const uint64_t ph = f2(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xFFFF0000u));
@@ -1299,6 +1303,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             } else {
               accr[i & 1] = fadd2(accr[i & 1], ph);
             }
+          }
+          if (KV8) {
+            const float inv = __shfl_sync(0xffffffffu, vinv, c >> 4);
+            acc[0] = ffma2(fadd2(sum[0], sum[1]), f2(inv, inv), acc[0]);
           }
         };
         auto pair_sum = [](const uint64_t* a) {
@@ -1326,12 +1334,12 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             exp16(std::false_type{}, 16 * c, x[c & 1], m_ref, pk + 8 * c, nullptr);
           }
           const float ts = pair_sum(acc);
-          settled = !__any_sync(0xffffffffu, valid && !(ts <= kMaxSum));   // also inf / nan
+          settled = !__any_sync(0xffffffffu, valid && !(ts <= (KV8 ? kMaxSumF16 : kMaxSum)));   // also inf / nan
           if (settled) {
             tmem_st32(tS, pk);
             tmem_st32(tS + 32, pk + 32);
             l += ts;
-            lr += pair_sum(accr);
+            if (!KV8) lr += pair_sum(accr);
             if (valid && ts > kRaiseSum) grow = ceilf(lg2_approx(ts));
           }
         }
@@ -1400,7 +1408,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_ld32(tS + c, x);
             tmem_wait_ld();
             reg_fence32(x);
-            if (ONE || dual) {
+            if (!KV8 && (ONE || dual)) {
               exp16(std::true_type{}, c, x, mb, y, y + 8);
               exp16(std::true_type{}, c + 16, x + 16, mb, y + 16, y + 24);
               tmem_st32(tS + c, y);
@@ -1412,7 +1420,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
           const float ts = pair_sum(acc);
           l += ts;
-          lr += ONE || dual ? ts : pair_sum(accr);
+          if (!KV8) lr += ONE || dual ? ts : pair_sum(accr);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1439,6 +1447,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (part) bars->part_lost[part - 1] = 1;
       }
       const bool use0 = steps > 0, use1 = dual && (steps == 0 || s.ie - s.ib > 1);
+      if (KV8) lr = l;
+      const float opow = pow2_of(eref);                 // codes: O's, but for P's 2^kUpP
       float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
       if (dual) {
@@ -1447,7 +1457,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float* oth = mls + ((t ^ 1) * 128 + r) * 3;
         own[0] = m_ref;
         own[1] = l;
-        own[2] = lr;
+        own[2] = KV8 ? opow : lr;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->joined);
         // Only the time limit ends this wait, not the abort flag: a row's two
@@ -1465,11 +1475,13 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
         w1 = mo == -INFINITY ? 0.f : ex2_approx(mo - M);
         l = fmaf(w0, l, w1 * oth[1]);
-        lr = fmaf(w0, lr, w1 * oth[2]);
+        lr = KV8 ? l : fmaf(w0, lr, w1 * oth[2]);
+        if (KV8) w1 *= oth[2] * (1.f / (1 << kUpP));
         m_ref = M;
         c_from = t * (D / 2);
         c_to = c_from + D / 2;
       }
+      if (KV8) w0 *= opow * (1.f / (1 << kUpP));
       const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
       const int tl = (dual ? 0 : t * p.tpt) + r / p.group;            // token of the item
       const int rh = r % p.group, head = s.g * p.group + rh;

@@ -92,12 +92,6 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // An 8 x 8 matrix of 16-bit elements, transposed: row lane / 4, columns 2 (lane %
 // 4) and the next.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {

@@ -14,8 +14,6 @@
 // to 2^-9 of the row's largest, and what the others lose is at most 2^-10, 2^-17
 // of that one.  Both products go into one accumulator and cost what one in bf16
 // does.  split_rows_kernel makes the parts, bound by HBM: 4 bytes per element.
-#include <cuda_fp16.h>
-
 #include "fa_fwd_paged.cuh"
 
 namespace fa {

@@ -404,23 +404,17 @@ def state(new, lens, page, Hq, Hkv, d, seed, causal=True, window=None, gain=1.0,
 def parts(new, Hq, Hkv):
     """What rounding takes, of each row: of P, relative to it and of each key; of q's elements, relative to the largest.
 
-    Few rows: P in fp16, 2^-11 or its floor; q as it is.  Others: P in one bf16 part
-    or two, of P as above; q, times a power of two that brings its largest element to
-    2^7 at least, as two e4m3 parts.  What the first leaves of an element of 8 bits has
+    P in fp16: 2^-11, or half of fp16's least step, 2^-25, of P times a power of two:
+    2^7 of P up to 1 where rows are few, 2^6 of P whose sum is 1/2 at least for
+    others; a value over the largest power of two is a code, 448 at most.  q: few rows
+    take it as it is; for others it is, times a power of two that brings its largest element to
+    2^7 at least, two e4m3 parts.  What the first leaves of an element of 8 bits has
     4, so the second loses at most half of e4m3's least step, 2^-10, 2^-17 of 2^7.
     """
     G = Hq // Hkv
-    tpt = 128 // G
     most = max(new) * G if max(new) * G <= 32 else G
     few = next((r for r in (8, 16, 24, 32) if most <= r), 0)
-    out = []
-    for n in new:
-        if n * G <= few:
-            out += [(2.0 ** -11, 2.0 ** -32, 0.0)] * n
-            continue
-        for i in range(n):
-            first = i // (2 * tpt) * 2 * tpt
-            out.append((2.0 ** -7 if n - first > tpt else 2.0 ** -15, 0.0, 2.0 ** -17))
+    out = [(2.0 ** -11, 2.0 ** -32, 0.0) if n * G <= few else (2.0 ** -11, 2.0 ** -30, 2.0 ** -17) for n in new for _ in range(n)]
     return np.array(out)
 
 
