@@ -25,6 +25,7 @@
 
 #include <algorithm>
 
+#include "fa_host_util.h"
 #include "fa_internal.h"
 #include "fa_norm_rope.cuh"
 #include "fa_ptx.cuh"
@@ -213,21 +214,19 @@ __device__ __forceinline__ void e4m3x2_floats(uint32_t c, float& a, float& b) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// Largest absolute value so far; what is not finite becomes NaN and counts
-// for nothing.
-__device__ __forceinline__ void take_max(uint64_t& v, float& top) {
-  float a, b;
-  f2split(v, a, b);
-  const bool fa_ = fabsf(a) < INFINITY, fb = fabsf(b) < INFINITY;
-  if (!fa_) a = __int_as_float(0x7fffffff);
-  if (!fb) b = __int_as_float(0x7fffffff);
-  top = fmax3(top, fa_ ? fabsf(a) : 0.f, fb ? fabsf(b) : 0.f);
-  v = f2(a, b);
-}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
-// One head of a block, of the keys or the values.
+// 16 bytes from global to shared memory, asynchronously; zeros without `bytes`.
+__device__ __forceinline__ void copy_async16(uint4* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// One head of a block, of the keys or the values.  `mine`: TURN's 8 KB (4 at d =
+// 64) of shared memory of this warp, 32 bytes per lane and load.
 template <int D, bool TURN, bool INTER>
-__device__ __forceinline__ void write_block(const QuantAppendParams& q, const Block& k, int lane, int h, bool values) {
+__device__ __forceinline__ void write_block(const QuantAppendParams& q, const Block& k, int lane, int h, bool values,
+                                            [[maybe_unused]] uint4* mine) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;                // rows per load
   constexpr int NL = 16 / RPS;                 // loads of a block
@@ -241,60 +240,162 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
     if (lane == 0) record_status(p.status, FA_ERR_POSITION);
     hi = max(p.max_pos - k.p0, 0);
   }
+  const bool turn = TURN && !values;
+  // Values: the rows are in registers.  Keys that are normed and turned: in shared
+  // memory, each lane's own pieces, first as they came and then as floats; so the
+  // work on a row is one loop's body and not one per row, and the kernel's registers
+  // leave room for twice the warps.
   Vec8<__nv_bfloat16> x[NL];
+  if (turn) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int r = i * RPS + sub;
-    if (r >= k.lo && r < hi) x[i].load(src + (r - k.lo) * stride);
-    else x[i].zero();
+    for (int i = 0; i < NL; ++i) {
+      const int r = i * RPS + sub;
+      const bool in = r >= k.lo && r < hi;
+      copy_async16(mine + 64 * i + lane, in ? src + (r - k.lo) * stride : src, in ? 16 : 0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = i * RPS + sub;
+      if (r >= k.lo && r < hi) x[i].load(src + (r - k.lo) * stride);
+      else x[i].zero();
+    }
   }
-  if (page < 0 || page >= p.num_pages) {
-    if (lane == 0) record_status(p.status, FA_ERR_PAGE);
+  if (page < 0 || page >= p.num_pages || k.lo >= hi) {
+    if (turn) copies_wait();
+    if (lane == 0 && (page < 0 || page >= p.num_pages)) record_status(p.status, FA_ERR_PAGE);
     return;
   }
-  if (k.lo >= hi) return;
   const long long row = ((long long)page << p.page_shift) + (k.p0 & (p.page_size - 1));
   uint8_t* scale = (values ? q.v_scales : q.k_scales) + (row >> 4) * p.Hkv + h;
   uint8_t* dst = static_cast<uint8_t*>(values ? p.v_out : p.k_out) + (row * p.Hkv + h) * D + 8 * l;
   const int was = k.lo > 0 ? min(max((int)*scale, kScaleLow + 127), kScaleHigh + 127) - 127 : kScaleLow;
 
-  const bool turn = TURN && !values;
-  const bool on = 8 * l < p.rot;
-  const int ml = mate_lane(p, l);
-  uint64_t z[NL][4];
+  const int first = k.lo / RPS, last = (hi - 1) / RPS;     // loads with a row that is written
   float top = 0.f;
+  uint64_t none = 0;                           // becomes NaN by what is not finite
+  auto take = [&](const uint64_t* z) {
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) z[i][j] = x[i].pair(j);
-    if (turn) {
-      const int r = i * RPS + sub;
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      f2split(z[j], a, b);
+      top = fmax3(top, fabsf(a), fabsf(b));
+      none = ffma2(z[j], 0, none);
+    }
+  };
+  if (turn) {
+    const bool on = 8 * l < p.rot;
+    const int ml = mate_lane(p, l);
+    copies_wait();
+#pragma unroll 2
+    for (int i = first; i <= last; ++i) {
+      Vec8<__nv_bfloat16> y;
+      y.from(mine + 64 * i + lane);
       Angles ang;
-      load_angles(p, k.p0 + min(max(r, k.lo), hi - 1), l, false, ang);
+      load_angles(p, k.p0 + min(max(i * RPS + sub, k.lo), hi - 1), l, false, ang);
       Turn f;
       make_turn<INTER>(ang, p.k_weight, l, ml, f);
-      norm_rope_row<D, INTER>(p, x[i], f, p.k_weight != nullptr, sub * LPR + ml, on, z[i]);
-    }
+      uint64_t z[4];
+      norm_rope_row<D, INTER>(p, y, f, p.k_weight != nullptr, sub * LPR + ml, on, z);
+      take(z);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) take_max(z[i][j], top);
+      for (int j = 0; j < 2; ++j)
+        reinterpret_cast<ulonglong2*>(mine)[64 * i + 32 * j + lane] = make_ulonglong2(z[2 * j], z[2 * j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      uint64_t z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = x[i].pair(j);
+      take(z);
+    }
+  }
+  // A value's floats are made anew each time: kept, they would take twice the registers.
+  auto again = [&] {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+r"(x[i].w[j]));
+  };
+  auto turned = [&](int i, uint64_t* z) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const ulonglong2 v = reinterpret_cast<const ulonglong2*>(mine)[64 * i + 32 * j + lane];
+      z[2 * j] = v.x;
+      z[2 * j + 1] = v.y;
+    }
+  };
+  float na, nb;
+  f2split(none, na, nb);
+  const bool some = __any_sync(0xffffffffu, !(na + nb == 0.f));
+  if (!turn) again();
+  if (some) {                                  // the maximum of the others
+    top = 0.f;
+    auto take_finite = [&](const uint64_t* z) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a, b;
+        f2split(z[j], a, b);
+        top = fmax3(top, finite(a) ? fabsf(a) : 0.f, finite(b) ? fabsf(b) : 0.f);
+      }
+    };
+    if (turn) {
+#pragma unroll 1
+      for (int i = first; i <= last; ++i) {
+        uint64_t z[4];
+        turned(i, z);
+        take_finite(z);
+      }
+    } else {
+#pragma unroll 1
+      for (int n = 0; n < NL; ++n)
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        if (i != n) continue;
+        uint64_t z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = x[i].pair(j);
+        take_finite(z);
+      }
+    }
   }
   const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   // 448 = 1.75 2^8
   int e = (int)(m >> 23) - 127 - 8 + ((m & 0x7fffffu) > 0x600000u);
   e = max(min(max(e, kScaleLow), kScaleHigh), was);
   const float inv = pow2(-e);
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
+  auto put = [&](int i, const uint64_t* z) {
     const int r = i * RPS + sub;
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float a, b;
-      f2split(z[i][j], a, b);
+      f2split(z[j], a, b);
+      if (some) {                              // (e4m3 has no infinity)
+        if (!finite(a)) a = NAN;
+        if (!finite(b)) b = NAN;
+      }
       c[j] = e4m3x2(a * inv, b * inv);
     }
     if (r >= k.lo && r < hi)
       *reinterpret_cast<uint2*>(dst + r * p.Hkv * D) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  };
+  if (turn) {
+#pragma unroll 2
+    for (int i = first; i <= last; ++i) {
+      uint64_t z[4];
+      turned(i, z);
+      put(i, z);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      uint64_t z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = x[i].pair(j);
+      put(i, z);
+    }
   }
   if (k.lo > 0 && e > was) {                   // the older codes under the new scale
     const float down = pow2(max(was - e, -126));
@@ -316,18 +417,22 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
   if (lane == 0) *scale = (uint8_t)(e + 127);
 }
 
-// TURN: with q, norm and rotation; the first q.block_ctas CTAs have the blocks,
-// the others the query heads.
+// TURN: with q, norm and rotation; q.block_ctas CTAs, every q.block_every-th, have
+// the blocks, the others the query heads: those wait for memory where these take
+// all that it gives (8000 tokens of 32 heads on 8: one after the other 49 us,
+// mixed MIX_US).
 template <int D, bool TURN, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const QuantAppendParams q) {
+__global__ void __launch_bounds__(kThreads, TURN ? 3 : 4) append_fp8_kernel(const QuantAppendParams q) {
   const NormRopeParams& p = q.n;
+  extern __shared__ uint4 rows[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (TURN && blockIdx.x >= q.block_ctas) {
+  const unsigned nth = TURN ? blockIdx.x / q.block_every : blockIdx.x;
+  if (TURN && (nth * q.block_every != blockIdx.x || nth >= q.block_ctas)) {
     Unit u;
-    if (unit_at(p, (blockIdx.x - q.block_ctas) * kWarps + warp, u)) query_rows<D, INTER, 4>(p, u, lane);
+    if (unit_at(p, (blockIdx.x - min(nth + 1, q.block_ctas)) * kWarps + warp, u)) query_rows<D, INTER, 4>(p, u, lane);
     return;
   }
-  const unsigned w = blockIdx.x * kWarps + warp;
+  const unsigned w = nth * kWarps + warp;
   const unsigned per = 2 * p.Hkv;              // warps of a block
   const int at = (int)(w / per), rest = (int)(w - at * per);
   if (at >= q.blocks) return;
@@ -343,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const QuantAppe
   }
   Block k;
   if (!block_at(q, at, lane, rest == 0, k)) return;
-  write_block<D, TURN, INTER>(q, k, lane, rest % p.Hkv, rest >= p.Hkv);
+  write_block<D, TURN, INTER>(q, k, lane, rest % p.Hkv, rest >= p.Hkv, rows + warp * (4 * D));
 }
 
 template <int D>
@@ -369,9 +474,13 @@ int launch_d(QuantAppendParams q, bool turn, cudaStream_t stream) {
   if (grid >= (1ll << 31) / kWarps || blocks >= (1ll << 31) / (2 * p.Hkv)) return (int)cudaErrorInvalidConfiguration;
   q.blocks = (int)blocks;
   q.block_ctas = (unsigned)ctas;
+  q.block_every = (unsigned)(grid / ctas);
   auto kern = !turn ? append_fp8_kernel<D, false, false>
                     : p.interleaved ? append_fp8_kernel<D, true, true> : append_fp8_kernel<D, true, false>;
-  kern<<<(unsigned)grid, kThreads, 0, stream>>>(q);
+  const int smem = turn ? kWarps * 64 * D : 0;
+  if (turn)
+    if (const int e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return e;
+  kern<<<(unsigned)grid, kThreads, smem, stream>>>(q);
   return (int)cudaGetLastError();
 }
 
