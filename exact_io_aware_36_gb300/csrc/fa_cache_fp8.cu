@@ -63,6 +63,59 @@ __device__ __forceinline__ void make_turn(const Angles& ang, const float* weight
   }
 }
 
+// The same of many rows, of which each has its own angles: the weights of a lane's
+// elements, and of their partners with the sign of the sine.
+struct Weights {
+  uint64_t a[4], b[4];
+};
+
+template <bool INTER>
+__device__ __forceinline__ void make_weights(const NormRopeParams& p, const float* weight, int l, int mate, Weights& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.a[i] = w.b[i] = f2(1.f, 1.f);
+  if (weight) {
+    load_weights(weight, l, w.a);
+    load_weights(weight, mate, w.b);
+  }
+  const float sg = 8 * l < p.rot / 2 ? -1.f : 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w.b[i] = INTER ? fmul2(swap_pair(w.b[i]), f2(-1.f, 1.f)) : fmul2(w.b[i], f2(sg, sg));
+}
+
+template <bool INTER>
+__device__ __forceinline__ void turn_of(const NormRopeParams& p, int pos, int l, const Weights& w, Turn& f) {
+  if (8 * l >= p.rot) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.wc[i] = w.a[i];
+      f.ws[i] = 0;
+    }
+    return;
+  }
+  const int half = p.rot / 2, at = INTER ? 4 * l : 8 * l < half ? 8 * l : 8 * l - half;
+  const float4* cs = reinterpret_cast<const float4*>(p.cos + (long long)pos * half + at);
+  const float4* sn = reinterpret_cast<const float4*>(p.sin + (long long)pos * half + at);
+  const float4 c = __ldg(cs), s = __ldg(sn);
+  if (INTER) {
+    const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.wc[i] = fmul2(f2(cv[i], cv[i]), w.a[i]);
+      f.ws[i] = fmul2(f2(sv[i], sv[i]), w.b[i]);
+    }
+  } else {
+    const float4 d = __ldg(cs + 1), t = __ldg(sn + 1);
+    f.wc[0] = fmul2(f2(c.x, c.y), w.a[0]);
+    f.wc[1] = fmul2(f2(c.z, c.w), w.a[1]);
+    f.wc[2] = fmul2(f2(d.x, d.y), w.a[2]);
+    f.wc[3] = fmul2(f2(d.z, d.w), w.a[3]);
+    f.ws[0] = fmul2(f2(s.x, s.y), w.b[0]);
+    f.ws[1] = fmul2(f2(s.z, s.w), w.b[1]);
+    f.ws[2] = fmul2(f2(t.x, t.y), w.b[2]);
+    f.ws[3] = fmul2(f2(t.z, t.w), w.b[3]);
+  }
+}
+
 // Warp-collective.
 template <int D, bool INTER>
 __device__ __forceinline__ void norm_rope_row(const NormRopeParams& p, const Vec8<__nv_bfloat16>& x, const Turn& f, bool norm,
@@ -80,12 +133,26 @@ __device__ __forceinline__ void norm_rope_row(const NormRopeParams& p, const Vec
   for (int i = 0; i < 4; ++i) z[i] = fmul2(ffma2(x.pair(i), f.wc[i], fmul2(y.pair(i), f.ws[i])), r2);
 }
 
-// This warp's sets of its token's query heads.
+// This warp's sets of its token's query heads, AHEAD of them at a time while the
+// next are on their way; the first before the token's place is known.
 template <int D, bool INTER, int AHEAD>
 __device__ __forceinline__ void query_rows(const NormRopeParams& p, const Unit& u, int lane) {
   constexpr int LPR = D / 8;
   constexpr int RPS = 32 / LPR;                // rows per set
   const int l = lane & (LPR - 1), sub = lane / LPR;
+  const Heads hd = heads_of<RPS>(u, 0, p.sets_q, sub);
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + u.t * p.q_stride + hd.h * D + 8 * l;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + (u.t * p.Hq + hd.h) * D + 8 * l;
+  const int left = p.Hq - hd.h;                // the lane's heads: every RPS-th
+  Vec8<__nv_bfloat16> x[AHEAD], y[AHEAD];
+  auto fetch = [&](int k, Vec8<__nv_bfloat16>* v) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (k + i < hd.sets && left > (k + i) * RPS) v[i].load(src + (k + i) * RPS * D);
+      else v[i].zero();
+    }
+  };
+  fetch(0, x);
   int pos;
   long long row;
   if (!locate(p, u.t, lane, &pos, &row)) return;
@@ -97,34 +164,24 @@ __device__ __forceinline__ void query_rows(const NormRopeParams& p, const Unit& 
   load_angles(p, pos, l, false, ang);
   const bool on = 8 * l < p.rot;
   const int ml = mate_lane(p, l);
-  const Heads hd = heads_of<RPS>(u, 0, p.sets_q, sub);
   Turn f;
   make_turn<INTER>(ang, p.q_weight, l, ml, f);
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + u.t * p.q_stride + hd.h * D + 8 * l;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + (u.t * p.Hq + hd.h) * D + 8 * l;
-  int left = p.Hq - hd.h;                      // the lane's heads: every RPS-th
   for (int k = 0; k < hd.sets; k += AHEAD) {
-    Vec8<__nv_bfloat16> x[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      if (k + i < hd.sets && left > i * RPS) x[i].load(src + i * RPS * D);
-      else x[i].zero();
-    }
+    fetch(k + AHEAD, y);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (k + i >= hd.sets) break;
       uint64_t z[4];
       norm_rope_row<D, INTER>(p, x[i], f, p.q_weight != nullptr, sub * LPR + ml, on, z);
-      if (left > i * RPS) {
+      if (left > (k + i) * RPS) {
         Vec8<__nv_bfloat16> v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v.set(j, z[j]);
-        v.store(dst + i * RPS * D);
+        v.store(dst + (k + i) * RPS * D);
       }
     }
-    src += AHEAD * RPS * D;
-    dst += AHEAD * RPS * D;
-    left -= AHEAD * RPS;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) x[i] = y[i];
   }
 }
 
@@ -168,21 +225,19 @@ __device__ __forceinline__ bool block_at(const QuantAppendParams& q, int at, int
     j = (int)(at - first);
   }
   if (k.b >= p.B) return false;
-  int c0, n;
+  // (all loads before the first of their checks)
+  const int L = __ldg(p.cache_seqlens + k.b);
+  int c0 = k.b * p.N, n = p.N;
   if (p.cu_seqlens) {
+    const int begin = __ldg(p.cu_seqlens), c1 = __ldg(p.cu_seqlens + k.b + 1);
     c0 = __ldg(p.cu_seqlens + k.b);
-    const int c1 = __ldg(p.cu_seqlens + k.b + 1);
-    if (c0 < 0 || c1 < c0 || (long long)c1 > p.T || c1 - c0 > p.N || __ldg(p.cu_seqlens) != 0) {
+    if (begin != 0 || c0 < 0 || c1 < c0 || (long long)c1 > p.T || c1 - c0 > p.N) {
       if (report && lane == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
       return false;
     }
     n = c1 - c0;
-  } else {
-    c0 = k.b * p.N;
-    n = p.N;
   }
   if (n == 0) return false;
-  const int L = __ldg(p.cache_seqlens + k.b);
   if (L < n || (long long)L > (long long)p.max_pages * p.page_size) {
     if (report && lane == 0) record_status(p.status, FA_ERR_CU_SEQLENS);
     return false;
@@ -222,9 +277,10 @@ __device__ __forceinline__ void copy_async16(uint4* dst, const void* src, uint32
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// One head of a block, of the keys or the values.  `mine`: TURN's 8 KB (4 at d =
-// 64) of shared memory of this warp, 32 bytes per lane and load.
-template <int D, bool TURN, bool INTER>
+// One head of a block, of the keys or the values.  TURN: keys that are normed and
+// turned; `mine`: their 8 KB (4 at d = 64) of shared memory of this warp, 32 bytes
+// per lane and load.
+template <int D, bool TURN, bool INTER, bool ROPE>
 __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Block& k, int lane, int h, bool values,
                                             [[maybe_unused]] uint4* mine) {
   constexpr int LPR = D / 8;
@@ -236,17 +292,15 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
   const long long stride = values ? p.v_stride : p.k_stride;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(values ? p.v : p.k) + k.t0 * stride + h * D + 8 * l;
   int hi = k.hi;
-  if (TURN && p.rot && k.p0 + hi > p.max_pos) {
+  if (ROPE && p.rot && k.p0 + hi > p.max_pos) {
     if (lane == 0) record_status(p.status, FA_ERR_POSITION);
     hi = max(p.max_pos - k.p0, 0);
   }
-  const bool turn = TURN && !values;
-  // Values: the rows are in registers.  Keys that are normed and turned: in shared
-  // memory, each lane's own pieces, first as they came and then as floats; so the
+  // The rows are in registers; those to be normed and turned in shared memory, each lane's own pieces, first as they came and then as floats; so the
   // work on a row is one loop's body and not one per row, and the kernel's registers
   // leave room for twice the warps.
   Vec8<__nv_bfloat16> x[NL];
-  if (turn) {
+  if constexpr (TURN) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int r = i * RPS + sub;
@@ -262,7 +316,7 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
     }
   }
   if (page < 0 || page >= p.num_pages || k.lo >= hi) {
-    if (turn) copies_wait();
+    if (TURN) copies_wait();
     if (lane == 0 && (page < 0 || page >= p.num_pages)) record_status(p.status, FA_ERR_PAGE);
     return;
   }
@@ -273,51 +327,47 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
 
   const int first = k.lo / RPS, last = (hi - 1) / RPS;     // loads with a row that is written
   float top = 0.f;
-  uint64_t none = 0;                           // becomes NaN by what is not finite
-  auto take = [&](const uint64_t* z) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a, b;
-      f2split(z[j], a, b);
-      top = fmax3(top, fabsf(a), fabsf(b));
-      none = ffma2(z[j], 0, none);
-    }
-  };
-  if (turn) {
+  bool some;                                   // something is not finite
+  if constexpr (TURN) {
     const bool on = 8 * l < p.rot;
     const int ml = mate_lane(p, l);
+    Weights w;
+    make_weights<INTER>(p, p.k_weight, l, ml, w);
     copies_wait();
+    uint64_t none = 0;                         // becomes NaN by what is not finite
 #pragma unroll 2
     for (int i = first; i <= last; ++i) {
       Vec8<__nv_bfloat16> y;
       y.from(mine + 64 * i + lane);
-      Angles ang;
-      load_angles(p, k.p0 + min(max(i * RPS + sub, k.lo), hi - 1), l, false, ang);
       Turn f;
-      make_turn<INTER>(ang, p.k_weight, l, ml, f);
+      turn_of<INTER>(p, k.p0 + min(max(i * RPS + sub, k.lo), hi - 1), l, w, f);
       uint64_t z[4];
       norm_rope_row<D, INTER>(p, y, f, p.k_weight != nullptr, sub * LPR + ml, on, z);
-      take(z);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a, b;
+        f2split(z[j], a, b);
+        top = fmax3(top, fabsf(a), fabsf(b));
+        none = ffma2(z[j], 0, none);
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         reinterpret_cast<ulonglong2*>(mine)[64 * i + 32 * j + lane] = make_ulonglong2(z[2 * j], z[2 * j + 1]);
     }
+    float na, nb;
+    f2split(none, na, nb);
+    some = !(na + nb == 0.f);
   } else {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      uint64_t z[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = x[i].pair(j);
-      take(z);
-    }
-  }
-  // A value's floats are made anew each time: kept, they would take twice the registers.
-  auto again = [&] {
+    // absolute values of bf16 are in the order of their bits
+    uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < NL; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+r"(x[i].w[j]));
-  };
+      for (int j = 0; j < 4; ++j) most = __vmaxu2(most, x[i].w[j] & 0x7fff7fffu);
+    most = max(most >> 16, most & 0xffffu);
+    top = __uint_as_float(most << 16);
+    some = most >= 0x7f80u;
+  }
   auto turned = [&](int i, uint64_t* z) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -326,38 +376,32 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
       z[2 * j + 1] = v.y;
     }
   };
-  float na, nb;
-  f2split(none, na, nb);
-  const bool some = __any_sync(0xffffffffu, !(na + nb == 0.f));
-  if (!turn) again();
-  if (some) {                                  // the maximum of the others
+  if (__any_sync(0xffffffffu, some)) {         // the maximum of the others; these become NaN (e4m3 has no infinity)
     top = 0.f;
-    auto take_finite = [&](const uint64_t* z) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float a, b;
-        f2split(z[j], a, b);
-        top = fmax3(top, finite(a) ? fabsf(a) : 0.f, finite(b) ? fabsf(b) : 0.f);
-      }
-    };
-    if (turn) {
+    if constexpr (TURN) {
 #pragma unroll 1
-      for (int i = first; i <= last; ++i) {
-        uint64_t z[4];
-        turned(i, z);
-        take_finite(z);
+      for (int n = 64 * first; n < 64 * (last + 1); n += 32) {
+        float4 z = reinterpret_cast<const float4*>(mine)[n + lane];
+        float* v = &z.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (finite(v[j])) top = fmaxf(top, fabsf(v[j]));
+          else v[j] = NAN;
+        }
+        reinterpret_cast<float4*>(mine)[n + lane] = z;
       }
     } else {
-#pragma unroll 1
-      for (int n = 0; n < NL; ++n)
+      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        if (i != n) continue;
-        uint64_t z[4];
+      for (int i = 0; i < NL; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = x[i].pair(j);
-        take_finite(z);
-      }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = x[i].w[j] & 0x7fff7fffu;
+          const uint32_t odd = __vcmpgeu2(a, 0x7f807f80u);
+          most = __vmaxu2(most, a & ~odd);
+          x[i].w[j] |= odd & 0x7fff7fffu;
+        }
+      top = __uint_as_float(max(most >> 16, most & 0xffffu) << 16);
     }
   }
   const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
@@ -371,17 +415,13 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float a, b;
-      f2split(z[j], a, b);
-      if (some) {                              // (e4m3 has no infinity)
-        if (!finite(a)) a = NAN;
-        if (!finite(b)) b = NAN;
-      }
-      c[j] = e4m3x2(a * inv, b * inv);
+      f2split(fmul2(z[j], f2(inv, inv)), a, b);
+      c[j] = e4m3x2(a, b);
     }
     if (r >= k.lo && r < hi)
       *reinterpret_cast<uint2*>(dst + r * p.Hkv * D) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
   };
-  if (turn) {
+  if constexpr (TURN) {
 #pragma unroll 2
     for (int i = first; i <= last; ++i) {
       uint64_t z[4];
@@ -417,22 +457,19 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
   if (lane == 0) *scale = (uint8_t)(e + 127);
 }
 
-// TURN: with q, norm and rotation; q.block_ctas CTAs, every q.block_every-th, have
-// the blocks, the others the query heads: those wait for memory where these take
-// all that it gives (8000 tokens of 32 heads on 8: one after the other 49 us,
-// mixed MIX_US).
+// TURN: with q, norm and rotation; the first q.block_ctas CTAs have the blocks,
+// the others the query heads.
 template <int D, bool TURN, bool INTER>
 __global__ void __launch_bounds__(kThreads, TURN ? 3 : 4) append_fp8_kernel(const QuantAppendParams q) {
   const NormRopeParams& p = q.n;
   extern __shared__ uint4 rows[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned nth = TURN ? blockIdx.x / q.block_every : blockIdx.x;
-  if (TURN && (nth * q.block_every != blockIdx.x || nth >= q.block_ctas)) {
+  if (TURN && blockIdx.x >= q.block_ctas) {
     Unit u;
-    if (unit_at(p, (blockIdx.x - min(nth + 1, q.block_ctas)) * kWarps + warp, u)) query_rows<D, INTER, 4>(p, u, lane);
+    if (unit_at(p, (blockIdx.x - q.block_ctas) * kWarps + warp, u)) query_rows<D, INTER, 4>(p, u, lane);
     return;
   }
-  const unsigned w = nth * kWarps + warp;
+  const unsigned w = blockIdx.x * kWarps + warp;
   const unsigned per = 2 * p.Hkv;              // warps of a block
   const int at = (int)(w / per), rest = (int)(w - at * per);
   if (at >= q.blocks) return;
@@ -448,7 +485,9 @@ __global__ void __launch_bounds__(kThreads, TURN ? 3 : 4) append_fp8_kernel(cons
   }
   Block k;
   if (!block_at(q, at, lane, rest == 0, k)) return;
-  write_block<D, TURN, INTER>(q, k, lane, rest % p.Hkv, rest >= p.Hkv, rows + warp * (4 * D));
+  const int h = rest < p.Hkv ? rest : rest - p.Hkv;
+  if (TURN && rest < p.Hkv) write_block<D, TURN, INTER, TURN>(q, k, lane, h, false, rows + warp * (4 * D));
+  else write_block<D, false, false, TURN>(q, k, lane, h, rest >= p.Hkv, nullptr);
 }
 
 template <int D>
@@ -474,7 +513,6 @@ int launch_d(QuantAppendParams q, bool turn, cudaStream_t stream) {
   if (grid >= (1ll << 31) / kWarps || blocks >= (1ll << 31) / (2 * p.Hkv)) return (int)cudaErrorInvalidConfiguration;
   q.blocks = (int)blocks;
   q.block_ctas = (unsigned)ctas;
-  q.block_every = (unsigned)(grid / ctas);
   auto kern = !turn ? append_fp8_kernel<D, false, false>
                     : p.interleaved ? append_fp8_kernel<D, true, true> : append_fp8_kernel<D, true, false>;
   const int smem = turn ? kWarps * 64 * D : 0;

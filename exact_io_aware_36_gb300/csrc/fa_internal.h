@@ -161,7 +161,7 @@ struct QuantAppendParams {
   uint8_t* k_scales;           // [num_pages, page_size / 16, Hkv]: exponent + 127
   uint8_t* v_scales;
   int per_seq, blocks;         // block numbers per sequence (0: by place in cu_seqlens), and of all
-  unsigned block_ctas, block_every;   // CTAs that have blocks, every how manieth of all
+  unsigned block_ctas;
 };
 
 // Exponents that a scale of a cache in 8 bits takes.  Below the least, a
