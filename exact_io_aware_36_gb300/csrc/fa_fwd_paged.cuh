@@ -1543,17 +1543,17 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
 // following ones, in their order; an item of which a CTA has no part to show
-// is left alone.  One warp per row, D / 32 columns per lane;
+// is left alone.  A warp has RPW rows, D / 32 columns per lane;
 // four parts' loads at a time, so that a row costs two waits for memory: what
 // the parts are, and the parts.
-template <int D>
-__device__ __forceinline__ void merge_parts(const PagedParams& p, const int nctas) {
+template <int D, int RPW>
+__device__ __forceinline__ void merge_parts(const PagedParams& p, const int nctas, const int y) {
   const int c = blockIdx.x;
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int row0 = y * 8 * RPW + (threadIdx.x >> 5);
   const int4 it = p.part_meta[2 * c + 1];
   int kind = c + 1 + lane < nctas ? p.part_meta[2 * (c + 1 + lane)].x : 0;
-  if (it.x == 0 || row >= it.z * p.group) return;
+  if (it.x == 0 || row0 >= it.z * p.group) return;
   // parts: slot 2 c + 1, then slot 2 c' of c' = c + 1 .. until an end (kind 2)
   int nparts = 1;
   for (int c0 = c + 1;; c0 += 32) {
@@ -1569,68 +1569,79 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
   }
   constexpr int PER = D / 32;
   struct alignas(4 * PER) Cols { float v[PER]; };
-  Cols o;
+#pragma unroll 1
+  for (int i = 0; i < RPW; ++i) {
+    const int row = row0 + 8 * i;
+    if (i > 0 && row >= it.z * p.group) break;
+    Cols o;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o.v[i] = 0.f;
-  float M = -INFINITY, l = 0.f, lr = 0.f;
-  for (int s0 = 0; s0 < nparts; s0 += 4) {
-    float4 ml[4];
-    Cols x[4];
+    for (int i = 0; i < PER; ++i) o.v[i] = 0.f;
+    float M = -INFINITY, l = 0.f, lr = 0.f;
+    for (int s0 = 0; s0 < nparts; s0 += 4) {
+      float4 ml[4];
+      Cols x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = min(s0 + i, nparts - 1);
-      const long long at = (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row;
-      ml[i] = *reinterpret_cast<const float4*>(p.part_ml + at * 4);
-      x[i] = *reinterpret_cast<const Cols*>(p.part_o + at * D + lane * PER);
+      for (int i = 0; i < 4; ++i) {
+        const int s = min(s0 + i, nparts - 1);
+        const long long at = (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row;
+        ml[i] = *reinterpret_cast<const float4*>(p.part_ml + at * 4);
+        x[i] = *reinterpret_cast<const Cols*>(p.part_o + at * D + lane * PER);
+      }
+      float mx = M;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s0 + i < nparts) mx = fmaxf(mx, ml[i].x);
+      const float a = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+      l *= a;
+      lr *= a;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) o.v[k] *= a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // no key seen there, or (l not 0) a score that is not a number
+        if (s0 + i >= nparts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
+        const float w = ex2_approx(ml[i].x - mx);
+        l = fmaf(w, ml[i].y, l);
+        lr = fmaf(w, ml[i].z, lr);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x[i].v[k], o.v[k]);
+      }
+      M = mx;
     }
-    float mx = M;
+    const float inv = lr > 0.f ? 1.f / lr : 0.f;
+    const long long tok = it.y + row / p.group;
+    const int h = it.w * p.group + row % p.group;
+    const long long at = (tok * p.Hq + h) * D + lane * PER;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (s0 + i < nparts) mx = fmaxf(mx, ml[i].x);
-    const float a = M == -INFINITY ? 0.f : ex2_approx(M - mx);
-    l *= a;
-    lr *= a;
+    for (int k = 0; k < PER; ++k) o.v[k] *= inv;
+    if (p.o_f32) {
+      *reinterpret_cast<Cols*>(static_cast<float*>(p.o) + at) = o;
+    } else {
 #pragma unroll
-    for (int k = 0; k < PER; ++k) o.v[k] *= a;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // no key seen there, or (l not 0) a score that is not a number
-      if (s0 + i >= nparts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
-      const float w = ex2_approx(ml[i].x - mx);
-      l = fmaf(w, ml[i].y, l);
-      lr = fmaf(w, ml[i].z, lr);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x[i].v[k], o.v[k]);
+      for (int k = 0; k < PER; k += 2)
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at + k) = pack_bf16x2(o.v[k], o.v[k + 1]);
     }
-    M = mx;
+    if (lane == 0) p.lse[(long long)h * p.T + tok] = l == 0.f ? -INFINITY : (M + lg2_approx(l)) * kLn2;
   }
-  const float inv = lr > 0.f ? 1.f / lr : 0.f;
-  const long long tok = it.y + row / p.group;
-  const int h = it.w * p.group + row % p.group;
-  const long long at = (tok * p.Hq + h) * D + lane * PER;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) o.v[k] *= inv;
-  if (p.o_f32) {
-    *reinterpret_cast<Cols*>(static_cast<float*>(p.o) + at) = o;
-  } else {
-#pragma unroll
-    for (int k = 0; k < PER; k += 2)
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at + k) = pack_bf16x2(o.v[k], o.v[k + 1]);
-  }
-  if (lane == 0) p.lse[(long long)h * p.T + tok] = l == 0.f ? -INFINITY : (M + lg2_approx(l)) * kLn2;
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
   grid_dependency_wait();
-  merge_parts<D>(p, nctas);
+  merge_parts<D, 1>(p, nctas, blockIdx.y);
 }
 
-// Those of the two kernels of a call over codes.
+// Those of the two kernels of a call over codes: `ym` rows of blocks for those of
+// `many`, of whose up to 256 rows an item a warp takes four (a block costs more than
+// its rows: two kernels' parts of a mixed batch 18.8 us with one row per warp, MERGE_US
+// with four), the others for those of `few`.
 template <int D>
-__global__ void __launch_bounds__(256) paged_merge_two_kernel(const PagedParams p, const PagedParams q, const int nctas) {
+__global__ void __launch_bounds__(256)
+paged_merge_two_kernel(const PagedParams few, const PagedParams many, const int ym, const int nctas) {
   grid_dependency_wait();
-  merge_parts<D>(blockIdx.z ? q : p, nctas);
+  const int y = blockIdx.y;
+  if (y < ym) merge_parts<D, 4>(many, nctas, y);
+  else merge_parts<D, 1>(few, nctas, y - ym);
 }
 
 // Codes: begins while the kernel that makes q's parts runs; the merge is the

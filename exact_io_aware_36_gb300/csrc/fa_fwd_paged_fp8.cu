@@ -69,8 +69,7 @@ int launch_two(const PagedParams& few, const PagedParams& many, cudaStream_t str
   int nsm = 0;
   if (const int e = sm_count(&nsm)) return e;
   const int grid = std::min(nsm, kPagedCtas);
-  const int rows = std::max(1, std::max(few.B ? few.part_rows : 0, many.B ? many.part_rows : 0));
-  const dim3 merge(grid, (rows + 7) / 8, few.B && many.B ? 2 : 1);
+  const int ym = many.B ? (many.part_rows + 31) / 32 : 0, yf = few.B ? std::max(1, (few.part_rows + 7) / 8) : 0;
   if (many.B) {
     const long long blocks = (many.T * many.Hq * (D / 8) + 255) / 256;
     if (blocks >= (1ll << 31)) return (int)cudaErrorInvalidConfiguration;
@@ -80,8 +79,7 @@ int launch_two(const PagedParams& few, const PagedParams& many, cudaStream_t str
   }
   if (few.B)
     if (const int e = launch_fwd_paged_few(few, grid, many.B != 0, stream)) return e;
-  if (few.B && many.B) return launch_dependent(paged_merge_two_kernel<D>, merge, dim3(256), 0, stream, few, many, grid);
-  return launch_dependent(paged_merge_kernel<D>, merge, dim3(256), 0, stream, few.B ? few : many, grid);
+  return launch_dependent(paged_merge_two_kernel<D>, dim3(grid, ym + yf), dim3(256), 0, stream, few, many, ym, grid);
 }
 
 }  // namespace
