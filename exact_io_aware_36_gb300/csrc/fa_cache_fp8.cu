@@ -125,7 +125,12 @@ __device__ __forceinline__ void norm_rope_row(const NormRopeParams& p, const Vec
     uint64_t ss = fmul2(x.pair(0), x.pair(0));
 #pragma unroll
     for (int i = 1; i < 4; ++i) ss = ffma2(x.pair(i), x.pair(i), ss);
-    r = rsqrtf(row_sum<D / 8>(pair_sum(ss)) * (1.f / D) + p.eps);
+    const float v = row_sum<D / 8>(pair_sum(ss)) * (1.f / D) + p.eps;
+    r = rsqrtf(v);
+    // one step of Newton's method: a code next to its rounding's border shows the
+    // last bit of r
+    const float off = fmaf(-v * r, r, 1.f);
+    if (fabsf(off) < 1.f) r = fmaf(0.5f * r, off, r);
   }
   const uint64_t r2 = f2(r, r);
   const Partners<__nv_bfloat16, INTER> y(p, x, src_lane, on);

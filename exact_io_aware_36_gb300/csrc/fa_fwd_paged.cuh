@@ -1268,15 +1268,21 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // p = 2^(x - mb) of 16 scores from column c on: 8 packed pairs, and
         // with LOW what the rounding left of them; sums of p, of the rounded p
         uint64_t acc[2], accr[2];
-        auto exp16 = [&](auto low_part, int c, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
+        // (codes: what their block takes, asked for ahead of them)
+        struct Of16 { float c2, vlog, vinv; };
+        auto of16 = [&](int c) -> Of16 {
+          if (!KV8) return {c2, 0.f, 1.f};
+          return {c2_of(c), __shfl_sync(0xffffffffu, vlog, c >> 4), __shfl_sync(0xffffffffu, vinv, c >> 4)};
+        };
+        auto exp16 = [&](auto low_part, int c, const Of16& of, const uint32_t* x, float mb, uint32_t* hi, uint32_t* lo) {
           constexpr bool LOW = decltype(low_part)::value;
-          const float mv = KV8 ? mb - __shfl_sync(0xffffffffu, vlog, c >> 4) : mb;
+          const float mv = KV8 ? mb - of.vlog : mb;
           uint64_t bm = f2(-mv, -mv);
           if (ALIBI) {
             const float b0 = fmaf(slope2, (float)c, base - mv);
             bm = f2(b0, b0 + slope2);
           }
-          const float c2c = c2_of(c);
+          const float c2c = of.c2;
           const uint64_t step = f2(2.f * slope2, 2.f * slope2), c2p = f2(c2c, c2c);
           uint64_t sum[2] = {0, 0};                     // codes: of these 16
 #pragma unroll
@@ -1304,10 +1310,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               accr[i & 1] = fadd2(accr[i & 1], ph);
             }
           }
-          if (KV8) {
-            const float inv = __shfl_sync(0xffffffffu, vinv, c >> 4);
-            acc[0] = ffma2(fadd2(sum[0], sum[1]), f2(inv, inv), acc[0]);
-          }
+          if (KV8) acc[0] = ffma2(fadd2(sum[0], sum[1]), f2(of.vinv, of.vinv), acc[0]);
         };
         auto pair_sum = [](const uint64_t* a) {
           float x, y;
@@ -1328,10 +1331,11 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           tmem_ld16(tS, x[0]);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
+            const Of16 of = of16(16 * c);
             tmem_wait_ld();
             reg_fence16(x[c & 1]);
             if (c < 7) tmem_ld16(tS + 16 * (c + 1), x[(c + 1) & 1]);
-            exp16(std::false_type{}, 16 * c, x[c & 1], m_ref, pk + 8 * c, nullptr);
+            exp16(std::false_type{}, 16 * c, of, x[c & 1], m_ref, pk + 8 * c, nullptr);
           }
           const float ts = pair_sum(acc);
           settled = !__any_sync(0xffffffffu, valid && !(ts <= (KV8 ? kMaxSumF16 : kMaxSum)));   // also inf / nan
@@ -1353,6 +1357,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int c = 0; c < 128; c += 32) {
             uint32_t x[32];
             tmem_ld32(tS + c, x);
+            const float ca = c2_of(c), cb = c2_of(c + 16);
             tmem_wait_ld();
             reg_fence32(x);
             if (masked) {
@@ -1365,7 +1370,6 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                   if (c + i < lb) x[i] = __float_as_uint(-INFINITY);
               tmem_st32(tS + c, x);
             }
-            const float ca = c2_of(c), cb = c2_of(c + 16);
             float m4[4] = {KV8 ? -INFINITY : mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -1406,15 +1410,16 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int c = 0; c < 128; c += 32) {
             uint32_t x[32], y[32];
             tmem_ld32(tS + c, x);
+            const Of16 of0 = of16(c), of1 = of16(c + 16);
             tmem_wait_ld();
             reg_fence32(x);
             if (!KV8 && (ONE || dual)) {
-              exp16(std::true_type{}, c, x, mb, y, y + 8);
-              exp16(std::true_type{}, c + 16, x + 16, mb, y + 16, y + 24);
+              exp16(std::true_type{}, c, of0, x, mb, y, y + 8);
+              exp16(std::true_type{}, c + 16, of1, x + 16, mb, y + 16, y + 24);
               tmem_st32(tS + c, y);
             } else {
-              exp16(std::false_type{}, c, x, mb, y, nullptr);
-              exp16(std::false_type{}, c + 16, x + 16, mb, y + 8, nullptr);
+              exp16(std::false_type{}, c, of0, x, mb, y, nullptr);
+              exp16(std::false_type{}, c + 16, of1, x + 16, mb, y + 8, nullptr);
               tmem_st16(tS + c / 2, y);
             }
           }
