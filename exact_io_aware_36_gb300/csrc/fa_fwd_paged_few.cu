@@ -134,6 +134,9 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       mbar_init(&bars->seg_full[i], 1);
       mbar_init(&bars->seg_empty[i], W + 1);           // all but the warp that finds them
     }
+#ifdef FA_PAGED_STOP
+    mbar_init(&bars->never, 1);
+#endif
     bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -148,6 +151,13 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_warp_inl(bar, parity, wc); };
   // The run's items: segs[n % kSegs] is item n (ie < 0: the end).
   Seg* segs = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
+  auto wait_seg = [&](int n) -> bool {
+#ifdef FA_PAGED_STOP
+    if (warp == g_stop[0] && (int)blockIdx.x == g_stop[1] && n == g_stop[2])
+      return wait_warp(&bars->never, 0, WaitCtx{&bars->abort_flag, p.status, kStopLimitNs});
+#endif
+    return wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1);
+  };
   auto first_step = [](const Seg& s) { return max((s.k.hi_all - s.ie + 1) * 4, s.k.vlo >> 5); };
   auto end_step = [](const Seg& s) { return min((s.k.hi_all - s.ib + 1) * 4, (s.k.vhi + 31) >> 5); };
 
@@ -198,7 +208,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     }
     for (int n = 0; ok; ++n) {
       if (values) {
-        if (!(ok = wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1))) break;
+        if (!(ok = wait_seg(n))) break;
         s = segs[n % kSegs];
         more = s.ie >= 0;
       }
@@ -343,8 +353,8 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   };
   // Items n and n + 1 are known; the same answer for every warp.
   auto known = [&](int n) {
-    bool ok = wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1);
-    if (ok && segs[n % kSegs].ie >= 0) ok = wait(&bars->seg_full[(n + 1) % kSegs], ((n + 1) / kSegs) & 1);
+    bool ok = wait_seg(n);
+    if (ok && segs[n % kSegs].ie >= 0) ok = wait_seg(n + 1);
     return !named_bar_any(1, 32 * W, !ok);
   };
   bool go = known(0) && segs[0].ie >= 0;
@@ -757,6 +767,13 @@ int launch_few(const PagedParams& p, int grid, bool after, cudaStream_t stream) 
 }
 
 }  // namespace
+
+#ifdef FA_PAGED_STOP
+extern "C" int fa_selftest_paged_few_stop(int warp, int cta, int item) {
+  const int at[3] = {warp, cta, item};
+  return (int)cudaMemcpyToSymbol(g_stop, at, sizeof(at));
+}
+#endif
 
 int launch_fwd_paged_few(PagedParams p, int grid, bool after, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);

@@ -84,6 +84,13 @@ int launch_two(const PagedParams& few, const PagedParams& many, cudaStream_t str
 
 }  // namespace
 
+#ifdef FA_PAGED_STOP
+extern "C" int fa_selftest_paged_fp8_stop(int warp, int cta, int item) {
+  const int at[3] = {warp, cta, item};
+  return (int)cudaMemcpyToSymbol(g_stop, at, sizeof(at));
+}
+#endif
+
 int launch_fwd_paged_fp8(const PagedParams& few, const PagedParams& many, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return (few.B ? few.d : many.d) == 128 ? launch_two<128>(few, many, stream) : launch_two<64>(few, many, stream);
