@@ -103,6 +103,7 @@ constexpr int kLoadWarp = 8;           // codes: also the walker
 constexpr int kWalkWarp = 10;          // bf16 pages alone
 constexpr int kConvWarp = 10;          // codes alone: the first of kConvWarps
 constexpr int kConvWarps = 2;
+constexpr int kBarBytes = 576;         // barriers and what the plan finds
 constexpr int kSegs = 4;               // items that the walker may be ahead
 constexpr float kTau = 8.0f;           // lazy rescale: raise m beyond this (log2 units)
 constexpr float kRaiseSum = 256.0f;    // 2^kTau
@@ -141,7 +142,7 @@ struct Cfg {
   static constexpr int SEG_OFF = ML_OFF + 2 * 128 * 3 * 4;          // ring of items
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;              // a copy of the parameters
   static constexpr int BAR_OFF = PAR_OFF + 256;
-  static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
+  static constexpr int SMEM_BYTES = BAR_OFF + kBarBytes + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   // the work plan's prefix sums borrow the K/V slots before the first load
   static_assert(kPagedMaxBatch * 8 <= NS * (K_SLOT + TILE_BYTES), "plan");
@@ -156,6 +157,7 @@ struct Bars {
   uint64_t o_done, o_free, drain;
   uint64_t joined;              // (m, l, l~) of both streams' rows of a one-tile item are there
   uint64_t stage_full[4], stage_empty[4];   // codes: V's on their way
+  uint64_t p_half[2], half_done[2];         // codes, two tiles: P of 64 keys, its product
 #ifdef FA_PAGED_STOP
   uint64_t never;               // nothing arrives on it
 #endif
@@ -168,7 +170,7 @@ struct Bars {
   long long w0, w1, base;
   int b, g, qb;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 #ifdef FA_PAGED_STOP
 // Test build: the wait of warp g_stop[0] of CTA g_stop[1] for its item number
@@ -523,6 +525,21 @@ __device__ __forceinline__ int exponent_of(uint32_t word, uint32_t shift) {
   return (int)min(word >> shift & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
 }
 
+// wait_warp_slow of one thread.
+static __device__ __noinline__ bool wait_thread_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status,
+                                                     unsigned long long limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      record_status(status, FA_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // 2^e for e from -127 to 127.
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float(e > -127 ? (e + 127) << 23 : 0x00400000); }
 
@@ -551,6 +568,8 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
       mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->p_half[t], 4);
+      mbar_init(&bars->half_done[t], 1);
     }
     for (int s = 0; s < C::NS; ++s) {
       // codes: K, the exponents, V in f16
@@ -735,7 +754,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int gs = 0, nseg = 0;
     unsigned q_par = 0;          // bit x: parity of Q buffer x's next load
     int qsel = 0, flip = 0;
-    unsigned p_par = 0;          // bit t: parity of stream t's next p_full
+    unsigned p_par = 0, h_par = 0;   // bit t: parity of stream t's next p_full, p_half
     // The step before, whose PV products are due: streams (bit t), those
     // that begin an item there (bit t), whether its item is a one-tile one,
     // whether it ends its item, and the V rows [vlo, vhi) that are visible.
@@ -750,7 +769,32 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       __syncwarp();
     };
+    // Codes, two tiles: products of the keys' half h.
+    auto pv_half = [&](int t, int h, int sl, uint32_t accumulate) {
+      const uint64_t vd = desc_add(vdesc0, sl * C::TILE_BYTES + h * 4 * 2048);
+      const uint32_t colP = tmem + (t ? C::S_COL1 : C::S_COL0) + h * 32, colO = tmem + (t ? C::O_COL1 : C::O_COL0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_ts(colO, colP + kk * 8, desc_add(vd, kk * 2048), IDESC_O, kk > 0 ? 1u : accumulate);
+    };
     auto issue_pv = [&](int t, int sl) -> bool {
+      if (KV8 && !ONE && !pv_dual) {
+        if (!wait(&bars->p_half[t], h_par >> t & 1)) return false;
+        h_par ^= 1u << t;
+        const bool first = (pv_first >> t) & 1;
+        if (first && nseg > 0 && !wait(&bars->o_free, (nseg - 1) & 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          pv_half(t, 0, sl, !first);
+          mma_commit(&bars->half_done[t]);
+        }
+        __syncwarp();
+        if (!wait(&bars->p_full[t], p_par >> t & 1)) return false;
+        p_par ^= 1u << t;
+        tc_fence_after();
+        if (lane == 0) pv_half(t, 1, sl, 1u);
+        __syncwarp();
+        return true;
+      }
       if (!wait(&bars->p_full[t], p_par >> t & 1)) return false;
       p_par ^= 1u << t;
       // the first PV_t of an item overwrites O_t, which the item before
@@ -813,6 +857,42 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // filled.  P1 is asked for while the last products of the first batch
           // run.
           const uint64_t kd = desc_add(kdesc0, sl * C::K_SLOT), vd = desc_add(vdesc0, sl * C::TILE_BYTES);
+          if constexpr (KV8) {
+            // Four parts: each stream's P of 64 keys, then of the others and S.  The next
+            // part's P is asked for before the last products of one.  One lane does it
+            // all, straight on, so that the descriptors are constants but for the slot.
+            auto ready_bar = [&](int k) { return k & 1 ? &bars->p_full[k >> 1] : &bars->p_half[k >> 1]; };
+            auto ready_par = [&](int k) { return (k & 1 ? p_par : h_par) >> (k >> 1) & 1; };
+            if (lane == 0) {
+              bool there = mbar_try_wait(ready_bar(0), ready_par(0));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int t = k >> 1;
+                if (!there && !(ok = wait_thread_slow(ready_bar(k), ready_par(k), wc.abort_flag, wc.status, wc.limit_ns))) break;
+                tc_fence_after();
+                pv_half(t, k & 1, sl, 1u);
+                if (k & 1) {
+                  const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0);
+#pragma unroll
+                  for (int kk = 0; kk < D / 16; ++kk) {
+                    if (k < 3 && kk == D / 16 - 2) there = mbar_try_wait(ready_bar(k + 1), ready_par(k + 1));
+                    s_product(colS, desc_add(qdesc0, t * C::TILE_BYTES), kd, kk);
+                  }
+                  mma_commit(&bars->s_full[t]);
+                  if (t) mma_commit(&bars->kv_empty[sl]);
+                } else {
+                  mma_commit(&bars->half_done[t]);
+                  there = mbar_try_wait(ready_bar(k + 1), ready_par(k + 1));
+                }
+              }
+            }
+            if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0))) break;
+            p_par ^= 3u;
+            h_par ^= 3u;
+            v_lo = vlo - kt * 128;
+            v_hi = vhi - kt * 128;
+            continue;
+          }
           auto batch = [&](int t, bool ask) -> bool {
             const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0), colO = tmem + (t ? C::O_COL1 : C::O_COL0);
             bool there = false;
@@ -1181,6 +1261,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int nseg = 0, flip = 0;
     int gs = 0;                  // steps before this item
     int njoin = 0;               // one-tile items before this one
+    int nhalf = 0;               // codes: tiles whose P went in halves
     // A warp whose wait ran out leaves; the others' waits for it run out or
     // see the abort flag.
     while (true) {
@@ -1227,8 +1308,14 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float grow = 0.f;  // log2 by which the reference is to rise before the next tile
       for (int j = 0; ok && j < steps; ++j, ++cs, n0 -= dual ? 256 : 128) {
         if (!(ok = wait(&bars->s_full[t], cs & 1))) break;
+        // Codes, two tiles: P of the first 64 keys is given away before the others'.
+        const bool halves = KV8 && !ONE && !dual;
         if (!warp_rows) {                               // no row of this warp holds a token
-          if (lane == 0) mbar_arrive(&bars->p_full[t]);
+          if (lane == 0) {
+            if (halves) mbar_arrive(&bars->p_half[t]);
+            mbar_arrive(&bars->p_full[t]);
+          }
+          nhalf += halves;
           continue;
         }
         tc_fence_after();
@@ -1317,7 +1404,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           f2split(fadd2(a[0], a[1]), x, y);
           return x + y;
         };
-        bool settled = false;
+        bool settled = false, given = false;            // given: P of the first 64 keys
         // Tiles on the diagonal, at the end or at the band's lower edge hold
         // scores of keys that a row does not see.
         const bool masked = n0 + 127 > diag || n0 < low;
@@ -1326,25 +1413,71 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // shows that it may stand.  P and O are floats, so a reference that
           // is too low costs no precision: a sum up to 2^40 stands, and one
           // above 2^8 raises the reference for the next tile.
-          uint32_t pk[64], x[2][16];
-          acc[0] = acc[1] = accr[0] = accr[1] = 0;
-          tmem_ld16(tS, x[0]);
+if constexpr (KV8) {
+            // The same for 64 keys and then for the others.
+            uint32_t pk[32], x[2][16];
+            auto half = [&](int h) -> float {
+              acc[0] = acc[1] = 0;
+              tmem_ld16(tS + 64 * h, x[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const Of16 of = of16(16 * c);
-            tmem_wait_ld();
-            reg_fence16(x[c & 1]);
-            if (c < 7) tmem_ld16(tS + 16 * (c + 1), x[(c + 1) & 1]);
-            exp16(std::false_type{}, 16 * c, of, x[c & 1], m_ref, pk + 8 * c, nullptr);
-          }
-          const float ts = pair_sum(acc);
-          settled = !__any_sync(0xffffffffu, valid && !(ts <= (KV8 ? kMaxSumF16 : kMaxSum)));   // also inf / nan
-          if (settled) {
-            tmem_st32(tS, pk);
-            tmem_st32(tS + 32, pk + 32);
-            l += ts;
-            if (!KV8) lr += pair_sum(accr);
-            if (valid && ts > kRaiseSum) grow = ceilf(lg2_approx(ts));
+              for (int c = 0; c < 4; ++c) {
+                const Of16 of = of16(64 * h + 16 * c);
+                tmem_wait_ld();
+                reg_fence16(x[c & 1]);
+                if (c < 3) tmem_ld16(tS + 64 * h + 16 * (c + 1), x[(c + 1) & 1]);
+                exp16(std::false_type{}, 64 * h + 16 * c, of, x[c & 1], m_ref, pk + 8 * c, nullptr);
+              }
+              return pair_sum(acc);
+            };
+            float ts = half(0);
+            settled = !__any_sync(0xffffffffu, valid && !(ts <= kMaxSumF16));
+            if (settled) {
+              tmem_st32(tS, pk);
+              tmem_wait_st();
+              tc_fence_before();
+              if (warp == 0) {                          // on behalf of the MMA issuer, as below
+                ++vslot;
+                if (!(ok = wait(&bars->kv_full[vslot % C::NS], (vslot / C::NS) & 1))) break;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->p_half[t]);
+              given = true;
+              const float tb = half(1);
+              if (!__any_sync(0xffffffffu, valid && !(tb <= kMaxSumF16))) {
+                tmem_st32(tS + 32, pk);
+                ts += tb;
+                l += ts;
+                if (valid && ts > kRaiseSum) grow = ceilf(lg2_approx(ts));
+              } else {
+                // Rare: the first half's product stays under the reference it was
+                // given away with, and O takes the new one when that is done.
+                l += ts;
+                if (!(ok = wait(&bars->half_done[t], nhalf & 1))) break;
+                tc_fence_after();
+                settled = false;
+              }
+            }
+          } else {
+            uint32_t pk[64], x[2][16];
+            acc[0] = acc[1] = accr[0] = accr[1] = 0;
+            tmem_ld16(tS, x[0]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const Of16 of = of16(16 * c);
+              tmem_wait_ld();
+              reg_fence16(x[c & 1]);
+              if (c < 7) tmem_ld16(tS + 16 * (c + 1), x[(c + 1) & 1]);
+              exp16(std::false_type{}, 16 * c, of, x[c & 1], m_ref, pk + 8 * c, nullptr);
+            }
+            const float ts = pair_sum(acc);
+            settled = !__any_sync(0xffffffffu, valid && !(ts <= kMaxSum));   // also inf / nan
+            if (settled) {
+              tmem_st32(tS, pk);
+              tmem_st32(tS + 32, pk + 32);
+              l += ts;
+              lr += pair_sum(accr);
+              if (valid && ts > kRaiseSum) grow = ceilf(lg2_approx(ts));
+            }
           }
         }
         if (!settled) {
@@ -1352,9 +1485,10 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // 2^40, and every tile of a one-tile item (HBM sets its pace).
           // Masked scores become -inf, in TMEM too, whatever the slots hold.
           const int ub = kend - n0, lb = p.causal ? ub - p.window : 0;
+          const int c_first = given ? 64 : 0;
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = c_first; c < 128; c += 32) {
             uint32_t x[32];
             tmem_ld32(tS + c, x);
             const float ca = c2_of(c), cb = c2_of(c + 16);
@@ -1407,7 +1541,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // P over the scores just read: with two parts each 16 keys' high and
           // low part take the 16 columns of their scores, else 16 keys take 8
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = c_first; c < 128; c += 32) {
             uint32_t x[32], y[32];
             tmem_ld32(tS + c, x);
             const Of16 of0 = of16(c), of1 = of16(c + 16);
@@ -1430,12 +1564,16 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_wait_st();
         tc_fence_before();
         // On behalf of the MMA issuer: the next step's slot has been loaded.
-        if (!ONE && warp == 0 && !dual) {
+        if (!ONE && warp == 0 && !dual && !given) {
           ++vslot;
           if (!(ok = wait(&bars->kv_full[vslot % C::NS], (vslot / C::NS) & 1))) break;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+        if (lane == 0) {
+          if (halves && !given) mbar_arrive(&bars->p_half[t]);
+          mbar_arrive(&bars->p_full[t]);
+        }
+        nhalf += halves;
       }
       // ---------------------------------------------------------- epilogue
       if (!ok || !wait(&bars->o_done, nseg & 1)) break;

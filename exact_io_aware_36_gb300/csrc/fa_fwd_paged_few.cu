@@ -54,7 +54,7 @@ struct Few {
   static constexpr int Q_BYTES = Q_FRAGS + ROWS * 8;
   // Tiles of the ring: what the rest leaves of shared memory, at most 192 KB (what
   // HBM's latency asks for is about 60).
-  static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 12 + 2 * Q_BYTES + kSegs * 96 + 256 + 512 + 1024;
+  static constexpr int REST = W * ROWS * (RED_STRIDE * 4 + 8) + ROWS * 12 + 2 * Q_BYTES + kSegs * 96 + 256 + kBarBytes + 1024;
   static constexpr int FIT = (227 * 1024 - REST) / (TILE_BYTES + 128 + 16);
   static constexpr int NS = FIT < 196608 / TILE_BYTES ? FIT : 196608 / TILE_BYTES;
   static constexpr int RING_OFF = 0;
@@ -68,7 +68,7 @@ struct Few {
   static constexpr int PAR_OFF = SEG_OFF + kSegs * 96;
   static constexpr int RINGBAR_OFF = PAR_OFF + 256;         // full and empty of the ring's tiles
   static constexpr int BAR_OFF = RINGBAR_OFF + NS * 16;
-  static constexpr int SMEM_BYTES = BAR_OFF + 512 + 1024;
+  static constexpr int SMEM_BYTES = BAR_OFF + kBarBytes + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   // Each tile's steps belong to different warps, and a warp's next step lies at
   // most NS - 1 tiles on.
