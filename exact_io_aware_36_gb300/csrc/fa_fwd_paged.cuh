@@ -112,16 +112,19 @@ constexpr int kUpP = 6;                // codes: P in f16 is times 2^6, ..
 constexpr float kMaxSumF16 = 1000.0f;  // .. and no more than 2^16
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
-// Of an item of the kernel for few rows (p.head_few): an item more costs a CTA
-// 7000 cycles, a tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands
-// for.  Counted in full where there are about as many items as SMs or more (16
-// caches of 8 heads: 132 us with 16, 125 with 44); of fewer the runs, which must be
-// longer than a head, would leave SMs idle (16 items of 7 tiles: 15.9 us with 44,
-// 13.7 with 16).
+// The same over codes, measured again (least squares over the CTAs of eight batches,
+// d = 128): 4075 cycles a tile of a two-tile item and 2420 of another, 21800 and 6040
+// beside them (d = 64: 3670, 2240, 14100, 4390).  A mixed batch's CTAs ended 23 %
+// after their mean with bf16's weights.
+constexpr int kWeightTwoCodes = 18, kWeightOneCodes = 11, kHeadTwoCodes = 88, kHeadOneCodes = 26;
+// Of an item of the kernel for few rows: an item more costs a CTA 7000 cycles, a
+// tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands for (16 caches of
+// 8 heads: 132 us with 16, 125 with 44).
 constexpr int kHeadFew = 44;
 // A CTA's run is at least this long, so that none lies between the beginnings
 // of an item's first two tiles: an item's parts are in CTAs next to each other.
 constexpr int kMinRunTwo = kHeadTwo + kWeightTwo + 2, kMinRunOne = kHeadOne + kWeightOne + 2;
+constexpr int kMinRunTwoCodes = kWeightTwoCodes + 2, kMinRunOneCodes = kWeightOneCodes + 2;
 
 template <int D, bool KV8>
 struct Cfg {
@@ -239,10 +242,15 @@ __device__ __forceinline__ void block_geometry(const PagedParams& p, int n, int 
   k.vhi = p.causal ? k.f[0] + k.nt[0] + k.nt[1] : L;
 }
 
-__device__ __forceinline__ int tile_weight(const Block& k) { return k.two ? kWeightTwo : kWeightOne; }
+template <bool PICK>
+__device__ __forceinline__ int tile_weight(const PagedParams& p, const Block& k) {
+  if (PICK && !p.few) return k.two ? kWeightTwoCodes : kWeightOneCodes;
+  return k.two ? kWeightTwo : kWeightOne;
+}
 template <bool PICK>
 __device__ __forceinline__ int head_weight(const PagedParams& p, const Block& k) {
-  return k.two ? kHeadTwo : PICK && p.few ? p.head_few : kHeadOne;
+  if (PICK) return p.few ? kHeadFew : k.two ? kHeadTwoCodes : kHeadOneCodes;
+  return k.two ? kHeadTwo : kHeadOne;
 }
 
 // Weight of the block of query tokens from tok0 on (0 behind the last).  Not
@@ -253,7 +261,7 @@ static __device__ __noinline__ int block_weight(const PagedParams& p, int n, int
   if (tok0 >= n) return 0;
   Block k;
   block_geometry(p, n, L, tok0, k);
-  return head_weight<PICK>(p, k) + k.kt * tile_weight(k);
+  return head_weight<PICK>(p, k) + k.kt * tile_weight<PICK>(p, k);
 }
 
 // A part of an item, as the walker passes it on: steps [ib, ie) of the item's
@@ -302,10 +310,18 @@ __device__ __forceinline__ bool walk_next(const PagedParams& p, Walk& w, Seg& s)
     block_geometry(p, w.n, w.L, tok0, s.k);
     // On the line an item is its head and then its tiles; the first tile
     // begins with the head.  A CTA has the tiles that begin in its run.
-    const int wt = tile_weight(s.k), head = head_weight<PICK>(p, s.k);
+    const int wt = tile_weight<PICK>(p, s.k), head = head_weight<PICK>(p, s.k);
     const long long len = head + (long long)s.k.kt * wt;
-    s.ib = w.base >= w.w0 ? 0 : max(1, ((int)(w.w0 - w.base) - head + wt - 1) / wt);
-    s.ie = w.w1 - w.base >= len ? s.k.kt : min(s.k.kt, max(1, ((int)(w.w1 - w.base) - head + wt - 1) / wt));
+    if (PICK) {
+      // Codes: the first tile begins behind the head, so that a run that ends in an
+      // item's head leaves the item to the next.
+      const long long t0 = w.base + head;
+      s.ib = w.w0 <= t0 ? 0 : (int)((w.w0 - t0 + wt - 1) / wt);
+      s.ie = w.w1 <= t0 ? 0 : (int)min((long long)s.k.kt, (w.w1 - t0 + wt - 1) / wt);
+    } else {
+      s.ib = w.base >= w.w0 ? 0 : max(1, ((int)(w.w0 - w.base) - head + wt - 1) / wt);
+      s.ie = w.w1 - w.base >= len ? s.k.kt : min(s.k.kt, max(1, ((int)(w.w1 - w.base) - head + wt - 1) / wt));
+    }
     s.b = w.b;
     s.L = w.L;
     s.g = w.g;
@@ -525,6 +541,17 @@ __device__ __forceinline__ int exponent_of(uint32_t word, uint32_t shift) {
   return (int)min(word >> shift & 0xffu, (uint32_t)kScaleHigh + 127) - 127;
 }
 
+// Whether the phase is over, without a wait (mbar_try_wait may take its time).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 // wait_warp_slow of one thread.
 static __device__ __noinline__ bool wait_thread_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status,
                                                      unsigned long long limit_ns) {
@@ -612,7 +639,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       reinterpret_cast<uint4*>(smem + C::Q_OFF + i / per * (C::TILE_BYTES / 2) + rows_box * D)[i % per] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-  make_plan<kThreads, KV8>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), ONE ? kMinRunOne : kMinRunTwo);
+  make_plan<kThreads, KV8>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::K_OFF), KV8 ? (ONE ? kMinRunOneCodes : kMinRunTwoCodes) : ONE ? kMinRunOne : kMinRunTwo);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -875,7 +902,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                   const uint32_t colS = tmem + (t ? C::S_COL1 : C::S_COL0);
 #pragma unroll
                   for (int kk = 0; kk < D / 16; ++kk) {
-                    if (k < 3 && kk == D / 16 - 2) there = mbar_try_wait(ready_bar(k + 1), ready_par(k + 1));
+                    if (k < 3 && kk == D / 16 - 2) there = mbar_test(ready_bar(k + 1), ready_par(k + 1));
                     s_product(colS, desc_add(qdesc0, t * C::TILE_BYTES), kd, kk);
                   }
                   mma_commit(&bars->s_full[t]);

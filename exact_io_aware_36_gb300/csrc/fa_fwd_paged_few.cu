@@ -143,7 +143,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   }
   fence_mbarrier_init();
   __syncthreads();
-  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), p.head_few + kWeightOne + 2);
+  make_plan<C::NT, true>(ps, bars, reinterpret_cast<unsigned long long*>(smem + C::RING_OFF), kWeightOne + 2);
   fence_proxy_async_smem();                            // (the plan's sums lay where TMA will write)
   __syncthreads();
   grid_launch_dependents();
@@ -777,7 +777,6 @@ extern "C" int fa_selftest_paged_few_stop(int warp, int cta, int item) {
 
 int launch_fwd_paged_few(PagedParams p, int grid, bool after, void* stream_) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  p.head_few = (long long)p.B * p.Hkv * 2 >= grid ? kHeadFew : kHeadOne;
   if (p.few_rows <= 8) return p.d == 128 ? launch_few<128, 1>(p, grid, after, stream) : launch_few<64, 1>(p, grid, after, stream);
   if (p.few_rows <= 16) return p.d == 128 ? launch_few<128, 2>(p, grid, after, stream) : launch_few<64, 2>(p, grid, after, stream);
   if (p.few_rows <= 24) return p.d == 128 ? launch_few<128, 3>(p, grid, after, stream) : launch_few<64, 3>(p, grid, after, stream);

@@ -221,7 +221,6 @@ struct PagedParams {
   float scale, scale_log2;
   int few_rows, few;           // codes: sequences of up to few_rows rows per kv head
                                // are another kernel's (few: the others are)
-  int head_few;                // that kernel's weight of an item beside its tiles
   // codes: workspace, q 2^q_exps as the sum of two e4m3 parts, [2][T, Hq, d], and
   // its rows' exponents [T, Hq]
   uint8_t* q_codes;
