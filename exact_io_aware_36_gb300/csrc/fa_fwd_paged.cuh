@@ -82,6 +82,27 @@
 // are taken off the record.  Rows are right or as they were.
 // TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D);
 // P overwrites S: 64 columns, or all 128 (each 16 keys' high part, then low).
+//
+// Codes (KV8).  With k = 2^ek ck and v = 2^ev cv, one pair of exponents for every
+// 16 keys:
+//   S  = 2^(ek - up) (Qhi + Qlo) ck: the keys' codes go to the tensor cores as they
+//        are, e4m3 by e4m3 at twice the rate of bf16, and q 2^up is the sum of two
+//        e4m3 parts (fa_fwd_paged_fp8.cu).  The exponents are in the softmax's scale.
+//   O  = 2^(er - 6) sum_j P_j cv_j,  P_j = 2^(S_j - m + ev_j - er + 6),  er the largest
+//        ev so far: two warps turn the values' codes to f16, which holds them exactly
+//        and without a scale (two instructions for four codes; turned to bf16 with
+//        their scales they took five times as many, and the two chunks 1817 us), and
+//        P, in f16 too, takes their powers of two.  l is the sum of P without them,
+//        in float32.  P has 11 bits here, so one part does for one-tile items too; it
+//        is at most 2^16, so a tile's sum past 1000 (of 64 keys) is not let stand.
+// Warp 8 is walker and producer (K's codes and the exponents into the slot, V's codes
+// into a stage), warps 10 and 11 turn V, 64 rows of a tile each, and write it where
+// TMA would have.  In two-tile items a tile's P is given away in halves of 64 keys: the
+// first half's product runs while the softmax takes the second (1457 -> 1434 us), and
+// the registers of half of P suffice.
+// Bound by the step's chain, softmax (1900 cycles) and products (2600 of the step's
+// 4000), as with bf16: two chunks of 2048 tokens behind 24k-32k keys, 32 heads on 8,
+// d = 128: 1430 us, 1277 TFLOP/s, 65 % of the measured cuBLAS rate.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -1803,7 +1824,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, c
 
 // Those of the two kernels of a call over codes: `ym` rows of blocks for those of
 // `many`, of whose up to 256 rows an item a warp takes four (a block costs more than
-// its rows: two kernels' parts of a mixed batch 18.8 us with one row per warp, MERGE_US
+// its rows: the parts of a mixed batch, not in L2, 18.8 us with one row per warp, 16.4
 // with four), the others for those of `few`.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -1814,8 +1835,8 @@ paged_merge_two_kernel(const PagedParams few, const PagedParams many, const int 
   else merge_parts<D, 1>(few, nctas, y - ym);
 }
 
-// Codes: begins while the kernel that makes q's parts runs; the merge is the
-// caller's.
+// Codes: begins while the kernel that makes q's parts runs, and waits for it behind
+// the plan; the merge is the caller's.
 template <int D, bool ALIBI, bool ONE, bool KV8>
 int launch_impl(const PagedParams& p, cudaStream_t stream) {
   using C = Cfg<D, KV8>;

@@ -570,6 +570,54 @@ def test_every_code_and_scale(d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [40, 150])
+def test_every_code_and_scale_under_many_rows(d, n):
+    """The same for sequences that bring one tile of rows and more."""
+    import torch as t
+    B, H = 220, 4
+    codes = t.arange(256, dtype=t.int32).to(t.uint8)
+    vals = codes.repeat(-(-H * d // 256))[:H * d].view(H, d) if H * d >= 256 else codes[:H * d].view(H, d)
+    pool = vals.expand(B, 16, H, d).contiguous().cuda()
+    scales = t.arange(27, 27 + B, dtype=t.uint8)[:, None, None].expand(B, 1, H).contiguous().cuda()
+    table = t.arange(B, dtype=t.int32, device="cuda")[:, None].contiguous()
+    q = t.zeros(B * n, H, d, dtype=t.bfloat16, device="cuda")
+    one = t.full((B,), 1, dtype=t.int32, device="cuda")
+    o, lse = fa.attention_forward_paged_fp8(q, t.zeros_like(pool), pool, scales, scales, table, one, causal=False,
+                                            out_dtype=t.float32, check=True)
+    want = t.from_numpy(P8.values(pool.cpu().numpy(), scales.cpu().numpy())[:, 0]).cuda()
+    assert t.equal(t.nan_to_num(o.double(), 1e300).view(B, n, H, d), t.nan_to_num(want, 1e300)[:, None].expand(-1, n, -1, -1))
+    assert bool((lse == 0).all())
+    q[..., 0] = 1                                            # and as a key: the score of element 0
+    key = t.zeros_like(pool)
+    key[:, 0, :, 0] = t.arange(B, dtype=t.int32, device="cuda").to(t.uint8)[:, None]
+    _, lse = fa.attention_forward_paged_fp8(q, key, t.zeros_like(pool), scales.fill_(120), scales, table, one, causal=False, check=True)
+    score = P8.values(key.cpu().numpy(), scales.cpu().numpy())[:, 0, 0, 0] * d ** -0.5
+    got = npf(lse)[0].reshape(B, n)
+    # relative: the scale's, log2 e's, ln 2's and the products' roundings, 6 2^-24; absolute: m - 6 (2^-22), exp2 and log2
+    # as the device has them (2^-22 relative and absolute)
+    assert np.allclose(got, score[:, None], rtol=2.0 ** -21, atol=2.0 ** -20, equal_nan=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,lens", [([1, 1], [900, 300]), ([150], [900]), ([40, 1], [700, 300]), ([300], [300])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_far_apart(new, lens, d):
+    """Rows of 2^20 down to 2^-100, rows of zeros, and rows whose elements lie 2^-16 apart."""
+    import torch as t
+    q, codes, scales, table, cs, cu = state(new, lens, 16, 4, 2, d, 7)
+    g = t.Generator().manual_seed(2)
+    live = scales[0] != 255
+    scales[0] = t.where(live, scales[0] - 20, scales[0])
+    far = t.tensor([2.0 ** 20, 2.0 ** 18, 1.0, 2.0 ** -100, 0.0])[t.randint(0, 5, q.shape[:2], generator=g)].cuda()
+    q = (q.float() * far[..., None]).bfloat16()
+    near = t.tensor([1.0, 2.0 ** -8, 2.0 ** -11, 2.0 ** -16])[t.randint(0, 4, q.shape, generator=g)].cuda()
+    q[:, ::2] = (q.float() * near).bfloat16()[:, ::2]
+    out = attend(q, codes, scales, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    check(out, q, codes, scales, table, lens, new, 16)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("new,lens,bad", [([1, 2], [20000, 60], [0, 2]), ([1, 5, 1], [300, 900, 1], [0, 3, 6]),
                                           ([150], [9000], [0, 70, 149]), ([1, 1], [5000, 60], [1])])
 def test_nan_rows_stay_nan_and_alone(new, lens, bad):
