@@ -562,10 +562,11 @@ fa_status fa_cache_copy_fp8(void* k_pages, void* v_pages, void* k_scales, void* 
  * q).  Products with the keys are exact but for elements of q below 2^-9 of its
  * row's largest, which are off by at most 2^-17 of that one (for sequences that
  * bring few rows, new tokens times Hq / Hkv, 2^-22 and 2^-39).  P is rounded once,
- * to 11 bits, and not below 2^-30 of the row's sum times the largest power of two
- * of its values.  As in the cache in bf16, a NaN among the values may reach rows
- * that do not see its key where other rows of their block of query tokens do;
- * slots that none of them sees do not count, whatever they hold.
+ * to 11 bits, and what falls below 2^-30 of the row's sum, times the largest power
+ * of two of the values that its block of query tokens sees, is lost.  As in the
+ * cache in bf16, a NaN among the values may reach rows that do not see its key
+ * where other rows of their block of query tokens do; slots that none of them sees
+ * do not count, whatever they hold.
  */
 size_t fa_fwd_paged_fp8_workspace_size(int Hq, int Hkv, int N, int d, long long total_tokens);
 
