@@ -38,13 +38,16 @@ namespace {
 template <int D, int NR>
 struct Few {
   static constexpr int ROWS = 8 * NR;
-  // Warps that take steps: as many as the registers of O (D NR / 4 of a lane)
-  // leave room for beside the two that bring the codes.
-  static constexpr int W = (NR * D <= 128 ? 16 : NR * D <= 256 ? 12 : 8) - 2;
+  // Warps that take steps: as many as do not spill beside the two that bring the
+  // codes; O alone takes D NR / 4 registers of a lane.  Warps in all, one token of 16
+  // caches (8 rows, d = 128): 8 108.4 us, 10 107.9, 12 107.4, 14 112.7, 16 116.2; four
+  // tokens of such (16 rows): 8 99.4, 10 97.3, 12 104.8; seven tokens of 40 sequences
+  // (32 rows of 64): 8 62.5, 12 54.8; five of 32 (24 rows): 8 123, 10 203.
+  static constexpr int W = (NR * D <= 192 ? 12 : NR * D > 256 ? 8 : D == 128 ? 10 : 12) - 2;
   static constexpr int NT = 32 * (W + 2);
   // Blocks of a step that are taken together: both, unless that spills (32 rows).
   // 24 rows, d = 128 (five tokens of 32 sequences, 32 heads on 8): 123 us, with one
-  // 131; with 10 warps of 168 registers, which spill, 153.
+  // 131.
   static constexpr int XB = NR <= 3 ? 2 : 1;
   static constexpr int POOL = 128 * D;                      // codes of a tile in one pool
   static constexpr int TILE_BYTES = 2 * POOL;

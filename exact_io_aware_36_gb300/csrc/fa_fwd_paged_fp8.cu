@@ -5,8 +5,8 @@
 // and the others (fa_fwd_paged.cuh).  The one for few rows begins on the SMs that
 // the other leaves.  Where the largest number of new tokens says that all
 // sequences are of one kind, only that kernel runs.  Up to 32 rows the one for few
-// is the faster: 16 caches of 1k-32k tokens, one token each, 121 us against 172 with
-// the other, five tokens of 32 sequences (20 rows) 123 against 139, a mixed batch 174
+// is the faster: 16 caches of 1k-32k tokens, one token each, 114 us against 172 with
+// the other, five tokens of 32 sequences (20 rows) 123 against 139, a mixed batch 170
 // against 187 with the other alone.
 //
 // For the others the products with the keys take the codes as they are, at twice

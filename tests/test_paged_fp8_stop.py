@@ -17,7 +17,7 @@ from tests.test_paged_fp8 import state
 
 pytestmark = pytest.mark.gpu
 
-MMA, TURN, VALUES = 9, 10, 15   # of many rows; 15: brings the values' codes to 8 rows of the other kernel
+MMA, TURN, VALUES = 9, 10, 11   # of many rows; 11: brings the values' codes to 8 rows of the other kernel
 
 
 @pytest.fixture(scope="module")
