@@ -571,11 +571,13 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[n][t][i] *= alpha;
           }
-          // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1
+          // P in O's unit: 2^(x - m + ev - eref + 7); its sum is brought back to 1.
+          // (x - m is at most 8, so with 2^-60 and less P is 0 in f16; a smaller
+          // one would make 0 of it in float32 too, and l would miss the key.)
           float lsv[XB], back[XB];
 #pragma unroll
           for (int x = 0; x < XB; ++x) {
-            const int up = max(ev[x] - eref + 7, -126);
+            const int up = max(ev[x] - eref + 7, -60);
             const bool on = passes == 1 || pass == x;
             lsv[x] = on ? (float)up : -1e6f;
             back[x] = pow2_cut(-up);

@@ -1,0 +1,51 @@
+"""A cache in 8 bits at the ends of its ranges: blocks of values very far apart,
+scales below and at the largest that a write makes, sequences of any number of
+new tokens.  Bounds are those that test_paged_fp8.py derives."""
+import pytest
+
+from oracle import paged_fp64 as P
+from tests.test_paged_fp8 import attend, check, state
+
+
+def value_scales(codes, scales, table, lens, page, step, bytes_of, zero):
+    """Every `step` slots of a sequence get one of `bytes_of` as the scale of their values, at random; those with `zero`
+    hold zeros."""
+    import torch as t
+    g = t.Generator().manual_seed(5)
+    H = scales[1].shape[2]
+    tab = table.cpu().numpy()
+    c, s = codes[1].view(t.uint8).view(-1, 16, *codes[1].shape[2:]), scales[1].view(-1, H)
+    for b, L in enumerate(lens):
+        blocks = t.from_numpy(P.slots(tab[b], L, page)[::16] // 16).cuda()
+        pick = t.randint(0, len(bytes_of), (-(-L // step), H), generator=g)
+        kind = t.tensor(bytes_of, dtype=t.uint8)[pick].repeat_interleave(step // 16, 0)[:len(blocks)].cuda()
+        s[blocks] = kind
+        x = c[blocks]
+        x[(kind == zero)[:, None, :, None].expand_as(x) & (x != 0x7f)] = 0
+        c[blocks] = x
+
+
+# one token of 8, 16, 24 and 32 heads, three of 8, five of 8 beside one of a chunk, five of 8 alone, a chunk
+MIXES = [([1] * 6, 8), ([1] * 6, 16), ([1] * 6, 24), ([1] * 6, 32), ([3] * 6, 8), ([5, 1, 1, 300, 1, 1], 8), ([5] * 6, 8),
+         ([300] * 2, 2)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,group", MIXES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", [100, 107, 110, 119])
+def test_zeros_beside_values_of_any_size_count_in_the_sum(new, group, d, e):
+    """Blocks of zeros take the least scale; the keys they stand for weigh what they do beside ordinary values."""
+    import torch as t
+    lens, page, Hkv = [3000 - 111 * b for b in range(len(new))], 32, 2
+    q, codes, scales, table, cs, cu = state(new, lens, page, Hkv * group, Hkv, d, e, gain=2.0)
+    kw = dict(cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    _, lse = attend(q, codes, scales, table, cs, **kw)
+    value_scales(codes, scales, table, lens, page, 32, [127 + e, 27, 27], 27)
+    if e >= 110:                                       # (a sum of many such values is past float32)
+        c = codes[1].view(t.uint8)
+        c[(c != 0) & (c != 0x7f)] = 1
+    O, got = attend(q, codes, scales, table, cs, **kw)
+    # the same scores, so each LSE is off by its own sum's share, 2^-20 (|lse| + 8) + 2^-22 |lse|
+    assert t.allclose(got, lse, rtol=2.0 ** -18, atol=2.0 ** -16)
+    check((O, got), q, codes, scales, table, lens, new, page)
