@@ -504,7 +504,7 @@ int launch_d(QuantAppendParams q, bool turn, cudaStream_t stream) {
   NormRopeParams& p = q.n;
   // numbers for the blocks: as many for every sequence, or by its place in
   // cu_seqlens, whichever takes fewer
-  const long long per_seq = (p.N + 14) / 16 + 1;
+  const long long per_seq = ((long long)p.N + 14) / 16 + 1;
   const long long even = per_seq * p.B, by_place = p.T / 16 + 3ll * p.B + 1;
   q.per_seq = !p.cu_seqlens || even <= by_place ? (int)per_seq : 0;
   const long long blocks = q.per_seq ? even : by_place;

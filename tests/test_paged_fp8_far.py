@@ -3,8 +3,12 @@ scales below and at the largest that a write makes, sequences of any number of
 new tokens.  Bounds are those that test_paged_fp8.py derives."""
 import pytest
 
+from exact_io_aware_36_gb300 import fa
 from oracle import paged_fp64 as P
-from tests.test_paged_fp8 import attend, check, state
+from oracle import paged_fp8 as P8
+from tests.test_cache_pages import cache
+from tests.test_norm_rope import npf
+from tests.test_paged_fp8 import attend, check, pools, raw, same_codes, state
 
 
 def value_scales(codes, scales, table, lens, page, step, bytes_of, zero):
@@ -49,3 +53,27 @@ def test_zeros_beside_values_of_any_size_count_in_the_sum(new, group, d, e):
     # the same scores, so each LSE is off by its own sum's share, 2^-20 (|lse| + 8) + 2^-22 |lse|
     assert t.allclose(got, lse, rtol=2.0 ** -18, atol=2.0 ** -16)
     check((O, got), q, codes, scales, table, lens, new, page)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [2**31 - 1, 2**31 - 14, 2**31 - 15])
+@pytest.mark.parametrize("B,Hkv", [(1, 2), (16, 8), (64, 8), (64, 2)])
+def test_writes_without_a_bound_on_the_new_tokens(most, B, Hkv):
+    """A max_seqlen that bounds nothing: every sequence's tokens are written."""
+    import torch as t
+    new = [1 + b % 5 for b in range(B)]
+    lens = [n + 7 * (b % 9) for b, n in enumerate(new)]
+    kp, _, table, cs, cu, g = cache(new, lens, 16, Hkv, 64, 8)
+    k, v = (t.randn(sum(new), Hkv, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    one = t.ones(max(lens), 16, device="cuda")
+    q = t.full_like(k, 5.0)
+    kw = dict(cu_seqlens=cu, max_seqlen=most, check=True)
+    for write in (lambda *c: fa.cache_append_fp8(k, v, *c, table, cs, **kw),
+                  lambda *c: fa.qk_norm_rope_append_fp8(k, k, v, *c, table, cs, cos=one, sin=0 * one, q_out=q, **kw)):
+        (kc, vc), (ks, vs) = pools(kp, g)
+        args = (table.cpu().numpy(), lens, cu.cpu().numpy(), 16)
+        want = [P8.append(raw(c), raw(s), npf(x), *args) for c, s, x in ((kc, ks, k), (vc, vs, v))]
+        write(kc, vc, ks, vs)
+        for c, s, w in ((kc, ks, want[0]), (vc, vs, want[1])):
+            assert (raw(s) == w[1]).all() and same_codes(raw(c), w[0])
+    assert t.equal(q, k)
