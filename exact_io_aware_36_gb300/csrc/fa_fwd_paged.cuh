@@ -193,6 +193,7 @@ struct Bars {
   unsigned long long warp_sum[16];
   long long w0, w1, base;
   int b, g, qb;
+  short unit[16];               // few rows: the power of two that each warp's O is over
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -590,6 +591,11 @@ static __device__ __noinline__ bool wait_thread_slow(uint64_t* bar, uint32_t par
 
 // 2^e for e from -127 to 127.
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float(e > -127 ? (e + 127) << 23 : 0x00400000); }
+
+// 2^e for e up to 127, down to the least that a float holds.
+__device__ __forceinline__ float pow2_any(int e) {
+  return __int_as_float(e >= -126 ? (e + 127) << 23 : 1 << (max(e, -149) + 149));
+}
 
 // ONE: no item has two tiles (the host knows from N).  KV8: the pages hold
 // codes.
@@ -1639,7 +1645,8 @@ if constexpr (KV8) {
       }
       const bool use0 = steps > 0, use1 = dual && (steps == 0 || s.ie - s.ib > 1);
       if (KV8) lr = l;
-      const float opow = pow2_of(eref);                 // codes: O's, but for P's 2^kUpP
+      int ounit = eref - kUpP;                          // codes: O is over this power of two, until it is divided:
+                                                        // what it is before may not be a float
       float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
       if (dual) {
@@ -1648,7 +1655,7 @@ if constexpr (KV8) {
         const float* oth = mls + ((t ^ 1) * 128 + r) * 3;
         own[0] = m_ref;
         own[1] = l;
-        own[2] = KV8 ? opow : lr;
+        own[2] = KV8 ? (float)ounit : lr;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->joined);
         // Only the time limit ends this wait, not the abort flag: a row's two
@@ -1667,12 +1674,16 @@ if constexpr (KV8) {
         w1 = mo == -INFINITY ? 0.f : ex2_approx(mo - M);
         l = fmaf(w0, l, w1 * oth[1]);
         lr = KV8 ? l : fmaf(w0, lr, w1 * oth[2]);
-        if (KV8) w1 *= oth[2] * (1.f / (1 << kUpP));
+        if (KV8) {
+          const int u = (int)oth[2], top = max(ounit, u);
+          w0 *= pow2_cut(ounit - top);
+          w1 *= pow2_cut(u - top);
+          ounit = top;
+        }
         m_ref = M;
         c_from = t * (D / 2);
         c_to = c_from + D / 2;
       }
-      if (KV8) w0 *= opow * (1.f / (1 << kUpP));
       const uint32_t tX = lane_base + (t ? C::O_COL0 : C::O_COL1);    // the other stream's O
       const int tl = (dual ? 0 : t * p.tpt) + r / p.group;            // token of the item
       const int rh = r % p.group, head = s.g * p.group + rh;
@@ -1683,8 +1694,11 @@ if constexpr (KV8) {
       const bool f32 = part || p.o_f32;                 // a part is float32, not divided
       char* out = part ? reinterpret_cast<char*>(p.part_o + prow * D)
                        : static_cast<char*>(p.o) + orow * D * (f32 ? 4 : 2);
-      float sc = 1.f;
-      if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
+      float sc = 1.f, opow = 1.f;
+      if (part == 0) {
+        sc = lr > 0.f ? 1.f / lr : 0.f;
+        if (KV8) opow = pow2_any(ounit);
+      }
       if (warp_rows) {
 #pragma unroll 1
         for (int c = c_from; c < c_to; c += 16) {
@@ -1700,6 +1714,7 @@ if constexpr (KV8) {
             v[i] = use0 ? __uint_as_float(a[i]) * w0 : 0.f;
             if (use1) v[i] = fmaf(__uint_as_float(b[i]), w1, v[i]);
             v[i] *= sc;
+            if (KV8) v[i] *= opow;
           }
           if (valid) store_row16(v, f32, out + c * (f32 ? 4 : 2));
         }
@@ -1710,7 +1725,7 @@ if constexpr (KV8) {
       if (valid && !(dual && t)) {                      // a one-tile item's rows: stream 0 reports
         if (part) {
           float* ml = p.part_ml + prow * 4;
-          *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, 0.f);
+          *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, KV8 ? (float)ounit : 0.f);
         } else {
           p.lse[(long long)head * p.T + tok] = l == 0.f ? -INFINITY : (m_ref + lg2_approx(l)) * kLn2;
         }
@@ -1734,10 +1749,11 @@ if constexpr (KV8) {
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
 // following ones, in their order; an item of which a CTA has no part to show
-// is left alone.  A warp has RPW rows, D / 32 columns per lane;
+// is left alone.  UNITS: O of a part is over the power of two that stands behind
+// its sums.  A warp has RPW rows, D / 32 columns per lane;
 // four parts' loads at a time, so that a row costs two waits for memory: what
 // the parts are, and the parts.
-template <int D, int RPW>
+template <int D, int RPW, bool UNITS>
 __device__ __forceinline__ void merge_parts(const PagedParams& p, const int nctas, const int y) {
   const int c = blockIdx.x;
   const int lane = threadIdx.x & 31;
@@ -1768,6 +1784,7 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
 #pragma unroll
     for (int i = 0; i < PER; ++i) o.v[i] = 0.f;
     float M = -INFINITY, l = 0.f, lr = 0.f;
+    int unit = -1000;                                   // O's
     for (int s0 = 0; s0 < nparts; s0 += 4) {
       float4 ml[4];
       Cols x[4];
@@ -1785,17 +1802,27 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
       const float a = M == -INFINITY ? 0.f : ex2_approx(M - mx);
       l *= a;
       lr *= a;
+      // no key seen there, or (l not 0) a score that is not a number
+      auto counts = [&](int i) { return s0 + i < nparts && (ml[i].x != -INFINITY || ml[i].y != 0.f); };
+      float ao = a;
+      if (UNITS) {
+        int top = unit;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) o.v[k] *= a;
+        for (int i = 0; i < 4; ++i)
+          if (counts(i)) top = max(top, (int)ml[i].w);
+        ao *= pow2_cut(unit - top);
+        unit = top;
+      }
+#pragma unroll
+      for (int k = 0; k < PER; ++k) o.v[k] *= ao;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // no key seen there, or (l not 0) a score that is not a number
-        if (s0 + i >= nparts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
-        const float w = ex2_approx(ml[i].x - mx);
+        if (!counts(i)) continue;
+        const float w = ex2_approx(ml[i].x - mx), wo = UNITS ? w * pow2_cut((int)ml[i].w - unit) : w;
         l = fmaf(w, ml[i].y, l);
         lr = fmaf(w, ml[i].z, lr);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x[i].v[k], o.v[k]);
+        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(wo, x[i].v[k], o.v[k]);
       }
       M = mx;
     }
@@ -1805,6 +1832,11 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
     const long long at = (tok * p.Hq + h) * D + lane * PER;
 #pragma unroll
     for (int k = 0; k < PER; ++k) o.v[k] *= inv;
+    if (UNITS) {
+      const float opow = pow2_any(unit);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) o.v[k] *= opow;
+    }
     if (p.o_f32) {
       *reinterpret_cast<Cols*>(static_cast<float*>(p.o) + at) = o;
     } else {
@@ -1819,7 +1851,7 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, const int nctas) {
   grid_dependency_wait();
-  merge_parts<D, 1>(p, nctas, blockIdx.y);
+  merge_parts<D, 1, false>(p, nctas, blockIdx.y);
 }
 
 // Those of the two kernels of a call over codes: `ym` rows of blocks for those of
@@ -1831,8 +1863,8 @@ __global__ void __launch_bounds__(256)
 paged_merge_two_kernel(const PagedParams few, const PagedParams many, const int ym, const int nctas) {
   grid_dependency_wait();
   const int y = blockIdx.y;
-  if (y < ym) merge_parts<D, 4>(many, nctas, y);
-  else merge_parts<D, 1>(few, nctas, y - ym);
+  if (y < ym) merge_parts<D, 4, true>(many, nctas, y);
+  else merge_parts<D, 1, true>(few, nctas, y - ym);
 }
 
 // Codes: begins while the kernel that makes q's parts runs, and waits for it behind

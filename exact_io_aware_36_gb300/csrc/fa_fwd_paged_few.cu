@@ -669,7 +669,11 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
         if (g8 == 0) mls[warp * C::ROWS + 8 * n + 2 * c4 + j] = make_float2(mref[n][j], x);
       }
+    if (lane == 0) bars->unit[warp] = (short)eref;
     meet();
+    // O stays over the warps' largest power of two until it is divided: what it is
+    // before may not be a float.
+    const int unit = __reduce_max_sync(0xffffffffu, lane < W ? (int)bars->unit[lane] : -1000);
     if (threadIdx.x < rows) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + threadIdx.x].x);
@@ -685,7 +689,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       for (int j = 0; j < 2; ++j) {
         float M = -INFINITY;
         for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + 8 * n + 2 * c4 + j].x);
-        const float a = (mref[n][j] == M ? 1.f : ex2_approx(mref[n][j] - M)) * pow2_cut(eref - 7);
+        const float a = (mref[n][j] == M ? 1.f : ex2_approx(mref[n][j] - M)) * pow2_cut(eref - unit);
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
           o[n][t][j] *= a;
@@ -727,11 +731,11 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const int tok = r / p.group, hq = s.g * p.group + r % p.group;
         const int col = (x >> 3) * (D / 8) + 8 * c + (x & 7);
         if (part == 0) {
-          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
-          v.x *= inv;
-          v.y *= inv;
-          v.z *= inv;
-          v.w *= inv;
+          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f, opow = pow2_any(unit - 7);
+          v.x = v.x * inv * opow;
+          v.y = v.y * inv * opow;
+          v.z = v.z * inv * opow;
+          v.w = v.w * inv * opow;
         }
         const long long at = part ? (prow + r) * D + col : ((long long)(s.tok + tok) * p.Hq + hq) * D + col;
         if (f32) {
@@ -741,7 +745,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
         if (c == 0 && x == 0) {
           if (part)
-            *reinterpret_cast<float4*>(p.part_ml + (prow + r) * 4) = make_float4(ml.x, ml.y, ml.y, 0.f);
+            *reinterpret_cast<float4*>(p.part_ml + (prow + r) * 4) = make_float4(ml.x, ml.y, ml.y, (float)(unit - 7));
           else
             p.lse[(long long)hq * p.T + s.tok + tok] = ml.y == 0.f ? -INFINITY : (ml.x + lg2_approx(ml.y)) * kLn2;
         }

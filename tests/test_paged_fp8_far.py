@@ -1,6 +1,7 @@
 """A cache in 8 bits at the ends of its ranges: blocks of values very far apart,
 scales below and at the largest that a write makes, sequences of any number of
 new tokens.  Bounds are those that test_paged_fp8.py derives."""
+import numpy as np
 import pytest
 
 from exact_io_aware_36_gb300 import fa
@@ -77,3 +78,39 @@ def test_writes_without_a_bound_on_the_new_tokens(most, B, Hkv):
         for c, s, w in ((kc, ks, want[0]), (vc, vs, want[1])):
             assert (raw(s) == w[1]).all() and same_codes(raw(c), w[0])
     assert t.equal(q, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,group", [(1, 1), (2, 8), (3, 8), (4, 8), (40, 1), (150, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_below_those_that_a_write_makes(n, group, d):
+    """One key in view: O is its value exactly under scales of 2^-127 to 2^-101 too."""
+    import torch as t
+    B, Hkv = 27, 2
+    vals = t.arange(256, dtype=t.int32).to(t.uint8)
+    for lo in range(0, 256, Hkv * d):
+        pool = vals.roll(-lo)[:Hkv * d].view(Hkv, d).expand(B, 16, Hkv, d).contiguous().cuda()
+        scales = t.arange(B, dtype=t.uint8)[:, None, None].expand(B, 1, Hkv).contiguous().cuda()
+        table = t.arange(B, dtype=t.int32, device="cuda")[:, None].contiguous()
+        q = t.zeros(B * n, Hkv * group, d, dtype=t.bfloat16, device="cuda")
+        one = t.full((B,), 1, dtype=t.int32, device="cuda")
+        o, _ = fa.attention_forward_paged_fp8(q, t.zeros_like(pool), pool, scales, scales, table, one, causal=False,
+                                              out_dtype=t.float32, check=True)
+        want = P8.values(pool.cpu().numpy(), scales.cpu().numpy())[:, 0].repeat(group, 1)
+        assert np.array_equal(npf(o).reshape(B, n, Hkv * group, d), want[:, None].repeat(n, 1), equal_nan=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,group", MIXES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("byte", [246, 245, 3])
+def test_many_values_at_the_ends_of_the_scales(new, group, d, byte):
+    """O lies within the values, so it is as good as ever, whether the sum of p v is past float32 or not."""
+    import torch as t
+    lens, page, Hkv = [2000 - 111 * b for b in range(len(new))], 32, 2
+    q, codes, scales, table, cs, cu = state(new, lens, page, Hkv * group, Hkv, d, byte)
+    c = codes[1].view(t.uint8)
+    c[..., ::2] &= 0x7f                                # half of the elements: no sign
+    value_scales(codes, scales, table, lens, page, 16, [byte, byte, byte - 1, byte - 3], 255)
+    out = attend(q, codes, scales, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    check(out, q, codes, scales, table, lens, new, page)
