@@ -332,7 +332,8 @@ __device__ __forceinline__ void write_block(const QuantAppendParams& q, const Bl
   const long long row = ((long long)page << p.page_shift) + (k.p0 & (p.page_size - 1));
   uint8_t* scale = (values ? q.v_scales : q.k_scales) + (row >> 4) * p.Hkv + h;
   uint8_t* dst = static_cast<uint8_t*>(values ? p.v_out : p.k_out) + (row * p.Hkv + h) * D + 8 * l;
-  const int was = k.lo > 0 ? min(max((int)*scale, kScaleLow + 127), kScaleHigh + 127) - 127 : kScaleLow;
+  // (a block's own scale, of another writer, may lie below the least that is written)
+  const int was = k.lo > 0 ? min((int)*scale, kScaleHigh + 127) - 127 : kScaleLow;
 
   const int first = k.lo / RPS, last = (hi - 1) / RPS;     // loads with a row that is written
   float top = 0.f;

@@ -57,7 +57,7 @@ def append(codes, scales, rows, table, lens, cu, page):
                 a = np.abs(x[np.isfinite(x)])
                 e = exponent(a.max() if a.size else 0.0)
                 if lo > first:
-                    was = min(max(int(s[blk, h]) - BIAS, LOW), HIGH)
+                    was = min(int(s[blk, h]) - BIAS, HIGH)
                     e = max(e, was)
                     if e > was:
                         old = VALUES[c[at[first:lo], h]]

@@ -114,3 +114,22 @@ def test_many_values_at_the_ends_of_the_scales(new, group, d, byte):
     value_scales(codes, scales, table, lens, page, 16, [byte, byte, byte - 1, byte - 3], 255)
     out = attend(q, codes, scales, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
     check(out, q, codes, scales, table, lens, new, page)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("byte", [0, 10, 26])
+@pytest.mark.parametrize("size", [2.0 ** -118, 2.0 ** -110, 2.0 ** -90, 1.0])
+def test_older_tokens_under_scales_that_no_write_makes(byte, size):
+    """A block whose own scale lies below the least of a write: its older codes are rounded to the new one."""
+    import torch as t
+    kp, _, table, cs, cu, g = cache([3, 1], [12, 40], 16, 2, 64, 8)
+    (kc, vc), (ks, vs) = pools(kp, g)
+    for c, s in ((kc, ks), (vc, vs)):
+        c.view(t.uint8).copy_(t.arange(c.numel(), device="cuda").view(c.shape) % 256)
+        s.fill_(byte)
+    k, v = (size * t.randn(4, 2, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    args = (table.cpu().numpy(), [12, 40], cu.cpu().numpy(), 16)
+    want = [P8.append(raw(c), raw(s), npf(x), *args) for c, s, x in ((kc, ks, k), (vc, vs, v))]
+    fa.cache_append_fp8(k, v, kc, vc, ks, vs, table, cs, cu_seqlens=cu, max_seqlen=3, check=True)
+    for c, s, w in ((kc, ks, want[0]), (vc, vs, want[1])):
+        assert (raw(s) == w[1]).all() and same_codes(raw(c), w[0])
