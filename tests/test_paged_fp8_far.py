@@ -9,7 +9,7 @@ from oracle import paged_fp64 as P
 from oracle import paged_fp8 as P8
 from tests.test_cache_pages import cache
 from tests.test_norm_rope import npf
-from tests.test_paged_fp8 import attend, check, pools, raw, same_codes, state
+from tests.test_paged_fp8 import attend, check, parts, pools, raw, same_codes, state
 
 
 def value_scales(codes, scales, table, lens, page, step, bytes_of, zero):
@@ -133,3 +133,43 @@ def test_older_tokens_under_scales_that_no_write_makes(byte, size):
     fa.cache_append_fp8(k, v, kc, vc, ks, vs, table, cs, cu_seqlens=cu, max_seqlen=3, check=True)
     for c, s, w in ((kc, ks, want[0]), (vc, vs, want[1])):
         assert (raw(s) == w[1]).all() and same_codes(raw(c), w[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,group", MIXES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gaps", [(8,), (9,), (10,), (16,), (20,), (1, 9, 10), (3, 12, 18)])
+def test_small_values_beside_large_ones(new, group, d, gaps):
+    """Columns in which the blocks of the largest scale hold zeros: O there is made of the smaller ones alone.
+
+    Scores are flat (gain 2^-10), so a row's keys weigh alike, the reference is within 2^s of every key, s = 2 |q| |k|
+    scale log2 e, and its sum is at least 2^-s of the number of its keys.  Of a key's P at most half of fp16's least
+    step is lost, 2^-25, over 2^6 at least, times a code of the largest scale: over the row 2^s 2^-31 448 2^e.  (More than
+    20 apart, P over the largest scale is below fp16's normal numbers where rows are many.)"""
+    import torch as t
+    lens, page, Hkv = [2000 - 111 * b for b in range(len(new))], 32, 2
+    top = 140
+    q, codes, scales, table, cs, cu = state(new, lens, page, Hkv * group, Hkv, d, sum(gaps), gain=2.0 ** -10)
+    scales[0][scales[0] != 255] -= 3                   # (|k| below 2^9)
+    value_scales(codes, scales, table, lens, page, 16, [top] + [top - g for g in gaps], 255)
+    c = codes[1].view(t.uint8).view(-1, 16, Hkv, d)
+    large = (scales[1].view(-1, Hkv) == top)[:, None, :, None].expand_as(c) & (c != 0x7f)
+    large[..., ::2] = False
+    c[large] = 0
+    O, lse = attend(q, codes, scales, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    check((O, lse), q, codes, scales, table, lens, new, page)
+    k, v = (P8.values(raw(c), raw(s)) for c, s in zip(codes, scales))
+    args = (np.where(table.cpu().numpy() < 0, 0, table.cpu().numpy()), lens, np.concatenate([[0], np.cumsum(new)]), page, d ** -0.5)
+    Or, lr = P.attention(npf(q), k, v, *args)
+    Ab = P.attention(npf(q), k, np.abs(v), *args)[0]
+    pr, _, pq = parts(new, Hkv * group, Hkv).T[:, :, None]
+    kn, qn = np.sqrt(np.nan_to_num((k * k).sum(-1))).max(), np.sqrt((npf(q) ** 2).sum(-1))
+    e = ((d + 8) * 2.0 ** -23 * qn + pq * np.abs(npf(q)).max(-1) * np.sqrt(d)) * kn * d ** -0.5 + 2.0 ** -21 * (np.abs(lr.T) + 8)
+    lost = 2.0 ** (2 * qn * kn * d ** -0.5 * np.log2(np.e)) * 2.0 ** -31 * 448 * 2.0 ** (top - 127)
+    tol = (2 * e[..., None] + pr[..., None] + 2.0 ** -20) * Ab + 2.0 ** -24 * np.abs(Or) + lost[..., None]
+    off = np.abs(npf(O) - Or)[..., 1::2] - tol[..., 1::2]
+    assert off.max() <= 0, float(off.max())
+    # And the bound says something: without the smaller blocks O would be past it nearly everywhere.  (20 apart, half of
+    # 2000 keys: O is of 100 2^-7 1000^1/2 / 2000 = 0.012, the bound 448 2^-18 = 0.0017 and less than a tenth of that, so
+    # |O| is below it with a probability of 0.12.)
+    assert (np.abs(Or) > tol)[..., 1::2].mean() > 0.75
