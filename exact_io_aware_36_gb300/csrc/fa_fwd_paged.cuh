@@ -597,6 +597,11 @@ __device__ __forceinline__ float pow2_any(int e) {
   return __int_as_float(e >= -126 ? (e + 127) << 23 : 1 << (max(e, -149) + 149));
 }
 
+// Codes: what is kept of O's power of two, the values' largest and P's, behind a
+// part's sums.  The part is not divided, and what l times the largest value is may
+// be no float; nor is what little a scale below those of a write leaves.
+__device__ __forceinline__ int part_power(int values, int p) { return values > 60 || values < kScaleLow ? values + p : 0; }
+
 // ONE: no item has two tiles (the host knows from N).  KV8: the pages hold
 // codes.
 template <int D, bool ALIBI, bool ONE, bool KV8>
@@ -1645,8 +1650,6 @@ if constexpr (KV8) {
       }
       const bool use0 = steps > 0, use1 = dual && (steps == 0 || s.ie - s.ib > 1);
       if (KV8) lr = l;
-      int ounit = eref - kUpP;                          // codes: O is over this power of two, until it is divided:
-                                                        // what it is before may not be a float
       float w0 = 1.f, w1 = 0.f;                         // of the own columns, of the other stream's
       int c_from = 0, c_to = D;
       if (dual) {
@@ -1655,7 +1658,7 @@ if constexpr (KV8) {
         const float* oth = mls + ((t ^ 1) * 128 + r) * 3;
         own[0] = m_ref;
         own[1] = l;
-        own[2] = KV8 ? (float)ounit : lr;
+        own[2] = KV8 ? __int_as_float(eref) : lr;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->joined);
         // Only the time limit ends this wait, not the abort flag: a row's two
@@ -1675,10 +1678,10 @@ if constexpr (KV8) {
         l = fmaf(w0, l, w1 * oth[1]);
         lr = KV8 ? l : fmaf(w0, lr, w1 * oth[2]);
         if (KV8) {
-          const int u = (int)oth[2], top = max(ounit, u);
-          w0 *= pow2_cut(ounit - top);
-          w1 *= pow2_cut(u - top);
-          ounit = top;
+          const int eo = __float_as_int(oth[2]), top = max(eref, eo);
+          w0 *= pow2_cut(eref - top);
+          w1 *= pow2_cut(eo - top);
+          eref = top;
         }
         m_ref = M;
         c_from = t * (D / 2);
@@ -1694,11 +1697,11 @@ if constexpr (KV8) {
       const bool f32 = part || p.o_f32;                 // a part is float32, not divided
       char* out = part ? reinterpret_cast<char*>(p.part_o + prow * D)
                        : static_cast<char*>(p.o) + orow * D * (f32 ? 4 : 2);
-      float sc = 1.f, opow = 1.f;
-      if (part == 0) {
-        sc = lr > 0.f ? 1.f / lr : 0.f;
-        if (KV8) opow = pow2_any(ounit);
-      }
+      float sc = 1.f;
+      if (part == 0) sc = lr > 0.f ? 1.f / lr : 0.f;
+      // codes: O is over 2^eref, and P was times 2^kUpP
+      const int kept = KV8 && part && (use0 || use1) ? part_power(eref, -kUpP) : 0;
+      const float opow = KV8 ? pow2_any(eref - kUpP - kept) : 1.f;
       if (warp_rows) {
 #pragma unroll 1
         for (int c = c_from; c < c_to; c += 16) {
@@ -1725,7 +1728,7 @@ if constexpr (KV8) {
       if (valid && !(dual && t)) {                      // a one-tile item's rows: stream 0 reports
         if (part) {
           float* ml = p.part_ml + prow * 4;
-          *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, KV8 ? (float)ounit : 0.f);
+          *reinterpret_cast<float4*>(ml) = make_float4(m_ref, l, lr, __int_as_float(kept));
         } else {
           p.lse[(long long)head * p.T + tok] = l == 0.f ? -INFINITY : (m_ref + lg2_approx(l)) * kLn2;
         }
@@ -1749,11 +1752,11 @@ if constexpr (KV8) {
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the
 // following ones, in their order; an item of which a CTA has no part to show
-// is left alone.  UNITS: O of a part is over the power of two that stands behind
-// its sums.  A warp has RPW rows, D / 32 columns per lane;
+// is left alone.  POWERS: O of a part may be over the power of two that stands behind
+// its sums (part_power).  A warp has RPW rows, D / 32 columns per lane;
 // four parts' loads at a time, so that a row costs two waits for memory: what
 // the parts are, and the parts.
-template <int D, int RPW, bool UNITS>
+template <int D, int RPW, bool POWERS>
 __device__ __forceinline__ void merge_parts(const PagedParams& p, const int nctas, const int y) {
   const int c = blockIdx.x;
   const int lane = threadIdx.x & 31;
@@ -1776,6 +1779,9 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
   }
   constexpr int PER = D / 32;
   struct alignas(4 * PER) Cols { float v[PER]; };
+  auto slot = [&](int s, int row) { return (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row; };
+  auto sums = [&](int s, int row) { return *reinterpret_cast<const float4*>(p.part_ml + slot(s, row) * 4); };
+  auto cols = [&](int s, int row) { return *reinterpret_cast<const Cols*>(p.part_o + slot(s, row) * D + lane * PER); };
 #pragma unroll 1
   for (int i = 0; i < RPW; ++i) {
     const int row = row0 + 8 * i;
@@ -1784,16 +1790,23 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
 #pragma unroll
     for (int i = 0; i < PER; ++i) o.v[i] = 0.f;
     float M = -INFINITY, l = 0.f, lr = 0.f;
-    int unit = -1000;                                   // O's
+    int powers = 0;                                     // not 0: some part's O is over a power of two
     for (int s0 = 0; s0 < nparts; s0 += 4) {
       float4 ml[4];
       Cols x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int s = min(s0 + i, nparts - 1);
-        const long long at = (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * p.part_rows + row;
-        ml[i] = *reinterpret_cast<const float4*>(p.part_ml + at * 4);
-        x[i] = *reinterpret_cast<const Cols*>(p.part_o + at * D + lane * PER);
+        ml[i] = sums(s, row);
+        // volatile: the columns are asked for with the sums, not behind their first use
+        // (one sequence of 777 tokens: 11.2 us, 11.6 otherwise)
+        const float* at = p.part_o + slot(s, row) * D + lane * PER;
+        if constexpr (PER == 4)
+          asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(x[i].v[0]), "=f"(x[i].v[1]), "=f"(x[i].v[2]), "=f"(x[i].v[3]) : "l"(at));
+        else
+          asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(x[i].v[0]), "=f"(x[i].v[1]) : "l"(at));
+        if (POWERS) powers |= __float_as_int(ml[i].w);
       }
       float mx = M;
 #pragma unroll
@@ -1802,29 +1815,40 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
       const float a = M == -INFINITY ? 0.f : ex2_approx(M - mx);
       l *= a;
       lr *= a;
-      // no key seen there, or (l not 0) a score that is not a number
-      auto counts = [&](int i) { return s0 + i < nparts && (ml[i].x != -INFINITY || ml[i].y != 0.f); };
-      float ao = a;
-      if (UNITS) {
-        int top = unit;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (counts(i)) top = max(top, (int)ml[i].w);
-        ao *= pow2_cut(unit - top);
-        unit = top;
-      }
-#pragma unroll
-      for (int k = 0; k < PER; ++k) o.v[k] *= ao;
+      for (int k = 0; k < PER; ++k) o.v[k] *= a;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (!counts(i)) continue;
-        const float w = ex2_approx(ml[i].x - mx), wo = UNITS ? w * pow2_cut((int)ml[i].w - unit) : w;
+        // no key seen there, or (l not 0) a score that is not a number
+        if (s0 + i >= nparts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
+        const float w = ex2_approx(ml[i].x - mx);
         l = fmaf(w, ml[i].y, l);
         lr = fmaf(w, ml[i].z, lr);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(wo, x[i].v[k], o.v[k]);
+        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x[i].v[k], o.v[k]);
       }
       M = mx;
+    }
+    float opow = 1.f;
+    if (POWERS && powers) {                             // O anew, over the largest power so far
+      int top = -1000;
+      M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) o.v[k] = 0.f;
+#pragma unroll 1
+      for (int s = 0; s < nparts; ++s) {
+        const float4 ml = sums(s, row);
+        const Cols x = cols(s, row);
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float mx = fmaxf(M, ml.x), a = M == -INFINITY ? 0.f : ex2_approx(M - mx), w = ex2_approx(ml.x - mx);
+        const int up = __float_as_int(ml.w), was = top;
+        top = max(top, up);
+        const float pa = pow2_any(was - top), pw = pow2_any(up - top);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) o.v[k] = fmaf(w, x.v[k] * pw, o.v[k] * a * pa);
+        M = mx;
+      }
+      opow = pow2_any(top);
     }
     const float inv = lr > 0.f ? 1.f / lr : 0.f;
     const long long tok = it.y + row / p.group;
@@ -1832,8 +1856,7 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const int ncta
     const long long at = (tok * p.Hq + h) * D + lane * PER;
 #pragma unroll
     for (int k = 0; k < PER; ++k) o.v[k] *= inv;
-    if (UNITS) {
-      const float opow = pow2_any(unit);
+    if (POWERS) {
 #pragma unroll
       for (int k = 0; k < PER; ++k) o.v[k] *= opow;
     }

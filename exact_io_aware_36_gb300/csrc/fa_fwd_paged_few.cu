@@ -699,6 +699,8 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const int part = s.ib > 0 ? 1 : s.ie < s.k.kt ? 2 : 0;
     const long long prow = (long long)(2 * (int)blockIdx.x + part - 1) * p.part_rows;
     const bool f32 = part || p.o_f32;                  // a part is float32, not divided
+    const int kept = part && unit >= -127 ? part_power(unit, -7) : 0;
+    const float opow = pow2_any(unit - 7 - kept);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {                 // 64 columns at a time
 #pragma unroll
@@ -731,12 +733,16 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const int tok = r / p.group, hq = s.g * p.group + r % p.group;
         const int col = (x >> 3) * (D / 8) + 8 * c + (x & 7);
         if (part == 0) {
-          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f, opow = pow2_any(unit - 7);
-          v.x = v.x * inv * opow;
-          v.y = v.y * inv * opow;
-          v.z = v.z * inv * opow;
-          v.w = v.w * inv * opow;
+          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+          v.x *= inv;
+          v.y *= inv;
+          v.z *= inv;
+          v.w *= inv;
         }
+        v.x *= opow;
+        v.y *= opow;
+        v.z *= opow;
+        v.w *= opow;
         const long long at = part ? (prow + r) * D + col : ((long long)(s.tok + tok) * p.Hq + hq) * D + col;
         if (f32) {
           *reinterpret_cast<float4*>((part ? p.part_o : static_cast<float*>(p.o)) + at) = v;
@@ -745,7 +751,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         }
         if (c == 0 && x == 0) {
           if (part)
-            *reinterpret_cast<float4*>(p.part_ml + (prow + r) * 4) = make_float4(ml.x, ml.y, ml.y, (float)(unit - 7));
+            *reinterpret_cast<float4*>(p.part_ml + (prow + r) * 4) = make_float4(ml.x, ml.y, ml.y, __int_as_float(kept));
           else
             p.lse[(long long)hq * p.T + s.tok + tok] = ml.y == 0.f ? -INFINITY : (ml.x + lg2_approx(ml.y)) * kLn2;
         }
