@@ -154,7 +154,7 @@ struct Cfg {
   static constexpr int TILE_BYTES = NB * BOX_BYTES;
   // slots: K of a step, V of the one before
   static constexpr int NS = D == 128 ? 2 : KV8 ? 4 : 5;
-  static constexpr int K_SLOT = KV8 ? 128 * D : TILE_BYTES;   // codes: K as it is, V in bf16
+  static constexpr int K_SLOT = KV8 ? 128 * D : TILE_BYTES;   // codes: K as it is, V in f16
   static constexpr int NV = D == 128 ? 3 : 4;       // codes: tiles of V's codes on their way
   static constexpr int NH = 8;                      // codes: steps whose exponents are kept
   static constexpr int Q_OFF = 0;
@@ -1472,7 +1472,7 @@ fwd_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // shows that it may stand.  P and O are floats, so a reference that
           // is too low costs no precision: a sum up to 2^40 stands, and one
           // above 2^8 raises the reference for the next tile.
-if constexpr (KV8) {
+          if constexpr (KV8) {
             // The same for 64 keys and then for the others.
             uint32_t pk[32], x[2][16];
             auto half = [&](int h) -> float {
@@ -1908,10 +1908,13 @@ int launch_impl(const PagedParams& p, cudaStream_t stream) {
   int nsm = 0;
   if (const int es = sm_count(&nsm)) return es;
   const int grid = std::min(nsm, kPagedCtas);
-  if (KV8) return launch_dependent(kern, dim3(grid), dim3(kThreads), C::SMEM_BYTES, stream, tq, tk, tv, p);
-  kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
-  if (const cudaError_t e = cudaGetLastError()) return (int)e;
-  return launch_dependent(paged_merge_kernel<D>, dim3(grid, std::max(1, (p.part_rows + 7) / 8)), dim3(256), 0, stream, p, grid);
+  if constexpr (KV8) {
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), C::SMEM_BYTES, stream, tq, tk, tv, p);
+  } else {
+    kern<<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+    if (const cudaError_t e = cudaGetLastError()) return (int)e;
+    return launch_dependent(paged_merge_kernel<D>, dim3(grid, std::max(1, (p.part_rows + 7) / 8)), dim3(256), 0, stream, p, grid);
+  }
 }
 
 template <int D, bool KV8>
