@@ -99,7 +99,9 @@
 // into a stage), warps 10 and 11 turn V, 64 rows of a tile each, and write it where
 // TMA would have.  In two-tile items a tile's P is given away in halves of 64 keys: the
 // first half's product runs while the softmax takes the second (1457 -> 1434 us), and
-// the registers of half of P suffice.
+// the registers of half of P suffice.  O stays over 2^(er - 6) until it is divided by
+// l: times it, values of 2^117 and more would have sums that are no floats.  A part
+// whose power lies that far from 1 takes it along (part_power).
 // Bound by the step's chain, softmax (1900 cycles) and products (2600 of the step's
 // 4000), as with bf16: two chunks of 2048 tokens behind 24k-32k keys, 32 heads on 8,
 // d = 128: 1430 us, 1277 TFLOP/s, 65 % of the measured cuBLAS rate.
@@ -133,14 +135,16 @@ constexpr int kUpP = 6;                // codes: P in f16 is times 2^6, ..
 constexpr float kMaxSumF16 = 1000.0f;  // .. and no more than 2^16
 constexpr int kWeightTwo = 9, kWeightOne = 8;   // of one key tile of an item
 constexpr int kHeadTwo = 36, kHeadOne = 16;     // of its Q, first tile and epilogue beside that
-// The same over codes, measured again (least squares over the CTAs of eight batches,
-// d = 128): 4075 cycles a tile of a two-tile item and 2420 of another, 21800 and 6040
-// beside them (d = 64: 3670, 2240, 14100, 4390).  A mixed batch's CTAs ended 23 %
-// after their mean with bf16's weights.
+// The same over codes, measured again (least squares over the CTAs of eight batches):
+// 4075 cycles a tile of a two-tile item and 2420 of another, 21800 and 6040 beside
+// them at d = 128, whose weights d = 64 takes too (3670, 2240, 14100, 4390: there an
+// item's head weighs 20 to 27 % too much).  A mixed batch's CTAs ended 23 % after their
+// mean with bf16's weights.
 constexpr int kWeightTwoCodes = 18, kWeightOneCodes = 11, kHeadTwoCodes = 88, kHeadOneCodes = 26;
-// Of an item of the kernel for few rows: an item more costs a CTA 7000 cycles, a
-// tile 1570 (d = 128), 3300 and 1220 (d = 64) beyond what 16 stands for (16 caches of
-// 8 heads: 132 us with 16, 125 with 44).
+// Of an item of the kernel for few rows, whose tiles are 8.  With 16 an item more cost
+// a CTA 7000 cycles beyond its weight and a tile 1570 at d = 128, 3300 and 1220 at
+// d = 64: 16 + 8 x 7000 / 1570 = 52 and 38, of which 44 lies between (16 caches of 8
+// heads: 132 us with 16, 125 with 44).
 constexpr int kHeadFew = 44;
 // A CTA's run is at least this long, so that none lies between the beginnings
 // of an item's first two tiles: an item's parts are in CTAs next to each other.

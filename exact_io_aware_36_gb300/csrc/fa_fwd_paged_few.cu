@@ -1,5 +1,6 @@
 // fa_fwd_paged_few.cu -- attention over pages of e4m3 codes where a sequence
-// brings few rows (new tokens x query heads of a kv head: at most 32), as in
+// brings few rows (new tokens x query heads of a kv head: at most 32 where no
+// sequence of the call brings more, else at most those of one token), as in
 // decoding: bound by the bytes of the cache.
 //
 //     S = scale Q K^T (+ ALiBi),   O = softmax(S) V,   k = 2^ek ck,  v = 2^ev cv
@@ -20,6 +21,7 @@
 //   P  is rounded to fp16 once (11 bits); m is a reference that a row's scores
 //      exceed by at most 2^8, and 2^7 P at most 2^15, so that P's normal range
 //      reaches down to 2^-21 and its smallest step is 2^-31.
+// O is over a power of two, that of the values it has met, until it is divided by l.
 // Both products are taken transposed (S^T = K Q^T, O^T = V^T P^T): keys and
 // elements of V fill the 16 rows of an instruction, and up to 8 rows of Q its
 // columns, so that eight rows cost half of what 16 x 8 the other way round would
@@ -38,11 +40,13 @@ namespace {
 template <int D, int NR>
 struct Few {
   static constexpr int ROWS = 8 * NR;
-  // Warps that take steps: as many as do not spill beside the two that bring the
-  // codes; O alone takes D NR / 4 registers of a lane.  Warps in all, one token of 16
-  // caches (8 rows, d = 128): 8 108.4 us, 10 107.9, 12 107.4, 14 112.7, 16 116.2; four
-  // tokens of such (16 rows): 8 99.4, 10 97.3, 12 104.8; seven tokens of 40 sequences
-  // (32 rows of 64): 8 62.5, 12 54.8; five of 32 (24 rows): 8 123, 10 203.
+  // Warps that take steps, beside the two that bring the codes; O alone takes D NR / 4
+  // registers of a lane.  9 to 12 warps in all have 168 registers a lane, 8 have 255,
+  // 13 to 16 have 128.  Measured with so many in all: one token of 16 caches (8 rows,
+  // d = 128) 8 108.4 us, 10 107.9, 12 107.4, 14 112.7, 16 116.2 (the last two spill);
+  // four tokens of such (16 rows) 8 99.4, 10 97.3, 12 104.8; seven tokens of 40
+  // sequences (32 rows of 64) 8 62.5, 12 54.8; five of 32 (24 rows) 8 123, 10 203 (it
+  // spills 404 bytes).  As chosen, 9 of the 16 instances spill 12 to 104 bytes.
   static constexpr int W = (NR * D <= 192 ? 12 : NR * D > 256 ? 8 : D == 128 ? 10 : 12) - 2;
   static constexpr int NT = 32 * (W + 2);
   // Blocks of a step that are taken together: both, unless that spills (32 rows).

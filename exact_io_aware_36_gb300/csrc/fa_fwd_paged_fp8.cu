@@ -4,10 +4,11 @@
 // Two kernels share a call: sequences that bring few rows (fa_fwd_paged_few.cu)
 // and the others (fa_fwd_paged.cuh).  The one for few rows begins on the SMs that
 // the other leaves.  Where the largest number of new tokens says that all
-// sequences are of one kind, only that kernel runs.  Up to 32 rows the one for few
-// is the faster: 16 caches of 1k-32k tokens, one token each, 114 us against 172 with
-// the other, five tokens of 32 sequences (20 rows) 123 against 139, a mixed batch 170
-// against 187 with the other alone.
+// sequences are of one kind, only that kernel runs: all of up to 32 rows, where the
+// one for few is the faster (16 caches of 1k-32k tokens, one token each, 107-115 us by
+// the box against 172 with the other; five tokens of 32 sequences, 20 rows, 123 against
+// 139).  In a batch of both kinds it has the sequences of one token (up to their rows,
+// in eights): 171 us against 187 with the other alone.
 //
 // For the others the products with the keys take the codes as they are, at twice
 // the rate of bf16, so q has to be e4m3 too: times a power of two that brings a

@@ -560,10 +560,13 @@ fa_status fa_cache_copy_fp8(void* k_pages, void* v_pages, void* k_scales, void* 
  * codes stand for, with fa_fwd_paged's arguments, masks, rows and errors and a
  * workspace of fa_fwd_paged_fp8_workspace_size bytes (total_tokens: the rows of
  * q).  Products with the keys are exact but for elements of q below 2^-9 of its
- * row's largest, which are off by at most 2^-17 of that one (for sequences that
- * bring few rows, new tokens times Hq / Hkv, 2^-22 and 2^-39).  P is rounded once,
- * to 11 bits, and what falls below 2^-30 of the row's sum, times the largest power
- * of two of the values that its block of query tokens sees, is lost.  As in the
+ * row's largest, which are off by at most 2^-17 of that one.  For sequences that
+ * bring few rows (new tokens times Hq / Hkv) these are 2^-22 and 2^-39: all of a
+ * call with N Hq / Hkv <= 32, and of another those of up to Hq / Hkv rows, rounded
+ * up to a multiple of 8, if Hq / Hkv <= 32.  P is rounded once, to 11 bits, and of O
+ * what falls below 2^-30 of the row's sum, times the largest power of two of the
+ * values that its block of query tokens sees, is lost.  The LSE does not depend on
+ * the values, and no scale makes the sum of P V overflow before its division.  As in the
  * cache in bf16, a NaN among the values may reach rows that do not see its key
  * where other rows of their block of query tokens do; slots that none of them sees
  * do not count, whatever they hold.
