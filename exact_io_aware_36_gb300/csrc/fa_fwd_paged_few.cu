@@ -673,10 +673,10 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
         if (g8 == 0) mls[warp * C::ROWS + 8 * n + 2 * c4 + j] = make_float2(mref[n][j], x);
       }
-    if (lane == 0) bars->unit[warp] = (short)eref;
+    if (lane == 0) bars->unit[warp] = (short)etop;
     meet();
-    // O stays over the warps' largest power of two until it is divided: what it is
-    // before may not be a float.
+    // O stays over the values' largest power of two that a warp met until it is divided:
+    // what it is before may not be a float.
     const int unit = __reduce_max_sync(0xffffffffu, lane < W ? (int)bars->unit[lane] : -1000);
     if (threadIdx.x < rows) {
       float M = -INFINITY, L = 0.f;

@@ -117,6 +117,20 @@ def test_many_values_at_the_ends_of_the_scales(new, group, d, byte):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new,group", MIXES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bytes_of", [(27, 246), (0, 246), (27, 100, 200, 246)])
+def test_the_largest_values_beside_the_smallest(new, group, d, bytes_of):
+    """O goes on in the units of small values where large ones came before, and is as good as ever in the end."""
+    import torch as t
+    lens, page, Hkv = [2000 - 111 * b for b in range(len(new))], 32, 2
+    q, codes, scales, table, cs, cu = state(new, lens, page, Hkv * group, Hkv, d, len(bytes_of))
+    value_scales(codes, scales, table, lens, page, 16, list(bytes_of), 255)
+    out = attend(q, codes, scales, table, cs, cu_seqlens=cu, max_seqlen=max(new), out_dtype=t.float32, check=True)
+    check(out, q, codes, scales, table, lens, new, page)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("byte", [0, 10, 26])
 @pytest.mark.parametrize("size", [2.0 ** -118, 2.0 ** -110, 2.0 ** -90, 1.0])
 def test_older_tokens_under_scales_that_no_write_makes(byte, size):
