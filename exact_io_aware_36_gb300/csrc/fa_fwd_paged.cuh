@@ -197,7 +197,7 @@ struct Bars {
   unsigned long long warp_sum[16];
   long long w0, w1, base;
   int b, g, qb;
-  short unit[16];               // few rows: the values' largest power of two that each warp met
+  int unit;                     // few rows: the values' largest power of two that a warp met in the item
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 

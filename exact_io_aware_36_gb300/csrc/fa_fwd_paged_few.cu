@@ -46,7 +46,7 @@ struct Few {
   // d = 128) 8 108.4 us, 10 107.9, 12 107.4, 14 112.7, 16 116.2 (the last two spill);
   // four tokens of such (16 rows) 8 99.4, 10 97.3, 12 104.8; seven tokens of 40
   // sequences (32 rows of 64) 8 62.5, 12 54.8; five of 32 (24 rows) 8 123, 10 203 (it
-  // spills 404 bytes).  As chosen, 9 of the 16 instances spill 12 to 104 bytes.
+  // spills 404 bytes).  As chosen, 8 of the 16 instances spill 4 to 104 bytes.
   static constexpr int W = (NR * D <= 192 ? 12 : NR * D > 256 ? 8 : D == 128 ? 10 : 12) - 2;
   static constexpr int NT = 32 * (W + 2);
   // Blocks of a step that are taken together: both, unless that spills (32 rows).
@@ -145,6 +145,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     mbar_init(&bars->never, 1);
 #endif
     bars->abort_flag = bars->part_lost[0] = bars->part_lost[1] = 0;
+    bars->unit = -1000;
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -673,11 +674,11 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         for (int q = 4; q < 32; q <<= 1) x += __shfl_xor_sync(0xffffffffu, x, q);
         if (g8 == 0) mls[warp * C::ROWS + 8 * n + 2 * c4 + j] = make_float2(mref[n][j], x);
       }
-    if (lane == 0) bars->unit[warp] = (short)etop;
+    if (lane == 0) atomicMax(&bars->unit, etop);
     meet();
     // O stays over the values' largest power of two that a warp met until it is divided:
     // what it is before may not be a float.
-    const int unit = __reduce_max_sync(0xffffffffu, lane < W ? (int)bars->unit[lane] : -1000);
+    const int unit = *(volatile int*)&bars->unit;
     if (threadIdx.x < rows) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w * C::ROWS + threadIdx.x].x);
@@ -723,6 +724,7 @@ fwd_paged_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       meet();
       const bool lost = s.lost != 0;
       if (lost && part && threadIdx.x == 0) bars->part_lost[part - 1] = 1;
+      if (threadIdx.x == 0) bars->unit = -1000;        // (read by all)
       for (int i = threadIdx.x; i < rows * 16 && !lost; i += 32 * W) {
         const int r = i >> 4, x = (i & 15) * 4;        // four columns of row r
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
